@@ -15,6 +15,9 @@ Entry points (same names as the C functions):
   msa_quantize_index_fp8, msa_index_pool_fp8, msa_index_topk_fp8, msa_forward_fp8_index,
   msa_forward_decode_paged_fp8_index,
   msa_index_prologue,
+  msa_dense_attn_decode_paged, msa_dense_attn_decode_paged_fp8,
+  msa_evict_paged, msa_evict_paged_fp8, msa_evict_workspace_size,
+  msa_add_rms_norm, msa_add_rms_norm_fp8,
   msa_workspace_size, msa_read_device_status.
 """
 from __future__ import annotations
@@ -58,6 +61,8 @@ class Op(enum.IntEnum):
     SPARSE_ATTN_DECODE_FP8 = 9
     FORWARD_FP8 = 10
     QUANTIZE_INDEX_FP8 = 12
+    DENSE_ATTN_DECODE = 13
+    DENSE_ATTN_DECODE_WEIGHT = 14
 
 
 DEVICE_TIMEOUT = 1
@@ -139,6 +144,29 @@ _lib.msa_forward_decode_paged_fp8_index.argtypes = [_P, _vp, _vp, _vp, _vp, _vp,
                                                     ctypes.c_int32, _i64, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.msa_index_prologue.restype = ctypes.c_int
 _lib.msa_index_prologue.argtypes = [_P, _vp, ctypes.c_int32, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_i32 = ctypes.c_int32
+_f32 = ctypes.c_float
+# problem, q, k, v, block table, stride, pages, weight, weight stride, o, lse, ws, bytes, stream
+_lib.msa_dense_attn_decode_paged.restype = ctypes.c_int
+_lib.msa_dense_attn_decode_paged.argtypes = [_P, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp, _vp, _sz, _vp]
+_lib.msa_dense_attn_decode_paged_fp8.restype = ctypes.c_int
+_lib.msa_dense_attn_decode_paged_fp8.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _vp,
+                                                 _vp, _sz, _vp]
+_lib.msa_evict_workspace_size.restype = ctypes.c_int
+_lib.msa_evict_workspace_size.argtypes = [_P, _i32, _i64, ctypes.POINTER(ctypes.c_size_t)]
+# problem, k, v, block table, stride, pages, weight, weight stride, budget, recent, new table, new stride, kept,
+# new weight, new weight stride, new cu_seqlens_k, ws, bytes, stream
+_lib.msa_evict_paged.restype = ctypes.c_int
+_lib.msa_evict_paged.argtypes = [_P, _vp, _vp, _vp, _i32, _i64, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _vp,
+                                 _vp, _sz, _vp]
+_lib.msa_evict_paged_fp8.restype = ctypes.c_int
+_lib.msa_evict_paged_fp8.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _i64, _i32, _i32, _vp, _i32, _vp,
+                                     _vp, _i64, _vp, _vp, _sz, _vp]
+# x, residual, gamma, rows, d_model, eps, sum, y (or y8, y_scale), stream
+_lib.msa_add_rms_norm.restype = ctypes.c_int
+_lib.msa_add_rms_norm.argtypes = [_vp, _vp, _vp, _i64, _i32, _f32, _vp, _vp, _vp]
+_lib.msa_add_rms_norm_fp8.restype = ctypes.c_int
+_lib.msa_add_rms_norm_fp8.argtypes = [_vp, _vp, _vp, _i64, _i32, _f32, _vp, _vp, _vp, _vp]
 _lib.msa_read_device_status.restype = ctypes.c_int
 _lib.msa_read_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]
 _lib.msa_set_stage_events.restype = ctypes.c_int
@@ -153,7 +181,9 @@ EXPORTED = ("msa_workspace_size", "msa_index_pool", "msa_topk_pooled", "msa_inde
             "msa_forward_decode_paged", "msa_quantize_kv_fp8", "msa_sparse_attn_prefill_fp8",
             "msa_sparse_attn_decode_fp8", "msa_forward_fp8", "msa_index_prologue",
             "msa_forward_decode_paged_fp8", "msa_quantize_index_fp8", "msa_index_pool_fp8", "msa_index_topk_fp8",
-            "msa_forward_fp8_index", "msa_forward_decode_paged_fp8_index")
+            "msa_forward_fp8_index", "msa_forward_decode_paged_fp8_index",
+            "msa_dense_attn_decode_paged", "msa_dense_attn_decode_paged_fp8", "msa_evict_workspace_size",
+            "msa_evict_paged", "msa_evict_paged_fp8", "msa_add_rms_norm", "msa_add_rms_norm_fp8")
 
 STAGES = ("plan", "index", "topk", "schedule", "attn", "combine")
 
@@ -373,6 +403,188 @@ def msa_index_prologue(problem: Problem, x, w_q, w_k, gamma_q, gamma_k, k_idx, q
                                    _ptr(gamma_q), _ptr(gamma_k), _ptr(q_idx), _ptr(k_idx), _ptr(ws), nws, _stream()),
            "msa_index_prologue")
     return q_idx
+
+
+# ---------------------------------------------------------------- dense decode attention, eviction, norm
+def _is(t, dtype, shape, name):
+    """A contiguous tensor of this type and shape (None = any size) on the current CUDA device."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        _need(t, dtype, name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if len(t.shape) != len(shape) or any(want is not None and n != want for n, want in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+
+
+def _paged(problem, dtype, k_cache, v_cache, block_table):
+    """Checks a paged cache and its table; returns the number of pages."""
+    _is(k_cache, dtype, (None, problem.hkv, 128), "k_cache")
+    _is(v_cache, dtype, k_cache.shape, "v_cache")
+    _is(block_table, torch.int32, (problem.num_seqs, None), "block_table")
+    _is(problem.cu_k, torch.int32, (None,), "cu_k")
+    if k_cache.shape[0] % 128:
+        raise ValueError("the caches must be whole pages of 128 rows")
+    return k_cache.shape[0] // 128
+
+
+def _scales(problem, pages, k_scale, v_scale):
+    _is(k_scale, torch.float32, (pages, problem.hkv), "k_scale")
+    _is(v_scale, torch.float32, (pages, problem.hkv), "v_scale")
+
+
+def _raw_stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _dense(problem, q, k, v, scales, block_table, weight, o, lse, ws):
+    pages = _paged(problem, torch.uint8 if scales else torch.bfloat16, k, v, block_table)
+    S, hq = problem.num_seqs, problem.hq
+    _is(q, torch.bfloat16, (S, hq, 128), "q")
+    stride = 0
+    if weight is not None:
+        _is(weight, torch.float32, (S, problem.hkv, None), "weight")
+        stride = weight.shape[2]
+    if o is None:
+        o = torch.empty_like(q)
+    else:
+        _is(o, torch.bfloat16, (S, hq, 128), "o")
+    if lse is None:
+        lse = torch.empty((S, hq), dtype=torch.float32, device=q.device)
+    else:
+        _is(lse, torch.float32, (S, hq), "lse")
+    ws, nws = _ws(problem, Op.DENSE_ATTN_DECODE if weight is None else Op.DENSE_ATTN_DECODE_WEIGHT, ws)
+    tail = (block_table.data_ptr(), block_table.shape[1], pages, None if weight is None else weight.data_ptr(), stride,
+            o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws, _raw_stream())
+    if scales:
+        _scales(problem, pages, *scales)
+        _check(_lib.msa_dense_attn_decode_paged_fp8(problem.c(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                                    scales[0].data_ptr(), scales[1].data_ptr(), *tail),
+               "msa_dense_attn_decode_paged_fp8")
+    else:
+        _check(_lib.msa_dense_attn_decode_paged(problem.c(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *tail),
+               "msa_dense_attn_decode_paged")
+    return o, lse
+
+
+def msa_dense_attn_decode_paged(problem: Problem, q, k_cache, v_cache, block_table, weight=None, o=None, lse=None,
+                                ws=None):
+    """Attention of one new token per sequence over every key of its paged cache ([num_pages * 128, Hkv, 128] rows,
+    block_table int32 [num_seqs, max_blocks]); any group size up to 128, cached lengths from 0 (o = 0, lse = -inf).
+    ``weight`` (fp32 [num_seqs, Hkv, >= max_k]) is added to in place: each cached key's attention weight, summed over
+    the group's heads.  Returns (o [num_seqs, Hq, 128] bf16, lse [num_seqs, Hq] fp32).  Workspace: op
+    DENSE_ATTN_DECODE, or DENSE_ATTN_DECODE_WEIGHT with a weight."""
+    return _dense(problem, q, k_cache, v_cache, None, block_table, weight, o, lse, ws)
+
+
+def msa_dense_attn_decode_paged_fp8(problem: Problem, q, k8_cache, v8_cache, k_scale, v_scale, block_table,
+                                    weight=None, o=None, lse=None, ws=None):
+    """msa_dense_attn_decode_paged over E4M3 pages (uint8 codes) with k_scale / v_scale [num_pages, Hkv]."""
+    return _dense(problem, q, k8_cache, v8_cache, (k_scale, v_scale), block_table, weight, o, lse, ws)
+
+
+def msa_evict_workspace_size(problem: Problem, budget: int, num_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.msa_evict_workspace_size(problem.c(), budget, num_pages, ctypes.byref(n)), "msa_evict_workspace_size")
+    return int(n.value)
+
+
+def evict_workspace(problem: Problem, budget: int, num_pages: int, device=None) -> torch.Tensor:
+    """A device buffer for msa_evict_paged and msa_evict_paged_fp8 over caches of ``num_pages`` pages."""
+    return torch.empty(msa_evict_workspace_size(problem, budget, num_pages), dtype=torch.uint8,
+                       device=device or problem.cu_k.device)
+
+
+def _evict(problem, k, v, scales, block_table, weight, new_block_table, budget, recent, kept, new_weight, new_cu_k, ws):
+    pages = _paged(problem, torch.uint8 if scales else torch.bfloat16, k, v, block_table)
+    S, hkv = problem.num_seqs, problem.hkv
+    _is(weight, torch.float32, (S, hkv, None), "weight")
+    _is(new_block_table, torch.int32, (S, None), "new_block_table")
+    if kept is None:
+        kept = torch.empty((S, hkv, budget), dtype=torch.int32, device=k.device)
+    else:
+        _is(kept, torch.int32, (S, hkv, budget), "kept")
+    if new_weight is None:
+        new_weight = torch.zeros((S, hkv, budget), dtype=torch.float32, device=k.device)
+    else:
+        _is(new_weight, torch.float32, (S, hkv, None), "new_weight")
+    if new_cu_k is None:
+        new_cu_k = torch.empty(S + 1, dtype=torch.int32, device=k.device)
+    else:
+        _is(new_cu_k, torch.int32, (S + 1,), "new_cu_k")
+    if ws is None:
+        ws = evict_workspace(problem, budget, pages)
+    tail = (block_table.data_ptr(), block_table.shape[1], pages, weight.data_ptr(), weight.shape[2], budget, recent,
+            new_block_table.data_ptr(), new_block_table.shape[1], kept.data_ptr(), new_weight.data_ptr(),
+            new_weight.shape[2], new_cu_k.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream())
+    if scales:
+        _scales(problem, pages, *scales)
+        _check(_lib.msa_evict_paged_fp8(problem.c(), k.data_ptr(), v.data_ptr(), scales[0].data_ptr(),
+                                        scales[1].data_ptr(), *tail), "msa_evict_paged_fp8")
+    else:
+        _check(_lib.msa_evict_paged(problem.c(), k.data_ptr(), v.data_ptr(), *tail), "msa_evict_paged")
+    return kept, new_weight, new_cu_k
+
+
+def msa_evict_paged(problem: Problem, k_cache, v_cache, block_table, weight, new_block_table, budget: int,
+                    recent: int = 0, kept=None, new_weight=None, new_cu_k=None, ws=None):
+    """Eviction by accumulated attention weight: per (sequence, KV head) the last ``recent`` slots and the others with
+    the largest ``weight`` (equal weights to the lower slot), ``budget`` in all, gathered in order into the pages of
+    ``new_block_table`` (pages of the same caches, apart from those of ``block_table``).  Returns (kept slots int32
+    [num_seqs, Hkv, budget], -1 padded; their weights [num_seqs, Hkv, budget], zeros behind the new length; prefix
+    sums of the new lengths int32 [num_seqs + 1]).  Workspace: evict_workspace."""
+    return _evict(problem, k_cache, v_cache, None, block_table, weight, new_block_table, budget, recent, kept,
+                  new_weight, new_cu_k, ws)
+
+
+def msa_evict_paged_fp8(problem: Problem, k8_cache, v8_cache, k_scale, v_scale, block_table, weight, new_block_table,
+                        budget: int, recent: int = 0, kept=None, new_weight=None, new_cu_k=None, ws=None):
+    """msa_evict_paged over E4M3 pages: the rows of a new page are rounded again at its scale (written to k_scale and
+    v_scale [num_pages, Hkv])."""
+    return _evict(problem, k8_cache, v8_cache, (k_scale, v_scale), block_table, weight, new_block_table, budget,
+                  recent, kept, new_weight, new_cu_k, ws)
+
+
+def _norm_args(x, gamma, residual, sum_out):
+    width = x.shape[-1]
+    _is(x, torch.bfloat16, x.shape, "x")
+    _is(gamma, torch.bfloat16, (width,), "gamma")
+    if residual is not None:
+        _is(residual, torch.bfloat16, x.shape, "residual")
+    if sum_out is None:
+        sum_out = torch.empty_like(x)
+    else:
+        _is(sum_out, torch.bfloat16, x.shape, "sum_out")
+    return (x.data_ptr(), None if residual is None else residual.data_ptr(), gamma.data_ptr(),
+            x.numel() // width if width else 0, width), sum_out
+
+
+def msa_add_rms_norm(x, gamma, residual=None, eps: float = 1e-6, sum_out=None, y=None):
+    """h = x + residual in fp32; returns (bf16(h), bf16(h / sqrt(mean(h^2) + eps) * gamma)) over the last dimension.
+    ``sum_out`` may be x or residual (in place)."""
+    args, sum_out = _norm_args(x, gamma, residual, sum_out)
+    if y is None:
+        y = torch.empty_like(x)
+    else:
+        _is(y, torch.bfloat16, x.shape, "y")
+    _check(_lib.msa_add_rms_norm(*args, eps, sum_out.data_ptr(), y.data_ptr(), _raw_stream()), "msa_add_rms_norm")
+    return sum_out, y
+
+
+def msa_add_rms_norm_fp8(x, gamma, residual=None, eps: float = 1e-6, sum_out=None, y8=None, y_scale=None):
+    """msa_add_rms_norm with the norm as E4M3 codes (uint8) and one fp32 scale per row (max |y| / 448, 1 when 0).
+    Returns (sum, y8, y_scale)."""
+    args, sum_out = _norm_args(x, gamma, residual, sum_out)
+    if y8 is None:
+        y8 = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    else:
+        _is(y8, torch.uint8, x.shape, "y8")
+    if y_scale is None:
+        y_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    else:
+        _is(y_scale, torch.float32, x.shape[:-1], "y_scale")
+    _check(_lib.msa_add_rms_norm_fp8(*args, eps, sum_out.data_ptr(), y8.data_ptr(), y_scale.data_ptr(),
+                                     _raw_stream()), "msa_add_rms_norm_fp8")
+    return sum_out, y8, y_scale
 
 
 # ---------------------------------------------------------------- fp8 K/V

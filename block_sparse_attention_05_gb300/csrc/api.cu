@@ -254,11 +254,11 @@ bool map_2d_u8(CUtensorMap& m, const void* ptr, long long rows, int cols, int bo
   return make_map(m, ptr, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
-// E4M3 codes [n, heads, 128] (one byte each), box = 128 codes x 1 head x 128 rows
-bool map_3d_u8(CUtensorMap& m, const void* ptr, long long n, int heads) {
+// E4M3 codes [n, heads, 128] (one byte each), box = 128 codes x 1 head x box_rows rows
+bool map_3d_u8(CUtensorMap& m, const void* ptr, long long n, int heads, int box_rows = 128) {
   cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n > 0 ? n : 1)};
   cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(heads) * 128};
-  cuuint32_t box[3] = {128, 1, 128};
+  cuuint32_t box[3] = {128, 1, static_cast<cuuint32_t>(box_rows)};
   return make_map(m, ptr, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
@@ -611,6 +611,234 @@ msa_status_t run_attn_decode(const msa_problem_t* p, Ctx& c, const void* q, cons
   return run_combine(p, c, idx, o, lse, false);
 }
 
+// ---------------------------------------------------------------- dense decode attention and eviction
+// A decode batch over a paged cache without the index: index_dim and topk of the problem are not looked at, any
+// group of up to 128 heads is taken, and a sequence may have no cached key.
+struct PagedDecode {
+  int S, N, hkv, G, max_k, max_nb;
+  float scale;
+};
+
+msa_status_t derive_paged(const msa_problem_t* p, PagedDecode& d) {
+  if (!p) return MSA_ERR_INVALID_ARG;
+  if (p->num_seqs < 1 || !p->cu_seqlens_k) return MSA_ERR_INVALID_ARG;
+  if (p->total_q != p->num_seqs || p->max_seqlen_q != 1) return MSA_ERR_INVALID_ARG;  // one query per sequence
+  if (p->total_k < 0 || p->max_seqlen_k < 0 || p->max_seqlen_k > p->total_k) return MSA_ERR_INVALID_ARG;
+  if (p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->num_q_heads % p->num_kv_heads) return MSA_ERR_INVALID_ARG;
+  if (p->head_dim <= 0 || p->block_size <= 0) return MSA_ERR_INVALID_ARG;
+  if (!(p->softmax_scale == p->softmax_scale) || std::isinf(p->softmax_scale)) return MSA_ERR_INVALID_ARG;
+  if (p->head_dim != 128 || p->block_size != 128) return MSA_ERR_UNSUPPORTED;
+  d.S = p->num_seqs;
+  d.N = p->total_k;
+  d.hkv = p->num_kv_heads;
+  d.G = p->num_q_heads / p->num_kv_heads;
+  if (d.G > 128 || d.hkv > 1024 || d.S > (1 << 20)) return MSA_ERR_UNSUPPORTED;
+  d.max_k = p->max_seqlen_k;
+  d.max_nb = (d.max_k + 127) / 128;
+  d.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
+  return MSA_OK;
+}
+
+struct DenseLayout {
+  size_t hdr, part_o, part_ml, meta, flags, logits, norm, total;
+};
+
+// The split never has more than dense_max_runs runs, so the size needs no device.
+int dense_max_runs(const PagedDecode& d) { return d.hkv >= kDenseMaxCtas ? 1 : kDenseMaxCtas / d.hkv; }
+long long dense_max_units(const PagedDecode& d) { return static_cast<long long>(d.N) / kDenseTile + d.S; }
+
+DenseLayout dense_layout(const PagedDecode& d, bool weight) {
+  DenseLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes);
+    return at;
+  };
+  const size_t ctas = static_cast<size_t>(dense_max_runs(d)) * d.hkv;
+  L.hdr = take(sizeof(WsHeader));
+  L.part_o = take(ctas * 2 * d.G * kHeadDim * sizeof(float));
+  L.part_ml = take(ctas * 2 * d.G * sizeof(float2));
+  L.meta = take(ctas * sizeof(int2));
+  L.flags = take(ctas * sizeof(uint32_t));
+  if (weight) {
+    L.logits = take(static_cast<size_t>(dense_max_units(d)) * d.hkv * d.G * kDenseTile * sizeof(float));
+    L.norm = take(static_cast<size_t>(d.S) * d.hkv * d.G * sizeof(float2));
+  }
+  L.total = off;
+  return L;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A block table and the pages it names (every argument that the paged calls share).
+msa_status_t check_paged(const PagedDecode& d, const void* k, const void* v, const int32_t* block_table,
+                         int32_t max_blocks_per_seq, int64_t num_pages) {
+  if (!k || !v || !block_table) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(block_table)) return MSA_ERR_ALIGNMENT;
+  if (num_pages < 1 || num_pages * 128 >= (1LL << 31)) return MSA_ERR_INVALID_ARG;
+  if (max_blocks_per_seq < d.max_nb) return MSA_ERR_INVALID_ARG;  // a row must hold every block of the longest sequence
+  return MSA_OK;
+}
+
+msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const void* k, const void* v,
+                          const float* k_scale, const float* v_scale, bool fp8, const int32_t* block_table,
+                          int32_t max_blocks_per_seq, int64_t num_pages, float* weight, int64_t weight_stride,
+                          void* o, float* lse, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  t_stage = -1;
+  t_error_detail[0] = 0;
+  PagedDecode d;
+  msa_status_t st = derive_paged(problem, d);
+  if (st != MSA_OK) return st;
+  if (!q || !o || !lse) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(o) || !aligned16(lse)) return MSA_ERR_ALIGNMENT;
+  if ((st = check_paged(d, k, v, block_table, max_blocks_per_seq, num_pages)) != MSA_OK) return st;
+  if (fp8 && (!k_scale || !v_scale)) return MSA_ERR_INVALID_ARG;
+  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(weight)) return MSA_ERR_ALIGNMENT;
+  if (weight && weight_stride < d.max_k) return MSA_ERR_INVALID_ARG;
+  const DenseLayout L = dense_layout(d, weight != nullptr);
+  if (!ws || ws_bytes < L.total) return MSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
+  DeviceFacts dev;
+  if ((st = device_facts(dev)) != MSA_OK) return st;
+  CUtensorMap tk, tv;
+  const long long rows = num_pages * 128;
+  if (fp8 ? (!map_3d_u8(tk, k, rows, d.hkv, kDenseTile) || !map_3d_u8(tv, v, rows, d.hkv, kDenseTile))
+          : (!map_3d(tk, k, rows, d.hkv, 1, kDenseTile) || !map_3d(tv, v, rows, d.hkv, 1, kDenseTile)))
+    return MSA_ERR_CUDA;
+  DenseDecodeParams p{};
+  p.num_seqs = d.S;
+  p.hkv = d.hkv;
+  p.group = d.G;
+  p.max_k = d.max_k;
+  p.total_k = d.N;
+  long long runs = static_cast<long long>(dense_decode_ctas_per_sm(d.G)) * dev.sms / d.hkv;
+  if (runs > dense_max_runs(d)) runs = dense_max_runs(d);
+  if (runs > dense_max_units(d)) runs = dense_max_units(d);
+  if (runs < 1) runs = 1;
+  p.groups = static_cast<int>(runs);
+  p.cu_k = problem->cu_seqlens_k;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.block_table = block_table;
+  p.bt_stride = max_blocks_per_seq;
+  p.n_pages = num_pages;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.o = static_cast<__nv_bfloat16*>(o);
+  p.lse = lse;
+  p.weight = weight;
+  p.weight_stride = weight_stride;
+  p.scale_log2 = d.scale * 1.4426950408889634f;
+  p.hdr = at<WsHeader>(ws, L.hdr);
+  p.part_o = at<float>(ws, L.part_o);
+  p.part_ml = at<float2>(ws, L.part_ml);
+  p.meta = at<int2>(ws, L.meta);
+  p.flags = at<uint32_t>(ws, L.flags);
+  p.logits = weight ? at<float>(ws, L.logits) : nullptr;
+  p.norm = weight ? at<float2>(ws, L.norm) : nullptr;
+  StageScope scope(MSA_STAGE_ATTN, reinterpret_cast<cudaStream_t>(stream));
+  return cuda_status(launch_dense_decode(tk, tv, p, fp8, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status_t check_evict(const msa_problem_t* problem, int32_t budget, int64_t num_pages, PagedDecode& d) {
+  const msa_status_t st = derive_paged(problem, d);
+  if (st != MSA_OK) return st;
+  if (budget < 1) return MSA_ERR_INVALID_ARG;
+  if (num_pages < 1 || num_pages * 128 >= (1LL << 31)) return MSA_ERR_INVALID_ARG;
+  return MSA_OK;
+}
+
+size_t evict_bytes(int64_t num_pages) {
+  return align_up(sizeof(WsHeader)) + align_up(sizeof(uint32_t) * static_cast<size_t>(num_pages));
+}
+
+msa_status_t evict(const msa_problem_t* problem, void* k, void* v, float* k_scale, float* v_scale, bool fp8,
+                   const int32_t* block_table, int32_t max_blocks_per_seq, int64_t num_pages, const float* weight,
+                   int64_t weight_stride, int32_t budget, int32_t recent, const int32_t* new_block_table,
+                   int32_t new_max_blocks_per_seq, int32_t* kept, float* new_weight, int64_t new_weight_stride,
+                   int32_t* new_cu_seqlens_k, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  t_stage = -1;
+  t_error_detail[0] = 0;
+  PagedDecode d;
+  msa_status_t st = check_evict(problem, budget, num_pages, d);
+  if (st != MSA_OK) return st;
+  if ((st = check_paged(d, k, v, block_table, max_blocks_per_seq, num_pages)) != MSA_OK) return st;
+  if (!weight || !new_block_table || !kept || !new_weight || !new_cu_seqlens_k) return MSA_ERR_INVALID_ARG;
+  if (fp8 && (!k_scale || !v_scale)) return MSA_ERR_INVALID_ARG;
+  if (!aligned4(k_scale) || !aligned4(v_scale) || !aligned4(weight) || !aligned4(new_block_table) ||
+      !aligned4(kept) || !aligned4(new_weight) || !aligned4(new_cu_seqlens_k))
+    return MSA_ERR_ALIGNMENT;
+  if (recent < 0 || recent > budget) return MSA_ERR_INVALID_ARG;
+  const int new_max = d.max_k < budget ? d.max_k : budget;
+  const int new_blocks = (new_max + 127) / 128;
+  if (weight_stride < d.max_k || new_weight_stride < new_max || new_max_blocks_per_seq < new_blocks)
+    return MSA_ERR_INVALID_ARG;
+  if (new_weight == weight || new_cu_seqlens_k == problem->cu_seqlens_k) return MSA_ERR_INVALID_ARG;
+  if (static_cast<long long>(d.S) * d.hkv > 0x7FFFFFFFLL || static_cast<long long>(d.S) * new_blocks > 0x7FFFFFFFLL)
+    return MSA_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < evict_bytes(num_pages)) return MSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
+  DeviceFacts dev;
+  if ((st = device_facts(dev)) != MSA_OK) return st;
+  EvictParams p{};
+  p.num_seqs = d.S;
+  p.hkv = d.hkv;
+  p.max_k = d.max_k;
+  p.total_k = d.N;
+  p.budget = budget;
+  p.recent = recent;
+  p.new_blocks = new_blocks;
+  p.cu_k = problem->cu_seqlens_k;
+  p.k = k;
+  p.v = v;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.block_table = block_table;
+  p.bt_stride = max_blocks_per_seq;
+  p.new_table = new_block_table;
+  p.new_stride = new_max_blocks_per_seq;
+  p.n_pages = num_pages;
+  p.weight = weight;
+  p.weight_stride = weight_stride;
+  p.new_weight = new_weight;
+  p.new_weight_stride = new_weight_stride;
+  p.kept = kept;
+  p.new_cu_k = new_cu_seqlens_k;
+  p.hdr = at<WsHeader>(ws, 0);
+  p.marks = at<uint32_t>(ws, align_up(sizeof(WsHeader)));
+  p.clear_bytes = evict_bytes(num_pages);
+  return cuda_status(launch_evict(p, fp8, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status_t add_rms_norm(const void* x, const void* residual, const void* gamma, int64_t rows, int32_t d_model,
+                          float eps, void* sum, void* y, void* y8, float* y_scale, bool fp8, msa_stream_t stream) {
+  t_stage = -1;
+  t_error_detail[0] = 0;
+  if (rows < 0 || d_model < 1 || !(eps >= 0.f) || std::isinf(eps)) return MSA_ERR_INVALID_ARG;
+  if (d_model > (1 << 16) || rows > 0x7FFFFFFFLL) return MSA_ERR_UNSUPPORTED;
+  if (rows == 0) return MSA_OK;
+  if (!x || !gamma) return MSA_ERR_INVALID_ARG;
+  if (fp8 ? (!y8 || !y_scale) : !y) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(gamma) || !aligned16(sum) || !aligned16(y) ||
+      !aligned16(y8) || !aligned4(y_scale))
+    return MSA_ERR_ALIGNMENT;
+  DeviceFacts dev;
+  const msa_status_t st = device_facts(dev);
+  if (st != MSA_OK) return st;
+  NormParams p{};
+  p.rows = rows;
+  p.width = d_model;
+  p.eps = eps;
+  p.x = static_cast<const __nv_bfloat16*>(x);
+  p.residual = static_cast<const __nv_bfloat16*>(residual);
+  p.gamma = static_cast<const __nv_bfloat16*>(gamma);
+  p.sum = static_cast<__nv_bfloat16*>(sum);
+  p.y = static_cast<__nv_bfloat16*>(y);
+  p.y8 = static_cast<uint8_t*>(y8);
+  p.scale = y_scale;
+  return cuda_status(launch_add_rms_norm(p, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 }  // namespace msa
 
@@ -719,7 +947,13 @@ const char* msa_status_string(msa_status_t s) {
 
 msa_status_t msa_workspace_size(const msa_problem_t* problem, msa_op_t op, size_t* bytes) {
   if (!bytes) return MSA_ERR_INVALID_ARG;
-  if (op < MSA_OP_INDEX_POOL || op > MSA_OP_QUANTIZE_INDEX_FP8) return MSA_ERR_INVALID_ARG;
+  if (op < MSA_OP_INDEX_POOL || op > MSA_OP_DENSE_ATTN_DECODE_WEIGHT) return MSA_ERR_INVALID_ARG;
+  if (op == MSA_OP_DENSE_ATTN_DECODE || op == MSA_OP_DENSE_ATTN_DECODE_WEIGHT) {
+    PagedDecode pd;
+    const msa_status_t ps = derive_paged(problem, pd);
+    if (ps == MSA_OK) *bytes = dense_layout(pd, op == MSA_OP_DENSE_ATTN_DECODE_WEIGHT).total;
+    return ps;
+  }
   Derived d;
   msa_status_t st = derive(problem, d);
   if (st != MSA_OK) return st;
@@ -1197,6 +1431,68 @@ msa_status_t msa_forward_decode_paged_fp8_index(const msa_problem_t* problem, co
   if ((st = run_plan(problem, c, 0)) != MSA_OK) return st;
   if ((st = run_index_decode(problem, c, q_idx8, k_idx8_cache, idx)) != MSA_OK) return st;
   return run_attn_decode(problem, c, q, k8_cache, v8_cache, idx, o, lse);
+}
+
+// ---------------------------------------------------------------- dense decode attention, eviction, norm
+msa_status_t msa_dense_attn_decode_paged(const msa_problem_t* problem, const void* q, const void* k_cache,
+                                         const void* v_cache, const int32_t* block_table, int32_t max_blocks_per_seq,
+                                         int64_t num_pages, float* weight, int64_t weight_stride, void* o, float* lse,
+                                         void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  return dense_decode(problem, q, k_cache, v_cache, nullptr, nullptr, false, block_table, max_blocks_per_seq,
+                      num_pages, weight, weight_stride, o, lse, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_dense_attn_decode_paged_fp8(const msa_problem_t* problem, const void* q, const void* k8_cache,
+                                             const void* v8_cache, const float* k_scale, const float* v_scale,
+                                             const int32_t* block_table, int32_t max_blocks_per_seq,
+                                             int64_t num_pages, float* weight, int64_t weight_stride, void* o,
+                                             float* lse, void* workspace, size_t workspace_bytes,
+                                             msa_stream_t stream) {
+  return dense_decode(problem, q, k8_cache, v8_cache, k_scale, v_scale, true, block_table, max_blocks_per_seq,
+                      num_pages, weight, weight_stride, o, lse, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_evict_workspace_size(const msa_problem_t* problem, int32_t budget, int64_t num_pages,
+                                      size_t* bytes) {
+  if (!bytes) return MSA_ERR_INVALID_ARG;
+  PagedDecode d;
+  const msa_status_t st = check_evict(problem, budget, num_pages, d);
+  if (st == MSA_OK) *bytes = evict_bytes(num_pages);
+  return st;
+}
+
+msa_status_t msa_evict_paged(const msa_problem_t* problem, void* k_cache, void* v_cache, const int32_t* block_table,
+                             int32_t max_blocks_per_seq, int64_t num_pages, const float* weight,
+                             int64_t weight_stride, int32_t budget, int32_t recent, const int32_t* new_block_table,
+                             int32_t new_max_blocks_per_seq, int32_t* kept, float* new_weight,
+                             int64_t new_weight_stride, int32_t* new_cu_seqlens_k, void* workspace,
+                             size_t workspace_bytes, msa_stream_t stream) {
+  return evict(problem, k_cache, v_cache, nullptr, nullptr, false, block_table, max_blocks_per_seq, num_pages, weight,
+               weight_stride, budget, recent, new_block_table, new_max_blocks_per_seq, kept, new_weight,
+               new_weight_stride, new_cu_seqlens_k, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_evict_paged_fp8(const msa_problem_t* problem, void* k8_cache, void* v8_cache, float* k_scale,
+                                 float* v_scale, const int32_t* block_table, int32_t max_blocks_per_seq,
+                                 int64_t num_pages, const float* weight, int64_t weight_stride, int32_t budget,
+                                 int32_t recent, const int32_t* new_block_table, int32_t new_max_blocks_per_seq,
+                                 int32_t* kept, float* new_weight, int64_t new_weight_stride,
+                                 int32_t* new_cu_seqlens_k, void* workspace, size_t workspace_bytes,
+                                 msa_stream_t stream) {
+  return evict(problem, k8_cache, v8_cache, k_scale, v_scale, true, block_table, max_blocks_per_seq, num_pages,
+               weight, weight_stride, budget, recent, new_block_table, new_max_blocks_per_seq, kept, new_weight,
+               new_weight_stride, new_cu_seqlens_k, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_add_rms_norm(const void* x, const void* residual, const void* gamma, int64_t rows, int32_t d_model,
+                              float eps, void* sum, void* y, msa_stream_t stream) {
+  return add_rms_norm(x, residual, gamma, rows, d_model, eps, sum, y, nullptr, nullptr, false, stream);
+}
+
+msa_status_t msa_add_rms_norm_fp8(const void* x, const void* residual, const void* gamma, int64_t rows,
+                                  int32_t d_model, float eps, void* sum, void* y8, float* y_scale,
+                                  msa_stream_t stream) {
+  return add_rms_norm(x, residual, gamma, rows, d_model, eps, sum, nullptr, y8, y_scale, true, stream);
 }
 
 msa_status_t msa_read_device_status(const void* workspace, uint32_t* flags, msa_stream_t stream) {

@@ -1,0 +1,856 @@
+// dense_decode.cu -- attention of one new token per sequence over every key of
+// a paged cache (the full-attention layers beside the sparse ones), and the
+// accumulation of each cached key's attention weight.
+//
+// For query head h of KV head g and cached key j (log2 units, c = scale * log2 e):
+//   s[h,j] = c q_h . k_j,  m_h = max_j s,  l_h = sum_j 2^(s - m),
+//   o_h = sum_j 2^(s - m) v_j / l_h,  lse_h = (m + log2 l) ln 2,
+//   weight[g,j] += sum over the group's heads of 2^(s[h,j] - m_h) / l_h.
+//
+// Bound: K and V are read once and each value meets G query heads (4 G flops a
+// byte in bf16, 64 at G = 16), so HBM bounds the call until G nears 128.
+//
+// Work split: a unit is 64 keys of one sequence.  All units of the batch, in
+// order, are cut into `groups` equal runs and CTA (run, KV head) takes one:
+// every CTA streams the same number of bytes whatever the lengths, and the CTAs
+// of the KV heads walk the same pages at the same time (a page's rows hold all
+// heads).  A sequence that lies inside one run is finished by its CTA; one that
+// crosses runs leaves an unnormalised partial (O, m, l) per run, and the join
+// kernel merges them.  A run has at most one sequence that continues from the
+// run before and one that continues in the next, so two partial slots per CTA
+// are enough whatever the batch.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace msa {
+
+namespace {
+
+constexpr int kTile = kDenseTile;  // keys of a unit and of a ring stage
+constexpr float kLn2 = 0.6931471805599453f;
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+// D += A(16x16, row) * B(16x8, col), bf16 or fp16 inputs, fp32 accumulate.
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (F16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// 2^(a - b) with 0 for a = -inf whatever b (b may be -inf too)
+__device__ __forceinline__ float exp2_diff(float a, float b) {
+  return a == -INFINITY ? 0.0f : exp2_approx(a - b);
+}
+// 1 / l of a sum of weights; 0 when every weight is 0 (all logits -inf), as for a row without keys
+__device__ __forceinline__ float inverse(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+// what turns a logit of the row into its weight: (maximum, 1 / sum)
+__device__ __forceinline__ float2 row_norm(float m, float l) {
+  return make_float2(m == -INFINITY ? 0.0f : m, inverse(l));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// (a, b) as a bf16 pair plus a bf16 pair of what its rounding left
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_bf16(a - __low2float(h), b - __high2float(h));
+}
+// two E4M3 codes (low 16 bits) -> fp16 pair; exact
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(codes)));
+  return r;
+}
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// ---------------------------------------------------------------- the run of a CTA
+struct Run {
+  long long lo, hi, total;  // units [lo, hi) of `total`
+  int runs;                 // runs that hold units: min(groups, total)
+  int seq;                  // sequence of unit lo
+  int off;                  // lo's unit within it
+};
+struct RunSmem {
+  int warp_sum[32];
+  int seq, off;
+};
+
+__device__ __forceinline__ int units_of(int len) { return (len + kTile - 1) / kTile; }
+
+// Cuts the batch's units and finds run g of `groups`.  Every thread of the CTA
+// calls it; returns false (for every thread) when cu_seqlens contradict the host sizes.
+__device__ bool find_run(const int32_t* cu, int num_seqs, int max_k, int total_k, int g, int groups, RunSmem& sm,
+                         Run& r) {
+  const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = T >> 5;
+  const int per = (num_seqs + T - 1) / T;
+  const int s0 = min(num_seqs, t * per), s1 = min(num_seqs, s0 + per);
+  int sum = 0;
+  bool bad = t == 0 && (cu[0] != 0 || cu[num_seqs] != total_k);
+  int prev = s0 < s1 ? cu[s0] : 0;
+  for (int s = s0; s < s1; ++s) {
+    const int next = cu[s + 1], len = next - prev;
+    bad |= prev < 0 || next < prev || len > max_k;
+    sum += units_of(len);
+    prev = next;
+  }
+  if (__syncthreads_or(bad)) return false;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) sm.warp_sum[warp] = incl;
+  __syncthreads();
+  int base = 0, total = 0;
+  for (int w = 0; w < nw; ++w) {
+    const int v = sm.warp_sum[w];
+    if (w < warp) base += v;
+    total += v;
+  }
+  base += incl - sum;  // units before this thread's sequences
+  r.total = total;
+  r.runs = min(groups, total);
+  r.lo = g < r.runs ? r.total * g / r.runs : r.total;
+  r.hi = g < r.runs ? r.total * (g + 1) / r.runs : r.total;
+  if (r.lo < r.hi && base <= r.lo && r.lo < base + sum) {  // one thread
+    int u = base, s = s0;
+    for (;; ++s) {
+      const int n = units_of(cu[s + 1] - cu[s]);
+      if (u + n > r.lo) break;
+      u += n;
+    }
+    sm.seq = s;
+    sm.off = static_cast<int>(r.lo - u);
+  }
+  __syncthreads();
+  r.seq = sm.seq;
+  r.off = sm.off;
+  return true;
+}
+
+// Walks a run's segments: the parts of its sequences that it covers.
+struct Segment {
+  int seq, len, off, count;  // units [off, off + count) of a sequence of `len` keys
+  long long unit;            // the first one's number in the batch
+  bool first, last;          // begins / ends the sequence
+};
+struct Walker {
+  const int32_t* cu;
+  long long at, hi;
+  int seq, off;
+  __device__ Walker(const int32_t* cu_, const Run& r) : cu(cu_), at(r.lo), hi(r.hi), seq(r.seq), off(r.off) {}
+  __device__ bool next(Segment& g) {
+    if (at >= hi) return false;
+    int len, n;
+    for (;;) {
+      len = cu[seq + 1] - cu[seq];
+      n = units_of(len);
+      if (off < n) break;
+      ++seq;  // an empty sequence
+      off = 0;
+    }
+    const long long left = hi - at;
+    g.seq = seq;
+    g.len = len;
+    g.off = off;
+    g.count = static_cast<int>(n - off < left ? n - off : left);
+    g.unit = at;
+    g.first = off == 0;
+    g.last = off + g.count == n;
+    at += g.count;
+    ++seq;
+    off = 0;
+    return true;
+  }
+};
+
+// ---------------------------------------------------------------- split kernel
+// MG head tiles of 16 rows by KG key tiles of 16: MG * KG compute warps, warp
+// (mg, kg) taking heads 16 mg .. of the group and keys 16 kg, 16 (kg + KG), ..
+// of a unit, and one warp that feeds the ring.
+template <int MG, bool FP8>
+struct SplitCfg {
+  static constexpr int kKG = MG <= 2 ? 4 : 8 / MG;
+  static constexpr int kWarps = MG * kKG;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static constexpr int kCtasPerSm = MG == 1 ? 2 : 1;
+  static constexpr int kRowBytes = FP8 ? 128 : 256;
+  static constexpr int kHalf = kTile * kRowBytes;  // K or V of a stage
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = (MG == 1 ? 3 : 6) * (FP8 ? 2 : 1);
+  static constexpr int kExchange = kKG > 1 ? kWarps * 4096 : 0;  // half of each warp's O
+  static constexpr int kMl = kWarps * 16 * 8;
+  static constexpr size_t kSmem = kStages * kStage + kExchange + kMl + kStages * 24 + 16 + sizeof(RunSmem);
+};
+
+// Byte offset of (row, 16-byte chunk) in a stage's K or V: TMA's 128-byte
+// swizzle; bf16 rows are two 64-dim halves, each kTile rows of 128 bytes.
+__device__ __forceinline__ uint32_t tile_off(int row, int chunk) {
+  return (chunk >> 3) * (kTile * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+}
+
+template <int MG, bool FP8, bool LOGITS>
+__global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>::kCtasPerSm)
+    dense_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                       DenseDecodeParams p) {
+  using C = SplitCfg<MG, FP8>;
+  constexpr int KG = C::kKG;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* ring = smem;
+  float* xch = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kStages * C::kStage + C::kExchange);  // [warp][16] (m, l)
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage + C::kExchange + C::kMl);
+  uint64_t* empty = full + C::kStages;
+  float2* scales = reinterpret_cast<float2*>(empty + C::kStages);  // fp8: the stage's (K, V) scales
+  int* abort_flag = reinterpret_cast<int*>(scales + C::kStages);
+  uint32_t* err = reinterpret_cast<uint32_t*>(abort_flag + 1);
+  RunSmem& run_sm = *reinterpret_cast<RunSmem*>(err + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv;
+  const int G = p.group;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], C::kWarps);
+    }
+    *abort_flag = 0;
+    *err = 0;
+    fence_mbar_init();
+  }
+  Run run;
+  const bool fine = find_run(p.cu_k, p.num_seqs, p.max_k, p.total_k, g, p.groups, run_sm, run);  // synchronises
+  if (!fine) {
+    if (threadIdx.x == 0) {
+      p.flags[blockIdx.x] = kFlagBadSeqlens;
+      p.meta[blockIdx.x] = make_int2(-1, 0);
+    }
+    return;
+  }
+
+  // empty sequences: o = 0, lse = -inf
+  for (int s = g; s < p.num_seqs; s += p.groups) {
+    if (p.cu_k[s + 1] != p.cu_k[s]) continue;
+    const long long row0 = static_cast<long long>(s) * p.hkv * G + static_cast<long long>(head) * G;
+    for (int i = threadIdx.x; i < G * 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(p.o + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < G; i += C::kThreads) p.lse[row0 + i] = -INFINITY;
+  }
+
+  Walker walk(p.cu_k, run);
+  Segment sg;
+  uint32_t issued = 0;  // the feeding lane's fills
+  if (warp == C::kWarps) {
+    // ------------------------------------------------------------ producer
+    uint32_t fills = 0, bad = 0;
+    bool stopped = false;
+    while (!stopped && walk.next(sg)) {
+      const int first_page = sg.off * kTile / kBlock, last_page = (sg.off + sg.count - 1) * kTile / kBlock;
+      const int32_t* table = p.block_table + static_cast<long long>(sg.seq) * p.bt_stride;
+      int base = first_page;
+      int row = 0;
+      float sk = 1.0f, sv = 1.0f;
+      for (int u = sg.off; u < sg.off + sg.count; ++u) {
+        const int page = u * kTile / kBlock;
+        if (u == sg.off || page - base >= 32) {  // the next 32 pages' rows and scales, one per lane
+          if (u != sg.off) base += 32;
+          row = 0;
+          if (base + lane <= last_page) {
+            const int e = table[base + lane];
+            if (e < 0 || e >= p.n_pages) {
+              bad = 1;
+              row = static_cast<int>(p.n_pages) * kBlock;  // past the cache: TMA reads zeros
+            } else {
+              row = e * kBlock;
+              if (FP8) {
+                sk = p.k_scale[static_cast<long long>(e) * p.hkv + head];
+                sv = p.v_scale[static_cast<long long>(e) * p.hkv + head];
+              }
+            }
+          }
+        }
+        const int r = __shfl_sync(0xFFFFFFFFu, row, page - base) + (u * kTile) % kBlock;
+        float tk = 1.0f, tv = 1.0f;
+        if (FP8) {
+          tk = __shfl_sync(0xFFFFFFFFu, sk, page - base);
+          tv = __shfl_sync(0xFFFFFFFFu, sv, page - base);
+        }
+        if (lane == 0) {
+          const int st = fills % C::kStages;
+          const uint32_t n = fills / C::kStages;
+          if (n > 0 && !mbar_wait(&empty[st], (n - 1) & 1, abort_flag)) {
+            *abort_flag = 1;
+            atomicOr(err, kFlagTimeout);
+          } else {
+            uint8_t* dk = ring + st * C::kStage;
+            uint8_t* dv = dk + C::kHalf;
+            if (FP8) scales[st] = make_float2(tk, tv);
+            mbar_arrive_expect_tx(&full[st], C::kStage);
+            tma_load_3d(dk, &tm_k, &full[st], 0, head, r);
+            if (!FP8) tma_load_3d(dk + kTile * 128, &tm_k, &full[st], 64, head, r);
+            tma_load_3d(dv, &tm_v, &full[st], 0, head, r);
+            if (!FP8) tma_load_3d(dv + kTile * 128, &tm_v, &full[st], 64, head, r);
+            ++issued;
+          }
+        }
+        stopped = __any_sync(0xFFFFFFFFu, *reinterpret_cast<volatile int*>(abort_flag)) != 0;
+        if (stopped) break;
+        ++fills;
+      }
+    }
+    if (bad) atomicOr(err, kFlagBadIndex);
+  } else {
+    // ------------------------------------------------------------ compute
+    const int mg = warp / KG, kg = warp % KG;
+    const int t4 = lane & 3, r0 = mg * 16 + (lane >> 2), r1 = r0 + 8;  // this thread's two head rows
+    uint32_t fills = 0;
+    bool ok = true;
+    int sent_seq = -1, sent_last = 0;
+    while (walk.next(sg)) {
+      // Q fragments (A operand).  bf16: dims 16 kk + 2 t4 (+ 8); fp8: the order
+      // in which a 4-byte word of codes widens, dims 16 kk + 4 t4 .. + 3, as
+      // fp16 scaled per row by the power of two that brings max |q| to [1, 2)
+      // (exact but for values 2^-24 below the row's largest).
+      uint32_t qa[8][4];
+      float qs0 = p.scale_log2, qs1 = p.scale_log2;
+      {
+        const __nv_bfloat16* q = p.q + (static_cast<long long>(sg.seq) * p.hkv + head) * G * kHeadDim;
+        const uint32_t* q0 = reinterpret_cast<const uint32_t*>(q + r0 * kHeadDim);
+        const uint32_t* q1 = reinterpret_cast<const uint32_t*>(q + r1 * kHeadDim);
+        if (!FP8) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            qa[kk][0] = r0 < G ? q0[8 * kk + t4] : 0;
+            qa[kk][1] = r1 < G ? q1[8 * kk + t4] : 0;
+            qa[kk][2] = r0 < G ? q0[8 * kk + 4 + t4] : 0;
+            qa[kk][3] = r1 < G ? q1[8 * kk + 4 + t4] : 0;
+          }
+        } else {
+          uint32_t m0 = 0, m1 = 0;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            qa[kk][0] = r0 < G ? q0[8 * kk + 2 * t4] : 0;
+            qa[kk][1] = r1 < G ? q1[8 * kk + 2 * t4] : 0;
+            qa[kk][2] = r0 < G ? q0[8 * kk + 2 * t4 + 1] : 0;
+            qa[kk][3] = r1 < G ? q1[8 * kk + 2 * t4 + 1] : 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t w = max(qa[kk][j] & 0x7FFFu, (qa[kk][j] >> 16) & 0x7FFFu);
+              if (j & 1) m1 = max(m1, w); else m0 = max(m0, w);
+            }
+          }
+#pragma unroll
+          for (int o = 1; o < 4; o <<= 1) {
+            m0 = max(m0, __shfl_xor_sync(0xFFFFFFFFu, m0, o));
+            m1 = max(m1, __shfl_xor_sync(0xFFFFFFFFu, m1, o));
+          }
+          // exponent of the row's largest value, 0 for zero, subnormal, inf or NaN rows
+          const int x0 = static_cast<int>(m0 >> 7), x1 = static_cast<int>(m1 >> 7);
+          const int e0 = (x0 > 0 && x0 < 255) ? min(max(x0 - 127, -120), 120) : 0;
+          const int e1 = (x1 > 0 && x1 < 255) ? min(max(x1 - 127, -120), 120) : 0;
+          const float i0 = __uint_as_float(static_cast<uint32_t>(127 - e0) << 23);
+          const float i1 = __uint_as_float(static_cast<uint32_t>(127 - e1) << 23);
+          qs0 *= __uint_as_float(static_cast<uint32_t>(127 + e0) << 23);
+          qs1 *= __uint_as_float(static_cast<uint32_t>(127 + e1) << 23);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float f = (j & 1) ? i1 : i0;
+              qa[kk][j] = pack_f16(__uint_as_float(qa[kk][j] << 16) * f,
+                                   __uint_as_float(qa[kk][j] & 0xFFFF0000u) * f);
+            }
+        }
+      }
+      float o[16][4];
+#pragma unroll
+      for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
+      float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
+      float ref0 = -INFINITY, ref1 = -INFINITY;  // fp8: O's own reference (see below)
+
+      for (int u = sg.off; u < sg.off + sg.count; ++u, ++fills) {
+        const int st = fills % C::kStages;
+        if (ok && !mbar_wait_warp(&full[st], (fills / C::kStages) & 1, abort_flag)) {
+          ok = false;  // keep walking: the segments' barriers below need every warp
+          if (lane == 0) {
+            *reinterpret_cast<volatile int*>(abort_flag) = 1;
+            atomicOr(err, kFlagTimeout);
+          }
+        }
+        if (!ok) continue;
+        const uint32_t kt = smem_u32(ring + st * C::kStage), vt = kt + C::kHalf;
+        const int valid = sg.len - u * kTile;  // keys of this unit (may exceed kTile)
+        float c0 = qs0, c1 = qs1, lv = 0.0f;
+        if (FP8) {
+          const float2 sc = scales[st];
+          c0 *= sc.x;
+          c1 *= sc.x;
+          lv = log2f(sc.y);
+        }
+#pragma unroll
+        for (int sub = 0; sub < kTile / 16 / KG; ++sub) {
+          const int key0 = (sub * KG + kg) * 16;
+          if (key0 >= valid) continue;  // uniform in the warp
+          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+          const int krow = key0 + (lane & 7) + ((lane >> 4) << 3);
+          if (!FP8) {
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              uint32_t b[4];
+              ldsm_x4(kt + tile_off(krow, 2 * kk + ((lane >> 3) & 1)), b);
+              mma16<false>(s0, qa[kk], b[0], b[1]);
+              mma16<false>(s1, qa[kk], b[2], b[3]);
+            }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < 8; kk += 2) {  // one load: 16-byte chunks kk and kk + 1 of 16 keys
+              uint32_t b[4];
+              ldsm_x4(kt + tile_off(krow, kk + ((lane >> 3) & 1)), b);
+              mma16<true>(s0, qa[kk], e4m3x2_to_f16x2(b[0]), e4m3x2_to_f16x2(b[0] >> 16));
+              mma16<true>(s1, qa[kk], e4m3x2_to_f16x2(b[2]), e4m3x2_to_f16x2(b[2] >> 16));
+              mma16<true>(s0, qa[kk + 1], e4m3x2_to_f16x2(b[1]), e4m3x2_to_f16x2(b[1] >> 16));
+              mma16<true>(s1, qa[kk + 1], e4m3x2_to_f16x2(b[3]), e4m3x2_to_f16x2(b[3] >> 16));
+            }
+          }
+          const bool tail = key0 + 16 > valid;
+          if (tail) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (key0 + 2 * t4 + i >= valid) s0[i] = s0[2 + i] = -INFINITY;
+              if (key0 + 8 + 2 * t4 + i >= valid) s1[i] = s1[2 + i] = -INFINITY;
+            }
+          }
+          if (LOGITS) {
+            float* w = p.logits + ((sg.unit + (u - sg.off)) * p.hkv + head) * static_cast<long long>(G) * kTile;
+            const int at = key0 + 2 * t4;
+            if (r0 < G) {
+              *reinterpret_cast<float2*>(w + r0 * kTile + at) = make_float2(s0[0] * c0, s0[1] * c0);
+              *reinterpret_cast<float2*>(w + r0 * kTile + at + 8) = make_float2(s1[0] * c0, s1[1] * c0);
+            }
+            if (r1 < G) {
+              *reinterpret_cast<float2*>(w + r1 * kTile + at) = make_float2(s0[2] * c1, s0[3] * c1);
+              *reinterpret_cast<float2*>(w + r1 * kTile + at + 8) = make_float2(s1[2] * c1, s1[3] * c1);
+            }
+          }
+          float x0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
+          float x1 = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
+#pragma unroll
+          for (int of = 1; of < 4; of <<= 1) {
+            x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, of));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, of));
+          }
+          const float n0 = fmaxf(m0, x0 * c0), n1 = fmaxf(m1, x1 * c1);  // the factors are positive
+          float a0 = exp2_diff(m0, n0), a1 = exp2_diff(m1, n1);
+          l0 *= a0;
+          l1 *= a1;
+          m0 = n0;
+          m1 = n1;
+          // fp8: O is kept relative to its own reference, the running maximum of
+          // m + log2(V scale), so that the weights of the codes fit fp16 whatever
+          // the pages' scales: at most 2^14, with fp16's full 11 bits down to
+          // 2^-28 of the largest.
+          float f0 = 1.0f, f1 = 1.0f;
+          if (FP8) {
+            const float y0 = fmaxf(ref0, n0 + lv), y1 = fmaxf(ref1, n1 + lv);
+            a0 = exp2_diff(ref0, y0);
+            a1 = exp2_diff(ref1, y1);
+            ref0 = y0;
+            ref1 = y1;
+            f0 = exp2_diff(n0 + lv + 14.0f, y0);
+            f1 = exp2_diff(n1 + lv + 14.0f, y1);
+          }
+          if (__any_sync(0xFFFFFFFFu, a0 != 1.0f || a1 != 1.0f)) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              o[j][0] *= a0; o[j][1] *= a0; o[j][2] *= a1; o[j][3] *= a1;
+            }
+          }
+          const float e0 = n0 == -INFINITY ? 0.0f : n0, e1 = n1 == -INFINITY ? 0.0f : n1;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            s0[i] = exp2_approx(fmaf(s0[i], c0, -e0));
+            s1[i] = exp2_approx(fmaf(s1[i], c0, -e0));
+            s0[2 + i] = exp2_approx(fmaf(s0[2 + i], c1, -e1));
+            s1[2 + i] = exp2_approx(fmaf(s1[2 + i], c1, -e1));
+          }
+          l0 += (s0[0] + s0[1]) + (s1[0] + s1[1]);
+          l1 += (s0[2] + s0[3]) + (s1[2] + s1[3]);
+          // P as the A operand.  bf16 V: the weights as a bf16 value and the bf16
+          // rest (16 significant bits; one bf16 alone would add half as much error
+          // again as the output's own rounding).  fp8: one fp16 value.
+          uint32_t ph[4], pl[4];
+          if (!FP8) {
+            split_bf16(s0[0], s0[1], ph[0], pl[0]);
+            split_bf16(s0[2], s0[3], ph[1], pl[1]);
+            split_bf16(s1[0], s1[1], ph[2], pl[2]);
+            split_bf16(s1[2], s1[3], ph[3], pl[3]);
+          } else {
+            ph[0] = pack_f16(s0[0] * f0, s0[1] * f0);
+            ph[1] = pack_f16(s0[2] * f1, s0[3] * f1);
+            ph[2] = pack_f16(s1[0] * f0, s1[1] * f0);
+            ph[3] = pack_f16(s1[2] * f1, s1[3] * f1);
+          }
+          // rows past the sequence's end hold anything (0 * NaN): V words of such keys become 0
+          uint32_t k0 = 0xFFFFFFFFu, k1 = 0xFFFFFFFFu;
+          if (tail) {
+            const int a = valid - key0 - 2 * t4, b = a - 8;
+            k0 = a >= 2 ? 0xFFFFFFFFu : a == 1 ? 0xFFFFu : 0u;
+            k1 = b >= 2 ? 0xFFFFFFFFu : b == 1 ? 0xFFFFu : 0u;
+          }
+          const int vrow = key0 + (lane & 7) + (((lane >> 3) & 1) << 3);
+          if (!FP8) {
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {  // dims 8 j .. 8 j + 15
+              uint32_t b[4];
+              ldsm_x4_trans(vt + tile_off(vrow, j + (lane >> 4)), b);
+              b[0] &= k0; b[1] &= k1; b[2] &= k0; b[3] &= k1;
+              mma16<false>(o[j], ph, b[0], b[1]);
+              mma16<false>(o[j + 1], ph, b[2], b[3]);
+              mma16<false>(o[j], pl, b[0], b[1]);
+              mma16<false>(o[j + 1], pl, b[2], b[3]);
+            }
+          } else {
+            // A 16-bit word of the transposed load is two adjacent dims of one
+            // key, so a register holds (key 2 t4: dims d, d + 1; key 2 t4 + 1:
+            // d, d + 1) with d = 16 c + 2 (lane / 4): accumulator tile 2 c takes
+            // the even dims of chunk c, tile 2 c + 1 the odd ones.
+#pragma unroll
+            for (int c = 0; c < 8; c += 2) {
+              uint32_t b[4];
+              ldsm_x4_trans(vt + tile_off(vrow, c + (lane >> 4)), b);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i] & ((i & 1) ? k1 : k0), 0, 0x3120);
+              mma16<true>(o[2 * c], ph, e4m3x2_to_f16x2(b[0]), e4m3x2_to_f16x2(b[1]));
+              mma16<true>(o[2 * c + 1], ph, e4m3x2_to_f16x2(b[0] >> 16), e4m3x2_to_f16x2(b[1] >> 16));
+              mma16<true>(o[2 * c + 2], ph, e4m3x2_to_f16x2(b[2]), e4m3x2_to_f16x2(b[3]));
+              mma16<true>(o[2 * c + 3], ph, e4m3x2_to_f16x2(b[2] >> 16), e4m3x2_to_f16x2(b[3] >> 16));
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+      }
+
+      // ---- merge of the segment's KG key shares
+#pragma unroll
+      for (int of = 1; of < 4; of <<= 1) {
+        l0 += __shfl_xor_sync(0xFFFFFFFFu, l0, of);
+        l1 += __shfl_xor_sync(0xFFFFFFFFu, l1, of);
+      }
+      float b0 = 1.0f, b1 = 1.0f;  // factor of this warp's O
+      if (FP8) {
+        b0 = exp2_diff(ref0, m0 + 14.0f);
+        b1 = exp2_diff(ref1, m1 + 14.0f);
+      }
+      if (KG > 1) {
+        if (t4 == 0) {
+          ml[warp * 16 + (lane >> 2)] = make_float2(m0, l0);
+          ml[warp * 16 + 8 + (lane >> 2)] = make_float2(m1, l1);
+        }
+        named_sync(1 + mg, 32 * KG);
+        float M0 = -INFINITY, M1 = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          M0 = fmaxf(M0, ml[(mg * KG + k) * 16 + (lane >> 2)].x);
+          M1 = fmaxf(M1, ml[(mg * KG + k) * 16 + 8 + (lane >> 2)].x);
+        }
+        float L0 = 0.0f, L1 = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+          const float2 a = ml[(mg * KG + k) * 16 + (lane >> 2)], b = ml[(mg * KG + k) * 16 + 8 + (lane >> 2)];
+          L0 += a.y * exp2_diff(a.x, M0);
+          L1 += b.y * exp2_diff(b.x, M1);
+        }
+        b0 *= exp2_diff(m0, M0);
+        b1 *= exp2_diff(m1, M1);
+        m0 = M0; m1 = M1; l0 = L0; l1 = L1;
+      }
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        o[j][0] *= b0; o[j][1] *= b0; o[j][2] *= b1; o[j][3] *= b1;
+      }
+      // Butterfly: partners swap halves of their accumulator tiles, so that after
+      // log2(KG) steps warp kg holds the sums of 16 / KG tiles from `tile0`.
+      int tile0 = 0;
+      float* mine = xch + warp * 1024 + lane;
+      if (KG > 1) {
+        constexpr int d = KG / 2;
+        const bool upper = (kg & d) != 0;
+        const float* theirs = xch + (warp ^ d) * 1024 + lane;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mine[(j * 4 + i) * 32] = upper ? o[j][i] : o[j + 8][i];
+        named_sync(1 + mg, 32 * KG);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] = (upper ? o[j + 8][i] : o[j][i]) + theirs[(j * 4 + i) * 32];
+        tile0 = upper ? 8 : 0;
+      }
+      if (KG > 2) {
+        const bool upper = (kg & 1) != 0;
+        const float* theirs = xch + (warp ^ 1) * 1024 + lane;
+        named_sync(1 + mg, 32 * KG);  // the first step's values are read
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mine[(j * 4 + i) * 32] = upper ? o[j][i] : o[j + 4][i];
+        named_sync(1 + mg, 32 * KG);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[j][i] = (upper ? o[j + 4][i] : o[j][i]) + theirs[(j * 4 + i) * 32];
+        tile0 += upper ? 4 : 0;
+      }
+
+      // ---- the finished output, or this run's partial
+      const bool whole = sg.first && sg.last;
+      const long long out_row = (static_cast<long long>(sg.seq) * p.hkv + head) * G;
+      const long long part_row = (static_cast<long long>(blockIdx.x) * 2 + (sg.first ? 1 : 0)) * G;
+      const float v0 = whole ? inverse(l0) : 1.0f, v1 = whole ? inverse(l1) : 1.0f;
+#pragma unroll
+      for (int j = 0; j < 16 / KG; j += 2) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = half ? r1 : r0;
+          const float f = half ? v1 : v0;
+          // four values and the dims of the first two and the last two
+          float w[4];
+          int da, db;
+          if (!FP8) {
+            w[0] = o[j][2 * half] * f; w[1] = o[j][2 * half + 1] * f;
+            w[2] = o[j + 1][2 * half] * f; w[3] = o[j + 1][2 * half + 1] * f;
+            da = (tile0 + j) * 8 + 2 * t4;
+            db = da + 8;
+          } else {
+            w[0] = o[j][2 * half] * f; w[1] = o[j + 1][2 * half] * f;
+            w[2] = o[j][2 * half + 1] * f; w[3] = o[j + 1][2 * half + 1] * f;
+            da = (tile0 + j) * 8 + 4 * t4;
+            db = da + 2;
+          }
+          if (r < G) {
+            if (whole) {
+              uint32_t* d = reinterpret_cast<uint32_t*>(p.o + (out_row + r) * kHeadDim);
+              d[da >> 1] = pack_bf16(w[0], w[1]);
+              d[db >> 1] = pack_bf16(w[2], w[3]);
+            } else {
+              float* d = p.part_o + (part_row + r) * kHeadDim;
+              *reinterpret_cast<float2*>(d + da) = make_float2(w[0], w[1]);
+              *reinterpret_cast<float2*>(d + db) = make_float2(w[2], w[3]);
+            }
+          }
+        }
+      }
+      if (kg == 0 && t4 == 0) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const int r = half ? r1 : r0;
+          const float m = half ? m1 : m0, l = half ? l1 : l0;
+          if (r < G) {
+            if (whole) {
+              p.lse[out_row + r] = (m + log2f(l)) * kLn2;
+              if (LOGITS) p.norm[out_row + r] = row_norm(m, l);
+            } else {
+              p.part_ml[part_row + r] = make_float2(m, l);
+            }
+          }
+        }
+      }
+      if (sg.first && !sg.last) {
+        // the run that holds the sequence's last unit: lo(x) = floor(total x / runs) <= u < lo(x + 1)
+        const long long end = sg.unit + units_of(sg.len) - 1;
+        sent_seq = sg.seq;
+        sent_last = static_cast<int>(((end + 1) * run.runs - 1) / run.total);
+      }
+    }
+    if (warp == 0 && lane == 0) p.meta[blockIdx.x] = make_int2(sent_seq, sent_last);
+  }
+  __syncthreads();
+  if (*abort_flag && issued > 0)  // no copy may land after this CTA has left
+    for (uint32_t f = issued > C::kStages ? issued - C::kStages : 0; f < issued; ++f)
+      mbar_wait(&full[f % C::kStages], (f / C::kStages) & 1, nullptr);
+  if (threadIdx.x == 0) p.flags[blockIdx.x] = *err;
+}
+
+// ---------------------------------------------------------------- join
+// CTA (run, KV head; four head rows): when a sequence begins in the run and
+// goes on behind it, merges that sequence's partials, four warps to a row.
+__global__ void __launch_bounds__(512) dense_join_kernel(DenseDecodeParams p) {
+  __shared__ float acc[4][4][kHeadDim];
+  __shared__ float accl[4][4];
+  __shared__ uint32_t all_flags;
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    if (threadIdx.x == 0) all_flags = 0;
+    __syncthreads();
+    uint32_t f = 0;
+    for (int i = threadIdx.x; i < p.groups * p.hkv; i += blockDim.x) f |= p.flags[i];
+    if (f) atomicOr(&all_flags, f);
+    __syncthreads();
+    if (threadIdx.x == 0) p.hdr->status = all_flags;
+  }
+  const int2 meta = p.meta[blockIdx.x];
+  if (meta.x < 0) return;
+  const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv, G = p.group;
+  const int row = blockIdx.y * 4 + (warp >> 2), sub = warp & 3;
+  const int n = meta.y - g + 1;
+  const bool on = row < G;
+  auto part = [&](int i) {  // row of run g + i's partial: its first run ends it in slot 1, the others begin with it
+    return ((static_cast<long long>(g + i) * p.hkv + head) * 2 + (i == 0 ? 1 : 0)) * G + row;
+  };
+  float M = -INFINITY;
+  if (on)
+    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[part(i)].x);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.0f;
+  if (on) {
+#pragma unroll 8
+    for (int i = sub; i < n; i += 4) {
+      const long long at = part(i);
+      const float2 x = p.part_ml[at];
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 4);
+      const float f = exp2_diff(x.x, M);
+      l += x.y * f;
+      a.x += v.x * f;
+      a.y += v.y * f;
+      a.z += v.z * f;
+      a.w += v.w * f;
+    }
+  }
+  *reinterpret_cast<float4*>(&acc[warp >> 2][sub][lane * 4]) = a;
+  if (lane == 0) accl[warp >> 2][sub] = l;
+  __syncthreads();
+  if (sub != 0 || !on) return;
+  const int rr = warp >> 2;
+  l = (accl[rr][0] + accl[rr][1]) + (accl[rr][2] + accl[rr][3]);
+  const float inv = inverse(l);
+  float w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int d = lane * 4 + j;
+    w[j] = ((acc[rr][0][d] + acc[rr][1][d]) + (acc[rr][2][d] + acc[rr][3][d])) * inv;
+  }
+  const long long out = (static_cast<long long>(meta.x) * p.hkv + head) * G + row;
+  *reinterpret_cast<uint2*>(p.o + out * kHeadDim + lane * 4) = make_uint2(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]));
+  if (lane == 0) {
+    p.lse[out] = (M + log2f(l)) * kLn2;
+    if (p.norm) p.norm[out] = row_norm(M, l);
+  }
+}
+
+// ---------------------------------------------------------------- weights
+// weight[s, g, j] += sum over the group's heads of 2^(s[h,j] - m_h) / l_h, from
+// the logits that the split kernel left.  The heads are added in order: one
+// thread per key, no atomics.
+constexpr int kWeightThreads = 512;
+__global__ void __launch_bounds__(kWeightThreads) dense_weight_kernel(DenseDecodeParams p) {
+  __shared__ RunSmem run_sm;
+  __shared__ float2 norm[128];
+  griddep_wait();
+  if (p.hdr->status & kFlagTimeout) return;  // logits are missing
+  const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv, G = p.group;
+  Run run;
+  if (!find_run(p.cu_k, p.num_seqs, p.max_k, p.total_k, g, p.groups, run_sm, run)) return;
+  Walker walk(p.cu_k, run);
+  Segment sg;
+  const int key = threadIdx.x % kTile, lane_unit = threadIdx.x / kTile;
+  while (walk.next(sg)) {
+    __syncthreads();
+    const long long row = (static_cast<long long>(sg.seq) * p.hkv + head);
+    if (threadIdx.x < G) norm[threadIdx.x] = p.norm[row * G + threadIdx.x];
+    __syncthreads();
+    for (int i = lane_unit; i < sg.count; i += kWeightThreads / kTile) {
+      const int j = (sg.off + i) * kTile + key;
+      if (j >= sg.len) continue;
+      const float* s = p.logits + ((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) * kTile + key;
+      float sum = 0.0f;
+#pragma unroll 8
+      for (int h = 0; h < G; ++h) {
+        const float2 n = norm[h];
+        sum += exp2_approx(s[h * kTile] - n.x) * n.y;
+      }
+      p.weight[row * p.weight_stride + j] += sum;
+    }
+  }
+}
+
+template <int MG, bool FP8>
+cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p,
+                         cudaStream_t stream) {
+  using C = SplitCfg<MG, FP8>;
+  auto* fn = p.logits ? dense_split_kernel<MG, FP8, true> : dense_split_kernel<MG, FP8, false>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
+  if (e != cudaSuccess) return e;
+  fn<<<p.groups * p.hkv, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
+template <bool FP8>
+cudaError_t launch_split_for(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p,
+                             cudaStream_t stream) {
+  if (p.group <= 16) return launch_split<1, FP8>(tk, tv, p, stream);
+  if (p.group <= 32) return launch_split<2, FP8>(tk, tv, p, stream);
+  if (p.group <= 64) return launch_split<4, FP8>(tk, tv, p, stream);
+  return launch_split<8, FP8>(tk, tv, p, stream);
+}
+
+}  // namespace
+
+int dense_decode_ctas_per_sm(int group) { return group <= 16 ? 2 : 1; }
+
+cudaError_t launch_dense_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p, bool fp8,
+                                cudaStream_t stream) {
+  cudaError_t e = fp8 ? launch_split_for<true>(tk, tv, p, stream) : launch_split_for<false>(tk, tv, p, stream);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(dense_join_kernel, dim3(p.groups * p.hkv, (p.group + 3) / 4), dim3(512), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  if (!p.weight) return cudaSuccess;
+  e = launch_pdl(dense_weight_kernel, dim3(p.groups * p.hkv), dim3(kWeightThreads), 0, stream, p);
+  if (e != cudaSuccess) return e;
+  note_launches(1);
+  return cudaSuccess;
+}
+
+}  // namespace msa

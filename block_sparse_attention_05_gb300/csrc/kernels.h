@@ -274,4 +274,77 @@ struct CombineParams {
 // f16_partials: the partial outputs are fp16 (prefill) rather than bf16 (decode).
 cudaError_t launch_combine(const CombineParams& p, bool f16_partials, cudaStream_t stream);
 
+// ---------------------------------------------------------------- dense decode attention
+// One new token per sequence over every key of a paged cache.
+constexpr int kDenseTile = 64;      // keys of a work unit
+constexpr int kDenseMaxCtas = 320;  // CTAs of the split at most (two per SM), or num_kv_heads where that is more
+struct DenseDecodeParams {
+  int num_seqs, hkv, group, max_k, total_k;
+  int groups;                   // runs the batch is cut into; groups * hkv CTAs
+  const int32_t* cu_k;
+  const __nv_bfloat16* q;       // [num_seqs, hkv * group, 128]
+  const int32_t* block_table;   // [num_seqs, bt_stride]
+  int bt_stride;
+  long long n_pages;
+  const float* k_scale;         // fp8: [n_pages, hkv]
+  const float* v_scale;
+  __nv_bfloat16* o;             // [num_seqs, hkv * group, 128]
+  float* lse;                   // [num_seqs, hkv * group]
+  float* weight;                // [num_seqs, hkv, weight_stride] or null
+  long long weight_stride;
+  float scale_log2;             // softmax scale * log2(e)
+  // workspace
+  WsHeader* hdr;                // only the status is written
+  float* part_o;                // [groups, hkv, 2, group, 128]: slot 1 the sequence that goes on behind the run
+  float2* part_ml;              // [groups, hkv, 2, group] (maximum in log2 units, sum)
+  int2* meta;                   // [groups, hkv] (sequence that begins here and goes on or -1, its last run)
+  uint32_t* flags;              // [groups, hkv] device error flags
+  float* logits;                // with weight: [units, hkv, group, kDenseTile] in log2 units; else null
+  float2* norm;                 // with weight: [num_seqs, hkv * group] (maximum, 1 / sum); else null
+};
+int dense_decode_ctas_per_sm(int group);
+cudaError_t launch_dense_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p, bool fp8,
+                                cudaStream_t stream);
+
+// ---------------------------------------------------------------- eviction
+struct EvictParams {
+  int num_seqs, hkv, max_k, total_k, budget, recent;
+  int new_blocks;               // pages of the longest new sequence (bound)
+  const int32_t* cu_k;
+  void* k;                      // [n_pages * 128, hkv, 128] bf16, or E4M3 codes
+  void* v;
+  float* k_scale;               // fp8: [n_pages, hkv]
+  float* v_scale;
+  const int32_t* block_table;
+  int bt_stride;
+  const int32_t* new_table;
+  int new_stride;
+  long long n_pages;
+  const float* weight;          // [num_seqs, hkv, weight_stride]
+  long long weight_stride;
+  float* new_weight;            // [num_seqs, hkv, new_weight_stride]
+  long long new_weight_stride;
+  int32_t* kept;                // [num_seqs, hkv, budget]
+  int32_t* new_cu_k;            // [num_seqs + 1]
+  WsHeader* hdr;
+  uint32_t* marks;              // [n_pages] behind the header
+  size_t clear_bytes;           // header and marks
+};
+cudaError_t launch_evict(const EvictParams& p, bool fp8, cudaStream_t stream);
+
+// ---------------------------------------------------------------- residual sum and norm
+struct NormParams {
+  long long rows;
+  int width;
+  float eps;
+  const __nv_bfloat16* x;         // [rows, width]
+  const __nv_bfloat16* residual;  // [rows, width] or null
+  const __nv_bfloat16* gamma;     // [width]
+  __nv_bfloat16* sum;             // [rows, width] or null
+  __nv_bfloat16* y;               // [rows, width], or
+  uint8_t* y8;                    // E4M3 codes with
+  float* scale;                   // one scale per row
+};
+cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream);
+
 }  // namespace msa

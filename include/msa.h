@@ -100,8 +100,8 @@ typedef enum msa_status {
 #define MSA_DEVICE_TIMEOUT 1u        /* a kernel wait exceeded its time limit */
 #define MSA_DEVICE_BAD_SEQLENS 2u    /* cu_seqlens disagree with the host sizes */
 #define MSA_DEVICE_BAD_INDEX 4u      /* a computed index failed its check (checked builds), or a block-table
-                                        entry of msa_forward_decode_paged(_fp8)(_index) named a page outside
-                                        the cache */
+                                        entry of a paged call named a page outside the cache (or, for
+                                        msa_evict_paged, a page that it may not write) */
 
 typedef struct msa_problem {
   int32_t num_seqs;              /* >= 1 */
@@ -132,7 +132,9 @@ typedef enum msa_op {
   MSA_OP_SPARSE_ATTN_DECODE_FP8 = 9,  /* msa_sparse_attn_decode_fp8 */
   MSA_OP_FORWARD_FP8 = 10,       /* msa_forward_fp8 */
   MSA_OP_INDEX_PROLOGUE = 11,    /* msa_index_prologue */
-  MSA_OP_QUANTIZE_INDEX_FP8 = 12 /* msa_quantize_index_fp8 */
+  MSA_OP_QUANTIZE_INDEX_FP8 = 12,/* msa_quantize_index_fp8 */
+  MSA_OP_DENSE_ATTN_DECODE = 13, /* msa_dense_attn_decode_paged(_fp8), weight = NULL */
+  MSA_OP_DENSE_ATTN_DECODE_WEIGHT = 14 /* the same with a weight */
 } msa_op_t;
 
 /* Workspace bytes that `op` needs for `problem` (host-only; no CUDA call).
@@ -414,6 +416,123 @@ msa_status_t msa_forward_decode_paged_fp8_index(const msa_problem_t *problem, co
                                                 const int32_t *block_table, int32_t max_blocks_per_seq,
                                                 int64_t num_pages, int32_t *idx, void *o, float *lse,
                                                 void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The full-attention layers beside the sparse ones, over the same pages: the
+ * dense attention of a decode step, eviction from a cache by the attention
+ * weight its keys have received, and the residual sum and norm in front of a
+ * layer's projections.
+ *
+ * msa_dense_attn_decode_paged: exact softmax attention of the one new query of
+ * each sequence over ALL its cached keys.  For query head h of group g
+ *   s[h,j] = softmax_scale * q_h . k_j,   lse_h = ln sum_j exp(s[h,j]),
+ *   o_h = sum_j exp(s[h,j] - lse_h) v_j,
+ * and, with a weight array, for every cached key j (in place)
+ *   weight[g,j] += sum over the heads h of group g of exp(s[h,j] - lse_h).
+ *   problem     a decode batch (max_seqlen_q = 1, total_q = num_seqs; query i
+ *               is sequence i, cu_seqlens_q is not read).  cu_seqlens_k gives
+ *               the cached lengths; a length of 0 is allowed (o = 0, lse =
+ *               -inf).  index_dim and topk are not looked at.  head_dim =
+ *               block_size = 128; any group size num_q_heads / num_kv_heads
+ *               from 1 to 128, num_kv_heads <= 1024, num_seqs <= 2^20.
+ *   k_cache, v_cache, block_table, max_blocks_per_seq, num_pages
+ *               as for msa_forward_decode_paged; what the rows past a
+ *               sequence's last key hold does not matter.  Sequences may share
+ *               pages.
+ *   weight      fp32 [num_seqs, num_kv_heads, weight_stride], weight_stride >=
+ *               max_seqlen_k, 4-byte aligned, or NULL.  Entries past a
+ *               sequence's length are left as they were.  One thread adds the
+ *               group's heads in order: the sums do not depend on timing.
+ *   o, lse      written for every sequence.
+ * Workspace: op MSA_OP_DENSE_ATTN_DECODE, or MSA_OP_DENSE_ATTN_DECODE_WEIGHT
+ * with a weight (it then holds the logits: 4 bytes per query head and key).
+ * Lengths that contradict the host sizes make the kernels skip the call
+ * (MSA_DEVICE_BAD_SEQLENS); a page outside the cache reads as zeros
+ * (MSA_DEVICE_BAD_INDEX).
+ * ------------------------------------------------------------------------ */
+msa_status_t msa_dense_attn_decode_paged(const msa_problem_t *problem, const void *q, const void *k_cache,
+                                         const void *v_cache, const int32_t *block_table,
+                                         int32_t max_blocks_per_seq, int64_t num_pages, float *weight,
+                                         int64_t weight_stride, void *o, float *lse, void *workspace,
+                                         size_t workspace_bytes, msa_stream_t stream);
+
+/* The same over E4M3 pages with one scale per (page, KV head), positive and
+ * finite, as for msa_forward_decode_paged_fp8: the attention over the
+ * dequantized values. */
+msa_status_t msa_dense_attn_decode_paged_fp8(const msa_problem_t *problem, const void *q, const void *k8_cache,
+                                             const void *v8_cache, const float *k_scale, const float *v_scale,
+                                             const int32_t *block_table, int32_t max_blocks_per_seq,
+                                             int64_t num_pages, float *weight, int64_t weight_stride, void *o,
+                                             float *lse, void *workspace, size_t workspace_bytes,
+                                             msa_stream_t stream);
+
+/* Workspace bytes of msa_evict_paged and msa_evict_paged_fp8 (host-only). */
+msa_status_t msa_evict_workspace_size(const msa_problem_t *problem, int32_t budget, int64_t num_pages,
+                                      size_t *bytes);
+
+/* Eviction by accumulated weight.  Per sequence (n cached keys) and KV head: when
+ * n <= budget every slot is kept; else the last `recent` slots (0 <= recent <=
+ * budget, budget >= 1) and, of the others, the budget - recent with the
+ * largest weight -- equal weights (-0 = +0) to the lower slot, NaN below every
+ * number.  The kept slots of a head, in ascending order, become slots 0 ..
+ * min(n, budget) - 1 of the sequence's pages in new_block_table: every sequence
+ * of the call moves to its new pages (leave out of the batch what is to stay
+ * where it is), and its old pages are the caller's to reuse.  The heads of a
+ * page then hold different tokens at one slot, so a cache that is evicted from
+ * serves dense attention, not the block selection of the sparse layers.
+ *   problem, caches, block_table, num_pages   as above; the caches are read
+ *               through block_table and written through new_block_table.
+ *   weight      fp32 [num_seqs, num_kv_heads, weight_stride >= max_seqlen_k]
+ *   new_block_table  int32 [num_seqs, new_max_blocks_per_seq], at least
+ *               ceil(min(max_seqlen_k, budget) / 128) wide.  Its pages must be
+ *               apart from those of block_table and named once: a page that is
+ *               not, or that is outside the cache, is not written and raises
+ *               MSA_DEVICE_BAD_INDEX (a page outside the cache in block_table
+ *               reads as zeros and raises it too).
+ *   kept        int32 [num_seqs, num_kv_heads, budget] (written): the kept slots,
+ *               ascending, -1 at the tail.
+ *   new_weight  fp32 [num_seqs, num_kv_heads, new_weight_stride >=
+ *               min(max_seqlen_k, budget)] (written): the kept slots' weights;
+ *               entries past the new length are left as they were.  Not `weight`.
+ *   new_cu_seqlens_k  int32 [num_seqs + 1] (written): prefix sums of
+ *               min(n, budget).  Not the problem's.
+ * Rows of a new page past the new length are left as they were. */
+msa_status_t msa_evict_paged(const msa_problem_t *problem, void *k_cache, void *v_cache, const int32_t *block_table,
+                             int32_t max_blocks_per_seq, int64_t num_pages, const float *weight,
+                             int64_t weight_stride, int32_t budget, int32_t recent, const int32_t *new_block_table,
+                             int32_t new_max_blocks_per_seq, int32_t *kept, float *new_weight,
+                             int64_t new_weight_stride, int32_t *new_cu_seqlens_k, void *workspace,
+                             size_t workspace_bytes, msa_stream_t stream);
+
+/* The same over E4M3 pages.  A page has one scale per KV head, so a new page's
+ * rows are rounded again: value = code * scale of the page it came from, scale
+ * = max |value| / 448 over the new page's rows (1 when that is 0), code =
+ * round-to-nearest-even(value / scale) in fp32, saturated. */
+msa_status_t msa_evict_paged_fp8(const msa_problem_t *problem, void *k8_cache, void *v8_cache, float *k_scale,
+                                 float *v_scale, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                 int64_t num_pages, const float *weight, int64_t weight_stride, int32_t budget,
+                                 int32_t recent, const int32_t *new_block_table, int32_t new_max_blocks_per_seq,
+                                 int32_t *kept, float *new_weight, int64_t new_weight_stride,
+                                 int32_t *new_cu_seqlens_k, void *workspace, size_t workspace_bytes,
+                                 msa_stream_t stream);
+
+/* Residual sum and root-mean-square norm, for each of `rows` rows of d_model
+ * elements (1 .. 65536):
+ *   h = x + residual   (fp32; residual = NULL: h = x),   sum = bf16(h),
+ *   y = h / sqrt(mean(h^2) + eps) * gamma   (from h before its rounding, bf16)
+ *   x, residual, sum, y  [rows, d_model] bf16, gamma [d_model] bf16, 16-byte
+ *   aligned; sum may be NULL.  sum may be x or residual (in place), and y may be
+ *   one that sum is not; other outputs must not overlap an input.
+ * No workspace; rows = 0 is no work. */
+msa_status_t msa_add_rms_norm(const void *x, const void *residual, const void *gamma, int64_t rows, int32_t d_model,
+                              float eps, void *sum, void *y, msa_stream_t stream);
+
+/* The same with y as E4M3 codes y8 [rows, d_model] (16-byte aligned) and one
+ * scale per row y_scale [rows] (4-byte aligned): scale = max |y| / 448 (1 when
+ * that is 0), code = round-to-nearest-even(y / scale) in fp32, saturated. */
+msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const void *gamma, int64_t rows,
+                                  int32_t d_model, float eps, void *sum, void *y8, float *y_scale,
+                                  msa_stream_t stream);
 
 /* Waits for `stream`, then returns in *flags the MSA_DEVICE_* bits that the
  * last call on this workspace raised (0 = none).  workspace = NULL reads the
