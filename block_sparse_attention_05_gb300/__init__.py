@@ -406,63 +406,94 @@ def msa_index_prologue(problem: Problem, x, w_q, w_k, gamma_q, gamma_k, k_idx, q
 
 
 # ---------------------------------------------------------------- dense decode attention, eviction, norm
-def _is(t, dtype, shape, name):
-    """A contiguous tensor of this type and shape (None = any size) on the current CUDA device."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
-        _need(t, dtype, name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
-    if len(t.shape) != len(shape) or any(want is not None and n != want for n, want in zip(t.shape, shape)):
+# The current device and stream as plain numbers: torch's own accessors, without the objects that torch.cuda's
+# functions make around them (3 us a call on the host, as much as a small kernel takes).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+               or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
+def _refuse(t, dtype, dev, name):
+    _need(t, dtype, name)
+    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+
+
+def _is(t, dtype, shape, dev, name):
+    """A contiguous tensor of this type and shape on the current CUDA device `dev`."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, dtype, dev, name)
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
 
 
-def _paged(problem, dtype, k_cache, v_cache, block_table):
-    """Checks a paged cache and its table; returns the number of pages."""
-    _is(k_cache, dtype, (None, problem.hkv, 128), "k_cache")
-    _is(v_cache, dtype, k_cache.shape, "v_cache")
-    _is(block_table, torch.int32, (problem.num_seqs, None), "block_table")
-    _is(problem.cu_k, torch.int32, (None,), "cu_k")
-    if k_cache.shape[0] % 128:
+def _c_paged(problem):
+    """Problem.c() for the calls below, checked (every field that they read), with plain integers for the pointers."""
+    cu_q, cu_k = problem.cu_q, problem.cu_k
+    if not cu_q.is_cuda:
+        _need(cu_q, torch.int32, "cu_q")
+    n = cu_q.shape[0] - 1
+    dev = _current_device()
+    _is(cu_q, torch.int32, (n + 1,), dev, "cu_q")
+    at_k = _is(cu_k, torch.int32, (n + 1,), dev, "cu_k")
+    return n, dev, MsaProblem(n, cu_q.data_ptr(), at_k, problem.total_q, problem.total_k, problem.max_q, problem.max_k,
+                              problem.hq, problem.hkv, problem.head_dim, problem.d_idx, problem.block, problem.topk,
+                              problem.scale)
+
+
+def _table(t, n, dev, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected [num_seqs, max_blocks], got {list(t.shape)}")
+    return _is(t, torch.int32, (n, t.shape[1]), dev, name)
+
+
+def _pages(problem, dev, dtype, k_cache, v_cache, scales):
+    """Checks a paged cache; returns the number of pages and the addresses of the caches and scales."""
+    rows = k_cache.shape[0]
+    shape = (rows, problem.hkv, 128)
+    at = (_is(k_cache, dtype, shape, dev, "k_cache"), _is(v_cache, dtype, shape, dev, "v_cache"))
+    if rows % 128:
         raise ValueError("the caches must be whole pages of 128 rows")
-    return k_cache.shape[0] // 128
+    if scales:
+        shape = (rows // 128, problem.hkv)
+        at += (_is(scales[0], torch.float32, shape, dev, "k_scale"), _is(scales[1], torch.float32, shape, dev, "v_scale"))
+    return rows // 128, at
 
 
-def _scales(problem, pages, k_scale, v_scale):
-    _is(k_scale, torch.float32, (pages, problem.hkv), "k_scale")
-    _is(v_scale, torch.float32, (pages, problem.hkv), "v_scale")
+def _weight(t, n, hkv, dev, name):
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected [num_seqs, num_kv_heads, tokens], got {list(t.shape)}")
+    return _is(t, torch.float32, (n, hkv, t.shape[2]), dev, name)
 
 
-def _raw_stream():
-    return torch.cuda.current_stream().cuda_stream
+def _space(ws, nbytes, dev):
+    """The workspace's address and size; a buffer of its own where the caller gives none."""
+    if ws is None:
+        ws = torch.empty(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
+    elif not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != dev:
+        _refuse(ws, ws.dtype, dev, "ws")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _dense(problem, q, k, v, scales, block_table, weight, o, lse, ws):
-    pages = _paged(problem, torch.uint8 if scales else torch.bfloat16, k, v, block_table)
-    S, hq = problem.num_seqs, problem.hq
-    _is(q, torch.bfloat16, (S, hq, 128), "q")
-    stride = 0
+    S, dev, c = _c_paged(problem)
+    pages, caches = _pages(problem, dev, torch.uint8 if scales else torch.bfloat16, k, v, scales)
+    shape = (S, problem.hq, 128)
+    at_q, at_table = _is(q, torch.bfloat16, shape, dev, "q"), _table(block_table, S, dev, "block_table")
+    at_weight, stride, op = None, 0, Op.DENSE_ATTN_DECODE
     if weight is not None:
-        _is(weight, torch.float32, (S, problem.hkv, None), "weight")
-        stride = weight.shape[2]
+        at_weight, stride = _weight(weight, S, problem.hkv, dev, "weight"), weight.shape[2]
+        op = Op.DENSE_ATTN_DECODE_WEIGHT
     if o is None:
         o = torch.empty_like(q)
-    else:
-        _is(o, torch.bfloat16, (S, hq, 128), "o")
     if lse is None:
-        lse = torch.empty((S, hq), dtype=torch.float32, device=q.device)
-    else:
-        _is(lse, torch.float32, (S, hq), "lse")
-    ws, nws = _ws(problem, Op.DENSE_ATTN_DECODE if weight is None else Op.DENSE_ATTN_DECODE_WEIGHT, ws)
-    tail = (block_table.data_ptr(), block_table.shape[1], pages, None if weight is None else weight.data_ptr(), stride,
-            o.data_ptr(), lse.data_ptr(), ws.data_ptr(), nws, _raw_stream())
-    if scales:
-        _scales(problem, pages, *scales)
-        _check(_lib.msa_dense_attn_decode_paged_fp8(problem.c(), q.data_ptr(), k.data_ptr(), v.data_ptr(),
-                                                    scales[0].data_ptr(), scales[1].data_ptr(), *tail),
-               "msa_dense_attn_decode_paged_fp8")
-    else:
-        _check(_lib.msa_dense_attn_decode_paged(problem.c(), q.data_ptr(), k.data_ptr(), v.data_ptr(), *tail),
-               "msa_dense_attn_decode_paged")
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    at_o, at_lse = _is(o, torch.bfloat16, shape, dev, "o"), _is(lse, torch.float32, shape[:2], dev, "lse")
+    ws, at_ws, nws = _space(ws, lambda: msa_workspace_size(problem, op), dev)
+    fn, where = ((_lib.msa_dense_attn_decode_paged_fp8, "msa_dense_attn_decode_paged_fp8") if scales else
+                 (_lib.msa_dense_attn_decode_paged, "msa_dense_attn_decode_paged"))
+    _check(fn(c, at_q, *caches, at_table, block_table.shape[1], pages, at_weight, stride, at_o, at_lse, at_ws, nws,
+              _raw_stream(dev)), where)
     return o, lse
 
 
@@ -495,33 +526,26 @@ def evict_workspace(problem: Problem, budget: int, num_pages: int, device=None) 
 
 
 def _evict(problem, k, v, scales, block_table, weight, new_block_table, budget, recent, kept, new_weight, new_cu_k, ws):
-    pages = _paged(problem, torch.uint8 if scales else torch.bfloat16, k, v, block_table)
-    S, hkv = problem.num_seqs, problem.hkv
-    _is(weight, torch.float32, (S, hkv, None), "weight")
-    _is(new_block_table, torch.int32, (S, None), "new_block_table")
+    S, dev, c = _c_paged(problem)
+    hkv = problem.hkv
+    pages, caches = _pages(problem, dev, torch.uint8 if scales else torch.bfloat16, k, v, scales)
+    at_table, at_new = _table(block_table, S, dev, "block_table"), _table(new_block_table, S, dev, "new_block_table")
+    at_weight = _weight(weight, S, hkv, dev, "weight")
     if kept is None:
         kept = torch.empty((S, hkv, budget), dtype=torch.int32, device=k.device)
-    else:
-        _is(kept, torch.int32, (S, hkv, budget), "kept")
     if new_weight is None:
         new_weight = torch.zeros((S, hkv, budget), dtype=torch.float32, device=k.device)
-    else:
-        _is(new_weight, torch.float32, (S, hkv, None), "new_weight")
     if new_cu_k is None:
         new_cu_k = torch.empty(S + 1, dtype=torch.int32, device=k.device)
-    else:
-        _is(new_cu_k, torch.int32, (S + 1,), "new_cu_k")
-    if ws is None:
-        ws = evict_workspace(problem, budget, pages)
-    tail = (block_table.data_ptr(), block_table.shape[1], pages, weight.data_ptr(), weight.shape[2], budget, recent,
-            new_block_table.data_ptr(), new_block_table.shape[1], kept.data_ptr(), new_weight.data_ptr(),
-            new_weight.shape[2], new_cu_k.data_ptr(), ws.data_ptr(), ws.numel(), _raw_stream())
-    if scales:
-        _scales(problem, pages, *scales)
-        _check(_lib.msa_evict_paged_fp8(problem.c(), k.data_ptr(), v.data_ptr(), scales[0].data_ptr(),
-                                        scales[1].data_ptr(), *tail), "msa_evict_paged_fp8")
-    else:
-        _check(_lib.msa_evict_paged(problem.c(), k.data_ptr(), v.data_ptr(), *tail), "msa_evict_paged")
+    at_kept, at_cu = _is(kept, torch.int32, (S, hkv, budget), dev, "kept"), _is(new_cu_k, torch.int32, (S + 1,), dev,
+                                                                               "new_cu_k")
+    at_new_weight = _weight(new_weight, S, hkv, dev, "new_weight")
+    ws, at_ws, nws = _space(ws, lambda: msa_evict_workspace_size(problem, budget, pages), dev)
+    fn, where = ((_lib.msa_evict_paged_fp8, "msa_evict_paged_fp8") if scales else
+                 (_lib.msa_evict_paged, "msa_evict_paged"))
+    _check(fn(c, *caches, at_table, block_table.shape[1], pages, at_weight, weight.shape[2], budget, recent, at_new,
+              new_block_table.shape[1], at_kept, at_new_weight, new_weight.shape[2], at_cu, at_ws, nws,
+              _raw_stream(dev)), where)
     return kept, new_weight, new_cu_k
 
 
@@ -545,45 +569,42 @@ def msa_evict_paged_fp8(problem: Problem, k8_cache, v8_cache, k_scale, v_scale, 
 
 
 def _norm_args(x, gamma, residual, sum_out):
-    width = x.shape[-1]
-    _is(x, torch.bfloat16, x.shape, "x")
-    _is(gamma, torch.bfloat16, (width,), "gamma")
-    if residual is not None:
-        _is(residual, torch.bfloat16, x.shape, "residual")
+    if not x.is_cuda:
+        _need(x, torch.bfloat16, "x")
+    shape, dev = x.shape, _current_device()
+    if not shape:
+        raise ValueError("x: needs a dimension to normalise")
+    width = shape[-1]
+    at_x, at_gamma = _is(x, torch.bfloat16, shape, dev, "x"), _is(gamma, torch.bfloat16, (width,), dev, "gamma")
+    at_residual = None if residual is None else _is(residual, torch.bfloat16, shape, dev, "residual")
     if sum_out is None:
         sum_out = torch.empty_like(x)
-    else:
-        _is(sum_out, torch.bfloat16, x.shape, "sum_out")
-    return (x.data_ptr(), None if residual is None else residual.data_ptr(), gamma.data_ptr(),
-            x.numel() // width if width else 0, width), sum_out
+    at_sum = _is(sum_out, torch.bfloat16, shape, dev, "sum_out")
+    return shape, dev, sum_out, (at_x, at_residual, at_gamma, x.numel() // width if width else 0, width), at_sum
 
 
 def msa_add_rms_norm(x, gamma, residual=None, eps: float = 1e-6, sum_out=None, y=None):
     """h = x + residual in fp32; returns (bf16(h), bf16(h / sqrt(mean(h^2) + eps) * gamma)) over the last dimension.
-    ``sum_out`` may be x or residual (in place)."""
-    args, sum_out = _norm_args(x, gamma, residual, sum_out)
+    ``sum_out`` may be x or residual (in place), and ``y`` the other one."""
+    shape, dev, sum_out, args, at_sum = _norm_args(x, gamma, residual, sum_out)
     if y is None:
         y = torch.empty_like(x)
-    else:
-        _is(y, torch.bfloat16, x.shape, "y")
-    _check(_lib.msa_add_rms_norm(*args, eps, sum_out.data_ptr(), y.data_ptr(), _raw_stream()), "msa_add_rms_norm")
+    _check(_lib.msa_add_rms_norm(*args, eps, at_sum, _is(y, torch.bfloat16, shape, dev, "y"), _raw_stream(dev)),
+           "msa_add_rms_norm")
     return sum_out, y
 
 
 def msa_add_rms_norm_fp8(x, gamma, residual=None, eps: float = 1e-6, sum_out=None, y8=None, y_scale=None):
     """msa_add_rms_norm with the norm as E4M3 codes (uint8) and one fp32 scale per row (max |y| / 448, 1 when 0).
     Returns (sum, y8, y_scale)."""
-    args, sum_out = _norm_args(x, gamma, residual, sum_out)
+    shape, dev, sum_out, args, at_sum = _norm_args(x, gamma, residual, sum_out)
     if y8 is None:
-        y8 = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    else:
-        _is(y8, torch.uint8, x.shape, "y8")
+        y8 = torch.empty(shape, dtype=torch.uint8, device=x.device)
     if y_scale is None:
-        y_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    else:
-        _is(y_scale, torch.float32, x.shape[:-1], "y_scale")
-    _check(_lib.msa_add_rms_norm_fp8(*args, eps, sum_out.data_ptr(), y8.data_ptr(), y_scale.data_ptr(),
-                                     _raw_stream()), "msa_add_rms_norm_fp8")
+        y_scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
+    _check(_lib.msa_add_rms_norm_fp8(*args, eps, at_sum, _is(y8, torch.uint8, shape, dev, "y8"),
+                                     _is(y_scale, torch.float32, shape[:-1], dev, "y_scale"), _raw_stream(dev)),
+           "msa_add_rms_norm_fp8")
     return sum_out, y8, y_scale
 
 

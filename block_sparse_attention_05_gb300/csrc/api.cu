@@ -836,7 +836,7 @@ msa_status_t add_rms_norm(const void* x, const void* residual, const void* gamma
   p.y = static_cast<__nv_bfloat16*>(y);
   p.y8 = static_cast<uint8_t*>(y8);
   p.scale = y_scale;
-  return cuda_status(launch_add_rms_norm(p, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_add_rms_norm(p, dev.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // namespace

@@ -245,14 +245,39 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(EvictParam
 }
 
 // fp8: a new page has one scale per head, so its rows are gathered, their
-// values' maximum taken, and the codes rounded again at the new scale.
+// largest value taken, and the codes rounded again.  A value is code * scale of
+// its old page, the new code the rounding of code * ratio with ratio = old scale
+// * 448 / max.  Codes and scales of few significant bits meet midpoints of
+// E4M3 exactly, so the product is rounded once and from more bits than fp32's;
+// a page that keeps its largest value keeps its codes.
+__device__ __forceinline__ float2 e4m3_values(uint32_t codes) {  // of two codes
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3)));
+}
+
+// x * (hi + lo), x and hi >= 0, as a float that rounds to fewer bits the way the exact product does: truncated, with
+// the lowest bit set when that left something.  hi + lo has 45 bits or more; the product of a code (4 bits) and a
+// quotient of (24-bit scale * 448) by (4-bit code * 24-bit scale) is a midpoint or at least 2^-33 of itself away
+// from one, so a remainder below 2^-40 is none.
+__device__ __forceinline__ float mul_to_odd(float x, float hi, float lo) {
+  const float q0 = x * hi, e0 = fmaf(x, lo, fmaf(x, hi, -q0));
+  const float q = q0 + e0, e = e0 - (q - q0);  // |e| at most half a step of q
+  if (!(fabsf(e) > q * 0x1p-40f)) return q;  // NaN too
+  return __uint_as_float((e < 0.0f ? __float_as_uint(q) - 1u : __float_as_uint(q)) | 1u);
+}
+
+struct PageScale {
+  unsigned long long key[kGatherThreads / 32];
+  float inv_hi, inv_lo;  // 448 / max
+};
+
 template <bool V>
-__device__ __forceinline__ void gather_fp8(const EvictParams& p, int page, int rows, int h, const int* src, float* red) {
+__device__ __forceinline__ void gather_fp8(const EvictParams& p, int page, int rows, int h, const int* src,
+                                           PageScale& sm) {
   const uint4* cache = reinterpret_cast<const uint4*>(V ? p.v : p.k);
   float* scales = V ? p.v_scale : p.k_scale;
   uint4 c[4];
   float sc[4];
-  float top = 0.0f;
+  unsigned long long top = 0;  // largest |value|: the exact product of code and scale as two floats, by their bits
 #pragma unroll
   for (int i = 0; i < 4; ++i) {  // 128 rows x 8 chunks of 16 codes over 256 threads
     const int at = i * kGatherThreads + threadIdx.x, r = at >> 3, col = at & 7;
@@ -262,39 +287,54 @@ __device__ __forceinline__ void gather_fp8(const EvictParams& p, int page, int r
       c[i] = cache[(static_cast<long long>(src[r]) * p.hkv + h) * 8 + col];
       sc[i] = scales[static_cast<long long>(src[r] / kBlock) * p.hkv + h];
     }
-    const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))),
-                                                        __NV_E4M3);
-      const float2 f = __half22float2(__half2(hr));
-      top = fmaxf(top, fmaxf(fabsf(f.x * sc[i]), fabsf(f.y * sc[i])));
-    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-  __syncthreads();  // red free
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = top;
-  __syncthreads();
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+    uint32_t m = 0;  // largest |code|, NaN (0x7F) left out
 #pragma unroll
-  for (int w = 0; w < kGatherThreads / 32; ++w) top = fmaxf(top, red[w]);
-  float scale = __fdiv_rn(top, 448.0f);
-  if (!(scale > 0.0f)) scale = 1.0f;
-  if (threadIdx.x == 0) scales[static_cast<long long>(page) * p.hkv + h] = scale;
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a = w[j] & 0x7F7F7F7Fu;
+      m = __vmaxu4(m, a & ~__vcmpeq4(a, 0x7F7F7F7Fu));
+    }
+    m = max(max(m & 0xFFu, (m >> 8) & 0xFFu), max((m >> 16) & 0xFFu, m >> 24));
+    const float x = e4m3_values(m).x;
+    const float hi = __fmul_rz(x, sc[i]), lo = fmaf(x, sc[i], -hi);  // lo >= 0
+    const unsigned long long key = (static_cast<unsigned long long>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
+    top = key > top ? key : top;
+  }
+  top = warp_max_u64(top);
+  if ((threadIdx.x & 31) == 0) sm.key[threadIdx.x >> 5] = top;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kGatherThreads / 32; ++w) top = sm.key[w] > top ? sm.key[w] : top;
+    const double value = static_cast<double>(__uint_as_float(static_cast<uint32_t>(top >> 32))) +
+                         static_cast<double>(__uint_as_float(static_cast<uint32_t>(top)));
+    const bool some = value >= 0x1p-118;  // below, 448 / value is no fp32 number: codes 0
+    scales[static_cast<long long>(page) * p.hkv + h] = some ? static_cast<float>(value / 448.0) : 1.0f;
+    const double inv = some ? 448.0 / value : 0.0;
+    sm.inv_hi = static_cast<float>(inv);
+    sm.inv_lo = static_cast<float>(inv - static_cast<double>(sm.inv_hi));
+  }
+  __syncthreads();
+  const float ih = sm.inv_hi, il = sm.inv_lo;
   uint4* out = reinterpret_cast<uint4*>(V ? p.v : p.k);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = i * kGatherThreads + threadIdx.x, r = at >> 3, col = at & 7;
     if (r >= rows) continue;
+    float hi = sc[i] * ih, lo = fmaf(sc[i], il, fmaf(sc[i], ih, -hi));
+    if (!(hi < 1e30f)) hi = 1e30f, lo = 0.0f;  // a scale so far above the values that their codes are 0
     const uint32_t w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
     uint32_t q[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w[j >> 1] >> (16 * (j & 1))),
-                                                        __NV_E4M3);
-      const float2 f = __half22float2(__half2(hr));
-      const float2 y = make_float2(__fdiv_rn(f.x * sc[i], scale), __fdiv_rn(f.y * sc[i], scale));
-      q[j >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3)) << (16 * (j & 1));
+      const uint32_t pair = w[j >> 1] >> (16 * (j & 1));
+      const float2 f = e4m3_values(pair & 0x7F7Fu);
+      const float2 y = make_float2(mul_to_odd(f.x, hi, lo), mul_to_odd(f.y, hi, lo));
+      const uint32_t code = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
+      q[j >> 1] |= (code | (pair & 0x8080u)) << (16 * (j & 1));
     }
     out[((static_cast<long long>(page) * kBlock + r) * p.hkv + h) * 8 + col] = make_uint4(q[0], q[1], q[2], q[3]);
   }
@@ -302,7 +342,7 @@ __device__ __forceinline__ void gather_fp8(const EvictParams& p, int page, int r
 
 __global__ void __launch_bounds__(kGatherThreads) evict_gather_fp8_kernel(EvictParams p) {
   __shared__ int src[kHeads][kBlock];
-  __shared__ float red[kGatherThreads / 32];
+  __shared__ PageScale scale[2];
   griddep_wait();
   if (p.hdr->status & kFlagBadSeqlens) return;
   const int s = blockIdx.x / p.new_blocks, b = blockIdx.x % p.new_blocks;
@@ -318,8 +358,8 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_fp8_kernel(EvictP
   source_rows(p, s, b, rows, h0, heads, n, src);
   __syncthreads();
   for (int h = 0; h < heads; ++h) {
-    gather_fp8<false>(p, page, rows, h0 + h, src[h], red);
-    gather_fp8<true>(p, page, rows, h0 + h, src[h], red);
+    gather_fp8<false>(p, page, rows, h0 + h, src[h], scale[0]);
+    gather_fp8<true>(p, page, rows, h0 + h, src[h], scale[1]);
   }
 }
 

@@ -345,6 +345,6 @@ struct NormParams {
   uint8_t* y8;                    // E4M3 codes with
   float* scale;                   // one scale per row
 };
-cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream);
+cudaError_t launch_add_rms_norm(const NormParams& p, int sms, cudaStream_t stream);
 
 }  // namespace msa

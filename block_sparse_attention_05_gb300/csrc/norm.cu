@@ -40,47 +40,68 @@ __device__ __forceinline__ float block_reduce(float v, float* red) {
   return t;
 }
 
-// VEC elements per access (8: 16-byte accesses, for widths that are a multiple
-// of 8; 1: any width), CH accesses per thread.
-template <int VEC, int CH, bool FP8>
+__device__ __forceinline__ void unpack8(const uint4& a, float (&f)[8]) {
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = __uint_as_float(w[j] << 16);
+    f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+}
+
+// One CTA per row, CH chunks of 8 elements per thread.  Chunks are aligned in
+// the tensor as a whole, so every access is 16 bytes whatever the width: with
+// ODD (a width that is no multiple of 8) a row begins `lead` elements into its
+// first chunk, elements of its neighbours in the first and last chunk count as
+// 0 and are not written, and the tensor's last, partial chunk is read by element.
+template <int CH, bool FP8, bool ODD>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormParams p) {
   __shared__ float red[2][32];
-  const long long row = blockIdx.x;
-  const int T = blockDim.x, n = p.width / VEC;
-  const __nv_bfloat16* x = p.x + row * p.width;
-  const __nv_bfloat16* res = p.residual ? p.residual + row * p.width : nullptr;
-  float h[CH][VEC];
-  float sq = 0.0f;
+  const int T = blockDim.x;
+  const long long start = blockIdx.x * static_cast<long long>(p.width);
+  const int lead = ODD ? static_cast<int>(start & 7) : 0;
+  const long long base = start - lead, end = p.rows * p.width;
+  const int n = (lead + p.width + 7) >> 3;
+  // elements [lo, hi) of chunk i are the row's
+  auto lo_of = [&](int i) { return ODD && i == 0 ? lead : 0; };
+  auto hi_of = [&](int i) { return ODD ? min(8, lead + p.width - 8 * i) : 8; };
+  float h[CH][8];
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = c * T + threadIdx.x;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) h[c][j] = 0.0f;
-    if (i < n) {
-      if (VEC == 8) {
-        const uint4 a = reinterpret_cast<const uint4*>(x)[i];
-        const uint32_t wa[4] = {a.x, a.y, a.z, a.w};
+    for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
+    if (i >= n) continue;
+    const long long at = base + 8ll * i;
+    if (!ODD || at + 8 <= end) {
+      unpack8(*reinterpret_cast<const uint4*>(p.x + at), h[c]);
+      if (p.residual) {
+        float r[8];
+        unpack8(*reinterpret_cast<const uint4*>(p.residual + at), r);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          h[c][2 * j % VEC] = __uint_as_float(wa[j] << 16);
-          h[c][(2 * j + 1) % VEC] = __uint_as_float(wa[j] & 0xFFFF0000u);
-        }
-        if (res) {
-          const uint4 b = reinterpret_cast<const uint4*>(res)[i];
-          const uint32_t wb[4] = {b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            h[c][2 * j % VEC] += __uint_as_float(wb[j] << 16);
-            h[c][(2 * j + 1) % VEC] += __uint_as_float(wb[j] & 0xFFFF0000u);
-          }
-        }
-      } else {
-        h[c][0] = __bfloat162float(x[i]);
-        if (res) h[c][0] += __bfloat162float(res[i]);
+        for (int j = 0; j < 8; ++j) h[c][j] += r[j];
       }
+    } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) sq = fmaf(h[c][j], h[c][j], sq);
+      for (int j = 0; j < 8; ++j)
+        if (at + j < end)
+          h[c][j] = __bfloat162float(p.x[at + j]) + (p.residual ? __bfloat162float(p.residual[at + j]) : 0.0f);
     }
+  }
+  float sq = 0.0f;
+#pragma unroll
+  for (int c = 0; c < CH; ++c) {
+    const int i = c * T + threadIdx.x;
+    if (ODD) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < lo_of(i) || j >= hi_of(i)) h[c][j] = 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sq = fmaf(h[c][j], h[c][j], sq);
   }
   // every thread has read its elements, so the outputs below may overwrite x or the residual in place
   const float total = block_reduce<AddOp>(sq, red[0]);
@@ -90,57 +111,71 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormParams p) {
   for (int c = 0; c < CH; ++c) {
     const int i = c * T + threadIdx.x;
     if (i >= n) continue;
-    if (VEC == 8) {
-      if (p.sum)
-        reinterpret_cast<uint4*>(p.sum + row * p.width)[i] =
-            make_uint4(pack2(h[c][0], h[c][1 % VEC]), pack2(h[c][2 % VEC], h[c][3 % VEC]),
-                       pack2(h[c][4 % VEC], h[c][5 % VEC]), pack2(h[c][6 % VEC], h[c][7 % VEC]));
-      const uint4 gm = reinterpret_cast<const uint4*>(p.gamma)[i];
-      const uint32_t w[4] = {gm.x, gm.y, gm.z, gm.w};
+    const long long at = base + 8ll * i;
+    const int lo = lo_of(i), hi = hi_of(i);
+    const bool full = !ODD || (lo == 0 && hi == 8);
+    if (p.sum) {
+      if (full) {
+        *reinterpret_cast<uint4*>(p.sum + at) = pack8(h[c]);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[c][2 * j % VEC] = h[c][2 * j % VEC] * r * __uint_as_float(w[j] << 16);
-        h[c][(2 * j + 1) % VEC] = h[c][(2 * j + 1) % VEC] * r * __uint_as_float(w[j] & 0xFFFF0000u);
+        for (int j = 0; j < 8; ++j)
+          if (j >= lo && j < hi) p.sum[at + j] = __float2bfloat16_rn(h[c][j]);
       }
-      if (!FP8)
-        reinterpret_cast<uint4*>(p.y + row * p.width)[i] =
-            make_uint4(pack2(h[c][0], h[c][1 % VEC]), pack2(h[c][2 % VEC], h[c][3 % VEC]),
-                       pack2(h[c][4 % VEC], h[c][5 % VEC]), pack2(h[c][6 % VEC], h[c][7 % VEC]));
-    } else {
-      if (p.sum) p.sum[row * p.width + i] = __float2bfloat16_rn(h[c][0]);
-      h[c][0] = h[c][0] * r * __bfloat162float(p.gamma[i]);
-      if (!FP8) p.y[row * p.width + i] = __float2bfloat16_rn(h[c][0]);
     }
-    if (FP8)
+    if (!ODD) {
+      float gm[8];
+      unpack8(reinterpret_cast<const uint4*>(p.gamma)[i], gm);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) top = fmaxf(top, fabsf(h[c][j]));
+      for (int j = 0; j < 8; ++j) h[c][j] = h[c][j] * r * gm[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= lo && j < hi) h[c][j] = h[c][j] * r * __bfloat162float(p.gamma[8 * i + j - lead]);
+    }
+    if (FP8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(h[c][j]));
+    } else if (full) {
+      *reinterpret_cast<uint4*>(p.y + at) = pack8(h[c]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= lo && j < hi) p.y[at + j] = __float2bfloat16_rn(h[c][j]);
+    }
   }
   if (!FP8) return;
   top = block_reduce<MaxOp>(top, red[1]);
   float scale = __fdiv_rn(top, 448.0f);
   if (!(scale > 0.0f)) scale = 1.0f;
-  if (threadIdx.x == 0) p.scale[row] = scale;
+  if (threadIdx.x == 0) p.scale[blockIdx.x] = scale;
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = c * T + threadIdx.x;
     if (i >= n) continue;
-    if (VEC == 8) {
-      uint32_t q[2] = {0, 0};
+    const long long at = base + 8ll * i;
+    const int lo = lo_of(i), hi = hi_of(i);
+    uint32_t q[2] = {0, 0};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = make_float2(__fdiv_rn(h[c][2 * j % VEC], scale), __fdiv_rn(h[c][(2 * j + 1) % VEC], scale));
-        q[j >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << (16 * (j & 1));
-      }
-      reinterpret_cast<uint2*>(p.y8 + row * p.width)[i] = make_uint2(q[0], q[1]);
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = make_float2(__fdiv_rn(h[c][2 * j], scale), __fdiv_rn(h[c][2 * j + 1], scale));
+      q[j >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << (16 * (j & 1));
+    }
+    if (!ODD || (lo == 0 && hi == 8)) {
+      *reinterpret_cast<uint2*>(p.y8 + at) = make_uint2(q[0], q[1]);
     } else {
-      p.y8[row * p.width + i] = __nv_cvt_float_to_fp8(__fdiv_rn(h[c][0], scale), __NV_SATFINITE, __NV_E4M3);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j >= lo && j < hi) p.y8[at + j] = static_cast<uint8_t>(q[j >> 2] >> (8 * (j & 3)));
     }
   }
 }
 
-template <int VEC, int CH>
+template <int CH>
 cudaError_t launch_norm(const NormParams& p, int threads, cudaStream_t stream) {
-  auto* fn = p.y8 ? add_rms_norm_kernel<VEC, CH, true> : add_rms_norm_kernel<VEC, CH, false>;
+  const bool odd = p.width % 8 != 0;
+  auto* fn = p.y8 ? (odd ? add_rms_norm_kernel<CH, true, true> : add_rms_norm_kernel<CH, true, false>)
+                  : (odd ? add_rms_norm_kernel<CH, false, true> : add_rms_norm_kernel<CH, false, false>);
   fn<<<static_cast<unsigned>(p.rows), threads, 0, stream>>>(p);
   note_launches(1);
   return cudaGetLastError();
@@ -148,20 +183,13 @@ cudaError_t launch_norm(const NormParams& p, int threads, cudaStream_t stream) {
 
 }  // namespace
 
-cudaError_t launch_add_rms_norm(const NormParams& p, cudaStream_t stream) {
-  const bool vec = p.width % 8 == 0;
-  const int n = vec ? p.width / 8 : p.width;
-  // as few threads as keep CH at 4 (32 or 4 elements in flight per input), then more accesses per thread
-  int threads = ((n + 3) / 4 + 31) / 32 * 32;
-  if (threads > 1024) threads = 1024;
-  const int ch = (n + threads - 1) / threads;
-  if (vec) {
-    if (ch <= 4) return launch_norm<8, 4>(p, threads, stream);
-    return launch_norm<8, 8>(p, threads, stream);   // up to 65,536 elements
-  }
-  if (ch <= 4) return launch_norm<1, 4>(p, threads, stream);
-  if (ch <= 16) return launch_norm<1, 16>(p, threads, stream);
-  return launch_norm<1, 64>(p, threads, stream);    // up to 65,536 elements
+cudaError_t launch_add_rms_norm(const NormParams& p, int sms, cudaStream_t stream) {
+  const int n = (p.width + (p.width % 8 ? 14 : 7)) / 8;  // chunks of a row at most (8,193)
+  auto threads_for = [&](int ch) { return ((n + ch - 1) / ch + 31) / 32 * 32; };
+  // few rows: latency, one chunk per thread; many: four, so that more rows are in flight per SM
+  if (n <= 1024 && p.rows <= 4 * sms) return launch_norm<1>(p, threads_for(1), stream);
+  if (n <= 4 * 1024) return launch_norm<4>(p, threads_for(4), stream);
+  return launch_norm<9>(p, threads_for(9), stream);
 }
 
 }  // namespace msa

@@ -506,8 +506,10 @@ msa_status_t msa_evict_paged(const msa_problem_t *problem, void *k_cache, void *
 
 /* The same over E4M3 pages.  A page has one scale per KV head, so a new page's
  * rows are rounded again: value = code * scale of the page it came from, scale
- * = max |value| / 448 over the new page's rows (1 when that is 0), code =
- * round-to-nearest-even(value / scale) in fp32, saturated. */
+ * = fp32(max |value| / 448) over the new page's rows (1, and codes 0, when the
+ * largest is below 2^-118), code =
+ * round-to-nearest-even of the exact value * 448 / max |value| (so a page that
+ * keeps its largest value keeps its codes). */
 msa_status_t msa_evict_paged_fp8(const msa_problem_t *problem, void *k8_cache, void *v8_cache, float *k_scale,
                                  float *v_scale, const int32_t *block_table, int32_t max_blocks_per_seq,
                                  int64_t num_pages, const float *weight, int64_t weight_stride, int32_t budget,
@@ -521,8 +523,8 @@ msa_status_t msa_evict_paged_fp8(const msa_problem_t *problem, void *k8_cache, v
  *   h = x + residual   (fp32; residual = NULL: h = x),   sum = bf16(h),
  *   y = h / sqrt(mean(h^2) + eps) * gamma   (from h before its rounding, bf16)
  *   x, residual, sum, y  [rows, d_model] bf16, gamma [d_model] bf16, 16-byte
- *   aligned; sum may be NULL.  sum may be x or residual (in place), and y may be
- *   one that sum is not; other outputs must not overlap an input.
+ *   aligned; sum may be NULL.  sum may be x or residual (in place), and y the
+ *   other one; outputs must not overlap otherwise, nor in part.
  * No workspace; rows = 0 is no work. */
 msa_status_t msa_add_rms_norm(const void *x, const void *residual, const void *gamma, int64_t rows, int32_t d_model,
                               float eps, void *sum, void *y, msa_stream_t stream);

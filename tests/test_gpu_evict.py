@@ -20,6 +20,13 @@ def msa():
     return m
 
 
+def _codes(x):
+    """E4M3 codes of 64-bit values within +-448, rounded to nearest even once (a conversion by way of fp32 rounds
+    twice and can miss a midpoint): 4 significant bits, the smallest step 2^-9."""
+    step = torch.exp2(torch.floor(torch.log2(x.abs().clamp(min=2.0 ** -6))) - 3)
+    return (torch.round(x / step) * step).float().to(torch.float8_e4m3fn).view(torch.uint8)
+
+
 class Cache:
     def __init__(self, msa, lens, hkv, budget, recent, fp8=False, seed=0, stride=None):
         host = torch.Generator().manual_seed(seed)
@@ -73,15 +80,14 @@ class Cache:
                     k[to, g], v[to, g] = self.k[fr, g], self.v[fr, g]
                     continue
                 for new, old, sc, osc in ((k, self.k, ks, self.ks), (v, self.v, vs, self.vs)):
-                    val = old[fr, g].view(torch.float8_e4m3fn).float() * osc[fr // PAGE, g][:, None]
+                    val = old[fr, g].view(torch.float8_e4m3fn).double() * osc[fr // PAGE, g].double()[:, None]
                     for b in range(blocks(m)):
                         part = val[b * PAGE:(b + 1) * PAGE]
                         top = part.abs().amax()
-                        # a division of two tensors: by a number torch would multiply by its rounded inverse
-                        scale = top / torch.full_like(top, 448.0) if top > 0 else torch.ones_like(top)
                         rows = to[b * PAGE:(b + 1) * PAGE]
-                        new[rows, g] = (part / scale).to(torch.float8_e4m3fn).view(torch.uint8)
-                        sc[rows[0] // PAGE, g] = scale
+                        new[rows, g] = _codes(part * 448 / top if top > 0 else part)
+                        # a division of two tensors: by a number torch multiplies by its rounded inverse
+                        sc[rows[0] // PAGE, g] = (top / torch.full_like(top, 448)).float() if top > 0 else 1.0
         return k, v, ks, vs, kept.cuda(), weights, torch.tensor(cu, dtype=torch.int32, device="cuda")
 
     def check(self, msa):
