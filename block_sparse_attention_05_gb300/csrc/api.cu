@@ -632,7 +632,7 @@ msa_status_t derive_paged(const msa_problem_t* p, PagedDecode& d) {
   d.N = p->total_k;
   d.hkv = p->num_kv_heads;
   d.G = p->num_q_heads / p->num_kv_heads;
-  if (d.G > 128 || d.hkv > 1024 || d.S > (1 << 20)) return MSA_ERR_UNSUPPORTED;
+  if (d.G > 128 || d.hkv > 1024 || d.S > (1 << 20) || p->max_seqlen_k > (1 << 30)) return MSA_ERR_UNSUPPORTED;
   d.max_k = p->max_seqlen_k;
   d.max_nb = (d.max_k + 127) / 128;
   d.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
@@ -659,7 +659,7 @@ DenseLayout dense_layout(const PagedDecode& d, bool weight) {
   L.hdr = take(sizeof(WsHeader));
   L.part_o = take(ctas * 2 * d.G * kHeadDim * sizeof(float));
   L.part_ml = take(ctas * 2 * d.G * sizeof(float2));
-  L.meta = take(ctas * sizeof(int2));
+  L.meta = take(static_cast<size_t>(d.S < dense_max_runs(d) ? d.S : dense_max_runs(d)) * d.hkv * sizeof(int4));
   L.flags = take(ctas * sizeof(uint32_t));
   if (weight) {
     L.logits = take(static_cast<size_t>(dense_max_units(d)) * d.hkv * d.G * kDenseTile * sizeof(float));
@@ -732,7 +732,8 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   p.hdr = at<WsHeader>(ws, L.hdr);
   p.part_o = at<float>(ws, L.part_o);
   p.part_ml = at<float2>(ws, L.part_ml);
-  p.meta = at<int2>(ws, L.meta);
+  p.meta = at<int4>(ws, L.meta);
+  p.by_seq = d.S <= p.groups;
   p.flags = at<uint32_t>(ws, L.flags);
   p.logits = weight ? at<float>(ws, L.logits) : nullptr;
   p.norm = weight ? at<float2>(ws, L.norm) : nullptr;
@@ -774,7 +775,7 @@ msa_status_t evict(const msa_problem_t* problem, void* k, void* v, float* k_scal
   if (weight_stride < d.max_k || new_weight_stride < new_max || new_max_blocks_per_seq < new_blocks)
     return MSA_ERR_INVALID_ARG;
   if (new_weight == weight || new_cu_seqlens_k == problem->cu_seqlens_k) return MSA_ERR_INVALID_ARG;
-  if (static_cast<long long>(d.S) * d.hkv > 0x7FFFFFFFLL || static_cast<long long>(d.S) * new_blocks > 0x7FFFFFFFLL)
+  if (static_cast<long long>(d.S) * d.hkv > 0x0FFFFFFFLL || static_cast<long long>(d.S) * new_blocks > 0x0FFFFFFFLL)
     return MSA_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < evict_bytes(num_pages)) return MSA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
@@ -807,7 +808,7 @@ msa_status_t evict(const msa_problem_t* problem, void* k, void* v, float* k_scal
   p.hdr = at<WsHeader>(ws, 0);
   p.marks = at<uint32_t>(ws, align_up(sizeof(WsHeader)));
   p.clear_bytes = evict_bytes(num_pages);
-  return cuda_status(launch_evict(p, fp8, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_evict(p, fp8, dev.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 msa_status_t add_rms_norm(const void* x, const void* residual, const void* gamma, int64_t rows, int32_t d_model,

@@ -199,12 +199,20 @@ struct Walker {
 };
 
 // ---------------------------------------------------------------- split kernel
-// MG head tiles of 16 rows by KG key tiles of 16: MG * KG compute warps, warp
-// (mg, kg) taking heads 16 mg .. of the group and keys 16 kg, 16 (kg + KG), ..
-// of a unit, and one warp that feeds the ring.
+// MG head tiles of 16 rows, each with KG compute warps, and one warp that feeds
+// the ring.  A warp takes NS key tiles of 16 at a time (independent chains of
+// MMAs, one softmax update for all of them): a unit's 64 keys are shared by
+// 4 / NS of a head tile's warps, and KG / (4 / NS) such teams take the units in
+// turn.  A ring stage always falls to the same team (stages are a multiple of
+// the teams): a warp that had not waited for a stage's previous fill could take
+// an older phase of its barrier for the next one.
 template <int MG, bool FP8>
 struct SplitCfg {
   static constexpr int kKG = MG <= 2 ? 4 : 8 / MG;
+  static constexpr int kNS = MG == 1 ? (FP8 ? 2 : 1) : MG == 2 ? 2 : 4;
+  static constexpr int kTeam = kTile / 16 / kNS;   // warps of a head tile that share a unit
+  static constexpr int kTeams = kKG / kTeam;
+  static_assert(kTeam * kTeams == kKG, "every warp belongs to a team");
   static constexpr int kWarps = MG * kKG;
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kCtasPerSm = MG == 1 ? 2 : 1;
@@ -212,6 +220,7 @@ struct SplitCfg {
   static constexpr int kHalf = kTile * kRowBytes;  // K or V of a stage
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = (MG == 1 ? 3 : 6) * (FP8 ? 2 : 1);
+  static_assert(kStages % kTeams == 0, "a stage's fills belong to one team");
   static constexpr int kExchange = kKG > 1 ? kWarps * 4096 : 0;  // half of each warp's O
   static constexpr int kMl = kWarps * 16 * 8;
   static constexpr size_t kSmem = kStages * kStage + kExchange + kMl + kStages * 24 + 16 + sizeof(RunSmem);
@@ -228,7 +237,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     dense_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                        DenseDecodeParams p) {
   using C = SplitCfg<MG, FP8>;
-  constexpr int KG = C::kKG;
+  constexpr int KG = C::kKG, NS = C::kNS;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;
   float* xch = reinterpret_cast<float*>(smem + C::kStages * C::kStage);
@@ -246,7 +255,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], C::kWarps);
+      mbar_init(&empty[i], MG * C::kTeam);
     }
     *abort_flag = 0;
     *err = 0;
@@ -257,14 +266,16 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
   if (!fine) {
     if (threadIdx.x == 0) {
       p.flags[blockIdx.x] = kFlagBadSeqlens;
-      p.meta[blockIdx.x] = make_int2(-1, 0);
+      if (!p.by_seq) p.meta[blockIdx.x].x = -1;
     }
+    if (p.by_seq && g < p.num_seqs && threadIdx.x == 0) p.meta[g * p.hkv + head].x = -1;  // num_seqs <= groups
     return;
   }
 
   // empty sequences: o = 0, lse = -inf
   for (int s = g; s < p.num_seqs; s += p.groups) {
     if (p.cu_k[s + 1] != p.cu_k[s]) continue;
+    if (p.by_seq && threadIdx.x == 0) p.meta[s * p.hkv + head].x = -1;
     const long long row0 = static_cast<long long>(s) * p.hkv * G + static_cast<long long>(head) * G;
     for (int i = threadIdx.x; i < G * 16; i += C::kThreads)
       reinterpret_cast<uint4*>(p.o + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
@@ -277,6 +288,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
   if (warp == C::kWarps) {
     // ------------------------------------------------------------ producer
     uint32_t fills = 0, bad = 0;
+    const uint64_t policy = l2_evict_first();  // with logits: K and V pass through, the logits are to stay in L2
     bool stopped = false;
     while (!stopped && walk.next(sg)) {
       const int first_page = sg.off * kTile / kBlock, last_page = (sg.off + sg.count - 1) * kTile / kBlock;
@@ -320,10 +332,14 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
             uint8_t* dv = dk + C::kHalf;
             if (FP8) scales[st] = make_float2(tk, tv);
             mbar_arrive_expect_tx(&full[st], C::kStage);
-            tma_load_3d(dk, &tm_k, &full[st], 0, head, r);
-            if (!FP8) tma_load_3d(dk + kTile * 128, &tm_k, &full[st], 64, head, r);
-            tma_load_3d(dv, &tm_v, &full[st], 0, head, r);
-            if (!FP8) tma_load_3d(dv + kTile * 128, &tm_v, &full[st], 64, head, r);
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, int dim) {
+              if (LOGITS) tma_load_3d_policy(dst, map, &full[st], dim, head, r, policy);
+              else tma_load_3d(dst, map, &full[st], dim, head, r);
+            };
+            load(dk, &tm_k, 0);
+            if (!FP8) load(dk + kTile * 128, &tm_k, 64);
+            load(dv, &tm_v, 0);
+            if (!FP8) load(dv + kTile * 128, &tm_v, 64);
             ++issued;
           }
         }
@@ -339,7 +355,8 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     const int t4 = lane & 3, r0 = mg * 16 + (lane >> 2), r1 = r0 + 8;  // this thread's two head rows
     uint32_t fills = 0;
     bool ok = true;
-    int sent_seq = -1, sent_last = 0;
+    const int team = kg / C::kTeam;
+    int4 crossing = make_int4(-1, 0, 0, 0);  // the sequence that begins in this run and goes on
     while (walk.next(sg)) {
       // Q fragments (A operand).  bf16: dims 16 kk + 2 t4 (+ 8); fp8: the order
       // in which a 4-byte word of codes widens, dims 16 kk + 4 t4 .. + 3, as
@@ -405,6 +422,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
       float ref0 = -INFINITY, ref1 = -INFINITY;  // fp8: O's own reference (see below)
 
       for (int u = sg.off; u < sg.off + sg.count; ++u, ++fills) {
+        if (C::kTeams > 1 && static_cast<int>(fills % C::kTeams) != team) continue;
         const int st = fills % C::kStages;
         if (ok && !mbar_wait_warp(&full[st], (fills / C::kStages) & 1, abort_flag)) {
           ok = false;  // keep walking: the segments' barriers below need every warp
@@ -415,61 +433,69 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
         }
         if (!ok) continue;
         const uint32_t kt = smem_u32(ring + st * C::kStage), vt = kt + C::kHalf;
-        const int valid = sg.len - u * kTile;  // keys of this unit (may exceed kTile)
-        float c0 = qs0, c1 = qs1, lv = 0.0f;
-        if (FP8) {
-          const float2 sc = scales[st];
-          c0 *= sc.x;
-          c1 *= sc.x;
-          lv = log2f(sc.y);
-        }
+        const int key0 = kg % C::kTeam * (NS * 16);
+        const int valid = sg.len - u * kTile - key0;  // keys of this warp's share that exist (may exceed it)
+        if (valid > 0) {                              // uniform in the warp
+          float c0 = qs0, c1 = qs1, lv = 0.0f;
+          if (FP8) {
+            const float2 sc = scales[st];
+            c0 *= sc.x;
+            c1 *= sc.x;
+            lv = log2f(sc.y);
+          }
+          // s[j]: keys key0 + 8 j + 2 t4 (+ 1) of rows r0 and r1
+          float s[2 * NS][4];
 #pragma unroll
-        for (int sub = 0; sub < kTile / 16 / KG; ++sub) {
-          const int key0 = (sub * KG + kg) * 16;
-          if (key0 >= valid) continue;  // uniform in the warp
-          float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int j = 0; j < 2 * NS; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[j][i] = 0.0f;
           const int krow = key0 + (lane & 7) + ((lane >> 4) << 3);
           if (!FP8) {
 #pragma unroll
-            for (int kk = 0; kk < 8; ++kk) {
-              uint32_t b[4];
-              ldsm_x4(kt + tile_off(krow, 2 * kk + ((lane >> 3) & 1)), b);
-              mma16<false>(s0, qa[kk], b[0], b[1]);
-              mma16<false>(s1, qa[kk], b[2], b[3]);
-            }
+            for (int kk = 0; kk < 8; ++kk)
+#pragma unroll
+              for (int n = 0; n < NS; ++n) {
+                uint32_t b[4];
+                ldsm_x4(kt + tile_off(krow + 16 * n, 2 * kk + ((lane >> 3) & 1)), b);
+                mma16<false>(s[2 * n], qa[kk], b[0], b[1]);
+                mma16<false>(s[2 * n + 1], qa[kk], b[2], b[3]);
+              }
           } else {
 #pragma unroll
-            for (int kk = 0; kk < 8; kk += 2) {  // one load: 16-byte chunks kk and kk + 1 of 16 keys
-              uint32_t b[4];
-              ldsm_x4(kt + tile_off(krow, kk + ((lane >> 3) & 1)), b);
-              mma16<true>(s0, qa[kk], e4m3x2_to_f16x2(b[0]), e4m3x2_to_f16x2(b[0] >> 16));
-              mma16<true>(s1, qa[kk], e4m3x2_to_f16x2(b[2]), e4m3x2_to_f16x2(b[2] >> 16));
-              mma16<true>(s0, qa[kk + 1], e4m3x2_to_f16x2(b[1]), e4m3x2_to_f16x2(b[1] >> 16));
-              mma16<true>(s1, qa[kk + 1], e4m3x2_to_f16x2(b[3]), e4m3x2_to_f16x2(b[3] >> 16));
-            }
+            for (int kk = 0; kk < 8; kk += 2)  // one load: 16-byte chunks kk and kk + 1 of 16 keys
+#pragma unroll
+              for (int n = 0; n < NS; ++n) {
+                uint32_t b[4];
+                ldsm_x4(kt + tile_off(krow + 16 * n, kk + ((lane >> 3) & 1)), b);
+                mma16<true>(s[2 * n], qa[kk], e4m3x2_to_f16x2(b[0]), e4m3x2_to_f16x2(b[0] >> 16));
+                mma16<true>(s[2 * n + 1], qa[kk], e4m3x2_to_f16x2(b[2]), e4m3x2_to_f16x2(b[2] >> 16));
+                mma16<true>(s[2 * n], qa[kk + 1], e4m3x2_to_f16x2(b[1]), e4m3x2_to_f16x2(b[1] >> 16));
+                mma16<true>(s[2 * n + 1], qa[kk + 1], e4m3x2_to_f16x2(b[3]), e4m3x2_to_f16x2(b[3] >> 16));
+              }
           }
-          const bool tail = key0 + 16 > valid;
+          const bool tail = valid < NS * 16;
           if (tail) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              if (key0 + 2 * t4 + i >= valid) s0[i] = s0[2 + i] = -INFINITY;
-              if (key0 + 8 + 2 * t4 + i >= valid) s1[i] = s1[2 + i] = -INFINITY;
-            }
+            for (int j = 0; j < 2 * NS; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                if (8 * j + 2 * t4 + i >= valid) s[j][i] = s[j][2 + i] = -INFINITY;
           }
           if (LOGITS) {
-            float* w = p.logits + ((sg.unit + (u - sg.off)) * p.hkv + head) * static_cast<long long>(G) * kTile;
-            const int at = key0 + 2 * t4;
-            if (r0 < G) {
-              *reinterpret_cast<float2*>(w + r0 * kTile + at) = make_float2(s0[0] * c0, s0[1] * c0);
-              *reinterpret_cast<float2*>(w + r0 * kTile + at + 8) = make_float2(s1[0] * c0, s1[1] * c0);
-            }
-            if (r1 < G) {
-              *reinterpret_cast<float2*>(w + r1 * kTile + at) = make_float2(s0[2] * c1, s0[3] * c1);
-              *reinterpret_cast<float2*>(w + r1 * kTile + at + 8) = make_float2(s1[2] * c1, s1[3] * c1);
+            float* w = p.logits + ((sg.unit + (u - sg.off)) * p.hkv + head) * static_cast<long long>(G) * kTile +
+                       key0 + 2 * t4;
+#pragma unroll
+            for (int j = 0; j < 2 * NS; ++j) {
+              if (r0 < G) *reinterpret_cast<float2*>(w + r0 * kTile + 8 * j) = make_float2(s[j][0] * c0, s[j][1] * c0);
+              if (r1 < G) *reinterpret_cast<float2*>(w + r1 * kTile + 8 * j) = make_float2(s[j][2] * c1, s[j][3] * c1);
             }
           }
-          float x0 = fmaxf(fmaxf(s0[0], s0[1]), fmaxf(s1[0], s1[1]));
-          float x1 = fmaxf(fmaxf(s0[2], s0[3]), fmaxf(s1[2], s1[3]));
+          float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 2 * NS; ++j) {
+            x0 = fmax3(x0, s[j][0], s[j][1]);
+            x1 = fmax3(x1, s[j][2], s[j][3]);
+          }
 #pragma unroll
           for (int of = 1; of < 4; of <<= 1) {
             x0 = fmaxf(x0, __shfl_xor_sync(0xFFFFFFFFu, x0, of));
@@ -503,63 +529,68 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
           }
           const float e0 = n0 == -INFINITY ? 0.0f : n0, e1 = n1 == -INFINITY ? 0.0f : n1;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            s0[i] = exp2_approx(fmaf(s0[i], c0, -e0));
-            s1[i] = exp2_approx(fmaf(s1[i], c0, -e0));
-            s0[2 + i] = exp2_approx(fmaf(s0[2 + i], c1, -e1));
-            s1[2 + i] = exp2_approx(fmaf(s1[2 + i], c1, -e1));
-          }
-          l0 += (s0[0] + s0[1]) + (s1[0] + s1[1]);
-          l1 += (s0[2] + s0[3]) + (s1[2] + s1[3]);
-          // P as the A operand.  bf16 V: the weights as a bf16 value and the bf16
-          // rest (16 significant bits; one bf16 alone would add half as much error
-          // again as the output's own rounding).  fp8: one fp16 value.
-          uint32_t ph[4], pl[4];
-          if (!FP8) {
-            split_bf16(s0[0], s0[1], ph[0], pl[0]);
-            split_bf16(s0[2], s0[3], ph[1], pl[1]);
-            split_bf16(s1[0], s1[1], ph[2], pl[2]);
-            split_bf16(s1[2], s1[3], ph[3], pl[3]);
-          } else {
-            ph[0] = pack_f16(s0[0] * f0, s0[1] * f0);
-            ph[1] = pack_f16(s0[2] * f1, s0[3] * f1);
-            ph[2] = pack_f16(s1[0] * f0, s1[1] * f0);
-            ph[3] = pack_f16(s1[2] * f1, s1[3] * f1);
-          }
-          // rows past the sequence's end hold anything (0 * NaN): V words of such keys become 0
-          uint32_t k0 = 0xFFFFFFFFu, k1 = 0xFFFFFFFFu;
-          if (tail) {
-            const int a = valid - key0 - 2 * t4, b = a - 8;
-            k0 = a >= 2 ? 0xFFFFFFFFu : a == 1 ? 0xFFFFu : 0u;
-            k1 = b >= 2 ? 0xFFFFFFFFu : b == 1 ? 0xFFFFu : 0u;
-          }
-          const int vrow = key0 + (lane & 7) + (((lane >> 3) & 1) << 3);
-          if (!FP8) {
+          for (int j = 0; j < 2 * NS; ++j) {
 #pragma unroll
-            for (int j = 0; j < 16; j += 2) {  // dims 8 j .. 8 j + 15
-              uint32_t b[4];
-              ldsm_x4_trans(vt + tile_off(vrow, j + (lane >> 4)), b);
-              b[0] &= k0; b[1] &= k1; b[2] &= k0; b[3] &= k1;
-              mma16<false>(o[j], ph, b[0], b[1]);
-              mma16<false>(o[j + 1], ph, b[2], b[3]);
-              mma16<false>(o[j], pl, b[0], b[1]);
-              mma16<false>(o[j + 1], pl, b[2], b[3]);
+            for (int i = 0; i < 2; ++i) {
+              s[j][i] = exp2_approx(fmaf(s[j][i], c0, -e0));
+              s[j][2 + i] = exp2_approx(fmaf(s[j][2 + i], c1, -e1));
             }
-          } else {
-            // A 16-bit word of the transposed load is two adjacent dims of one
-            // key, so a register holds (key 2 t4: dims d, d + 1; key 2 t4 + 1:
-            // d, d + 1) with d = 16 c + 2 (lane / 4): accumulator tile 2 c takes
-            // the even dims of chunk c, tile 2 c + 1 the odd ones.
+            l0 += s[j][0] + s[j][1];
+            l1 += s[j][2] + s[j][3];
+          }
 #pragma unroll
-            for (int c = 0; c < 8; c += 2) {
-              uint32_t b[4];
-              ldsm_x4_trans(vt + tile_off(vrow, c + (lane >> 4)), b);
+          for (int n = 0; n < NS; ++n) {
+            // P as the A operand.  bf16 V: the weights as a bf16 value and the bf16
+            // rest (16 significant bits; one bf16 alone would add half as much error
+            // again as the output's own rounding).  fp8: one fp16 value.
+            uint32_t ph[4], pl[4];
+            const float(&w0)[4] = s[2 * n], (&w1)[4] = s[2 * n + 1];
+            if (!FP8) {
+              split_bf16(w0[0], w0[1], ph[0], pl[0]);
+              split_bf16(w0[2], w0[3], ph[1], pl[1]);
+              split_bf16(w1[0], w1[1], ph[2], pl[2]);
+              split_bf16(w1[2], w1[3], ph[3], pl[3]);
+            } else {
+              ph[0] = pack_f16(w0[0] * f0, w0[1] * f0);
+              ph[1] = pack_f16(w0[2] * f1, w0[3] * f1);
+              ph[2] = pack_f16(w1[0] * f0, w1[1] * f0);
+              ph[3] = pack_f16(w1[2] * f1, w1[3] * f1);
+            }
+            // rows past the sequence's end hold anything (0 * NaN): V words of such keys become 0
+            uint32_t k0 = 0xFFFFFFFFu, k1 = 0xFFFFFFFFu;
+            if (tail) {
+              const int a = valid - 16 * n - 2 * t4, b = a - 8;
+              k0 = a >= 2 ? 0xFFFFFFFFu : a == 1 ? 0xFFFFu : 0u;
+              k1 = b >= 2 ? 0xFFFFFFFFu : b == 1 ? 0xFFFFu : 0u;
+            }
+            const int vrow = key0 + 16 * n + (lane & 7) + (((lane >> 3) & 1) << 3);
+            if (!FP8) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i] & ((i & 1) ? k1 : k0), 0, 0x3120);
-              mma16<true>(o[2 * c], ph, e4m3x2_to_f16x2(b[0]), e4m3x2_to_f16x2(b[1]));
-              mma16<true>(o[2 * c + 1], ph, e4m3x2_to_f16x2(b[0] >> 16), e4m3x2_to_f16x2(b[1] >> 16));
-              mma16<true>(o[2 * c + 2], ph, e4m3x2_to_f16x2(b[2]), e4m3x2_to_f16x2(b[3]));
-              mma16<true>(o[2 * c + 3], ph, e4m3x2_to_f16x2(b[2] >> 16), e4m3x2_to_f16x2(b[3] >> 16));
+              for (int j = 0; j < 16; j += 2) {  // dims 8 j .. 8 j + 15
+                uint32_t b[4];
+                ldsm_x4_trans(vt + tile_off(vrow, j + (lane >> 4)), b);
+                b[0] &= k0; b[1] &= k1; b[2] &= k0; b[3] &= k1;
+                mma16<false>(o[j], ph, b[0], b[1]);
+                mma16<false>(o[j + 1], ph, b[2], b[3]);
+                mma16<false>(o[j], pl, b[0], b[1]);
+                mma16<false>(o[j + 1], pl, b[2], b[3]);
+              }
+            } else {
+              // A 16-bit word of the transposed load is two adjacent dims of one
+              // key, so a register holds (key 2 t4: dims d, d + 1; key 2 t4 + 1:
+              // d, d + 1) with d = 16 c + 2 (lane / 4): accumulator tile 2 c takes
+              // the even dims of chunk c, tile 2 c + 1 the odd ones.
+#pragma unroll
+              for (int c = 0; c < 8; c += 2) {
+                uint32_t b[4];
+                ldsm_x4_trans(vt + tile_off(vrow, c + (lane >> 4)), b);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) b[i] = __byte_perm(b[i] & ((i & 1) ? k1 : k0), 0, 0x3120);
+                mma16<true>(o[2 * c], ph, e4m3x2_to_f16x2(b[0]), e4m3x2_to_f16x2(b[1]));
+                mma16<true>(o[2 * c + 1], ph, e4m3x2_to_f16x2(b[0] >> 16), e4m3x2_to_f16x2(b[1] >> 16));
+                mma16<true>(o[2 * c + 2], ph, e4m3x2_to_f16x2(b[2]), e4m3x2_to_f16x2(b[3]));
+                mma16<true>(o[2 * c + 3], ph, e4m3x2_to_f16x2(b[2] >> 16), e4m3x2_to_f16x2(b[3] >> 16));
+              }
             }
           }
         }
@@ -696,11 +727,12 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
       if (sg.first && !sg.last) {
         // the run that holds the sequence's last unit: lo(x) = floor(total x / runs) <= u < lo(x + 1)
         const long long end = sg.unit + units_of(sg.len) - 1;
-        sent_seq = sg.seq;
-        sent_last = static_cast<int>(((end + 1) * run.runs - 1) / run.total);
+        crossing = make_int4(sg.seq, g, static_cast<int>(((end + 1) * run.runs - 1) / run.total), 0);
       }
+      if (p.by_seq && sg.first && warp == 0 && lane == 0)
+        p.meta[sg.seq * p.hkv + head] = sg.last ? make_int4(-1, 0, 0, 0) : crossing;
     }
-    if (warp == 0 && lane == 0) p.meta[blockIdx.x] = make_int2(sent_seq, sent_last);
+    if (!p.by_seq && warp == 0 && lane == 0) p.meta[blockIdx.x] = crossing;
   }
   __syncthreads();
   if (*abort_flag && issued > 0)  // no copy may land after this CTA has left
@@ -710,80 +742,106 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
 }
 
 // ---------------------------------------------------------------- join
-// CTA (run, KV head; four head rows): when a sequence begins in the run and
-// goes on behind it, merges that sequence's partials, four warps to a row.
-__global__ void __launch_bounds__(512) dense_join_kernel(DenseDecodeParams p) {
-  __shared__ float acc[4][4][kHeadDim];
-  __shared__ float accl[4][4];
+// Merges the partials of a sequence that crosses runs.  CTA (entry of meta, KV
+// head; 8 / wpr head rows), wpr warps to a row, eight partials in flight each:
+// a sequence alone has as many partials as there are runs (and few rows to
+// spread them over), the sequences of a large batch have two or three.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseDecodeParams p, int wpr) {
+  __shared__ float4 acc[8][32];
+  __shared__ float2 ml[8];
   __shared__ uint32_t all_flags;
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int4 meta = p.meta[blockIdx.x];
   if (blockIdx.x == 0 && blockIdx.y == 0) {
     if (threadIdx.x == 0) all_flags = 0;
     __syncthreads();
     uint32_t f = 0;
-    for (int i = threadIdx.x; i < p.groups * p.hkv; i += blockDim.x) f |= p.flags[i];
+    for (int i = threadIdx.x; i < p.groups * p.hkv; i += kJoinThreads) f |= p.flags[i];
     if (f) atomicOr(&all_flags, f);
     __syncthreads();
     if (threadIdx.x == 0) p.hdr->status = all_flags;
   }
-  const int2 meta = p.meta[blockIdx.x];
   if (meta.x < 0) return;
-  const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv, G = p.group;
-  const int row = blockIdx.y * 4 + (warp >> 2), sub = warp & 3;
-  const int n = meta.y - g + 1;
-  const bool on = row < G;
-  auto part = [&](int i) {  // row of run g + i's partial: its first run ends it in slot 1, the others begin with it
-    return ((static_cast<long long>(g + i) * p.hkv + head) * 2 + (i == 0 ? 1 : 0)) * G + row;
-  };
-  float M = -INFINITY;
-  if (on)
-    for (int i = lane; i < n; i += 32) M = fmaxf(M, p.part_ml[part(i)].x);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, o));
+  const int head = blockIdx.x % p.hkv, G = p.group;
+  const int row = blockIdx.y * (8 / wpr) + warp / wpr, sub = warp % wpr;
+  const int n = meta.z - meta.y + 1;
+  float m = -INFINITY, l = 0.0f;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.0f;
-  if (on) {
-#pragma unroll 8
-    for (int i = sub; i < n; i += 4) {
-      const long long at = part(i);
-      const float2 x = p.part_ml[at];
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 4);
-      const float f = exp2_diff(x.x, M);
-      l += x.y * f;
-      a.x += v.x * f;
-      a.y += v.y * f;
-      a.z += v.z * f;
-      a.w += v.w * f;
+  if (row < G) {
+    // run meta.y + i's partial: the first run ends it in slot 1, the others begin with it in slot 0
+    const long long first = (static_cast<long long>(meta.y) * p.hkv + head) * 2;
+    for (int i0 = sub; i0 < n; i0 += 8 * wpr) {
+      float2 x[8];
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = i0 + u * wpr;
+        x[u] = make_float2(-INFINITY, 0.0f);
+        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i < n) {
+          const long long at = (first + static_cast<long long>(i) * p.hkv * 2 + (i == 0 ? 1 : 0)) * G + row;
+          x[u] = p.part_ml[at];
+          v[u] = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 4);
+        }
+      }
+      float nm = m;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) nm = fmaxf(nm, x[u].x);
+      const float k = exp2_diff(m, nm);
+      a.x *= k; a.y *= k; a.z *= k; a.w *= k;
+      l *= k;
+      m = nm;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float f = exp2_diff(x[u].x, m);
+        l = fmaf(x[u].y, f, l);
+        a.x = fmaf(v[u].x, f, a.x);
+        a.y = fmaf(v[u].y, f, a.y);
+        a.z = fmaf(v[u].z, f, a.z);
+        a.w = fmaf(v[u].w, f, a.w);
+      }
     }
   }
-  *reinterpret_cast<float4*>(&acc[warp >> 2][sub][lane * 4]) = a;
-  if (lane == 0) accl[warp >> 2][sub] = l;
-  __syncthreads();
-  if (sub != 0 || !on) return;
-  const int rr = warp >> 2;
-  l = (accl[rr][0] + accl[rr][1]) + (accl[rr][2] + accl[rr][3]);
-  const float inv = inverse(l);
-  float w[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int d = lane * 4 + j;
-    w[j] = ((acc[rr][0][d] + acc[rr][1][d]) + (acc[rr][2][d] + acc[rr][3][d])) * inv;
+  if (wpr > 1) {
+    acc[warp][lane] = a;
+    if (lane == 0) ml[warp] = make_float2(m, l);
+    __syncthreads();
+    if (sub != 0) return;
+    float M = m;
+    for (int w = 1; w < wpr; ++w) M = fmaxf(M, ml[warp + w].x);
+    float k = exp2_diff(m, M);
+    a.x *= k; a.y *= k; a.z *= k; a.w *= k;
+    l *= k;
+    m = M;
+    for (int w = 1; w < wpr; ++w) {
+      const float4 v = acc[warp + w][lane];
+      k = exp2_diff(ml[warp + w].x, M);
+      l = fmaf(ml[warp + w].y, k, l);
+      a.x = fmaf(v.x, k, a.x);
+      a.y = fmaf(v.y, k, a.y);
+      a.z = fmaf(v.z, k, a.z);
+      a.w = fmaf(v.w, k, a.w);
+    }
   }
+  if (row >= G) return;
+  const float inv = inverse(l);
   const long long out = (static_cast<long long>(meta.x) * p.hkv + head) * G + row;
-  *reinterpret_cast<uint2*>(p.o + out * kHeadDim + lane * 4) = make_uint2(pack_bf16(w[0], w[1]), pack_bf16(w[2], w[3]));
+  *reinterpret_cast<uint2*>(p.o + out * kHeadDim + lane * 4) =
+      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
   if (lane == 0) {
-    p.lse[out] = (M + log2f(l)) * kLn2;
-    if (p.norm) p.norm[out] = row_norm(M, l);
+    p.lse[out] = (m + log2f(l)) * kLn2;
+    if (p.norm) p.norm[out] = row_norm(m, l);
   }
 }
 
 // ---------------------------------------------------------------- weights
 // weight[s, g, j] += sum over the group's heads of 2^(s[h,j] - m_h) / l_h, from
-// the logits that the split kernel left.  The heads are added in order: one
-// thread per key, no atomics.
+// the logits that the split kernel left (mostly still in L2).  The heads are
+// added in order, four keys to a thread: no atomics.
 constexpr int kWeightThreads = 512;
-__global__ void __launch_bounds__(kWeightThreads) dense_weight_kernel(DenseDecodeParams p) {
+__global__ void __launch_bounds__(kWeightThreads, 2) dense_weight_kernel(DenseDecodeParams p) {
   __shared__ RunSmem run_sm;
   __shared__ float2 norm[128];
   griddep_wait();
@@ -793,23 +851,39 @@ __global__ void __launch_bounds__(kWeightThreads) dense_weight_kernel(DenseDecod
   if (!find_run(p.cu_k, p.num_seqs, p.max_k, p.total_k, g, p.groups, run_sm, run)) return;
   Walker walk(p.cu_k, run);
   Segment sg;
-  const int key = threadIdx.x % kTile, lane_unit = threadIdx.x / kTile;
+  constexpr int kPer = kTile / 4;  // threads of a unit
+  const int key = threadIdx.x % kPer * 4, first = threadIdx.x / kPer;
   while (walk.next(sg)) {
     __syncthreads();
-    const long long row = (static_cast<long long>(sg.seq) * p.hkv + head);
+    const long long row = static_cast<long long>(sg.seq) * p.hkv + head;
     if (threadIdx.x < G) norm[threadIdx.x] = p.norm[row * G + threadIdx.x];
     __syncthreads();
-    for (int i = lane_unit; i < sg.count; i += kWeightThreads / kTile) {
+    float* out = p.weight + row * p.weight_stride;
+    const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
+    for (int i = first; i < sg.count; i += kWeightThreads / kPer) {
       const int j = (sg.off + i) * kTile + key;
       if (j >= sg.len) continue;
       const float* s = p.logits + ((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) * kTile + key;
-      float sum = 0.0f;
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
       for (int h = 0; h < G; ++h) {
         const float2 n = norm[h];
-        sum += exp2_approx(s[h * kTile] - n.x) * n.y;
+        const float4 v = *reinterpret_cast<const float4*>(s + h * kTile);
+        sum.x += exp2_approx(v.x - n.x) * n.y;
+        sum.y += exp2_approx(v.y - n.x) * n.y;
+        sum.z += exp2_approx(v.z - n.x) * n.y;
+        sum.w += exp2_approx(v.w - n.x) * n.y;
       }
-      p.weight[row * p.weight_stride + j] += sum;
+      if (vec && j + 4 <= sg.len) {
+        float4* at = reinterpret_cast<float4*>(out + j);
+        const float4 old = *at;
+        *at = make_float4(old.x + sum.x, old.y + sum.y, old.z + sum.z, old.w + sum.w);
+      } else {
+        out[j] += sum.x;
+        if (j + 1 < sg.len) out[j + 1] += sum.y;
+        if (j + 2 < sg.len) out[j + 2] += sum.z;
+        if (j + 3 < sg.len) out[j + 3] += sum.w;
+      }
     }
   }
 }
@@ -843,7 +917,11 @@ cudaError_t launch_dense_decode(const CUtensorMap& tk, const CUtensorMap& tv, co
                                 cudaStream_t stream) {
   cudaError_t e = fp8 ? launch_split_for<true>(tk, tv, p, stream) : launch_split_for<false>(tk, tv, p, stream);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(dense_join_kernel, dim3(p.groups * p.hkv, (p.group + 3) / 4), dim3(512), 0, stream, p);
+  const int entries = p.by_seq ? p.num_seqs : p.groups;
+  int wpr = 1;  // warps to a row: one for every four partials that a sequence has on average, up to eight
+  while (wpr < 8 && p.groups / entries >= 8 * wpr) wpr *= 2;
+  e = launch_pdl(dense_join_kernel, dim3(entries * p.hkv, (p.group * wpr + 7) / 8), dim3(kJoinThreads), 0, stream, p,
+                 wpr);
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (!p.weight) return cudaSuccess;

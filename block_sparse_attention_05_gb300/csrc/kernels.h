@@ -297,7 +297,10 @@ struct DenseDecodeParams {
   WsHeader* hdr;                // only the status is written
   float* part_o;                // [groups, hkv, 2, group, 128]: slot 1 the sequence that goes on behind the run
   float2* part_ml;              // [groups, hkv, 2, group] (maximum in log2 units, sum)
-  int2* meta;                   // [groups, hkv] (sequence that begins here and goes on or -1, its last run)
+  // [entries, hkv] the sequences that cross runs: (sequence or -1, first run, last run), an entry per sequence (by_seq,
+  // num_seqs <= groups) or per run (the sequence that begins there and goes on)
+  int4* meta;
+  bool by_seq;
   uint32_t* flags;              // [groups, hkv] device error flags
   float* logits;                // with weight: [units, hkv, group, kDenseTile] in log2 units; else null
   float2* norm;                 // with weight: [num_seqs, hkv * group] (maximum, 1 / sum); else null
@@ -330,7 +333,7 @@ struct EvictParams {
   uint32_t* marks;              // [n_pages] behind the header
   size_t clear_bytes;           // header and marks
 };
-cudaError_t launch_evict(const EvictParams& p, bool fp8, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams& p, bool fp8, int sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- residual sum and norm
 struct NormParams {

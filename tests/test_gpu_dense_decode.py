@@ -194,6 +194,24 @@ def test_repeats_are_bit_equal(msa, fp8):
         assert torch.equal(o, o2) and torch.equal(lse, lse2) and torch.equal(first, b.weight)
 
 
+@pytest.mark.parametrize("hq,hkv", [(64, 4), (32, 1), (64, 1), (128, 1)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_many_calls_in_a_row(msa, hq, hkv, fp8):
+    """Calls that follow one another without a pause, over caches larger than L2: every one gives the first one's bits."""
+    b = Batch(msa, [1 + (i * 5021) % 16384 for i in range(32)], hq, hkv, fp8, True, seed=16)
+    start, ws = b.weight.clone(), b.ws(msa)
+    o, lse = b.call(msa, ws=ws)
+    first = b.weight.clone()
+    for _ in range(5):
+        b.weight.copy_(start)
+        outs = [b.call(msa, ws=ws)]
+        once = b.weight.clone()
+        outs += [b.call(msa, ws=ws) for _ in range(6)]
+        assert torch.equal(once, first) and msa.msa_read_device_status(ws) == 0
+        for o2, lse2 in outs:
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_outputs_given_by_the_caller_and_another_stream(msa):
     b = Batch(msa, [777, 12], 64, 4, False, False, seed=12)
     o, lse = b.call(msa)
