@@ -11,6 +11,8 @@
 // (512 bytes in bf16) and bounds the call.
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 
@@ -21,11 +23,11 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr uint32_t kMarkNew = 256u;  // page marks: 1 = a page of the batch's table, + 256 per entry of the new one
 
-// Larger key = larger weight; -0 = +0; NaN below -inf.
+// Larger key = larger weight; -0 = +0 (the addition makes them one); NaN below -inf.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-  if (w != w) return 0u;
-  const uint32_t u = __float_as_uint(w == 0.0f ? 0.0f : w);
-  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+  const uint32_t u = __float_as_uint(w + 0.0f);
+  const uint32_t k = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return w != w ? 0u : k;
 }
 
 // Sum of v over the CTA's threads before this one; `total` gets the sum over all.  sm: 33 words.
@@ -51,17 +53,12 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t v, uint32_t& total,
   return incl - v + (warp ? before : 0u);
 }
 
-// The first digit holds sign, exponent and two bits: the weights of a cache fall into a few dozen of its bins, so a
-// warp's counts would meet in the same words.  Four lane groups count into copies of their own.
-constexpr int kCopies = 4;
-
 // A word of the shared memory of CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t cluster_word(const uint32_t* p, uint32_t rank) {
   uint32_t v;
   asm volatile("{\n\t.reg .b32 a;\n\tmapa.shared::cluster.u32 a, %1, %2;\n\tld.shared::cluster.u32 %0, [a];\n\t}"
                : "=r"(v)
-               : "r"(smem_u32(p)), "r"(rank)
-               : "memory");
+               : "r"(smem_u32(p)), "r"(rank));
   return v;
 }
 
@@ -74,7 +71,6 @@ __device__ __forceinline__ uint32_t cluster_word(const uint32_t* p, uint32_t ran
 // load, or from registers when a share fits them.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p, int cs) {
   __shared__ uint32_t hist[3][2048];
-  __shared__ uint32_t spread[2048 * (kCopies - 1)];
   __shared__ uint32_t sm[33];
   __shared__ uint32_t pick[3][2];
   __shared__ uint32_t mine[2];  // kept for sure and equal to the threshold, in this CTA's share
@@ -93,8 +89,6 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     bad |= a < 0 || b < a || b - a > p.max_k;
   }
   for (int i = t; i < 3 * 2048; i += kSelThreads) hist[0][i] = 0;
-  for (int i = t; i < 2048 * (kCopies - 1); i += kSelThreads) spread[i] = 0;
-  uint32_t* const own_first = t % kCopies ? spread + (t % kCopies - 1) * 2048 : hist[0];
   if (__syncthreads_or(bad)) {
     if (t == 0 && blockIdx.x == 0) atomicOr(&p.hdr->status, kFlagBadSeqlens);
     return;  // the whole cluster
@@ -138,22 +132,26 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
   }
   const int free_n = n - p.recent, take = p.budget - p.recent;  // free_n > take
 
-  // this CTA's slots [c0, c1), four at a time
-  const int share = ((n + cs - 1) / cs + 3) & ~3;
+  // this CTA's slots [c0, c1), c0 a multiple of 16
+  const int share = ((n + cs - 1) / cs + 15) & ~15;
   const int c0 = min(n, rank * share), c1 = min(n, c0 + share);
   const bool vec = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
-  auto load4 = [&](int i) {  // slots i .. i + 3; past the share anything
-    if (vec && i + 4 <= c1) return *reinterpret_cast<const float4*>(w + i);
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < c1) v.x = w[i];
-    if (i + 1 < c1) v.y = w[i + 1];
-    if (i + 2 < c1) v.z = w[i + 2];
-    if (i + 3 < c1) v.w = w[i + 3];
-    return v;
+  auto all4 = [&](int i) {  // slots i .. i + 3, all of the share
+    return vec ? *reinterpret_cast<const float4*>(w + i) : make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  };
+  auto load4 = [&](int i) {  // past the share zeros
+    if (i + 4 <= c1) return all4(i);
+    return make_float4(i < c1 ? w[i] : 0.f, i + 1 < c1 ? w[i + 1] : 0.f, i + 2 < c1 ? w[i + 2] : 0.f, 0.f);
   };
   const bool once = c1 - c0 <= 4 * kSelThreads;
-  float4 held = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (once && c0 + 4 * t < c1) held = load4(c0 + 4 * t);
+  const int warp = t >> 5, lane = t & 31;
+  float held[4];  // slots c0 + 128 warp + 32 j + lane
+  if (once)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = c0 + 128 * warp + 32 * j + lane;
+      held[j] = i < c1 ? w[i] : 0.0f;
+    }
 
   uint32_t prefix = 0, mask = 0;
   uint32_t want = take;   // how many of the keys with this prefix are taken
@@ -165,31 +163,35 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = shifts[pass], bins = 1 << bits[pass];
-      auto count4 = [&](const float4& v, int i) {
-        const float f[4] = {v.x, v.y, v.z, v.w};
-        uint32_t* const counts = pass == 0 ? own_first : hist[pass];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t k = weight_key(f[j]);
-          if (i + j < end && (k & mask) == prefix) atomicAdd(&counts[(k >> shift) & (bins - 1)], 1u);
-        }
+      auto count = [&](float f, bool on) {
+        const uint32_t k = weight_key(f);
+        if (on && (k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
       };
       if (once) {
-        count4(held, c0 + 4 * t);
-      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) count(held[j], c0 + 128 * warp + 32 * j + lane < end);
+      } else if (end > c0) {
+        const int whole = c0 + (end - c0) / (16 * kSelThreads) * (16 * kSelThreads);
         int i = c0 + 4 * t;
-        for (; i + 12 * kSelThreads < end; i += 16 * kSelThreads) {  // four loads in flight
+        for (; i < whole; i += 16 * kSelThreads) {  // four loads in flight, nothing to check
           float4 v[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) v[u] = load4(i + 4 * u * kSelThreads);
+          for (int u = 0; u < 4; ++u) v[u] = all4(i + 4 * u * kSelThreads);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) count4(v[u], i + 4 * u * kSelThreads);
+          for (int u = 0; u < 4; ++u) {
+            count(v[u].x, true);
+            count(v[u].y, true);
+            count(v[u].z, true);
+            count(v[u].w, true);
+          }
         }
-        for (; i < end; i += 4 * kSelThreads) count4(load4(i), i);
-      }
-      if (pass == 0) {
-        __syncthreads();
-        for (int i = t; i < 2048; i += kSelThreads) hist[0][i] += spread[i] + spread[2048 + i] + spread[4096 + i];
+        for (; i < end; i += 4 * kSelThreads) {
+          const float4 v = load4(i);
+          count(v.x, true);
+          count(v.y, i + 1 < end);
+          count(v.z, i + 2 < end);
+          count(v.w, i + 3 < end);
+        }
       }
       sync_all();
       // thread t takes the bins from the top: bins - 1 - (2 t) and the one below (one bin for 10 bits)
@@ -197,10 +199,21 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       const int top = bins - 1 - per * t;
       const uint32_t own0 = hist[pass][top], own1 = per > 1 ? hist[pass][top - 1] : 0u;
       uint32_t n0 = own0, n1 = own1;
-      for (int r = 0; r < cs; ++r) {
-        if (r == rank) continue;
-        n0 += cluster_word(&hist[pass][top], r);
-        if (per > 1) n1 += cluster_word(&hist[pass][top - 1], r);
+      if (cs > 1) {
+        uint32_t v0[7], v1[7];  // all in flight at once
+#pragma unroll
+        for (int r = 1; r < 8; ++r) {
+          v0[r - 1] = v1[r - 1] = 0;
+          if (r >= cs) continue;
+          const int from = rank + r < cs ? rank + r : rank + r - cs;
+          v0[r - 1] = cluster_word(&hist[pass][top], from);
+          if (per > 1) v1[r - 1] = cluster_word(&hist[pass][top - 1], from);
+        }
+#pragma unroll
+        for (int r = 0; r < 7; ++r) {
+          n0 += v0[r];
+          n1 += v1[r];
+        }
       }
       uint32_t total;
       const uint32_t before = block_exclusive(n0 + n1, total, sm);
@@ -235,40 +248,51 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     sync_all();  // nobody leaves before its words are read
   }
 
-  // ordered compaction: keys above the threshold, the first `want` equal to it, and the window
-  for (int i0 = c0; i0 < c1; i0 += 4 * kSelThreads) {
-    const int i = i0 + 4 * t;
-    const float4 v4 = once ? held : (i < c1 ? load4(i) : make_float4(0.f, 0.f, 0.f, 0.f));
-    const float v[4] = {v4.x, v4.y, v4.z, v4.w};
-    uint32_t sure = 0, same = 0;  // bits
+  // Ordered compaction: keys above the threshold, the first `want` equal to it, and the window.  A warp takes 32 kRows
+  // neighbours, a row of 32 at a time, so that what it keeps of a row is written in one piece; the warps' places
+  // come from one scan of their counts.
+  const bool by_weight = take > 0;
+  auto compact = [&](auto rows, int i0) {
+    constexpr int kRows = decltype(rows)::value;
+    const int i = i0 + 32 * kRows * warp + lane;
+    float v[kRows];
+    uint32_t sure[kRows], same[kRows];  // a bit per lane
+    uint32_t n_sure = 0, n_same = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (i + j >= c1) continue;
-      if (i + j >= free_n) {
-        sure |= 1u << j;
-      } else if (take > 0) {
-        const uint32_t k = weight_key(v[j]);
-        if (k > prefix) sure |= 1u << j;
-        if (k == prefix) same |= 1u << j;
-      }
+    for (int j = 0; j < kRows; ++j) v[j] = kRows == 4 ? held[j & 3] : i + 32 * j < c1 ? w[i + 32 * j] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < kRows; ++j) {
+      const uint32_t k = weight_key(v[j]);
+      const bool in = i + 32 * j < c1, late = i + 32 * j >= free_n;
+      sure[j] = __ballot_sync(0xFFFFFFFFu, in && (late || (by_weight && k > prefix)));
+      same[j] = __ballot_sync(0xFFFFFFFFu, in && !late && by_weight && k == prefix);
+      n_sure += __popc(sure[j]);
+      n_same += __popc(same[j]);
     }
     uint32_t total;
-    const uint32_t x = block_exclusive(__popc(sure) | (__popc(same) << 16), total, sm);
-    uint32_t na = base + (x & 0xFFFFu), ne = ties + (x >> 16);
+    const uint32_t x = block_exclusive(lane == 0 ? n_sure | (n_same << 16) : 0u, total, sm);
+    const uint32_t at = __shfl_sync(0xFFFFFFFFu, x, 0);
+    uint32_t na = base + (at & 0xFFFFu), ne = ties + (at >> 16);
+    const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const bool a = (sure >> j) & 1u, e = (same >> j) & 1u;
-      if (a || (e && ne < want)) {
-        const uint32_t at = na + min(ne, want);
-        kept[at] = i + j;
-        nw[at] = v[j];
+    for (int j = 0; j < kRows; ++j) {
+      const uint32_t e = ne + __popc(same[j] & below);
+      const bool a = (sure[j] >> lane) & 1u, tie = ((same[j] >> lane) & 1u) && e < want;
+      if (a || tie) {
+        const uint32_t to = na + __popc(sure[j] & below) + min(e, want);
+        kept[to] = i + 32 * j;
+        nw[to] = v[j];
       }
-      na += a;
-      ne += e;
+      na += __popc(sure[j]);
+      ne += __popc(same[j]);
     }
     base += total & 0xFFFFu;
     ties += total >> 16;
-  }
+  };
+  if (once)
+    compact(std::integral_constant<int, 4>{}, c0);
+  else
+    for (int i0 = c0; i0 < c1; i0 += 8 * kSelThreads) compact(std::integral_constant<int, 8>{}, i0);
 }
 
 // Checks one entry of the new table: inside the cache, not a page of the batch's own table and named once.
@@ -406,20 +430,29 @@ __device__ __forceinline__ void load_codes(const EvictParams& p, const void* cac
   }
 }
 
+// Largest magnitude among 16 codes, NaN (0x7F) left out.
+__device__ __forceinline__ uint32_t largest_code(const uint4& c) {
+  const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) m = __vimax3_u16x2(m, w[j] & 0x007F007Fu, (w[j] >> 8) & 0x007F007Fu);
+  m = max(m & 0xFFFFu, m >> 16);
+  if (m == 0x7Fu) {
+    m = 0;
+    for (int i = 0; i < 16; ++i) {
+      const uint32_t a = (w[i >> 2] >> (8 * (i & 3))) & 0x7Fu;
+      if (a != 0x7Fu) m = max(m, a);
+    }
+  }
+  return m;
+}
+
 // The thread's largest |value|: the exact product of code and scale as two floats, by their bits.
 __device__ __forceinline__ unsigned long long largest(const Codes& x) {
   unsigned long long top = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
-    uint32_t m = 0;  // largest |code|, NaN (0x7F) left out
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a = w[j] & 0x7F7F7F7Fu;
-      m = __vmaxu4(m, a & ~__vcmpeq4(a, 0x7F7F7F7Fu));
-    }
-    m = max(max(m & 0xFFu, (m >> 8) & 0xFFu), max((m >> 16) & 0xFFu, m >> 24));
-    const float v = e4m3_values(m).x;
+    const float v = e4m3_values(largest_code(x.c[i])).x;
     const float hi = __fmul_rz(v, x.sc[i]), lo = fmaf(v, x.sc[i], -hi);  // lo >= 0
     const unsigned long long key = (static_cast<unsigned long long>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
     top = key > top ? key : top;
@@ -427,26 +460,33 @@ __device__ __forceinline__ unsigned long long largest(const Codes& x) {
   return top;
 }
 
+// The new code of every magnitude, for each old page that the rows come from: rounding a code takes a dozen
+// instructions, looking it up in 128 bytes of shared memory (a word per bank) three.
+__device__ __forceinline__ void fill_table(uint8_t (*table)[128], const float* page_scale, int pages, float2 inv) {
+  for (int i = threadIdx.x; i < pages * 128; i += kGatherThreads) {
+    const float sc = page_scale[i >> 7];
+    const int code = i & 127;
+    float hi = sc * inv.x, lo = fmaf(sc, inv.y, fmaf(sc, inv.x, -hi));
+    if (!(hi < 1e30f)) hi = 1e30f, lo = 0.0f;  // a scale so far above the values that their codes are 0
+    const float y = mul_to_odd(e4m3_values(code).x, hi, lo);
+    table[i >> 7][code] = code == 127 ? 127 : __nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3);
+  }
+}
+
 __device__ __forceinline__ void store_codes(const EvictParams& p, void* cache, long long row0, int rows, int h,
-                                            float inv_hi, float inv_lo, const Codes& x) {
+                                            const uint8_t (*table)[128], const uint8_t* which, const Codes& x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = i * kGatherThreads + threadIdx.x, r = at >> 3;
     if (r >= rows) continue;
-    float hi = x.sc[i] * inv_hi, lo = fmaf(x.sc[i], inv_lo, fmaf(x.sc[i], inv_hi, -hi));
-    if (!(hi < 1e30f)) hi = 1e30f, lo = 0.0f;  // a scale so far above the values that their codes are 0
-    // A product just below and one just above the exact one round alike unless a midpoint lies between: only then,
-    // four codes at a time, the exact way.
-    const float under = hi * (1.0f - 0x1p-21f), over = hi * (1.0f + 0x1p-21f);
+    const uint8_t* tab = table[which[r]];
     const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
     uint32_t q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 a = e4m3_values(w[j] & 0x7F7Fu), b = e4m3_values((w[j] >> 16) & 0x7F7Fu);
-      q[j] = e4m3x4(a.x * under, a.y * under, b.x * under, b.y * under);
-      if (q[j] != e4m3x4(a.x * over, a.y * over, b.x * over, b.y * over))
-        q[j] = e4m3x4(mul_to_odd(a.x, hi, lo), mul_to_odd(a.y, hi, lo), mul_to_odd(b.x, hi, lo), mul_to_odd(b.y, hi, lo));
-      q[j] |= w[j] & 0x80808080u;
+      const uint32_t a = tab[w[j] & 0x7Fu], b = tab[(w[j] >> 8) & 0x7Fu], c = tab[(w[j] >> 16) & 0x7Fu],
+                     d = tab[(w[j] >> 24) & 0x7Fu];
+      q[j] = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410) | (w[j] & 0x80808080u);
     }
     static_cast<uint4*>(cache)[((row0 + r) * p.hkv + h) * 8 + (at & 7)] = make_uint4(q[0], q[1], q[2], q[3]);
   }
@@ -455,43 +495,68 @@ __device__ __forceinline__ void store_codes(const EvictParams& p, void* cache, l
 // CTA (new page, KV head).
 __global__ void __launch_bounds__(kGatherThreads, 4) evict_gather_fp8_kernel(EvictParams p) {
   __shared__ int src[kBlock];
+  __shared__ uint8_t which[kBlock];             // the row's old page, numbered in order
+  __shared__ int changes[kBlock / 32];
+  __shared__ float page_scale[2][kBlock];       // K and V scale of each old page
   __shared__ unsigned long long keys[2][kGatherThreads / 32];
-  __shared__ float2 inv[2];  // 448 / max as two floats
+  __shared__ float2 inv[2];                     // 448 / max as two floats
+  __shared__ uint8_t table[2][kBlock][128];
   griddep_wait();
   const NewPage x = new_page(p, blockIdx.x);
   if (x.rows <= 0) return;
-  const int h = blockIdx.y;
-  if (threadIdx.x < x.rows)
-    src[threadIdx.x] = source_row(p, x.s, x.n, (static_cast<long long>(x.s) * p.hkv + h) * p.budget + x.b * kBlock + threadIdx.x);
+  const int h = blockIdx.y, t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (t < kBlock)
+    src[t] = t < x.rows
+                 ? source_row(p, x.s, x.n, (static_cast<long long>(x.s) * p.hkv + h) * p.budget + x.b * kBlock + t)
+                 : -1;
   if (!page_fine(p, x)) return;
   __syncthreads();
   Codes k, v;
   load_codes(p, p.k, p.k_scale, x.rows, h, src, k);
   load_codes(p, p.v, p.v_scale, x.rows, h, src, v);
+  // number the old pages: kept slots ascend, so a page's rows are neighbours
+  const int old = t < kBlock && src[t] >= 0 ? src[t] / kBlock : -1;
+  const bool change = t > 0 && t < x.rows && old != (src[t - 1] >= 0 ? src[t - 1] / kBlock : -1);
+  const uint32_t mask = __ballot_sync(0xFFFFFFFFu, change);
+  if (warp < kBlock / 32 && lane == 0) changes[warp] = __popc(mask);
   const unsigned long long tk = warp_max_u64(largest(k)), tv = warp_max_u64(largest(v));
-  const int warp = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
+  if (lane == 0) {
     keys[0][warp] = tk;
     keys[1][warp] = tv;
   }
   __syncthreads();
-  if (threadIdx.x < 64 && (threadIdx.x & 31) == 0) {  // one thread each for K and V
+  int pages = 1;
+#pragma unroll
+  for (int i = 0; i < kBlock / 32; ++i) pages += changes[i];
+  if (t < x.rows) {
+    int number = __popc(mask & (0xFFFFFFFFu >> (31 - lane)));
+    for (int i = 0; i < warp; ++i) number += changes[i];
+    which[t] = static_cast<uint8_t>(number);
+    if (change || t == 0) {
+      page_scale[0][number] = old >= 0 ? p.k_scale[static_cast<long long>(old) * p.hkv + h] : 0.0f;
+      page_scale[1][number] = old >= 0 ? p.v_scale[static_cast<long long>(old) * p.hkv + h] : 0.0f;
+    }
+  } else if (t >= kGatherThreads - 64 && lane == 0) {  // the last two warps: a thread each for K and V
+    const int kv = warp & 1;
     unsigned long long top = 0;
 #pragma unroll
-    for (int i = 0; i < kGatherThreads / 32; ++i) top = keys[warp][i] > top ? keys[warp][i] : top;
+    for (int i = 0; i < kGatherThreads / 32; ++i) top = keys[kv][i] > top ? keys[kv][i] : top;
     const double value = static_cast<double>(__uint_as_float(static_cast<uint32_t>(top >> 32))) +
                          static_cast<double>(__uint_as_float(static_cast<uint32_t>(top)));
     const bool some = value >= 0x1p-118;  // below, 448 / value is no fp32 number: codes 0
-    (warp ? p.v_scale : p.k_scale)[static_cast<long long>(x.page) * p.hkv + h] =
+    (kv ? p.v_scale : p.k_scale)[static_cast<long long>(x.page) * p.hkv + h] =
         some ? static_cast<float>(value / 448.0) : 1.0f;
     const double q = some ? 448.0 / value : 0.0;
     const float hi = static_cast<float>(q);
-    inv[warp] = make_float2(hi, static_cast<float>(q - static_cast<double>(hi)));
+    inv[kv] = make_float2(hi, static_cast<float>(q - static_cast<double>(hi)));
   }
   __syncthreads();
+  fill_table(table[0], page_scale[0], pages, inv[0]);
+  fill_table(table[1], page_scale[1], pages, inv[1]);
+  __syncthreads();
   const long long row0 = static_cast<long long>(x.page) * kBlock;
-  store_codes(p, p.k, row0, x.rows, h, inv[0].x, inv[0].y, k);
-  store_codes(p, p.v, row0, x.rows, h, inv[1].x, inv[1].y, v);
+  store_codes(p, p.k, row0, x.rows, h, table[0], which, k);
+  store_codes(p, p.v, row0, x.rows, h, table[1], which, v);
 }
 
 }  // namespace
@@ -500,10 +565,13 @@ cudaError_t launch_evict(const EvictParams& p, bool fp8, int sms, cudaStream_t s
   // the header's status and the marks behind it start at zero
   cudaError_t e = cudaMemsetAsync(p.hdr, 0, p.clear_bytes, stream);
   if (e != cudaSuccess) return e;
-  // CTAs per (sequence, head): one while those fill the GPU or a share would fall under 4,096 slots (one load per
-  // thread, held in registers); up to eight for few long sequences
-  int cs = 1;
-  while (cs < 8 && 2ll * cs * p.num_seqs * p.hkv <= sms && p.max_k / (2 * cs) >= 4 * kSelThreads) cs *= 2;
+  // CTAs per (sequence, head): at most eight (a portable cluster), none with a share under 4,096 slots (one load per
+  // thread, held in registers), and only as many as run at once: a cluster's CTAs, one to an SM, share one of the
+  // GPU's eight or so SM groups, so larger clusters leave more SMs over (16 clusters of 8 took two turns, 49 us
+  // against 25 us for 4 clusters, at 65,536 slots).
+  const long long rows = static_cast<long long>(p.num_seqs) * p.hkv;
+  int cs = rows <= sms / 19 ? 8 : rows <= sms / 6 ? 4 : rows <= sms / 2 ? 2 : 1;
+  while (cs > 1 && p.max_k / cs < 4 * kSelThreads) cs /= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.hkv * cs);
   cfg.blockDim = dim3(kSelThreads);

@@ -118,7 +118,7 @@ class Cache:
 @pytest.mark.parametrize("lens,budget,recent", [
     ([1], 1, 0), ([1], 1, 1), ([2], 1, 0), ([2], 1, 1), ([5], 3, 1), ([129], 128, 5), ([129], 128, 128), ([300], 129, 0),
     ([128], 128, 7), ([1000], 999, 0), ([700, 0, 3, 512, 513], 512, 64), ([0, 0], 4, 2), ([4095, 4096, 4097, 9000], 2000, 100),
-    ([5000], 4999, 1), ([5000], 1, 0), ([300] * 90, 100, 10), ([20, 30], 1000, 1000)])
+    ([5000], 4999, 1), ([5000], 1, 0), ([300] * 90, 100, 10), ([20, 30], 1000, 1000), ([20000, 40], 130, 2)])
 def test_lengths_and_budgets(msa, lens, budget, recent, fp8):
     Cache(msa, lens, 2, budget, recent, fp8, seed=len(lens) + budget).check(msa)
 
