@@ -701,8 +701,9 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
   DeviceFacts dev;
   if ((st = device_facts(dev)) != MSA_OK) return st;
-  CUtensorMap tk, tv;
+  CUtensorMap tq{}, tk, tv;
   const long long rows = num_pages * 128;
+  if (dense_decode_tc(d.G, fp8) && !map_3d(tq, q, d.S, d.hkv * d.G, d.G, 1)) return MSA_ERR_CUDA;
   if (fp8 ? (!map_3d_u8(tk, k, rows, d.hkv, kDenseTile) || !map_3d_u8(tv, v, rows, d.hkv, kDenseTile))
           : (!map_3d(tk, k, rows, d.hkv, 1, kDenseTile) || !map_3d(tv, v, rows, d.hkv, 1, kDenseTile)))
     return MSA_ERR_CUDA;
@@ -738,7 +739,7 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   p.logits = weight ? at<float>(ws, L.logits) : nullptr;
   p.norm = weight ? at<float2>(ws, L.norm) : nullptr;
   StageScope scope(MSA_STAGE_ATTN, reinterpret_cast<cudaStream_t>(stream));
-  return cuda_status(launch_dense_decode(tk, tv, p, fp8, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_dense_decode(tq, tk, tv, p, fp8, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 msa_status_t check_evict(const msa_problem_t* problem, int32_t budget, int64_t num_pages, PagedDecode& d) {

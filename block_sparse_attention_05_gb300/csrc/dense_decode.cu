@@ -741,6 +741,459 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
   if (threadIdx.x == 0) p.flags[blockIdx.x] = *err;
 }
 
+// ---------------------------------------------------------------- split kernel, large groups
+// Groups of many heads on the 5th-generation tensor cores: the group's heads are
+// the 128 rows of the MMAs (rows past the group hold zero queries), a unit's 64
+// keys their columns.
+//   S = Q K^T    128 x 64 x 128, two buffers in TMEM
+//   P = 2^(S c - m)   one row per thread; written to TMEM as a bf16 value and the
+//                bf16 rest (16 significant bits), the A operand of
+//   O += P V     128 x 128 x 64, twice (value and rest), accumulated in TMEM
+// m is a row's reference, not its maximum: O and l are rescaled only when a unit's
+// maximum passes it by more than 2^8, so a step of the running sum rarely waits
+// for the MMA before it.  The MMAs take half the time of a unit's 32 KB from HBM,
+// the softmax warps (64 exponentials a row) a little more.
+//
+// Warps: 0 feeds K, V and Q (TMA), 1 issues the MMAs, 2 owns TMEM, 4..7 softmax
+// and output.  S of the next unit is issued before P V of this one, so the
+// tensor cores work while the softmax warps do.
+struct TcCfg {
+  static constexpr int kThreads = 256;
+  static constexpr int kStages = 5;
+  static constexpr int kHalf = kTile * 256;      // K or V of a stage
+  static constexpr int kQBytes = 128 * 256;
+  static constexpr uint32_t kColS = 0, kColO = 128, kColP = 256;  // S, P: two buffers of 64 columns
+};
+struct TcSmem {
+  uint64_t k_full[TcCfg::kStages], k_empty[TcCfg::kStages], v_full[TcCfg::kStages], v_empty[TcCfg::kStages];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t o_free, mma_done;
+  RunSmem run;
+  uint32_t tmem_base;
+  int abort_flag;
+  uint32_t err;
+};
+constexpr size_t kTcSmemBytes = 2 * TcCfg::kQBytes + TcCfg::kStages * 2 * TcCfg::kHalf + sizeof(TcSmem);
+static_assert(kTcSmemBytes <= 227 * 1024, "one CTA's shared memory");
+
+// Multiplies this thread's row of O (128 TMEM columns) by f.  Rare; out of line to leave the softmax its registers.
+__device__ __noinline__ void rescale_o(uint32_t addr, float f) {
+  for (int c = 0; c < 128; c += 8) {
+    uint32_t w[8];
+    tmem_ld_8cols(addr + c, w);
+    tmem_ld_wait_regs8(w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f);
+    tmem_st_8cols(addr + c, w);
+  }
+  tmem_st_wait();
+}
+
+template <bool LOGITS>
+__global__ void __launch_bounds__(TcCfg::kThreads, 1)
+    dense_split_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, DenseDecodeParams p) {
+  using C = TcCfg;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* q_buf = smem;
+  uint8_t* ring = smem + 2 * C::kQBytes;
+  TcSmem& sm = *reinterpret_cast<TcSmem*>(smem + 2 * C::kQBytes + C::kStages * 2 * C::kHalf);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv;
+  const int G = p.group;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kStages; ++i) {
+      mbar_init(&sm.k_full[i], 1);
+      mbar_init(&sm.k_empty[i], 1);
+      mbar_init(&sm.v_full[i], 1);
+      mbar_init(&sm.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.q_full[i], 1);
+      mbar_init(&sm.q_empty[i], 1);
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.p_full[i], 128);
+      mbar_init(&sm.pv_done[i], 1);
+    }
+    mbar_init(&sm.o_free, 128);
+    mbar_init(&sm.mma_done, 1);
+    sm.abort_flag = 0;
+    sm.err = 0;
+    fence_mbar_init();
+  }
+  // queries of the rows past the group: zero once, the loads write the group's rows only
+  for (int i = threadIdx.x; i < 2 * C::kQBytes / 16; i += C::kThreads)
+    reinterpret_cast<uint4*>(q_buf)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  Run run;
+  const bool fine = find_run(p.cu_k, p.num_seqs, p.max_k, p.total_k, g, p.groups, sm.run, run);  // synchronises
+  if (!fine) {
+    if (threadIdx.x == 0) {
+      p.flags[blockIdx.x] = kFlagBadSeqlens;
+      if (!p.by_seq) p.meta[blockIdx.x].x = -1;
+    }
+    if (p.by_seq && g < p.num_seqs && threadIdx.x == 0) p.meta[g * p.hkv + head].x = -1;  // num_seqs <= groups
+    return;
+  }
+  if (warp == 2) {
+    tmem_alloc(&sm.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem_base;
+  volatile int* abort_flag = &sm.abort_flag;
+  auto gave_up = [&] {
+    *abort_flag = 1;
+    atomicOr(&sm.err, kFlagTimeout);
+  };
+
+  // empty sequences: o = 0, lse = -inf
+  for (int s = g; s < p.num_seqs; s += p.groups) {
+    if (p.cu_k[s + 1] != p.cu_k[s]) continue;
+    if (p.by_seq && threadIdx.x == 0) p.meta[s * p.hkv + head].x = -1;
+    const long long row0 = (static_cast<long long>(s) * p.hkv + head) * G;
+    for (int i = threadIdx.x; i < G * 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(p.o + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < G; i += C::kThreads) p.lse[row0 + i] = -INFINITY;
+  }
+
+  Walker walk(p.cu_k, run);
+  Segment sg;
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    uint32_t fills = 0, segs = 0, bad = 0;
+    uint32_t k_issued = 0, v_issued = 0, q_issued = 0;  // lane 0's
+    const uint64_t policy = l2_evict_first();
+    bool stopped = false;
+    while (!stopped && walk.next(sg)) {
+      if (lane == 0) {
+        const int qb = segs & 1;
+        if (segs >= 2 && !mbar_wait(&sm.q_empty[qb], ((segs >> 1) - 1) & 1, abort_flag)) {
+          gave_up();
+        } else {
+          uint8_t* dst = q_buf + qb * C::kQBytes;
+          mbar_arrive_expect_tx(&sm.q_full[qb], G * 256);
+          tma_load_3d(dst, &tm_q, &sm.q_full[qb], 0, head * G, sg.seq);
+          tma_load_3d(dst + 128 * 128, &tm_q, &sm.q_full[qb], 64, head * G, sg.seq);
+          ++q_issued;
+        }
+      }
+      ++segs;
+      const int last_page = (sg.off + sg.count - 1) * kTile / kBlock;
+      const int32_t* table = p.block_table + static_cast<long long>(sg.seq) * p.bt_stride;
+      int base = sg.off * kTile / kBlock, row = 0;
+      for (int u = sg.off; u < sg.off + sg.count; ++u) {
+        const int page = u * kTile / kBlock;
+        if (u == sg.off || page - base >= 32) {  // the next 32 pages' rows, one per lane
+          if (u != sg.off) base += 32;
+          row = 0;
+          if (base + lane <= last_page) {
+            const int e = table[base + lane];
+            if (e < 0 || e >= p.n_pages) {
+              bad = 1;
+              row = static_cast<int>(p.n_pages) * kBlock;  // past the cache: TMA reads zeros
+            } else {
+              row = e * kBlock;
+            }
+          }
+        }
+        const int r = __shfl_sync(0xFFFFFFFFu, row, page - base) + (u * kTile) % kBlock;
+        if (lane == 0) {
+          const int st = fills % C::kStages;
+          const uint32_t n = fills / C::kStages;
+          uint8_t* dk = ring + st * 2 * C::kHalf;
+          uint8_t* dv = dk + C::kHalf;
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int dim) {
+            if (LOGITS) tma_load_3d_policy(dst, map, bar, dim, head, r, policy);
+            else tma_load_3d(dst, map, bar, dim, head, r);
+          };
+          if (n > 0 && !mbar_wait(&sm.k_empty[st], (n - 1) & 1, abort_flag)) {
+            gave_up();
+          } else {
+            mbar_arrive_expect_tx(&sm.k_full[st], C::kHalf);
+            load(dk, &tm_k, &sm.k_full[st], 0);
+            load(dk + kTile * 128, &tm_k, &sm.k_full[st], 64);
+            ++k_issued;
+            if (n > 0 && !mbar_wait(&sm.v_empty[st], (n - 1) & 1, abort_flag)) {
+              gave_up();
+            } else {
+              mbar_arrive_expect_tx(&sm.v_full[st], C::kHalf);
+              load(dv, &tm_v, &sm.v_full[st], 0);
+              load(dv + kTile * 128, &tm_v, &sm.v_full[st], 64);
+              ++v_issued;
+            }
+          }
+        }
+        __syncwarp();
+        stopped = __any_sync(0xFFFFFFFFu, *abort_flag) != 0;
+        if (stopped) break;
+        ++fills;
+      }
+    }
+    if (bad) atomicOr(&sm.err, kFlagBadIndex);
+    if (lane == 0) {  // no copy may land after this CTA has left (all have, but after a wait that gave up)
+      auto drain = [&](uint64_t* full, uint32_t issued, uint32_t stages) {
+        for (uint32_t f = issued > stages ? issued - stages : 0; f < issued; ++f)
+          mbar_wait(&full[f % stages], (f / stages) & 1, nullptr);
+      };
+      drain(sm.k_full, k_issued, C::kStages);
+      drain(sm.v_full, v_issued, C::kStages);
+      drain(sm.q_full, q_issued, 2);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc_s = idesc_bf16(128, kTile, false), idesc_o = idesc_bf16(128, kHeadDim, true);
+      uint32_t f = 0, segs = 0;
+      bool ok = true;
+      bool prev_first = false;
+      uint32_t prev_seg = 0;
+      // O (+)= P V of unit x; `first` of its segment: a new accumulation, once the segment before has been read out
+      auto issue_pv = [&](uint32_t x, bool first, uint32_t seg) {
+        const int st = x % C::kStages, b = x & 1;
+        if (!mbar_wait(&sm.p_full[b], (x >> 1) & 1, abort_flag) ||
+            !mbar_wait(&sm.v_full[st], (x / C::kStages) & 1, abort_flag) ||
+            (first && seg > 0 && !mbar_wait(&sm.o_free, (seg - 1) & 1, abort_flag)))
+          return false;
+        tc_fence_after();
+        const uint32_t va = smem_u32(ring + st * 2 * C::kHalf + C::kHalf);
+        const uint32_t pc = tmem + C::kColP + b * 64, oc = tmem + C::kColO;
+#pragma unroll
+        for (int part = 0; part < 2; ++part)  // the value, then the rest
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            umma_bf16_ts(oc, pc + part * 32 + kk * 8, sdesc_sw128(va + kk * 2048, kTile * 128, 1024), idesc_o,
+                         (first && part == 0 && kk == 0) ? 0u : 1u);
+        umma_commit(&sm.v_empty[st]);
+        umma_commit(&sm.pv_done[b]);
+        return true;
+      };
+      while (ok && walk.next(sg)) {
+        const int qb = segs & 1;
+        if (!mbar_wait(&sm.q_full[qb], (segs >> 1) & 1, abort_flag)) {
+          gave_up();
+          ok = false;
+          break;
+        }
+        for (int i = 0; i < sg.count; ++i, ++f) {
+          const int st = f % C::kStages;
+          if (!mbar_wait(&sm.k_full[st], (f / C::kStages) & 1, abort_flag)) {
+            gave_up();
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // S buffer f & 1 is free: the softmax warps had read it when they wrote P of unit f - 2, which P V waited for
+          const uint32_t qa = smem_u32(q_buf + qb * C::kQBytes), ka = smem_u32(ring + st * 2 * C::kHalf);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            umma_bf16(tmem + C::kColS + (f & 1) * 64, sdesc_sw128(qa + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
+                      sdesc_sw128(ka + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk ? 1u : 0u);
+          umma_commit(&sm.s_full[f & 1]);
+          umma_commit(&sm.k_empty[st]);
+          if (i == sg.count - 1) umma_commit(&sm.q_empty[qb]);
+          if (f > 0 && !issue_pv(f - 1, prev_first, prev_seg)) {
+            gave_up();
+            ok = false;
+            break;
+          }
+          prev_first = i == 0;
+          prev_seg = segs;
+        }
+        ++segs;
+      }
+      if (ok && f > 0 && !issue_pv(f - 1, prev_first, prev_seg)) gave_up();
+      umma_commit(&sm.mma_done);
+      mbar_wait(&sm.mma_done, 0, nullptr);
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------ softmax and output
+    const int r = (warp & 3) * 32 + lane;  // TMEM lane = head of the group
+    const bool busy = (warp & 3) * 32 < G;  // a warp whose rows are all past the group only keeps the barriers going
+    const uint32_t la = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const float c = p.scale_log2;
+    uint32_t f = 0;
+    bool ok = true;
+    int4 crossing = make_int4(-1, 0, 0, 0);  // the sequence that begins in this run and goes on
+    while (ok && walk.next(sg)) {
+      float m = 0.0f;
+      float2 l2 = make_float2(0.0f, 0.0f);
+      for (int i = 0; i < sg.count; ++i, ++f) {
+        const int b = f & 1;
+        if (!mbar_wait_warp(&sm.s_full[b], (f >> 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        // P buffer b is free once P V of unit f - 2 has read it
+        if (f >= 2 && !mbar_wait_warp(&sm.pv_done[b], ((f >> 1) - 1) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int valid = sg.len - (sg.off + i) * kTile;
+        if (valid < kTile) {
+          // uniform: the sequence's last unit.  Its V rows past the end hold anything, and 0 * NaN is NaN: zero them.
+          const int st = f % C::kStages;
+          if (!mbar_wait_warp(&sm.v_full[st], (f / C::kStages) & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          uint8_t* v = ring + st * 2 * C::kHalf + C::kHalf;
+          for (int j = valid * 8 + r; j < kTile * 8; j += 128) {  // 16-byte pieces of the rows' two halves
+            reinterpret_cast<uint4*>(v)[j] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(v + kTile * 128)[j] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        if (busy) {
+          uint32_t va[32], vb[32];
+          float xa, xb;
+          tmem_ld_max_32cols(la + C::kColS + b * 64, va, xa);
+          tmem_ld_max_32cols(la + C::kColS + b * 64 + 32, vb, xb);
+          tmem_ld_wait_regs_max(va, xa);
+          tmem_regs_written(vb, xb);
+          if (valid < kTile) {
+            xa = xb = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (j >= valid) va[j] = 0xFF800000u;
+              if (j + 32 >= valid) vb[j] = 0xFF800000u;
+              xa = fmaxf(xa, __uint_as_float(va[j]));
+              xb = fmaxf(xb, __uint_as_float(vb[j]));
+            }
+          }
+          const float x = fmaxf(xa, xb) * c;
+          if (LOGITS && r < G) {
+            float* w = p.logits + (((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) + r) * kTile;
+            auto put = [&](const uint32_t (&v)[32], float* at) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint4 lo, hi;
+                lo.x = __float_as_uint(__uint_as_float(v[j]) * c); lo.y = __float_as_uint(__uint_as_float(v[j + 1]) * c);
+                lo.z = __float_as_uint(__uint_as_float(v[j + 2]) * c); lo.w = __float_as_uint(__uint_as_float(v[j + 3]) * c);
+                hi.x = __float_as_uint(__uint_as_float(v[j + 4]) * c); hi.y = __float_as_uint(__uint_as_float(v[j + 5]) * c);
+                hi.z = __float_as_uint(__uint_as_float(v[j + 6]) * c); hi.w = __float_as_uint(__uint_as_float(v[j + 7]) * c);
+                st_global_32b(at + j, lo, hi);
+              }
+            };
+            put(va, w);
+            put(vb, w + 32);
+          }
+          if (i == 0) {
+            m = x == -INFINITY ? 0.0f : x;
+          } else {
+            const bool need = x - m > 8.0f;
+            if (__any_sync(0xFFFFFFFFu, need)) {
+              // every P V so far must be in O before it is scaled
+              if (!mbar_wait_warp(&sm.pv_done[b ^ 1], ((f - 1) >> 1) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const float up = need ? ceilf(x - m) : 0.0f;
+              const float k = exp2_approx(-up);
+              rescale_o(la + C::kColO, k);
+              l2.x *= k;
+              l2.y *= k;
+              m += up;
+            }
+          }
+          const float2 c2 = make_float2(c, c), nm = make_float2(-m, -m);
+          auto weights = [&](const uint32_t (&v)[32], uint32_t col) {
+#pragma unroll
+            for (int h = 0; h < 32; h += 16) {
+              uint32_t hi[8], lo[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float2 z = ffma2(make_float2(__uint_as_float(v[h + 2 * j]), __uint_as_float(v[h + 2 * j + 1])), c2, nm);
+                const float2 w = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                l2 = fadd2(l2, w);
+                split_bf16(w.x, w.y, hi[j], lo[j]);
+              }
+              tmem_st_8cols(col + h / 2, hi);
+              tmem_st_8cols(col + 32 + h / 2, lo);
+            }
+          };
+          weights(va, la + C::kColP + b * 64);
+          weights(vb, la + C::kColP + b * 64 + 16);
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        mbar_arrive(&sm.p_full[b]);
+      }
+      if (!ok) break;
+
+      // ---- the segment's output
+      const uint32_t last = f - 1;
+      if (!mbar_wait_warp(&sm.pv_done[last & 1], (last >> 1) & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const bool whole = sg.first && sg.last;
+      const float l = l2.x + l2.y;
+      const long long out_row = (static_cast<long long>(sg.seq) * p.hkv + head) * G + r;
+      const long long part_row = (static_cast<long long>(blockIdx.x) * 2 + (sg.first ? 1 : 0)) * G + r;
+      if (busy) {
+        const float inv = inverse(l);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_ld_32cols(la + C::kColO + q * 32, v);
+          tmem_ld_wait_regs(v);
+          if (r >= G) continue;
+          if (whole) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                w[k] = pack_bf16(__uint_as_float(v[j + 2 * k]) * inv, __uint_as_float(v[j + 2 * k + 1]) * inv);
+              uint4* to = reinterpret_cast<uint4*>(p.o + out_row * kHeadDim + q * 32 + j);  // o is 16-byte aligned
+              to[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              to[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8)
+              st_global_32b(p.part_o + part_row * kHeadDim + q * 32 + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]),
+                            make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]));
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.o_free);
+      if (r < G) {
+        if (whole) {
+          p.lse[out_row] = (m + log2f(l)) * kLn2;
+          if (LOGITS) p.norm[out_row] = row_norm(m, l);
+        } else {
+          p.part_ml[part_row] = make_float2(m, l);
+        }
+      }
+      if (sg.first && !sg.last) {
+        const long long end = sg.unit + units_of(sg.len) - 1;
+        crossing = make_int4(sg.seq, g, static_cast<int>(((end + 1) * run.runs - 1) / run.total), 0);
+      }
+      if (p.by_seq && sg.first && r == 0) p.meta[sg.seq * p.hkv + head] = sg.last ? make_int4(-1, 0, 0, 0) : crossing;
+    }
+    if (!ok && lane == 0) gave_up();
+    if (!p.by_seq && r == 0) p.meta[blockIdx.x] = crossing;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (threadIdx.x == 0) p.flags[blockIdx.x] = sm.err;
+}
+
 // ---------------------------------------------------------------- join
 // Merges the partials of a sequence that crosses runs.  CTA (entry of meta, KV
 // head; 8 / wpr head rows), wpr warps to a row, eight partials in flight each:
@@ -888,6 +1341,16 @@ __global__ void __launch_bounds__(kWeightThreads, 2) dense_weight_kernel(DenseDe
   }
 }
 
+cudaError_t launch_split_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                            const DenseDecodeParams& p, cudaStream_t stream) {
+  auto* fn = p.logits ? dense_split_tc_kernel<true> : dense_split_tc_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTcSmemBytes));
+  if (e != cudaSuccess) return e;
+  fn<<<p.groups * p.hkv, TcCfg::kThreads, kTcSmemBytes, stream>>>(tq, tk, tv, p);
+  note_launches(1);
+  return cudaGetLastError();
+}
+
 template <int MG, bool FP8>
 cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p,
                          cudaStream_t stream) {
@@ -913,9 +1376,13 @@ cudaError_t launch_split_for(const CUtensorMap& tk, const CUtensorMap& tv, const
 
 int dense_decode_ctas_per_sm(int group) { return group <= 16 ? 2 : 1; }
 
-cudaError_t launch_dense_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p, bool fp8,
-                                cudaStream_t stream) {
-  cudaError_t e = fp8 ? launch_split_for<true>(tk, tv, p, stream) : launch_split_for<false>(tk, tv, p, stream);
+bool dense_decode_tc(int group, bool fp8) { return !fp8 && group > 32; }
+
+cudaError_t launch_dense_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const DenseDecodeParams& p, bool fp8, cudaStream_t stream) {
+  cudaError_t e = dense_decode_tc(p.group, fp8) ? launch_split_tc(tq, tk, tv, p, stream)
+                  : fp8                         ? launch_split_for<true>(tk, tv, p, stream)
+                                                : launch_split_for<false>(tk, tv, p, stream);
   if (e != cudaSuccess) return e;
   const int entries = p.by_seq ? p.num_seqs : p.groups;
   int wpr = 1;  // warps to a row: one for every four partials that a sequence has on average, up to eight

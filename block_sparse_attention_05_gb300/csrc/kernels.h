@@ -306,8 +306,9 @@ struct DenseDecodeParams {
   float2* norm;                 // with weight: [num_seqs, hkv * group] (maximum, 1 / sum); else null
 };
 int dense_decode_ctas_per_sm(int group);
-cudaError_t launch_dense_decode(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p, bool fp8,
-                                cudaStream_t stream);
+bool dense_decode_tc(int group, bool fp8);  // whether the split runs on tcgen05 and reads Q through tq
+cudaError_t launch_dense_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const DenseDecodeParams& p, bool fp8, cudaStream_t stream);
 
 // ---------------------------------------------------------------- eviction
 struct EvictParams {
