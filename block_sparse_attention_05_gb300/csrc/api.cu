@@ -645,7 +645,7 @@ struct DenseLayout {
 
 // The split never has more than dense_max_runs runs, so the size needs no device.
 int dense_max_runs(const PagedDecode& d) { return d.hkv >= kDenseMaxCtas ? 1 : kDenseMaxCtas / d.hkv; }
-long long dense_max_units(const PagedDecode& d) { return static_cast<long long>(d.N) / kDenseTile + d.S; }
+long long dense_max_units(const PagedDecode& d, int keys) { return static_cast<long long>(d.N) / keys + d.S; }
 
 DenseLayout dense_layout(const PagedDecode& d, bool weight) {
   DenseLayout L{};
@@ -662,7 +662,8 @@ DenseLayout dense_layout(const PagedDecode& d, bool weight) {
   L.meta = take(static_cast<size_t>(d.S < dense_max_runs(d) ? d.S : dense_max_runs(d)) * d.hkv * sizeof(int4));
   L.flags = take(ctas * sizeof(uint32_t));
   if (weight) {
-    L.logits = take(static_cast<size_t>(dense_max_units(d)) * d.hkv * d.G * kDenseTile * sizeof(float));
+    // units of 128 keys, or of 64 (fewer keys in all)
+    L.logits = take(static_cast<size_t>(dense_max_units(d, 128)) * 128 * d.hkv * d.G * sizeof(float));
     L.norm = take(static_cast<size_t>(d.S) * d.hkv * d.G * sizeof(float2));
   }
   L.total = off;
@@ -701,11 +702,13 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
   DeviceFacts dev;
   if ((st = device_facts(dev)) != MSA_OK) return st;
+  const bool tc = dense_decode_tc(d.G, fp8);
+  const int unit = tc ? 128 : kDenseTile;
   CUtensorMap tq{}, tk, tv;
   const long long rows = num_pages * 128;
-  if (dense_decode_tc(d.G, fp8) && !map_3d(tq, q, d.S, d.hkv * d.G, d.G, 1)) return MSA_ERR_CUDA;
+  if (tc && !map_3d(tq, q, d.S, d.hkv * d.G, d.G, 1)) return MSA_ERR_CUDA;
   if (fp8 ? (!map_3d_u8(tk, k, rows, d.hkv, kDenseTile) || !map_3d_u8(tv, v, rows, d.hkv, kDenseTile))
-          : (!map_3d(tk, k, rows, d.hkv, 1, kDenseTile) || !map_3d(tv, v, rows, d.hkv, 1, kDenseTile)))
+          : (!map_3d(tk, k, rows, d.hkv, 1, unit) || !map_3d(tv, v, rows, d.hkv, 1, unit)))
     return MSA_ERR_CUDA;
   DenseDecodeParams p{};
   p.num_seqs = d.S;
@@ -715,9 +718,10 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   p.total_k = d.N;
   long long runs = static_cast<long long>(dense_decode_ctas_per_sm(d.G)) * dev.sms / d.hkv;
   if (runs > dense_max_runs(d)) runs = dense_max_runs(d);
-  if (runs > dense_max_units(d)) runs = dense_max_units(d);
+  if (runs > dense_max_units(d, unit)) runs = dense_max_units(d, unit);
   if (runs < 1) runs = 1;
   p.groups = static_cast<int>(runs);
+  p.unit_shift = tc ? 7 : 6;
   p.cu_k = problem->cu_seqlens_k;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.block_table = block_table;

@@ -28,7 +28,7 @@ namespace msa {
 
 namespace {
 
-constexpr int kTile = kDenseTile;  // keys of a unit and of a ring stage
+constexpr int kTile = kDenseTile;  // keys of a unit and of a ring stage (small groups)
 constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -108,12 +108,14 @@ struct RunSmem {
   int seq, off;
 };
 
-__device__ __forceinline__ int units_of(int len) { return (len + kTile - 1) / kTile; }
+// Units of `1 << shift` keys in a sequence.
+__device__ __forceinline__ int units_of(int len, int shift) { return (len + (1 << shift) - 1) >> shift; }
 
 // Cuts the batch's units and finds run g of `groups`.  Every thread of the CTA
 // calls it; returns false (for every thread) when cu_seqlens contradict the host sizes.
-__device__ bool find_run(const int32_t* cu, int num_seqs, int max_k, int total_k, int g, int groups, RunSmem& sm,
-                         Run& r) {
+__device__ bool find_run(const DenseDecodeParams& p, int g, RunSmem& sm, Run& r) {
+  const int32_t* cu = p.cu_k;
+  const int num_seqs = p.num_seqs, max_k = p.max_k, total_k = p.total_k, groups = p.groups, shift = p.unit_shift;
   const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = T >> 5;
   const int per = (num_seqs + T - 1) / T;
   const int s0 = min(num_seqs, t * per), s1 = min(num_seqs, s0 + per);
@@ -123,7 +125,7 @@ __device__ bool find_run(const int32_t* cu, int num_seqs, int max_k, int total_k
   for (int s = s0; s < s1; ++s) {
     const int next = cu[s + 1], len = next - prev;
     bad |= prev < 0 || next < prev || len > max_k;
-    sum += units_of(len);
+    sum += units_of(len, shift);
     prev = next;
   }
   if (__syncthreads_or(bad)) return false;
@@ -149,7 +151,7 @@ __device__ bool find_run(const int32_t* cu, int num_seqs, int max_k, int total_k
   if (r.lo < r.hi && base <= r.lo && r.lo < base + sum) {  // one thread
     int u = base, s = s0;
     for (;; ++s) {
-      const int n = units_of(cu[s + 1] - cu[s]);
+      const int n = units_of(cu[s + 1] - cu[s], shift);
       if (u + n > r.lo) break;
       u += n;
     }
@@ -171,14 +173,15 @@ struct Segment {
 struct Walker {
   const int32_t* cu;
   long long at, hi;
-  int seq, off;
-  __device__ Walker(const int32_t* cu_, const Run& r) : cu(cu_), at(r.lo), hi(r.hi), seq(r.seq), off(r.off) {}
+  int seq, off, shift;
+  __device__ Walker(const DenseDecodeParams& p, const Run& r)
+      : cu(p.cu_k), at(r.lo), hi(r.hi), seq(r.seq), off(r.off), shift(p.unit_shift) {}
   __device__ bool next(Segment& g) {
     if (at >= hi) return false;
     int len, n;
     for (;;) {
       len = cu[seq + 1] - cu[seq];
-      n = units_of(len);
+      n = units_of(len, shift);
       if (off < n) break;
       ++seq;  // an empty sequence
       off = 0;
@@ -262,7 +265,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     fence_mbar_init();
   }
   Run run;
-  const bool fine = find_run(p.cu_k, p.num_seqs, p.max_k, p.total_k, g, p.groups, run_sm, run);  // synchronises
+  const bool fine = find_run(p, g, run_sm, run);  // synchronises
   if (!fine) {
     if (threadIdx.x == 0) {
       p.flags[blockIdx.x] = kFlagBadSeqlens;
@@ -282,7 +285,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     for (int i = threadIdx.x; i < G; i += C::kThreads) p.lse[row0 + i] = -INFINITY;
   }
 
-  Walker walk(p.cu_k, run);
+  Walker walk(p, run);
   Segment sg;
   uint32_t issued = 0;  // the feeding lane's fills
   if (warp == C::kWarps) {
@@ -726,7 +729,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
       }
       if (sg.first && !sg.last) {
         // the run that holds the sequence's last unit: lo(x) = floor(total x / runs) <= u < lo(x + 1)
-        const long long end = sg.unit + units_of(sg.len) - 1;
+        const long long end = sg.unit + units_of(sg.len, p.unit_shift) - 1;
         crossing = make_int4(sg.seq, g, static_cast<int>(((end + 1) * run.runs - 1) / run.total), 0);
       }
       if (p.by_seq && sg.first && warp == 0 && lane == 0)
@@ -743,38 +746,48 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
 
 // ---------------------------------------------------------------- split kernel, large groups
 // Groups of many heads on the 5th-generation tensor cores: the group's heads are
-// the 128 rows of the MMAs (rows past the group hold zero queries), a unit's 64
-// keys their columns.
-//   S = Q K^T    128 x 64 x 128, two buffers in TMEM
-//   P = 2^(S c - m)   one row per thread; written to TMEM as a bf16 value and the
-//                bf16 rest (16 significant bits), the A operand of
-//   O += P V     128 x 128 x 64, twice (value and rest), accumulated in TMEM
+// the 128 rows of the MMAs (rows past the group hold zero queries), a unit's 128
+// keys (a page) their columns.
+//   S = Q K^T    128 x 128 x 128
+//   P = 2^(S c - m)   one row per thread; written over S in TMEM as a bf16 value
+//                and the bf16 rest (16 significant bits), the A operand of
+//   O += P V     128 x 128 x 128, twice (value and rest), accumulated in TMEM
 // m is a row's reference, not its maximum: O and l are rescaled only when a unit's
-// maximum passes it by more than 2^8, so a step of the running sum rarely waits
-// for the MMA before it.  The MMAs take half the time of a unit's 32 KB from HBM,
-// the softmax warps (64 exponentials a row) a little more.
+// maximum passes it by more than 2^8.
 //
-// Warps: 0 feeds K, V and Q (TMA), 1 issues the MMAs, 2 owns TMEM, 4..7 softmax
-// and output.  S of the next unit is issued before P V of this one, so the
-// tensor cores work while the softmax warps do.
+// Per unit (64 KB of K and V, 1.4 us of an SM's share of HBM) the MMAs take 0.8 us
+// and a warpgroup's softmax 1.1 us, so two warpgroups take the units in turn,
+// each with its own S and O in TMEM (2 x (128 + 128) columns), m and l, merged at
+// the end of a segment: one computes P while the other's MMAs run.
+// Units of 64 keys ran at half this rate: an MMA with 64 columns takes as long as
+// one with 128, and issuing it and the commits (about 250 clocks each) held up the
+// one thread that does; here a unit has two commits, S done (K's stage is free,
+// its warpgroup may go on) and P V done (V's stage and S's columns are free).
+//
+// Warps: 0 feeds K and 3 feeds V (TMA), 1 issues the MMAs, 2 owns TMEM and feeds
+// Q, 4..7 and 8..11 softmax and output.
 struct TcCfg {
-  static constexpr int kThreads = 256;
-  static constexpr int kStages = 5;
-  static constexpr int kHalf = kTile * 256;      // K or V of a stage
-  static constexpr int kQBytes = 128 * 256;
-  static constexpr uint32_t kColS = 0, kColO = 128, kColP = 256;  // S, P: two buffers of 64 columns
+  static constexpr int kThreads = 384;
+  static constexpr int kKeys = 128;
+  static constexpr int kStages = 3;
+  static constexpr int kHalf = kKeys * 256;  // K or V of a stage
+  static constexpr uint32_t kColS = 0, kColO = 256;
 };
 struct TcSmem {
-  uint64_t k_full[TcCfg::kStages], k_empty[TcCfg::kStages], v_full[TcCfg::kStages], v_empty[TcCfg::kStages];
-  uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done[2];
-  uint64_t o_free, mma_done;
+  uint64_t k_full[TcCfg::kStages], v_full[TcCfg::kStages];
+  // S done by unit % 6: a stage's and a warpgroup's units each keep to barriers of their own, so every waiter sees
+  // every phase of the barriers it uses (one that skipped a phase could take an older one for its own)
+  uint64_t s_done[6];
+  uint64_t pv_done[TcCfg::kStages];
+  uint64_t p_full[2];
+  uint64_t q_full, q_empty, ml_full, o_free, mma_done;
+  float2 ml[2][128];  // (m, l) of each warpgroup's rows; m = -inf: no unit of the segment was its own
   RunSmem run;
   uint32_t tmem_base;
   int abort_flag;
   uint32_t err;
 };
-constexpr size_t kTcSmemBytes = 2 * TcCfg::kQBytes + TcCfg::kStages * 2 * TcCfg::kHalf + sizeof(TcSmem);
+constexpr size_t kTcSmemBytes = (TcCfg::kStages * 2 + 1) * TcCfg::kHalf + sizeof(TcSmem);
 static_assert(kTcSmemBytes <= 227 * 1024, "one CTA's shared memory");
 
 // Multiplies this thread's row of O (128 TMEM columns) by f.  Rare; out of line to leave the softmax its registers.
@@ -796,9 +809,9 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
                           const __grid_constant__ CUtensorMap tm_v, DenseDecodeParams p) {
   using C = TcCfg;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* q_buf = smem;
-  uint8_t* ring = smem + 2 * C::kQBytes;
-  TcSmem& sm = *reinterpret_cast<TcSmem*>(smem + 2 * C::kQBytes + C::kStages * 2 * C::kHalf);
+  uint8_t* ring = smem;                                     // stages of K and V: two 64-dim halves of 128 rows each
+  uint8_t* q_buf = smem + C::kStages * 2 * C::kHalf;        // the same layout
+  TcSmem& sm = *reinterpret_cast<TcSmem*>(q_buf + C::kHalf);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv;
   const int G = p.group;
@@ -806,29 +819,26 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sm.k_full[i], 1);
-      mbar_init(&sm.k_empty[i], 1);
       mbar_init(&sm.v_full[i], 1);
-      mbar_init(&sm.v_empty[i], 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sm.q_full[i], 1);
-      mbar_init(&sm.q_empty[i], 1);
-      mbar_init(&sm.s_full[i], 1);
-      mbar_init(&sm.p_full[i], 128);
       mbar_init(&sm.pv_done[i], 1);
     }
-    mbar_init(&sm.o_free, 128);
+    for (int i = 0; i < 6; ++i) mbar_init(&sm.s_done[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sm.p_full[i], 4);
+    mbar_init(&sm.q_full, 1);
+    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.ml_full, 8);
+    mbar_init(&sm.o_free, 8);
     mbar_init(&sm.mma_done, 1);
     sm.abort_flag = 0;
     sm.err = 0;
     fence_mbar_init();
   }
   // queries of the rows past the group: zero once, the loads write the group's rows only
-  for (int i = threadIdx.x; i < 2 * C::kQBytes / 16; i += C::kThreads)
-    reinterpret_cast<uint4*>(q_buf)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = threadIdx.x; i < (128 - G) * 16; i += C::kThreads)
+    reinterpret_cast<uint4*>(q_buf + (i & 8) * 2048)[G * 8 + (i >> 4) * 8 + (i & 7)] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   Run run;
-  const bool fine = find_run(p.cu_k, p.num_seqs, p.max_k, p.total_k, g, p.groups, sm.run, run);  // synchronises
+  const bool fine = find_run(p, g, sm.run, run);  // synchronises
   if (!fine) {
     if (threadIdx.x == 0) {
       p.flags[blockIdx.x] = kFlagBadSeqlens;
@@ -861,38 +871,24 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
     for (int i = threadIdx.x; i < G; i += C::kThreads) p.lse[row0 + i] = -INFINITY;
   }
 
-  Walker walk(p.cu_k, run);
+  Walker walk(p, run);
   Segment sg;
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    uint32_t fills = 0, segs = 0, bad = 0;
-    uint32_t k_issued = 0, v_issued = 0, q_issued = 0;  // lane 0's
-    const uint64_t policy = l2_evict_first();
+  if (warp == 0 || warp == 3) {
+    // ------------------------------------------------------------ producers: K, V
+    const CUtensorMap* map = warp == 0 ? &tm_k : &tm_v;
+    uint64_t* full = warp == 0 ? sm.k_full : sm.v_full;
+    uint8_t* const dst0 = ring + (warp == 0 ? 0 : C::kHalf);
+    uint32_t fills = 0, issued = 0, bad = 0;
+    const uint64_t policy = l2_evict_first();  // with logits: K and V pass through, the logits are to stay in L2
     bool stopped = false;
     while (!stopped && walk.next(sg)) {
-      if (lane == 0) {
-        const int qb = segs & 1;
-        if (segs >= 2 && !mbar_wait(&sm.q_empty[qb], ((segs >> 1) - 1) & 1, abort_flag)) {
-          gave_up();
-        } else {
-          uint8_t* dst = q_buf + qb * C::kQBytes;
-          mbar_arrive_expect_tx(&sm.q_full[qb], G * 256);
-          tma_load_3d(dst, &tm_q, &sm.q_full[qb], 0, head * G, sg.seq);
-          tma_load_3d(dst + 128 * 128, &tm_q, &sm.q_full[qb], 64, head * G, sg.seq);
-          ++q_issued;
-        }
-      }
-      ++segs;
-      const int last_page = (sg.off + sg.count - 1) * kTile / kBlock;
-      const int32_t* table = p.block_table + static_cast<long long>(sg.seq) * p.bt_stride;
-      int base = sg.off * kTile / kBlock, row = 0;
-      for (int u = sg.off; u < sg.off + sg.count; ++u) {
-        const int page = u * kTile / kBlock;
-        if (u == sg.off || page - base >= 32) {  // the next 32 pages' rows, one per lane
-          if (u != sg.off) base += 32;
+      const int32_t* table = p.block_table + static_cast<long long>(sg.seq) * p.bt_stride + sg.off;
+      int row = 0;
+      for (int i = 0; i < sg.count; ++i) {
+        if ((i & 31) == 0) {  // the next 32 pages' rows, one per lane
           row = 0;
-          if (base + lane <= last_page) {
-            const int e = table[base + lane];
+          if (i + lane < sg.count) {
+            const int e = table[i + lane];
             if (e < 0 || e >= p.n_pages) {
               bad = 1;
               row = static_cast<int>(p.n_pages) * kBlock;  // past the cache: TMA reads zeros
@@ -901,31 +897,26 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
             }
           }
         }
-        const int r = __shfl_sync(0xFFFFFFFFu, row, page - base) + (u * kTile) % kBlock;
+        const int r = __shfl_sync(0xFFFFFFFFu, row, i & 31);
         if (lane == 0) {
           const int st = fills % C::kStages;
-          const uint32_t n = fills / C::kStages;
-          uint8_t* dk = ring + st * 2 * C::kHalf;
-          uint8_t* dv = dk + C::kHalf;
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int dim) {
-            if (LOGITS) tma_load_3d_policy(dst, map, bar, dim, head, r, policy);
-            else tma_load_3d(dst, map, bar, dim, head, r);
-          };
-          if (n > 0 && !mbar_wait(&sm.k_empty[st], (n - 1) & 1, abort_flag)) {
+          bool free = true;  // the stage's last unit is done with
+          if (fills >= C::kStages) {
+            const uint32_t u = fills - C::kStages;
+            free = warp == 0 ? mbar_wait(&sm.s_done[u % 6], (u / 6) & 1, abort_flag)
+                             : mbar_wait(&sm.pv_done[st], (u / C::kStages) & 1, abort_flag);
+          }
+          if (!free) {
             gave_up();
           } else {
-            mbar_arrive_expect_tx(&sm.k_full[st], C::kHalf);
-            load(dk, &tm_k, &sm.k_full[st], 0);
-            load(dk + kTile * 128, &tm_k, &sm.k_full[st], 64);
-            ++k_issued;
-            if (n > 0 && !mbar_wait(&sm.v_empty[st], (n - 1) & 1, abort_flag)) {
-              gave_up();
-            } else {
-              mbar_arrive_expect_tx(&sm.v_full[st], C::kHalf);
-              load(dv, &tm_v, &sm.v_full[st], 0);
-              load(dv + kTile * 128, &tm_v, &sm.v_full[st], 64);
-              ++v_issued;
+            uint8_t* dst = dst0 + st * 2 * C::kHalf;
+            mbar_arrive_expect_tx(&full[st], C::kHalf);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (LOGITS) tma_load_3d_policy(dst + half * 16384, map, &full[st], half * 64, head, r, policy);
+              else tma_load_3d(dst + half * 16384, map, &full[st], half * 64, head, r);
             }
+            ++issued;
           }
         }
         __syncwarp();
@@ -935,175 +926,195 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
       }
     }
     if (bad) atomicOr(&sm.err, kFlagBadIndex);
-    if (lane == 0) {  // no copy may land after this CTA has left (all have, but after a wait that gave up)
-      auto drain = [&](uint64_t* full, uint32_t issued, uint32_t stages) {
-        for (uint32_t f = issued > stages ? issued - stages : 0; f < issued; ++f)
-          mbar_wait(&full[f % stages], (f / stages) & 1, nullptr);
-      };
-      drain(sm.k_full, k_issued, C::kStages);
-      drain(sm.v_full, v_issued, C::kStages);
-      drain(sm.q_full, q_issued, 2);
+    if (lane == 0)  // no copy may land after this CTA has left (all have, but after a wait that gave up)
+      for (uint32_t f = issued > C::kStages ? issued - C::kStages : 0; f < issued; ++f)
+        mbar_wait(&full[f % C::kStages], (f / C::kStages) & 1, nullptr);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ Q of each segment, once the one before has its last S
+    if (lane == 0) {
+      uint32_t segs = 0;
+      while (walk.next(sg)) {
+        if (segs > 0 && !mbar_wait(&sm.q_empty, (segs - 1) & 1, abort_flag)) {
+          gave_up();
+          break;
+        }
+        mbar_arrive_expect_tx(&sm.q_full, G * 256);
+        tma_load_3d(q_buf, &tm_q, &sm.q_full, 0, head * G, sg.seq);
+        tma_load_3d(q_buf + 16384, &tm_q, &sm.q_full, 64, head * G, sg.seq);
+        ++segs;
+      }
+      if (segs > 0) mbar_wait(&sm.q_full, (segs - 1) & 1, nullptr);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16(128, kTile, false), idesc_o = idesc_bf16(128, kHeadDim, true);
-      uint32_t f = 0, segs = 0;
-      bool ok = true;
-      bool prev_first = false;
-      uint32_t prev_seg = 0;
-      // O (+)= P V of unit x; `first` of its segment: a new accumulation, once the segment before has been read out
-      auto issue_pv = [&](uint32_t x, bool first, uint32_t seg) {
-        const int st = x % C::kStages, b = x & 1;
-        if (!mbar_wait(&sm.p_full[b], (x >> 1) & 1, abort_flag) ||
-            !mbar_wait(&sm.v_full[st], (x / C::kStages) & 1, abort_flag) ||
-            (first && seg > 0 && !mbar_wait(&sm.o_free, (seg - 1) & 1, abort_flag)))
+      const uint32_t idesc_s = idesc_bf16(128, C::kKeys, false), idesc_o = idesc_bf16(128, kHeadDim, true);
+      uint32_t fs = 0, fp = 0;          // units whose S, whose P V has been issued
+      uint32_t segs = 0, pv_segs = 0;   // segments begun on either side
+      uint32_t place = 0;               // a byte per warpgroup: its unit's place in the segment (0, 1, 2 and behind)
+      int i = 0;                        // the next unit's place
+      bool ok = true, more = walk.next(sg);
+      // S of unit fs
+      auto issue_s = [&] {
+        const int st = fs % C::kStages, b = fs & 1;
+        if (i == 0 && !mbar_wait(&sm.q_full, segs & 1, abort_flag)) return false;
+        // S's columns are free once P V of unit fs - 2 has read its P
+        if (fs >= 2 && !mbar_wait(&sm.pv_done[(fs - 2) % C::kStages], ((fs - 2) / C::kStages) & 1, abort_flag)) return false;
+        if (!mbar_wait(&sm.k_full[st], (fs / C::kStages) & 1, abort_flag)) return false;
+        tc_fence_after();
+        const uint32_t qa = smem_u32(q_buf), ka = smem_u32(ring + st * 2 * C::kHalf);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
+          umma_bf16(tmem + C::kColS + b * 128, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idesc_s,
+                    kk ? 1u : 0u);
+        }
+        umma_commit(&sm.s_done[fs % 6]);
+        place = (place & ~(0xFFu << (8 * b))) | (static_cast<uint32_t>(i < 2 ? i : 2) << (8 * b));
+        ++fs;
+        if (++i == sg.count) {
+          umma_commit(&sm.q_empty);
+          ++segs;
+          i = 0;
+          more = walk.next(sg);
+        }
+        return true;
+      };
+      // O (+)= P V of unit fp, in its warpgroup's accumulator: a new sum for the first two units of a segment, once
+      // the segment before has been read out
+      auto issue_pv = [&] {
+        const int st = fp % C::kStages, b = fp & 1;
+        const uint32_t at = (place >> (8 * b)) & 0xFFu;
+        if (at == 0) ++pv_segs;
+        if (!mbar_wait(&sm.p_full[b], (fp >> 1) & 1, abort_flag) ||
+            !mbar_wait(&sm.v_full[st], (fp / C::kStages) & 1, abort_flag) ||
+            (at < 2 && pv_segs > 1 && !mbar_wait(&sm.o_free, (pv_segs - 2) & 1, abort_flag)))
           return false;
         tc_fence_after();
         const uint32_t va = smem_u32(ring + st * 2 * C::kHalf + C::kHalf);
-        const uint32_t pc = tmem + C::kColP + b * 64, oc = tmem + C::kColO;
+        const uint32_t pc = tmem + C::kColS + b * 128, oc = tmem + C::kColO + b * 128;
+        // P of keys 32 c .. 32 c + 31: the values in columns 32 c .. + 15, the rests in 32 c + 16 .. + 31
 #pragma unroll
-        for (int part = 0; part < 2; ++part)  // the value, then the rest
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            umma_bf16_ts(oc, pc + part * 32 + kk * 8, sdesc_sw128(va + kk * 2048, kTile * 128, 1024), idesc_o,
-                         (first && part == 0 && kk == 0) ? 0u : 1u);
-        umma_commit(&sm.v_empty[st]);
-        umma_commit(&sm.pv_done[b]);
-        return true;
-      };
-      while (ok && walk.next(sg)) {
-        const int qb = segs & 1;
-        if (!mbar_wait(&sm.q_full[qb], (segs >> 1) & 1, abort_flag)) {
-          gave_up();
-          ok = false;
-          break;
-        }
-        for (int i = 0; i < sg.count; ++i, ++f) {
-          const int st = f % C::kStages;
-          if (!mbar_wait(&sm.k_full[st], (f / C::kStages) & 1, abort_flag)) {
-            gave_up();
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          // S buffer f & 1 is free: the softmax warps had read it when they wrote P of unit f - 2, which P V waited for
-          const uint32_t qa = smem_u32(q_buf + qb * C::kQBytes), ka = smem_u32(ring + st * 2 * C::kHalf);
+        for (int part = 0; part < 2; ++part)
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            umma_bf16(tmem + C::kColS + (f & 1) * 64, sdesc_sw128(qa + (kk >> 2) * 16384 + (kk & 3) * 32, 16, 1024),
-                      sdesc_sw128(ka + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024), idesc_s, kk ? 1u : 0u);
-          umma_commit(&sm.s_full[f & 1]);
-          umma_commit(&sm.k_empty[st]);
-          if (i == sg.count - 1) umma_commit(&sm.q_empty[qb]);
-          if (f > 0 && !issue_pv(f - 1, prev_first, prev_seg)) {
-            gave_up();
-            ok = false;
-            break;
-          }
-          prev_first = i == 0;
-          prev_seg = segs;
-        }
-        ++segs;
+            umma_bf16_ts(oc, pc + (kk >> 1) * 32 + (kk & 1) * 8 + part * 16, sdesc_sw128(va + kk * 2048, 16384, 1024),
+                         idesc_o, (at < 2 && part == 0 && kk == 0) ? 0u : 1u);
+        umma_commit(&sm.pv_done[st]);
+        ++fp;
+        return true;
+      };
+      while (ok && more) {
+        // S one unit ahead of P V
+        ok = issue_s() && (fs < 2 || issue_pv());
       }
-      if (ok && f > 0 && !issue_pv(f - 1, prev_first, prev_seg)) gave_up();
+      if (ok && fp < fs) ok = issue_pv();
+      if (!ok) gave_up();
       umma_commit(&sm.mma_done);
       mbar_wait(&sm.mma_done, 0, nullptr);
     }
-  } else if (warp >= 4) {
+  } else {
     // ------------------------------------------------------------ softmax and output
+    const int b = (warp >> 2) - 1;         // warpgroup: units of this parity
     const int r = (warp & 3) * 32 + lane;  // TMEM lane = head of the group
     const bool busy = (warp & 3) * 32 < G;  // a warp whose rows are all past the group only keeps the barriers going
     const uint32_t la = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_col = la + C::kColS + b * 128, o_col = la + C::kColO + b * 128;
     const float c = p.scale_log2;
-    uint32_t f = 0;
+    uint32_t f = 0, segs = 0;
     bool ok = true;
     int4 crossing = make_int4(-1, 0, 0, 0);  // the sequence that begins in this run and goes on
-    while (ok && walk.next(sg)) {
-      float m = 0.0f;
+    auto warp_arrive = [&](uint64_t* bar) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    for (; ok && walk.next(sg); ++segs) {
+      float m = -INFINITY;
       float2 l2 = make_float2(0.0f, 0.0f);
       for (int i = 0; i < sg.count; ++i, ++f) {
-        const int b = f & 1;
-        if (!mbar_wait_warp(&sm.s_full[b], (f >> 1) & 1, abort_flag)) {
+        if (static_cast<int>(f & 1) != b) continue;
+        if (!mbar_wait_warp(&sm.s_done[f % 6], (f / 6) & 1, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // P buffer b is free once P V of unit f - 2 has read it
-        if (f >= 2 && !mbar_wait_warp(&sm.pv_done[b], ((f >> 1) - 1) & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const int valid = sg.len - (sg.off + i) * kTile;
-        if (valid < kTile) {
-          // uniform: the sequence's last unit.  Its V rows past the end hold anything, and 0 * NaN is NaN: zero them.
+        const int valid = sg.len - (sg.off + i) * C::kKeys;
+        const bool tail = valid < C::kKeys;  // uniform: the sequence's last unit
+        if (tail) {
+          // Its V rows past the end hold anything, and 0 * NaN is NaN: zero them.  (The barrier is past the stage's
+          // earlier fills: S of this unit came after P V of the unit before the last.)
           const int st = f % C::kStages;
           if (!mbar_wait_warp(&sm.v_full[st], (f / C::kStages) & 1, abort_flag)) {
             ok = false;
             break;
           }
           uint8_t* v = ring + st * 2 * C::kHalf + C::kHalf;
-          for (int j = valid * 8 + r; j < kTile * 8; j += 128) {  // 16-byte pieces of the rows' two halves
+          for (int j = valid * 8 + r; j < C::kKeys * 8; j += 128) {  // 16-byte pieces of the rows' two halves
             reinterpret_cast<uint4*>(v)[j] = make_uint4(0, 0, 0, 0);
-            reinterpret_cast<uint4*>(v + kTile * 128)[j] = make_uint4(0, 0, 0, 0);
+            reinterpret_cast<uint4*>(v + 16384)[j] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
         if (busy) {
+          // the row's maximum over the unit, then its weights, 32 keys at a time
           uint32_t va[32], vb[32];
-          float xa, xb;
-          tmem_ld_max_32cols(la + C::kColS + b * 64, va, xa);
-          tmem_ld_max_32cols(la + C::kColS + b * 64 + 32, vb, xb);
-          tmem_ld_wait_regs_max(va, xa);
-          tmem_regs_written(vb, xb);
-          if (valid < kTile) {
-            xa = xb = -INFINITY;
+          float x = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              if (j >= valid) va[j] = 0xFF800000u;
-              if (j + 32 >= valid) vb[j] = 0xFF800000u;
-              xa = fmaxf(xa, __uint_as_float(va[j]));
-              xb = fmaxf(xb, __uint_as_float(vb[j]));
-            }
-          }
-          const float x = fmaxf(xa, xb) * c;
-          if (LOGITS && r < G) {
-            float* w = p.logits + (((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) + r) * kTile;
-            auto put = [&](const uint32_t (&v)[32], float* at) {
+          for (int q = 0; q < 2; ++q) {
+            float xa, xb;
+            tmem_ld_max_32cols(s_col + 64 * q, va, xa);
+            tmem_ld_max_32cols(s_col + 64 * q + 32, vb, xb);
+            tmem_ld_wait_regs_max(va, xa);
+            tmem_regs_written(vb, xb);
+            if (tail) {
+              xa = xb = -INFINITY;
 #pragma unroll
-              for (int j = 0; j < 32; j += 8) {
-                uint4 lo, hi;
-                lo.x = __float_as_uint(__uint_as_float(v[j]) * c); lo.y = __float_as_uint(__uint_as_float(v[j + 1]) * c);
-                lo.z = __float_as_uint(__uint_as_float(v[j + 2]) * c); lo.w = __float_as_uint(__uint_as_float(v[j + 3]) * c);
-                hi.x = __float_as_uint(__uint_as_float(v[j + 4]) * c); hi.y = __float_as_uint(__uint_as_float(v[j + 5]) * c);
-                hi.z = __float_as_uint(__uint_as_float(v[j + 6]) * c); hi.w = __float_as_uint(__uint_as_float(v[j + 7]) * c);
-                st_global_32b(at + j, lo, hi);
+              for (int j = 0; j < 32; ++j) {
+                if (64 * q + j < valid) xa = fmaxf(xa, __uint_as_float(va[j]));
+                if (64 * q + 32 + j < valid) xb = fmaxf(xb, __uint_as_float(vb[j]));
               }
-            };
-            put(va, w);
-            put(vb, w + 32);
+            }
+            x = fmax3(x, xa, xb);
           }
-          if (i == 0) {
+          x *= c;
+          if (i < 2) {  // this warpgroup's first unit of the segment
             m = x == -INFINITY ? 0.0f : x;
           } else {
             const bool need = x - m > 8.0f;
             if (__any_sync(0xFFFFFFFFu, need)) {
-              // every P V so far must be in O before it is scaled
-              if (!mbar_wait_warp(&sm.pv_done[b ^ 1], ((f - 1) >> 1) & 1, abort_flag)) {
+              // O is complete once P V of this warpgroup's unit before is done
+              if (!mbar_wait_warp(&sm.pv_done[(f - 2) % C::kStages], ((f - 2) / C::kStages) & 1, abort_flag)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
               const float up = need ? ceilf(x - m) : 0.0f;
               const float k = exp2_approx(-up);
-              rescale_o(la + C::kColO, k);
+              rescale_o(o_col, k);
               l2.x *= k;
               l2.y *= k;
               m += up;
             }
           }
+          float* logits = nullptr;
+          if (LOGITS && r < G)
+            logits = p.logits + (((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) + r) * C::kKeys;
           const float2 c2 = make_float2(c, c), nm = make_float2(-m, -m);
-          auto weights = [&](const uint32_t (&v)[32], uint32_t col) {
+          auto weights = [&](uint32_t (&v)[32], int q) {
+            if (tail) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (32 * q + j >= valid) v[j] = 0xFF800000u;
+            }
+            if (LOGITS && logits) {
+#pragma unroll
+              for (int j = 0; j < 32; j += 8) {
+                uint32_t w[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) w[k] = __float_as_uint(__uint_as_float(v[j + k]) * c);
+                st_global_32b(logits + 32 * q + j, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+              }
+            }
 #pragma unroll
             for (int h = 0; h < 32; h += 16) {
               uint32_t hi[8], lo[8];
@@ -1114,60 +1125,97 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
                 l2 = fadd2(l2, w);
                 split_bf16(w.x, w.y, hi[j], lo[j]);
               }
-              tmem_st_8cols(col + h / 2, hi);
-              tmem_st_8cols(col + 32 + h / 2, lo);
+              tmem_st_8cols(s_col + 32 * q + h / 2, hi);
+              tmem_st_8cols(s_col + 32 * q + 16 + h / 2, lo);
             }
           };
-          weights(va, la + C::kColP + b * 64);
-          weights(vb, la + C::kColP + b * 64 + 16);
+          tmem_ld_32cols(s_col, va);
+          tmem_ld_wait_regs(va);
+          tmem_ld_32cols(s_col + 32, vb);
+          weights(va, 0);
+          tmem_ld_wait_regs(vb);
+          tmem_ld_32cols(s_col + 64, va);
+          weights(vb, 1);
+          tmem_ld_wait_regs(va);
+          tmem_ld_32cols(s_col + 96, vb);
+          weights(va, 2);
+          tmem_ld_wait_regs(vb);
+          weights(vb, 3);
           tmem_st_wait();
+        } else {
+          m = 0.0f;  // O of these rows exists but is nobody's
         }
         tc_fence_before();
-        mbar_arrive(&sm.p_full[b]);
+        warp_arrive(&sm.p_full[b]);
       }
       if (!ok) break;
 
-      // ---- the segment's output
-      const uint32_t last = f - 1;
-      if (!mbar_wait_warp(&sm.pv_done[last & 1], (last >> 1) & 1, abort_flag)) {
+      // ---- the segment's output: this warpgroup's last P V done, (m, l) exchanged; each takes half of the dims
+      const uint32_t last = f - 1;                                   // the segment's last unit
+      const bool some = sg.count > 1 || static_cast<int>(last & 1) == b;
+      if (some) {
+        const uint32_t own = static_cast<int>(last & 1) == b ? last : last - 1;
+        if (!mbar_wait_warp(&sm.pv_done[own % C::kStages], (own / C::kStages) & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+      }
+      float l = l2.x + l2.y;
+      if (segs > 0 && !mbar_wait_warp(&sm.o_free, (segs - 1) & 1, abort_flag)) {  // the segment before's are read
+        ok = false;
+        break;
+      }
+      sm.ml[b][r] = make_float2(m, l);
+      warp_arrive(&sm.ml_full);
+      if (!mbar_wait_warp(&sm.ml_full, segs & 1, abort_flag)) {
         ok = false;
         break;
       }
       tc_fence_after();
+      const float2 other = sm.ml[b ^ 1][r];
+      const float top = fmaxf(m, other.x);
+      const float k_own = exp2_diff(m, top), k_other = exp2_diff(other.x, top);
+      l = b == 0 ? fmaf(l, k_own, other.y * k_other) : fmaf(other.y, k_other, l * k_own);  // the same in both warpgroups
+      m = top;
       const bool whole = sg.first && sg.last;
-      const float l = l2.x + l2.y;
       const long long out_row = (static_cast<long long>(sg.seq) * p.hkv + head) * G + r;
       const long long part_row = (static_cast<long long>(blockIdx.x) * 2 + (sg.first ? 1 : 0)) * G + r;
       if (busy) {
-        const float inv = inverse(l);
+        const bool none_own = !some, none_other = other.x == -INFINITY;  // uniform: their O holds an older segment
+        const float inv = whole ? inverse(l) : 1.0f;
+        const float f_own = k_own * inv, f_other = k_other * inv;
+        const uint32_t other_col = la + C::kColO + (b ^ 1) * 128;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[32];
-          tmem_ld_32cols(la + C::kColO + q * 32, v);
+        for (int q = 0; q < 2; ++q) {
+          const int dim = b * 64 + q * 32;
+          uint32_t v[32], w[32];
+          tmem_ld_32cols(o_col + dim, v);
+          tmem_ld_32cols(other_col + dim, w);
           tmem_ld_wait_regs(v);
+          tmem_ld_wait_regs(w);
+          float o[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            o[j] = (none_own ? 0.0f : __uint_as_float(v[j]) * f_own) + (none_other ? 0.0f : __uint_as_float(w[j]) * f_other);
           if (r >= G) continue;
           if (whole) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              uint32_t w[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                w[k] = pack_bf16(__uint_as_float(v[j + 2 * k]) * inv, __uint_as_float(v[j + 2 * k + 1]) * inv);
-              uint4* to = reinterpret_cast<uint4*>(p.o + out_row * kHeadDim + q * 32 + j);  // o is 16-byte aligned
-              to[0] = make_uint4(w[0], w[1], w[2], w[3]);
-              to[1] = make_uint4(w[4], w[5], w[6], w[7]);
-            }
+            for (int j = 0; j < 32; j += 8)  // o is 16-byte aligned
+              *reinterpret_cast<uint4*>(p.o + out_row * kHeadDim + dim + j) =
+                  make_uint4(pack_bf16(o[j], o[j + 1]), pack_bf16(o[j + 2], o[j + 3]), pack_bf16(o[j + 4], o[j + 5]),
+                             pack_bf16(o[j + 6], o[j + 7]));
           } else {
+            auto word = [&](int j) { return __float_as_uint(o[j]); };
 #pragma unroll
             for (int j = 0; j < 32; j += 8)
-              st_global_32b(p.part_o + part_row * kHeadDim + q * 32 + j, make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]),
-                            make_uint4(v[j + 4], v[j + 5], v[j + 6], v[j + 7]));
+              st_global_32b(p.part_o + part_row * kHeadDim + dim + j, make_uint4(word(j), word(j + 1), word(j + 2), word(j + 3)),
+                            make_uint4(word(j + 4), word(j + 5), word(j + 6), word(j + 7)));
           }
         }
       }
       tc_fence_before();
-      mbar_arrive(&sm.o_free);
-      if (r < G) {
+      warp_arrive(&sm.o_free);
+      if (b == 0 && r < G) {
         if (whole) {
           p.lse[out_row] = (m + log2f(l)) * kLn2;
           if (LOGITS) p.norm[out_row] = row_norm(m, l);
@@ -1176,13 +1224,14 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
         }
       }
       if (sg.first && !sg.last) {
-        const long long end = sg.unit + units_of(sg.len) - 1;
+        const long long end = sg.unit + units_of(sg.len, p.unit_shift) - 1;
         crossing = make_int4(sg.seq, g, static_cast<int>(((end + 1) * run.runs - 1) / run.total), 0);
       }
-      if (p.by_seq && sg.first && r == 0) p.meta[sg.seq * p.hkv + head] = sg.last ? make_int4(-1, 0, 0, 0) : crossing;
+      if (p.by_seq && sg.first && b == 0 && r == 0)
+        p.meta[sg.seq * p.hkv + head] = sg.last ? make_int4(-1, 0, 0, 0) : crossing;
     }
     if (!ok && lane == 0) gave_up();
-    if (!p.by_seq && r == 0) p.meta[blockIdx.x] = crossing;
+    if (!p.by_seq && b == 0 && r == 0) p.meta[blockIdx.x] = crossing;
   }
   __syncwarp();
   tc_fence_before();
@@ -1301,11 +1350,11 @@ __global__ void __launch_bounds__(kWeightThreads, 2) dense_weight_kernel(DenseDe
   if (p.hdr->status & kFlagTimeout) return;  // logits are missing
   const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv, G = p.group;
   Run run;
-  if (!find_run(p.cu_k, p.num_seqs, p.max_k, p.total_k, g, p.groups, run_sm, run)) return;
-  Walker walk(p.cu_k, run);
+  if (!find_run(p, g, run_sm, run)) return;
+  Walker walk(p, run);
   Segment sg;
-  constexpr int kPer = kTile / 4;  // threads of a unit
-  const int key = threadIdx.x % kPer * 4, first = threadIdx.x / kPer;
+  const int tile = 1 << p.unit_shift, per = tile / 4;  // keys and threads of a unit
+  const int key = threadIdx.x % per * 4, first = threadIdx.x / per;
   while (walk.next(sg)) {
     __syncthreads();
     const long long row = static_cast<long long>(sg.seq) * p.hkv + head;
@@ -1313,15 +1362,15 @@ __global__ void __launch_bounds__(kWeightThreads, 2) dense_weight_kernel(DenseDe
     __syncthreads();
     float* out = p.weight + row * p.weight_stride;
     const bool vec = (reinterpret_cast<uintptr_t>(out) & 15u) == 0;
-    for (int i = first; i < sg.count; i += kWeightThreads / kPer) {
-      const int j = (sg.off + i) * kTile + key;
+    for (int i = first; i < sg.count; i += kWeightThreads / per) {
+      const int j = ((sg.off + i) << p.unit_shift) + key;
       if (j >= sg.len) continue;
-      const float* s = p.logits + ((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) * kTile + key;
+      const float* s = p.logits + ((((sg.unit + i) * p.hkv + head) * G) << p.unit_shift) + key;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
       for (int h = 0; h < G; ++h) {
         const float2 n = norm[h];
-        const float4 v = *reinterpret_cast<const float4*>(s + h * kTile);
+        const float4 v = *reinterpret_cast<const float4*>(s + (h << p.unit_shift));
         sum.x += exp2_approx(v.x - n.x) * n.y;
         sum.y += exp2_approx(v.y - n.x) * n.y;
         sum.z += exp2_approx(v.z - n.x) * n.y;

@@ -276,11 +276,12 @@ cudaError_t launch_combine(const CombineParams& p, bool f16_partials, cudaStream
 
 // ---------------------------------------------------------------- dense decode attention
 // One new token per sequence over every key of a paged cache.
-constexpr int kDenseTile = 64;      // keys of a work unit
+constexpr int kDenseTile = 64;      // keys of a work unit (128 where the split runs on tcgen05)
 constexpr int kDenseMaxCtas = 320;  // CTAs of the split at most (two per SM), or num_kv_heads where that is more
 struct DenseDecodeParams {
   int num_seqs, hkv, group, max_k, total_k;
   int groups;                   // runs the batch is cut into; groups * hkv CTAs
+  int unit_shift;               // a work unit has 1 << unit_shift keys
   const int32_t* cu_k;
   const __nv_bfloat16* q;       // [num_seqs, hkv * group, 128]
   const int32_t* block_table;   // [num_seqs, bt_stride]
@@ -302,11 +303,12 @@ struct DenseDecodeParams {
   int4* meta;
   bool by_seq;
   uint32_t* flags;              // [groups, hkv] device error flags
-  float* logits;                // with weight: [units, hkv, group, kDenseTile] in log2 units; else null
+  float* logits;                // with weight: [units, hkv, group, unit's keys] in log2 units; else null
   float2* norm;                 // with weight: [num_seqs, hkv * group] (maximum, 1 / sum); else null
 };
 int dense_decode_ctas_per_sm(int group);
-bool dense_decode_tc(int group, bool fp8);  // whether the split runs on tcgen05 and reads Q through tq
+// Whether the split runs on tcgen05: units of 128 keys (the boxes of tk and tv), Q through tq (boxes of the group's heads).
+bool dense_decode_tc(int group, bool fp8);
 cudaError_t launch_dense_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const DenseDecodeParams& p, bool fp8, cudaStream_t stream);
 
