@@ -80,11 +80,16 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
   const __half2 v = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// (a, b) as a bf16 pair plus a bf16 pair of what its rounding left
+// (a, b) >= 0 as a bf16 pair, cut off, plus a bf16 pair of the rest, rounded: 2^-16 of the value is lost at most (the
+// rest of a value in [2^e, 2^(e+1)) is below 2^(e-7), half its last place 2^(e-16)).  Cutting off is a byte
+// permutation where rounding takes the conversion unit a second time: 0.75 against 1.02 us a unit of 64 keys at 128
+// heads.
 __device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = pack_bf16(a - __low2float(h), b - __high2float(h));
+  const uint32_t ua = __float_as_uint(a), ub = __float_as_uint(b);
+  hi = __byte_perm(ua, ub, 0x7632);
+  const float2 rest = ffma2(make_float2(__uint_as_float(ua & 0xFFFF0000u), __uint_as_float(ub & 0xFFFF0000u)),
+                            make_float2(-1.0f, -1.0f), make_float2(a, b));
+  lo = pack_bf16(rest.x, rest.y);
 }
 // two E4M3 codes (low 16 bits) -> fp16 pair; exact
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
