@@ -11,8 +11,6 @@
 // (512 bytes in bf16) and bounds the call.
 #include <cuda_fp8.h>
 
-#include <type_traits>
-
 #include "common.cuh"
 #include "kernels.h"
 
@@ -67,14 +65,21 @@ __device__ __forceinline__ uint32_t cluster_word(const uint32_t* p, uint32_t ran
 // three digits of a radix select; the CTAs' digit counts are added through
 // distributed shared memory, and each CTA finds the same digit.  What lies above
 // the threshold in a CTA's share follows from its own counts, so the kept slots
-// are written in one more pass.  Every pass reads the weights from L2, 16 bytes a
-// load, or from registers when a share fits them.
+// are written in one more pass.  Each weight is read from L2 once: its key stays
+// in shared memory (CACHED, shares of up to kSelKeys slots; larger ones read the
+// weights again for each pass).  What bounds it is the instructions of four passes
+// over the keys, about 30 a key.
+constexpr int kSelKeys = 48 * 1024;
+constexpr uint32_t kLate = 0xFFFFFFFFu;  // the key of a slot of the window: above every weight's
+
+template <bool CACHED>
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p, int cs) {
-  __shared__ uint32_t hist[3][2048];
+  extern __shared__ __align__(16) uint32_t keys[];  // CACHED: this CTA's share, in slot order
+  __shared__ uint32_t hist[2 * 2048 + 1024];
   __shared__ uint32_t sm[33];
   __shared__ uint32_t pick[3][2];
   __shared__ uint32_t mine[2];  // kept for sure and equal to the threshold, in this CTA's share
-  const int t = threadIdx.x;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int row = blockIdx.x / cs, s = row / p.hkv, g = row % p.hkv;
   auto sync_all = [&] {
@@ -88,7 +93,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     const int a = p.cu_k[i], b = p.cu_k[i + 1];
     bad |= a < 0 || b < a || b - a > p.max_k;
   }
-  for (int i = t; i < 3 * 2048; i += kSelThreads) hist[0][i] = 0;
+  for (int i = t; i < 2 * 2048 + 1024; i += kSelThreads) hist[i] = 0;
   if (__syncthreads_or(bad)) {
     if (t == 0 && blockIdx.x == 0) atomicOr(&p.hdr->status, kFlagBadSeqlens);
     return;  // the whole cluster
@@ -132,72 +137,78 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
   }
   const int free_n = n - p.recent, take = p.budget - p.recent;  // free_n > take
 
-  // this CTA's slots [c0, c1), c0 a multiple of 16
+  // this CTA's slots [c0, c1), c0 a multiple of 16; those before `end` are chosen by weight
   const int share = ((n + cs - 1) / cs + 15) & ~15;
   const int c0 = min(n, rank * share), c1 = min(n, c0 + share);
+  const int end = max(c0, min(c1, free_n));
   const bool vec = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
-  auto all4 = [&](int i) {  // slots i .. i + 3, all of the share
-    return vec ? *reinterpret_cast<const float4*>(w + i) : make_float4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-  };
-  auto load4 = [&](int i) {  // past the share zeros
-    if (i + 4 <= c1) return all4(i);
-    return make_float4(i < c1 ? w[i] : 0.f, i + 1 < c1 ? w[i + 1] : 0.f, i + 2 < c1 ? w[i + 2] : 0.f, 0.f);
-  };
-  const bool once = c1 - c0 <= 4 * kSelThreads;
-  const int warp = t >> 5, lane = t & 31;
-  float held[4];  // slots c0 + 128 warp + 32 j + lane
-  if (once)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = c0 + 128 * warp + 32 * j + lane;
-      held[j] = i < c1 ? w[i] : 0.0f;
+  // the keys of slots i .. i + 3; kLate in the window and past the share
+  auto load4 = [&](int i) {
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (vec && i + 4 <= c1) {
+      v = *reinterpret_cast<const float4*>(w + i);
+    } else {
+      if (i < c1) v.x = w[i];
+      if (i + 1 < c1) v.y = w[i + 1];
+      if (i + 2 < c1) v.z = w[i + 2];
+      if (i + 3 < c1) v.w = w[i + 3];
     }
+    return make_uint4(i < end ? weight_key(v.x) : kLate, i + 1 < end ? weight_key(v.y) : kLate,
+                      i + 2 < end ? weight_key(v.z) : kLate, i + 3 < end ? weight_key(v.w) : kLate);
+  };
 
-  uint32_t prefix = 0, mask = 0;
-  uint32_t want = take;   // how many of the keys with this prefix are taken
-  uint32_t above = 0;     // this thread's count of keys in the share that lie above the prefix
-  uint32_t equal = 0;     // keys of the share equal to the threshold (after the last digit)
+  uint32_t prefix = kLate - 1, mask = 0;  // no weight counts when the window takes the whole budget
+  uint32_t want = 0;                      // how many of the keys with this prefix are taken
+  uint32_t above = 0;                     // this thread's count of keys in the share that lie above the prefix
+  uint32_t equal = 0;                     // keys of the share equal to the threshold (after the last digit)
+  if (CACHED && take == 0) {
+    for (int i = c0 + 4 * t; i < c1; i += 4 * kSelThreads) *reinterpret_cast<uint4*>(keys + (i - c0)) = load4(i);
+    __syncthreads();
+  }
   if (take > 0) {
+    prefix = 0;
+    want = take;
     const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
-    const int end = min(c1, free_n);
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = shifts[pass], bins = 1 << bits[pass];
-      auto count = [&](float f, bool on) {
-        const uint32_t k = weight_key(f);
-        if (on && (k & mask) == prefix) atomicAdd(&hist[pass][(k >> shift) & (bins - 1)], 1u);
+      uint32_t* const counts = hist + 2048 * pass;
+      auto count = [&](uint32_t k) {
+        // the window's keys have all digits set, the first of them that of a NaN with its sign clear: no weight's
+        if (pass == 0 ? k != kLate : (k & mask) == prefix) atomicAdd(&counts[(k >> shift) & (bins - 1)], 1u);
       };
-      if (once) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) count(held[j], c0 + 128 * warp + 32 * j + lane < end);
-      } else if (end > c0) {
-        const int whole = c0 + (end - c0) / (16 * kSelThreads) * (16 * kSelThreads);
+      auto count4 = [&](const uint4& k) {
+        count(k.x);
+        count(k.y);
+        count(k.z);
+        count(k.w);
+      };
+      if (pass == 0 || !CACHED) {
         int i = c0 + 4 * t;
-        for (; i < whole; i += 16 * kSelThreads) {  // four loads in flight, nothing to check
-          float4 v[4];
+        for (; i + 12 * kSelThreads < c1; i += 16 * kSelThreads) {  // four loads in flight
+          uint4 k[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) v[u] = all4(i + 4 * u * kSelThreads);
+          for (int u = 0; u < 4; ++u) k[u] = load4(i + 4 * u * kSelThreads);
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            count(v[u].x, true);
-            count(v[u].y, true);
-            count(v[u].z, true);
-            count(v[u].w, true);
+            if (CACHED) *reinterpret_cast<uint4*>(keys + (i - c0 + 4 * u * kSelThreads)) = k[u];
+            count4(k[u]);
           }
         }
-        for (; i < end; i += 4 * kSelThreads) {
-          const float4 v = load4(i);
-          count(v.x, true);
-          count(v.y, i + 1 < end);
-          count(v.z, i + 2 < end);
-          count(v.w, i + 3 < end);
+        for (; i < c1; i += 4 * kSelThreads) {
+          const uint4 k = load4(i);
+          if (CACHED) *reinterpret_cast<uint4*>(keys + (i - c0)) = k;
+          count4(k);
         }
+      } else {
+#pragma unroll 2
+        for (int i = 4 * t; i < c1 - c0; i += 4 * kSelThreads) count4(*reinterpret_cast<const uint4*>(keys + i));
       }
       sync_all();
       // thread t takes the bins from the top: bins - 1 - (2 t) and the one below (one bin for 10 bits)
       const int per = bins / kSelThreads;
       const int top = bins - 1 - per * t;
-      const uint32_t own0 = hist[pass][top], own1 = per > 1 ? hist[pass][top - 1] : 0u;
+      const uint32_t own0 = counts[top], own1 = per > 1 ? counts[top - 1] : 0u;
       uint32_t n0 = own0, n1 = own1;
       if (cs > 1) {
         uint32_t v0[7], v1[7];  // all in flight at once
@@ -206,8 +217,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
           v0[r - 1] = v1[r - 1] = 0;
           if (r >= cs) continue;
           const int from = rank + r < cs ? rank + r : rank + r - cs;
-          v0[r - 1] = cluster_word(&hist[pass][top], from);
-          if (per > 1) v1[r - 1] = cluster_word(&hist[pass][top - 1], from);
+          v0[r - 1] = cluster_word(&counts[top], from);
+          if (per > 1) v1[r - 1] = cluster_word(&counts[top - 1], from);
         }
 #pragma unroll
         for (int r = 0; r < 7; ++r) {
@@ -225,7 +236,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       __syncthreads();
       const int digit = static_cast<int>(pick[pass][0]);
       above += (top > digit ? own0 : 0u) + (per > 1 && top - 1 > digit ? own1 : 0u);
-      equal = hist[pass][digit];
+      equal = counts[digit];
       prefix |= static_cast<uint32_t>(digit) << shift;
       mask |= static_cast<uint32_t>(bins - 1) << shift;
       want = pick[pass][1];
@@ -237,7 +248,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     uint32_t total;
     block_exclusive(above, total, sm);
     if (t == 0) {
-      mine[0] = total + max(0, c1 - max(c0, free_n));
+      mine[0] = total + (c1 - end);
       mine[1] = equal;
     }
     sync_all();
@@ -248,31 +259,29 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     sync_all();  // nobody leaves before its words are read
   }
 
-  // Ordered compaction: keys above the threshold, the first `want` equal to it, and the window.  A warp takes 32 kRows
-  // neighbours, a row of 32 at a time, so that what it keeps of a row is written in one piece; the warps' places
-  // come from one scan of their counts.
-  const bool by_weight = take > 0;
-  auto compact = [&](auto rows, int i0) {
-    constexpr int kRows = decltype(rows)::value;
+  // Ordered compaction: keys above the threshold (the window's among them) and the first `want` equal to it.  A warp
+  // takes 32 kRows neighbours, a row of 32 at a time, so that what it keeps of a row is written in one piece; the
+  // warps' places come from one scan of their counts.
+  constexpr int kRows = 8;
+  for (int i0 = c0; i0 < c1; i0 += kRows * kSelThreads) {
     const int i = i0 + 32 * kRows * warp + lane;
-    float v[kRows];
     uint32_t sure[kRows], same[kRows];  // a bit per lane
     uint32_t n_sure = 0, n_same = 0;
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) v[j] = kRows == 4 ? held[j & 3] : i + 32 * j < c1 ? w[i + 32 * j] : 0.0f;
-#pragma unroll
     for (int j = 0; j < kRows; ++j) {
-      const uint32_t k = weight_key(v[j]);
-      const bool in = i + 32 * j < c1, late = i + 32 * j >= free_n;
-      sure[j] = __ballot_sync(0xFFFFFFFFu, in && (late || (by_weight && k > prefix)));
-      same[j] = __ballot_sync(0xFFFFFFFFu, in && !late && by_weight && k == prefix);
+      const int at = i + 32 * j;
+      const bool in = at < c1;
+      uint32_t k = 0;
+      if (in) k = CACHED ? keys[at - c0] : at < end ? weight_key(w[at]) : kLate;
+      sure[j] = __ballot_sync(0xFFFFFFFFu, in && k > prefix);
+      same[j] = __ballot_sync(0xFFFFFFFFu, in && k == prefix);
       n_sure += __popc(sure[j]);
       n_same += __popc(same[j]);
     }
     uint32_t total;
     const uint32_t x = block_exclusive(lane == 0 ? n_sure | (n_same << 16) : 0u, total, sm);
-    const uint32_t at = __shfl_sync(0xFFFFFFFFu, x, 0);
-    uint32_t na = base + (at & 0xFFFFu), ne = ties + (at >> 16);
+    const uint32_t at0 = __shfl_sync(0xFFFFFFFFu, x, 0);
+    uint32_t na = base + (at0 & 0xFFFFu), ne = ties + (at0 >> 16);
     const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
@@ -281,18 +290,14 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       if (a || tie) {
         const uint32_t to = na + __popc(sure[j] & below) + min(e, want);
         kept[to] = i + 32 * j;
-        nw[to] = v[j];
+        nw[to] = w[i + 32 * j];
       }
       na += __popc(sure[j]);
       ne += __popc(same[j]);
     }
     base += total & 0xFFFFu;
     ties += total >> 16;
-  };
-  if (once)
-    compact(std::integral_constant<int, 4>{}, c0);
-  else
-    for (int i0 = c0; i0 < c1; i0 += 8 * kSelThreads) compact(std::integral_constant<int, 8>{}, i0);
+  }
 }
 
 // Checks one entry of the new table: inside the cache, not a page of the batch's own table and named once.
@@ -565,23 +570,31 @@ cudaError_t launch_evict(const EvictParams& p, bool fp8, int sms, cudaStream_t s
   // the header's status and the marks behind it start at zero
   cudaError_t e = cudaMemsetAsync(p.hdr, 0, p.clear_bytes, stream);
   if (e != cudaSuccess) return e;
-  // CTAs per (sequence, head): at most eight (a portable cluster), none with a share under 4,096 slots (one load per
-  // thread, held in registers), and only as many as run at once: a cluster's CTAs, one to an SM, share one of the
-  // GPU's eight or so SM groups, so larger clusters leave more SMs over (16 clusters of 8 took two turns, 49 us
+  // CTAs per (sequence, head): at most eight (a portable cluster), none with a share under 8,192 slots (the cluster's
+  // barriers and reads cost about 4 us), and only as many as run at once: a cluster's CTAs, one to an SM, share one
+  // of the GPU's eight or so SM groups, so larger clusters leave more SMs over (16 clusters of 8 took two turns, 49 us
   // against 25 us for 4 clusters, at 65,536 slots).
   const long long rows = static_cast<long long>(p.num_seqs) * p.hkv;
   int cs = rows <= sms / 19 ? 8 : rows <= sms / 6 ? 4 : rows <= sms / 2 ? 2 : 1;
-  while (cs > 1 && p.max_k / cs < 4 * kSelThreads) cs /= 2;
+  while (cs > 1 && p.max_k / cs < 8 * kSelThreads) cs /= 2;
+  const int share = ((p.max_k + cs - 1) / cs + 15) & ~15;  // the largest
+  const bool cached = share <= kSelKeys;
+  auto* fn = cached ? evict_select_kernel<true> : evict_select_kernel<false>;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.num_seqs) * p.hkv * cs);
+  cfg.gridDim = dim3(static_cast<unsigned>(rows) * cs);
   cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = cached ? static_cast<size_t>(share) * 4 : 0;
   cfg.stream = stream;
+  if (cfg.dynamicSmemBytes > 16 * 1024) {  // with the static part more than the default limit
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim = {static_cast<unsigned>(cs), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = cs > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, cs);
+  e = cudaLaunchKernelEx(&cfg, fn, p, cs);
   if (e != cudaSuccess) return e;
   note_launches(2);
   if (p.new_blocks == 0) return cudaSuccess;  // no cached key anywhere
