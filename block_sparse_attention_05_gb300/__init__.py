@@ -413,18 +413,18 @@ _raw_stream = (getattr(torch._C, "_cuda_getCurrentRawStream", None)
                or (lambda device: torch.cuda.current_stream(device).cuda_stream))
 
 
-def _refuse(t, dtype, dev, name):
+def _refuse(t, dtype, shape, dev, name):
     _need(t, dtype, name)
-    raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{dev}")
+    raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
 
 
 def _is(t, dtype, shape, dev, name):
-    """A contiguous tensor of this type and shape on the current CUDA device `dev`."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.get_device() != dev:
-        _refuse(t, dtype, dev, name)
-    if t.shape != shape:
-        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    """The address of a contiguous tensor of this type and shape on the current CUDA device `dev`."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape:
+        return t.data_ptr()
+    _refuse(t, dtype, shape, dev, name)
 
 
 def _c_paged(problem):
@@ -470,9 +470,9 @@ def _space(ws, nbytes, dev):
     """The workspace's address and size; a buffer of its own where the caller gives none."""
     if ws is None:
         ws = torch.empty(nbytes(), dtype=torch.uint8, device=f"cuda:{dev}")
-    elif not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != dev:
-        _refuse(ws, ws.dtype, dev, "ws")
-    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
+    elif ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(ws, ws.dtype, ws.shape, dev, "ws")
+    return ws, ws.data_ptr(), ws.nbytes
 
 
 def _dense(problem, q, k, v, scales, block_table, weight, o, lse, ws):
@@ -486,14 +486,21 @@ def _dense(problem, q, k, v, scales, block_table, weight, o, lse, ws):
         op = Op.DENSE_ATTN_DECODE_WEIGHT
     if o is None:
         o = torch.empty_like(q)
+        at_o = o.data_ptr()
+    else:
+        at_o = _is(o, torch.bfloat16, shape, dev, "o")
     if lse is None:
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
-    at_o, at_lse = _is(o, torch.bfloat16, shape, dev, "o"), _is(lse, torch.float32, shape[:2], dev, "lse")
+        lse = torch.empty((S, shape[1]), dtype=torch.float32, device=q.device)
+        at_lse = lse.data_ptr()
+    else:
+        at_lse = _is(lse, torch.float32, (S, shape[1]), dev, "lse")
     ws, at_ws, nws = _space(ws, lambda: msa_workspace_size(problem, op), dev)
     fn, where = ((_lib.msa_dense_attn_decode_paged_fp8, "msa_dense_attn_decode_paged_fp8") if scales else
                  (_lib.msa_dense_attn_decode_paged, "msa_dense_attn_decode_paged"))
-    _check(fn(c, at_q, *caches, at_table, block_table.shape[1], pages, at_weight, stride, at_o, at_lse, at_ws, nws,
-              _raw_stream(dev)), where)
+    status = fn(c, at_q, *caches, at_table, block_table.shape[1], pages, at_weight, stride, at_o, at_lse, at_ws, nws,
+                _raw_stream(dev))
+    if status:
+        raise MsaError(status, where)
     return o, lse
 
 
@@ -531,21 +538,28 @@ def _evict(problem, k, v, scales, block_table, weight, new_block_table, budget, 
     pages, caches = _pages(problem, dev, torch.uint8 if scales else torch.bfloat16, k, v, scales)
     at_table, at_new = _table(block_table, S, dev, "block_table"), _table(new_block_table, S, dev, "new_block_table")
     at_weight = _weight(weight, S, hkv, dev, "weight")
+    device = k.device
     if kept is None:
-        kept = torch.empty((S, hkv, budget), dtype=torch.int32, device=k.device)
+        kept = torch.empty((S, hkv, budget), dtype=torch.int32, device=device)
+        at_kept = kept.data_ptr()
+    else:
+        at_kept = _is(kept, torch.int32, (S, hkv, budget), dev, "kept")
     if new_weight is None:
-        new_weight = torch.zeros((S, hkv, budget), dtype=torch.float32, device=k.device)
-    if new_cu_k is None:
-        new_cu_k = torch.empty(S + 1, dtype=torch.int32, device=k.device)
-    at_kept, at_cu = _is(kept, torch.int32, (S, hkv, budget), dev, "kept"), _is(new_cu_k, torch.int32, (S + 1,), dev,
-                                                                               "new_cu_k")
+        new_weight = torch.zeros((S, hkv, budget), dtype=torch.float32, device=device)
     at_new_weight = _weight(new_weight, S, hkv, dev, "new_weight")
+    if new_cu_k is None:
+        new_cu_k = torch.empty(S + 1, dtype=torch.int32, device=device)
+        at_cu = new_cu_k.data_ptr()
+    else:
+        at_cu = _is(new_cu_k, torch.int32, (S + 1,), dev, "new_cu_k")
     ws, at_ws, nws = _space(ws, lambda: msa_evict_workspace_size(problem, budget, pages), dev)
     fn, where = ((_lib.msa_evict_paged_fp8, "msa_evict_paged_fp8") if scales else
                  (_lib.msa_evict_paged, "msa_evict_paged"))
-    _check(fn(c, *caches, at_table, block_table.shape[1], pages, at_weight, weight.shape[2], budget, recent, at_new,
-              new_block_table.shape[1], at_kept, at_new_weight, new_weight.shape[2], at_cu, at_ws, nws,
-              _raw_stream(dev)), where)
+    status = fn(c, *caches, at_table, block_table.shape[1], pages, at_weight, weight.shape[2], budget, recent, at_new,
+                new_block_table.shape[1], at_kept, at_new_weight, new_weight.shape[2], at_cu, at_ws, nws,
+                _raw_stream(dev))
+    if status:
+        raise MsaError(status, where)
     return kept, new_weight, new_cu_k
 
 
@@ -569,6 +583,7 @@ def msa_evict_paged_fp8(problem: Problem, k8_cache, v8_cache, k_scale, v_scale, 
 
 
 def _norm_args(x, gamma, residual, sum_out):
+    """Checked inputs: (device, sum, (x, residual, gamma, rows, width), address of sum)."""
     if not x.is_cuda:
         _need(x, torch.bfloat16, "x")
     shape, dev = x.shape, _current_device()
@@ -579,32 +594,45 @@ def _norm_args(x, gamma, residual, sum_out):
     at_residual = None if residual is None else _is(residual, torch.bfloat16, shape, dev, "residual")
     if sum_out is None:
         sum_out = torch.empty_like(x)
-    at_sum = _is(sum_out, torch.bfloat16, shape, dev, "sum_out")
-    return shape, dev, sum_out, (at_x, at_residual, at_gamma, x.numel() // width if width else 0, width), at_sum
+        at_sum = sum_out.data_ptr()
+    else:
+        at_sum = _is(sum_out, torch.bfloat16, shape, dev, "sum_out")
+    return dev, sum_out, (at_x, at_residual, at_gamma, x.numel() // width if width else 0, width), at_sum
 
 
 def msa_add_rms_norm(x, gamma, residual=None, eps: float = 1e-6, sum_out=None, y=None):
     """h = x + residual in fp32; returns (bf16(h), bf16(h / sqrt(mean(h^2) + eps) * gamma)) over the last dimension.
     ``sum_out`` may be x or residual (in place), and ``y`` the other one."""
-    shape, dev, sum_out, args, at_sum = _norm_args(x, gamma, residual, sum_out)
+    dev, sum_out, args, at_sum = _norm_args(x, gamma, residual, sum_out)
     if y is None:
         y = torch.empty_like(x)
-    _check(_lib.msa_add_rms_norm(*args, eps, at_sum, _is(y, torch.bfloat16, shape, dev, "y"), _raw_stream(dev)),
-           "msa_add_rms_norm")
+        at_y = y.data_ptr()
+    else:
+        at_y = _is(y, torch.bfloat16, x.shape, dev, "y")
+    status = _lib.msa_add_rms_norm(*args, eps, at_sum, at_y, _raw_stream(dev))
+    if status:
+        raise MsaError(status, "msa_add_rms_norm")
     return sum_out, y
 
 
 def msa_add_rms_norm_fp8(x, gamma, residual=None, eps: float = 1e-6, sum_out=None, y8=None, y_scale=None):
     """msa_add_rms_norm with the norm as E4M3 codes (uint8) and one fp32 scale per row (max |y| / 448, 1 when 0).
     Returns (sum, y8, y_scale)."""
-    shape, dev, sum_out, args, at_sum = _norm_args(x, gamma, residual, sum_out)
+    dev, sum_out, args, at_sum = _norm_args(x, gamma, residual, sum_out)
+    shape = x.shape
     if y8 is None:
         y8 = torch.empty(shape, dtype=torch.uint8, device=x.device)
+        at_y8 = y8.data_ptr()
+    else:
+        at_y8 = _is(y8, torch.uint8, shape, dev, "y8")
     if y_scale is None:
         y_scale = torch.empty(shape[:-1], dtype=torch.float32, device=x.device)
-    _check(_lib.msa_add_rms_norm_fp8(*args, eps, at_sum, _is(y8, torch.uint8, shape, dev, "y8"),
-                                     _is(y_scale, torch.float32, shape[:-1], dev, "y_scale"), _raw_stream(dev)),
-           "msa_add_rms_norm_fp8")
+        at_scale = y_scale.data_ptr()
+    else:
+        at_scale = _is(y_scale, torch.float32, shape[:-1], dev, "y_scale")
+    status = _lib.msa_add_rms_norm_fp8(*args, eps, at_sum, at_y8, at_scale, _raw_stream(dev))
+    if status:
+        raise MsaError(status, "msa_add_rms_norm_fp8")
     return sum_out, y8, y_scale
 
 
