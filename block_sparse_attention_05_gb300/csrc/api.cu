@@ -704,11 +704,14 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   if ((st = device_facts(dev)) != MSA_OK) return st;
   const bool tc = dense_decode_tc(d.G, fp8);
   const int unit = tc ? 128 : kDenseTile;
-  CUtensorMap tq{}, tk, tv;
+  DenseMaps maps{};
   const long long rows = num_pages * 128;
-  if (tc && !map_3d(tq, q, d.S, d.hkv * d.G, d.G, 1)) return MSA_ERR_CUDA;
-  if (fp8 ? (!map_3d_u8(tk, k, rows, d.hkv, kDenseTile) || !map_3d_u8(tv, v, rows, d.hkv, kDenseTile))
-          : (!map_3d(tk, k, rows, d.hkv, 1, unit) || !map_3d(tv, v, rows, d.hkv, 1, unit)))
+  auto map = [&](CUtensorMap& m, const void* cache, int box_rows) {
+    return fp8 ? map_3d_u8(m, cache, rows, d.hkv, box_rows) : map_3d(m, cache, rows, d.hkv, 1, box_rows);
+  };
+  if (!map(maps.k, k, unit) || !map(maps.v, v, unit)) return MSA_ERR_CUDA;
+  if (tc ? !map_3d(maps.q, q, d.S, d.hkv * d.G, d.G, 1)
+         : (!map(maps.k_tail, k, kDenseTail) || !map(maps.v_tail, v, kDenseTail)))
     return MSA_ERR_CUDA;
   DenseDecodeParams p{};
   p.num_seqs = d.S;
@@ -743,7 +746,7 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   p.logits = weight ? at<float>(ws, L.logits) : nullptr;
   p.norm = weight ? at<float2>(ws, L.norm) : nullptr;
   StageScope scope(MSA_STAGE_ATTN, reinterpret_cast<cudaStream_t>(stream));
-  return cuda_status(launch_dense_decode(tq, tk, tv, p, fp8, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_dense_decode(maps, p, fp8, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 msa_status_t check_evict(const msa_problem_t* problem, int32_t budget, int64_t num_pages, PagedDecode& d) {

@@ -242,8 +242,7 @@ __device__ __forceinline__ uint32_t tile_off(int row, int chunk) {
 
 template <int MG, bool FP8, bool LOGITS>
 __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>::kCtasPerSm)
-    dense_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                       DenseDecodeParams p) {
+    dense_split_kernel(const __grid_constant__ DenseMaps maps, DenseDecodeParams p) {
   using C = SplitCfg<MG, FP8>;
   constexpr int KG = C::kKG, NS = C::kNS;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -339,15 +338,28 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
             uint8_t* dk = ring + st * C::kStage;
             uint8_t* dv = dk + C::kHalf;
             if (FP8) scales[st] = make_float2(tk, tv);
-            mbar_arrive_expect_tx(&full[st], C::kStage);
-            auto load = [&](uint8_t* dst, const CUtensorMap* map, int dim) {
-              if (LOGITS) tma_load_3d_policy(dst, map, &full[st], dim, head, r, policy);
-              else tma_load_3d(dst, map, &full[st], dim, head, r);
+            auto load = [&](uint8_t* dst, const CUtensorMap* map, int dim, int row) {
+              if (LOGITS) tma_load_3d_policy(dst, map, &full[st], dim, head, row, policy);
+              else tma_load_3d(dst, map, &full[st], dim, head, row);
             };
-            load(dk, &tm_k, 0);
-            if (!FP8) load(dk + kTile * 128, &tm_k, 64);
-            load(dv, &tm_v, 0);
-            if (!FP8) load(dv + kTile * 128, &tm_v, 64);
+            const int valid = sg.len - u * kTile;
+            if (valid > kTile - kDenseTail) {
+              mbar_arrive_expect_tx(&full[st], C::kStage);
+              load(dk, &maps.k, 0, r);
+              if (!FP8) load(dk + kTile * 128, &maps.k, 64, r);
+              load(dv, &maps.v, 0, r);
+              if (!FP8) load(dv + kTile * 128, &maps.v, 64, r);
+            } else {  // a sequence's last unit: only as many rows as hold keys, 16 at a time
+              const int boxes = (valid + kDenseTail - 1) / kDenseTail;
+              mbar_arrive_expect_tx(&full[st], boxes * kDenseTail * 2 * C::kRowBytes);
+              for (int b = 0; b < boxes; ++b) {
+                const int at = b * kDenseTail * 128, row = r + b * kDenseTail;
+                load(dk + at, &maps.k_tail, 0, row);
+                if (!FP8) load(dk + kTile * 128 + at, &maps.k_tail, 64, row);
+                load(dv + at, &maps.v_tail, 0, row);
+                if (!FP8) load(dv + kTile * 128 + at, &maps.v_tail, 64, row);
+              }
+            }
             ++issued;
           }
         }
@@ -810,8 +822,7 @@ __device__ __noinline__ void rescale_o(uint32_t addr, float f) {
 
 template <bool LOGITS>
 __global__ void __launch_bounds__(TcCfg::kThreads, 1)
-    dense_split_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, DenseDecodeParams p) {
+    dense_split_tc_kernel(const __grid_constant__ DenseMaps maps, DenseDecodeParams p) {
   using C = TcCfg;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;                                     // stages of K and V: two 64-dim halves of 128 rows each
@@ -880,7 +891,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
   Segment sg;
   if (warp == 0 || warp == 3) {
     // ------------------------------------------------------------ producers: K, V
-    const CUtensorMap* map = warp == 0 ? &tm_k : &tm_v;
+    const CUtensorMap* map = warp == 0 ? &maps.k : &maps.v;
     uint64_t* full = warp == 0 ? sm.k_full : sm.v_full;
     uint8_t* const dst0 = ring + (warp == 0 ? 0 : C::kHalf);
     uint32_t fills = 0, issued = 0, bad = 0;
@@ -944,8 +955,8 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
           break;
         }
         mbar_arrive_expect_tx(&sm.q_full, G * 256);
-        tma_load_3d(q_buf, &tm_q, &sm.q_full, 0, head * G, sg.seq);
-        tma_load_3d(q_buf + 16384, &tm_q, &sm.q_full, 64, head * G, sg.seq);
+        tma_load_3d(q_buf, &maps.q, &sm.q_full, 0, head * G, sg.seq);
+        tma_load_3d(q_buf + 16384, &maps.q, &sm.q_full, 64, head * G, sg.seq);
         ++segs;
       }
       if (segs > 0) mbar_wait(&sm.q_full, (segs - 1) & 1, nullptr);
@@ -1395,35 +1406,32 @@ __global__ void __launch_bounds__(kWeightThreads, 2) dense_weight_kernel(DenseDe
   }
 }
 
-cudaError_t launch_split_tc(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                            const DenseDecodeParams& p, cudaStream_t stream) {
+cudaError_t launch_split_tc(const DenseMaps& maps, const DenseDecodeParams& p, cudaStream_t stream) {
   auto* fn = p.logits ? dense_split_tc_kernel<true> : dense_split_tc_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTcSmemBytes));
   if (e != cudaSuccess) return e;
-  fn<<<p.groups * p.hkv, TcCfg::kThreads, kTcSmemBytes, stream>>>(tq, tk, tv, p);
+  fn<<<p.groups * p.hkv, TcCfg::kThreads, kTcSmemBytes, stream>>>(maps, p);
   note_launches(1);
   return cudaGetLastError();
 }
 
 template <int MG, bool FP8>
-cudaError_t launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p,
-                         cudaStream_t stream) {
+cudaError_t launch_split(const DenseMaps& maps, const DenseDecodeParams& p, cudaStream_t stream) {
   using C = SplitCfg<MG, FP8>;
   auto* fn = p.logits ? dense_split_kernel<MG, FP8, true> : dense_split_kernel<MG, FP8, false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
-  fn<<<p.groups * p.hkv, C::kThreads, C::kSmem, stream>>>(tk, tv, p);
+  fn<<<p.groups * p.hkv, C::kThreads, C::kSmem, stream>>>(maps, p);
   note_launches(1);
   return cudaGetLastError();
 }
 
 template <bool FP8>
-cudaError_t launch_split_for(const CUtensorMap& tk, const CUtensorMap& tv, const DenseDecodeParams& p,
-                             cudaStream_t stream) {
-  if (p.group <= 16) return launch_split<1, FP8>(tk, tv, p, stream);
-  if (p.group <= 32) return launch_split<2, FP8>(tk, tv, p, stream);
-  if (p.group <= 64) return launch_split<4, FP8>(tk, tv, p, stream);
-  return launch_split<8, FP8>(tk, tv, p, stream);
+cudaError_t launch_split_for(const DenseMaps& maps, const DenseDecodeParams& p, cudaStream_t stream) {
+  if (p.group <= 16) return launch_split<1, FP8>(maps, p, stream);
+  if (p.group <= 32) return launch_split<2, FP8>(maps, p, stream);
+  if (p.group <= 64) return launch_split<4, FP8>(maps, p, stream);
+  return launch_split<8, FP8>(maps, p, stream);
 }
 
 }  // namespace
@@ -1432,11 +1440,10 @@ int dense_decode_ctas_per_sm(int group) { return group <= 16 ? 2 : 1; }
 
 bool dense_decode_tc(int group, bool fp8) { return !fp8 && group > 32; }
 
-cudaError_t launch_dense_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const DenseDecodeParams& p, bool fp8, cudaStream_t stream) {
-  cudaError_t e = dense_decode_tc(p.group, fp8) ? launch_split_tc(tq, tk, tv, p, stream)
-                  : fp8                         ? launch_split_for<true>(tk, tv, p, stream)
-                                                : launch_split_for<false>(tk, tv, p, stream);
+cudaError_t launch_dense_decode(const DenseMaps& maps, const DenseDecodeParams& p, bool fp8, cudaStream_t stream) {
+  cudaError_t e = dense_decode_tc(p.group, fp8) ? launch_split_tc(maps, p, stream)
+                  : fp8                         ? launch_split_for<true>(maps, p, stream)
+                                                : launch_split_for<false>(maps, p, stream);
   if (e != cudaSuccess) return e;
   const int entries = p.by_seq ? p.num_seqs : p.groups;
   int wpr = 1;  // warps to a row: one for every four partials that a sequence has on average, up to eight

@@ -307,10 +307,15 @@ struct DenseDecodeParams {
   float2* norm;                 // with weight: [num_seqs, hkv * group] (maximum, 1 / sum); else null
 };
 int dense_decode_ctas_per_sm(int group);
-// Whether the split runs on tcgen05: units of 128 keys (the boxes of tk and tv), Q through tq (boxes of the group's heads).
+// Whether the split runs on tcgen05 (units of 128 keys).
 bool dense_decode_tc(int group, bool fp8);
-cudaError_t launch_dense_decode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const DenseDecodeParams& p, bool fp8, cudaStream_t stream);
+constexpr int kDenseTail = 16;  // rows of the boxes that a sequence's last unit is loaded by
+struct DenseMaps {
+  CUtensorMap k, v;            // boxes of a unit's rows of one head (64 dims in bf16, 128 codes in fp8)
+  CUtensorMap k_tail, v_tail;  // boxes of kDenseTail rows (not on tcgen05)
+  CUtensorMap q;               // on tcgen05: boxes of 64 dims of a group's heads
+};
+cudaError_t launch_dense_decode(const DenseMaps& maps, const DenseDecodeParams& p, bool fp8, cudaStream_t stream);
 
 // ---------------------------------------------------------------- eviction
 struct EvictParams {
