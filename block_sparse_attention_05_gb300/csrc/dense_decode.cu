@@ -117,19 +117,44 @@ struct RunSmem {
 __device__ __forceinline__ int units_of(int len, int shift) { return (len + (1 << shift) - 1) >> shift; }
 
 // Cuts the batch's units and finds run g of `groups`.  Every thread of the CTA
-// calls it; returns false (for every thread) when cu_seqlens contradict the host sizes.
+// calls it; returns false (for every thread) when cu_seqlens contradict the host
+// sizes.  The CTA has passed a barrier when it returns.
 __device__ bool find_run(const DenseDecodeParams& p, int g, RunSmem& sm, Run& r) {
   const int32_t* cu = p.cu_k;
-  const int num_seqs = p.num_seqs, max_k = p.max_k, total_k = p.total_k, groups = p.groups, shift = p.unit_shift;
+  const int num_seqs = p.num_seqs, groups = p.groups, shift = p.unit_shift;
   const int T = blockDim.x, t = threadIdx.x, lane = t & 31, warp = t >> 5, nw = T >> 5;
+  if (num_seqs <= 32) {  // each warp for itself, a sequence per lane
+    const int start = lane < num_seqs ? cu[lane] : 0, stop = lane < num_seqs ? cu[lane + 1] : 0;
+    const int len = stop - start;
+    const bool bad = start < 0 || stop < start || len > p.max_k || (lane == 0 && start != 0) ||
+                     (lane == num_seqs - 1 && stop != p.total_k);
+    const int n = units_of(len, shift);
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    const bool any_bad = __any_sync(0xFFFFFFFFu, bad);
+    r.total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+    r.runs = min(groups, static_cast<int>(r.total));
+    r.lo = g < r.runs ? r.total * g / r.runs : r.total;
+    r.hi = g < r.runs ? r.total * (g + 1) / r.runs : r.total;
+    const uint32_t holds = __ballot_sync(0xFFFFFFFFu, incl > r.lo);  // the first such lane's sequence holds unit lo
+    r.seq = holds ? __ffs(holds) - 1 : 0;
+    r.off = static_cast<int>(r.lo - __shfl_sync(0xFFFFFFFFu, incl - n, r.seq));
+    __syncthreads();
+    return !any_bad;
+  }
   const int per = (num_seqs + T - 1) / T;
   const int s0 = min(num_seqs, t * per), s1 = min(num_seqs, s0 + per);
   int sum = 0;
-  bool bad = t == 0 && (cu[0] != 0 || cu[num_seqs] != total_k);
+  bool bad = false;
   int prev = s0 < s1 ? cu[s0] : 0;
+  if (t == 0) bad = prev != 0;
   for (int s = s0; s < s1; ++s) {
     const int next = cu[s + 1], len = next - prev;
-    bad |= prev < 0 || next < prev || len > max_k;
+    bad |= prev < 0 || next < prev || len > p.max_k || (s == num_seqs - 1 && next != p.total_k);
     sum += units_of(len, shift);
     prev = next;
   }
@@ -167,6 +192,19 @@ __device__ bool find_run(const DenseDecodeParams& p, int g, RunSmem& sm, Run& r)
   r.seq = sm.seq;
   r.off = sm.off;
   return true;
+}
+
+// Writes the empty sequences of a run's share (o = 0, lse = -inf): sequences g, g + groups, ..
+__device__ __forceinline__ void write_empty(const DenseDecodeParams& p, int g, int head, int t, int threads) {
+  const int G = p.group;
+  for (int s = g; s < p.num_seqs; s += p.groups) {
+    if (p.cu_k[s + 1] != p.cu_k[s]) continue;
+    if (p.by_seq && t == 0) p.meta[s * p.hkv + head].x = -1;
+    const long long row0 = (static_cast<long long>(s) * p.hkv + head) * G;
+    for (int i = t; i < G * 16; i += threads)
+      reinterpret_cast<uint4*>(p.o + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = t; i < G; i += threads) p.lse[row0 + i] = -INFINITY;
+  }
 }
 
 // Walks a run's segments: the parts of its sequences that it covers.
@@ -267,6 +305,8 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     *abort_flag = 0;
     *err = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
   }
   Run run;
   const bool fine = find_run(p, g, run_sm, run);  // synchronises
@@ -277,16 +317,6 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     }
     if (p.by_seq && g < p.num_seqs && threadIdx.x == 0) p.meta[g * p.hkv + head].x = -1;  // num_seqs <= groups
     return;
-  }
-
-  // empty sequences: o = 0, lse = -inf
-  for (int s = g; s < p.num_seqs; s += p.groups) {
-    if (p.cu_k[s + 1] != p.cu_k[s]) continue;
-    if (p.by_seq && threadIdx.x == 0) p.meta[s * p.hkv + head].x = -1;
-    const long long row0 = static_cast<long long>(s) * p.hkv * G + static_cast<long long>(head) * G;
-    for (int i = threadIdx.x; i < G * 16; i += C::kThreads)
-      reinterpret_cast<uint4*>(p.o + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = threadIdx.x; i < G; i += C::kThreads) p.lse[row0 + i] = -INFINITY;
   }
 
   Walker walk(p, run);
@@ -373,6 +403,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     // ------------------------------------------------------------ compute
     const int mg = warp / KG, kg = warp % KG;
     const int t4 = lane & 3, r0 = mg * 16 + (lane >> 2), r1 = r0 + 8;  // this thread's two head rows
+    write_empty(p, g, head, threadIdx.x, 32 * C::kWarps);
     uint32_t fills = 0;
     bool ok = true;
     const int team = kg / C::kTeam;
@@ -848,6 +879,9 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
     sm.abort_flag = 0;
     sm.err = 0;
     fence_mbar_init();
+    tma_prefetch_desc(&maps.k);
+    tma_prefetch_desc(&maps.v);
+    tma_prefetch_desc(&maps.q);
   }
   // queries of the rows past the group: zero once, the loads write the group's rows only
   for (int i = threadIdx.x; i < (128 - G) * 16; i += C::kThreads)
@@ -876,16 +910,6 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
     *abort_flag = 1;
     atomicOr(&sm.err, kFlagTimeout);
   };
-
-  // empty sequences: o = 0, lse = -inf
-  for (int s = g; s < p.num_seqs; s += p.groups) {
-    if (p.cu_k[s + 1] != p.cu_k[s]) continue;
-    if (p.by_seq && threadIdx.x == 0) p.meta[s * p.hkv + head].x = -1;
-    const long long row0 = (static_cast<long long>(s) * p.hkv + head) * G;
-    for (int i = threadIdx.x; i < G * 16; i += C::kThreads)
-      reinterpret_cast<uint4*>(p.o + row0 * kHeadDim)[i] = make_uint4(0, 0, 0, 0);
-    for (int i = threadIdx.x; i < G; i += C::kThreads) p.lse[row0 + i] = -INFINITY;
-  }
 
   Walker walk(p, run);
   Segment sg;
@@ -1040,6 +1064,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
     uint32_t f = 0, segs = 0;
     bool ok = true;
     int4 crossing = make_int4(-1, 0, 0, 0);  // the sequence that begins in this run and goes on
+    write_empty(p, g, head, threadIdx.x - 128, 256);
     auto warp_arrive = [&](uint64_t* bar) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
