@@ -71,14 +71,12 @@ __device__ __forceinline__ uint64_t global_ns() {
 // the stream drains; griddep_wait() returns once that kernel has completed and
 // its writes are visible (immediately when the kernel was launched without the
 // attribute).  Every such kernel calls it before touching memory the previous
-// kernel writes or reads.  The sparse path triggers no dependents early: on its
+// kernel writes or reads.  No kernel here triggers its dependents early: on the
 // decode chain an early trigger (dependent CTAs resident while the index scan
 // streams) measured 0.375 ms per decode_1m step against 0.343 without it and
 // 0.352 without programmatic launches at all.
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the kernel behind this one on the stream be set up once every CTA has called it (or left).
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------
 // mbarrier

@@ -1454,9 +1454,11 @@ cudaError_t launch_split(const DenseMaps& maps, const DenseDecodeParams& p, cuda
 template <bool FP8>
 cudaError_t launch_split_for(const DenseMaps& maps, const DenseDecodeParams& p, cudaStream_t stream) {
   if (p.group <= 16) return launch_split<1, FP8>(maps, p, stream);
-  if (p.group <= 32) return launch_split<2, FP8>(maps, p, stream);
-  if (p.group <= 64) return launch_split<4, FP8>(maps, p, stream);
-  return launch_split<8, FP8>(maps, p, stream);
+  if constexpr (FP8) {
+    if (p.group > 64) return launch_split<8, FP8>(maps, p, stream);
+    if (p.group > 32) return launch_split<4, FP8>(maps, p, stream);
+  }
+  return launch_split<2, FP8>(maps, p, stream);
 }
 
 }  // namespace
