@@ -478,19 +478,26 @@ __device__ __forceinline__ void fill_table(uint8_t (*table)[128], const float* p
   }
 }
 
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+
 __device__ __forceinline__ void store_codes(const EvictParams& p, void* cache, long long row0, int rows, int h,
                                             const uint8_t (*table)[128], const uint8_t* which, const Codes& x) {
+  const uint32_t tables = smem_u32(table);  // each on a 128-byte boundary: an entry's address is the two or'ed
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int at = i * kGatherThreads + threadIdx.x, r = at >> 3;
     if (r >= rows) continue;
-    const uint8_t* tab = table[which[r]];
+    const uint32_t tab = tables + which[r] * 128u;
     const uint32_t w[4] = {x.c[i].x, x.c[i].y, x.c[i].z, x.c[i].w};
     uint32_t q[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint32_t a = tab[w[j] & 0x7Fu], b = tab[(w[j] >> 8) & 0x7Fu], c = tab[(w[j] >> 16) & 0x7Fu],
-                     d = tab[(w[j] >> 24) & 0x7Fu];
+      const uint32_t a = lds_u8((w[j] & 0x7Fu) | tab), b = lds_u8(((w[j] >> 8) & 0x7Fu) | tab),
+                     c = lds_u8(((w[j] >> 16) & 0x7Fu) | tab), d = lds_u8(((w[j] >> 24) & 0x7Fu) | tab);
       q[j] = __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410) | (w[j] & 0x80808080u);
     }
     static_cast<uint4*>(cache)[((row0 + r) * p.hkv + h) * 8 + (at & 7)] = make_uint4(q[0], q[1], q[2], q[3]);
@@ -505,7 +512,7 @@ __global__ void __launch_bounds__(kGatherThreads, 4) evict_gather_fp8_kernel(Evi
   __shared__ float page_scale[2][kBlock];       // K and V scale of each old page
   __shared__ unsigned long long keys[2][kGatherThreads / 32];
   __shared__ float2 inv[2];                     // 448 / max as two floats
-  __shared__ uint8_t table[2][kBlock][128];
+  __shared__ __align__(128) uint8_t table[2][kBlock][128];
   griddep_wait();
   const NewPage x = new_page(p, blockIdx.x);
   if (x.rows <= 0) return;
