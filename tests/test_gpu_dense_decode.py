@@ -117,6 +117,17 @@ def test_long(msa, hq, hkv, fp8):
     Batch(msa, [60001, 17, 9000], hq, hkv, fp8, True, seed=3).check(msa)
 
 
+@pytest.mark.parametrize("lens,hq,hkv", [
+    ([(i * 97) % 800 for i in range(700)], 10, 2),      # many sequences, the last units claimed by who comes first
+    ([1, 200000, 0, 70000, 3], 16, 1),                  # long ones, claimed pieces inside a sequence
+    ([(i * 13) % 61 for i in range(5000)], 3, 1),       # more sequences than a warp looks through
+    ([90000] + [(i * 31) % 50 for i in range(4500)], 6, 3),
+])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_large_batches(msa, lens, hq, hkv, fp8):
+    Batch(msa, lens, hq, hkv, fp8, True, seed=len(lens)).check(msa)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_peaked_and_flat_logits(msa, fp8):
     Batch(msa, [3000, 129], 16, 1, fp8, True, seed=4, q_gain=60.0).check(msa)     # one key takes nearly all
