@@ -308,6 +308,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
   }
+  griddep_wait();  // set up while the kernel before it ends
   Run run;
   const bool fine = find_run(p, g, run_sm, run);  // synchronises
   if (!fine) {
@@ -887,6 +888,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
   for (int i = threadIdx.x; i < (128 - G) * 16; i += C::kThreads)
     reinterpret_cast<uint4*>(q_buf + (i & 8) * 2048)[G * 8 + (i >> 4) * 8 + (i & 7)] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
+  griddep_wait();  // set up while the kernel before it ends
   Run run;
   const bool fine = find_run(p, g, sm.run, run);  // synchronises
   if (!fine) {
@@ -1435,9 +1437,9 @@ cudaError_t launch_split_tc(const DenseMaps& maps, const DenseDecodeParams& p, c
   auto* fn = p.logits ? dense_split_tc_kernel<true> : dense_split_tc_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTcSmemBytes));
   if (e != cudaSuccess) return e;
-  fn<<<p.groups * p.hkv, TcCfg::kThreads, kTcSmemBytes, stream>>>(maps, p);
-  note_launches(1);
-  return cudaGetLastError();
+  e = launch_pdl(fn, dim3(p.groups * p.hkv), dim3(TcCfg::kThreads), kTcSmemBytes, stream, maps, p);
+  if (e == cudaSuccess) note_launches(1);
+  return e;
 }
 
 template <int MG, bool FP8>
@@ -1446,9 +1448,9 @@ cudaError_t launch_split(const DenseMaps& maps, const DenseDecodeParams& p, cuda
   auto* fn = p.logits ? dense_split_kernel<MG, FP8, true> : dense_split_kernel<MG, FP8, false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
-  fn<<<p.groups * p.hkv, C::kThreads, C::kSmem, stream>>>(maps, p);
-  note_launches(1);
-  return cudaGetLastError();
+  e = launch_pdl(fn, dim3(p.groups * p.hkv), dim3(C::kThreads), C::kSmem, stream, maps, p);
+  if (e == cudaSuccess) note_launches(1);
+  return e;
 }
 
 template <bool FP8>

@@ -67,6 +67,7 @@ constexpr int kWarpThreads = 256;
 template <int CH, bool FP8, bool ODD, bool WARP>
 __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) add_rms_norm_kernel(NormParams p, int lanes) {
   __shared__ float red[2][32];
+  griddep_wait();
   const int T = WARP ? lanes : blockDim.x, t = WARP ? threadIdx.x & (lanes - 1) : threadIdx.x;
   const long long row = WARP ? (blockIdx.x * static_cast<long long>(kWarpThreads) + threadIdx.x) / lanes : blockIdx.x;
   const long long start = row * p.width;
@@ -207,9 +208,10 @@ cudaError_t launch_norm(const NormParams& p, int threads, cudaStream_t stream) {
   auto* fn = p.y8 ? (odd ? add_rms_norm_kernel<CH, true, true, WARP> : add_rms_norm_kernel<CH, true, false, WARP>)
                   : (odd ? add_rms_norm_kernel<CH, false, true, WARP> : add_rms_norm_kernel<CH, false, false, WARP>);
   const long long ctas = WARP ? (p.rows * threads + kWarpThreads - 1) / kWarpThreads : p.rows;
-  fn<<<static_cast<unsigned>(ctas), WARP ? kWarpThreads : threads, 0, stream>>>(p, threads);
-  note_launches(1);
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(fn, dim3(static_cast<unsigned>(ctas)), dim3(WARP ? kWarpThreads : threads), 0, stream,
+                                   p, threads);
+  if (e == cudaSuccess) note_launches(1);
+  return e;
 }
 
 }  // namespace

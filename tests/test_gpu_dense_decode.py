@@ -260,6 +260,34 @@ def test_graph_replays_follow_the_inputs(msa, fp8):
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1]) and torch.equal(got[2], b.weight)
 
 
+def test_graph_behind_copies_and_memsets(msa):
+    """The call captured behind a memset and a copy of its own inputs, and behind itself."""
+    b = Batch(msa, [2000, 129], 64, 4, False, True, seed=17)
+    q, total = b.q.clone(), torch.empty_like(b.q)
+    ws = b.ws(msa)
+    o, lse = torch.empty_like(b.q), torch.empty(2, 64, dtype=torch.float32, device="cuda")
+    gamma = torch.ones(DIM, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        b.weight.zero_()
+        b.q.copy_(q)
+        b.call(msa, o=o, lse=lse, ws=ws)
+        b.call(msa, o=o, lse=lse, ws=ws)
+        msa.msa_add_rms_norm(o, gamma, residual=b.q, sum_out=total, y=o)
+
+    step()
+    torch.cuda.synchronize()
+    want = o.clone(), lse.clone(), b.weight.clone(), total.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for _ in range(3):
+        for t in (o, lse, b.weight, total):
+            t.fill_(7)
+        g.replay()
+        assert all(torch.equal(x, y) for x, y in zip(want, (o, lse, b.weight, total)))
+
+
 def test_lengths_that_contradict_the_sizes_skip_the_call(msa):
     b = Batch(msa, [300, 200], 16, 1, False, True, seed=14)
     good = b.prob.cu_k.clone()
