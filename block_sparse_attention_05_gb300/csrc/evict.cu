@@ -6,9 +6,10 @@
 // everything).  The kept slots, in their order, become slots 0 .. min(n, b) - 1
 // of the sequence's pages in a second block table.
 //
-// Two kernels: the selection reads each weight a few times from L2 (4 bytes a
-// cached key), the gather reads and writes each kept key's K and V rows once
-// (512 bytes in bf16) and bounds the call.
+// Three kernels, set up under one another's ends: a clear of the workspace's
+// header and page marks, the selection, which reads each weight once (4 bytes a
+// cached key), and the gather, which reads and writes each kept key's K and V
+// rows once (512 bytes in bf16) and bounds the call.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -87,6 +88,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     if (cs > 1) cluster_sync(); else __syncthreads();
   };
 
+  griddep_wait();
   // every CTA checks all lengths: a call whose lengths are wrong is skipped as a whole
   bool bad = t == 0 && (p.cu_k[0] != 0 || p.cu_k[p.num_seqs] != p.total_k);
   for (int i = t; i < p.num_seqs; i += kSelThreads) {
@@ -298,6 +300,15 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     base += total & 0xFFFFu;
     ties += total >> 16;
   }
+}
+
+// Zeroes the header and the marks behind it: a kernel in place of a memset, so that the three launches can be set up
+// under one another's ends.
+__global__ void __launch_bounds__(256) evict_clear_kernel(EvictParams p) {
+  griddep_wait();
+  uint4* to = reinterpret_cast<uint4*>(p.hdr);
+  const size_t n = p.clear_bytes / 16, step = static_cast<size_t>(gridDim.x) * 256;
+  for (size_t i = blockIdx.x * static_cast<size_t>(256) + threadIdx.x; i < n; i += step) to[i] = make_uint4(0, 0, 0, 0);
 }
 
 // Checks one entry of the new table: inside the cache, not a page of the batch's own table and named once.
@@ -574,8 +585,9 @@ __global__ void __launch_bounds__(kGatherThreads, 4) evict_gather_fp8_kernel(Evi
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, bool fp8, int sms, cudaStream_t stream) {
-  // the header's status and the marks behind it start at zero
-  cudaError_t e = cudaMemsetAsync(p.hdr, 0, p.clear_bytes, stream);
+  const size_t clear = (p.clear_bytes / 16 + 1023) / 1024;  // CTAs, four pieces a thread
+  cudaError_t e = launch_pdl(evict_clear_kernel, dim3(static_cast<unsigned>(clear < 4096 ? clear : 4096)), dim3(256), 0,
+                             stream, p);
   if (e != cudaSuccess) return e;
   // CTAs per (sequence, head): at most eight (a portable cluster), none with a share under 8,192 slots (the cluster's
   // barriers and reads cost about 4 us), and only as many as run at once: a cluster's CTAs, one to an SM, share one
@@ -596,11 +608,13 @@ cudaError_t launch_evict(const EvictParams& p, bool fp8, int sms, cudaStream_t s
     e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelKeys * 4);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {static_cast<unsigned>(cs), 1, 1};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(cs), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
   e = cudaLaunchKernelEx(&cfg, fn, p, cs);
   if (e != cudaSuccess) return e;
   note_launches(2);
