@@ -626,7 +626,7 @@ msa_status_t derive_paged(const msa_problem_t* p, PagedDecode& d) {
   if (p->total_k < 0 || p->max_seqlen_k < 0 || p->max_seqlen_k > p->total_k) return MSA_ERR_INVALID_ARG;
   if (p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->num_q_heads % p->num_kv_heads) return MSA_ERR_INVALID_ARG;
   if (p->head_dim <= 0 || p->block_size <= 0) return MSA_ERR_INVALID_ARG;
-  if (!(p->softmax_scale == p->softmax_scale) || std::isinf(p->softmax_scale)) return MSA_ERR_INVALID_ARG;
+  if (!(p->softmax_scale < 1e30f)) return MSA_ERR_INVALID_ARG;  // NaN, inf, or inf in log2 units
   if (p->head_dim != 128 || p->block_size != 128) return MSA_ERR_UNSUPPORTED;
   d.S = p->num_seqs;
   d.N = p->total_k;

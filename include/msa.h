@@ -435,7 +435,7 @@ msa_status_t msa_forward_decode_paged_fp8_index(const msa_problem_t *problem, co
  *               -inf).  index_dim and topk are not looked at.  head_dim =
  *               block_size = 128; any group size num_q_heads / num_kv_heads
  *               from 1 to 128, num_kv_heads <= 1024, num_seqs <= 2^20,
- *               max_seqlen_k <= 2^30.
+ *               max_seqlen_k <= 2^30, softmax_scale < 1e30.
  *   k_cache, v_cache, block_table, max_blocks_per_seq, num_pages
  *               as for msa_forward_decode_paged; what the rows past a
  *               sequence's last key hold does not matter.  Sequences may share

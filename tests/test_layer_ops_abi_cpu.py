@@ -29,7 +29,8 @@ BAD_PROBLEMS = [
     (dict(num_seqs=0, total_q=0), -1), (dict(cu_seqlens_k=None), -1), (dict(max_seqlen_q=2, total_q=8), -1),
     (dict(total_q=5), -1), (dict(total_k=-1), -1), (dict(max_seqlen_k=2000), -1), (dict(max_seqlen_k=-1), -1),
     (dict(num_q_heads=63), -1), (dict(num_kv_heads=0), -1), (dict(num_q_heads=0), -1),
-    (dict(softmax_scale=math.nan), -1), (dict(softmax_scale=math.inf), -1), (dict(head_dim=64), -2),
+    (dict(softmax_scale=math.nan), -1), (dict(softmax_scale=math.inf), -1), (dict(softmax_scale=3e38), -1),
+    (dict(head_dim=64), -2), (dict(max_seqlen_k=(1 << 30) + 1, total_k=(1 << 30) + 1), -2),
     (dict(block_size=64), -2), (dict(num_q_heads=129, num_kv_heads=1), -2),
     (dict(num_q_heads=1025, num_kv_heads=1025), -2), (dict(num_seqs=(1 << 20) + 1, total_q=(1 << 20) + 1), -2),
 ]
