@@ -702,7 +702,7 @@ msa_status_t dense_decode(const msa_problem_t* problem, const void* q, const voi
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
   DeviceFacts dev;
   if ((st = device_facts(dev)) != MSA_OK) return st;
-  const bool tc = dense_decode_tc(d.G, fp8);
+  const bool tc = dense_decode_tc(d.G);
   const int unit = tc ? 128 : kDenseTile;
   DenseMaps maps{};
   const long long rows = num_pages * 128;

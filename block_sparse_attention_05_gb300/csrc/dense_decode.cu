@@ -254,8 +254,9 @@ struct Walker {
 // an older phase of its barrier for the next one.
 template <int MG, bool FP8>
 struct SplitCfg {
-  static constexpr int kKG = MG <= 2 ? 4 : 8 / MG;
-  static constexpr int kNS = MG == 1 ? (FP8 ? 2 : 1) : MG == 2 ? 2 : 4;
+  static_assert(MG == 1 || MG == 2, "more heads: the tcgen05 kernel");
+  static constexpr int kKG = 4;
+  static constexpr int kNS = MG == 1 && !FP8 ? 1 : 2;
   static constexpr int kTeam = kTile / 16 / kNS;   // warps of a head tile that share a unit
   static constexpr int kTeams = kKG / kTeam;
   static_assert(kTeam * kTeams == kKG, "every warp belongs to a team");
@@ -813,30 +814,42 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
 // one thread that does; here a unit has two commits, S done (K's stage is free,
 // its warpgroup may go on) and P V done (V's stage and S's columns are free).
 //
+// E4M3 pages: the codes land in a ring of their own (two stages) and each softmax
+// warpgroup widens its units' while it waits for its MMAs, K to bf16 (the queries'
+// type) and V to fp16, both exact; the weights times the page's V scale are one
+// fp16 value, so P V is one product.  Once widened a code meets all heads: 42 us
+// for 80 MB of K and V where the small groups' kernel, which widens them for every
+// 16 heads, took 87 us at 128 heads and 51 us at 64.
+//
 // Warps: 0 feeds K and 3 feeds V (TMA), 1 issues the MMAs, 2 owns TMEM and feeds
 // Q, 4..7 and 8..11 softmax and output.
+template <bool FP8>
 struct TcCfg {
   static constexpr int kThreads = 384;
   static constexpr int kKeys = 128;
-  static constexpr int kStages = 3;
+  static constexpr int kStages = FP8 ? 2 : 3;
+  static constexpr int kCodes = kKeys * 128;  // fp8: K or V of a stage as it lands
   static constexpr int kHalf = kKeys * 256;  // K or V of a stage
   static constexpr uint32_t kColS = 0, kColO = 256;
 };
 struct TcSmem {
-  uint64_t k_full[TcCfg::kStages], v_full[TcCfg::kStages];
+  uint64_t k_full[3], v_full[3];
+  uint64_t k_empty[2], v_empty[2], k_ready[2], v_ready[2];  // fp8: codes read, values written
   // S done by unit % 6: a stage's and a warpgroup's units each keep to barriers of their own, so every waiter sees
   // every phase of the barriers it uses (one that skipped a phase could take an older one for its own)
   uint64_t s_done[6];
-  uint64_t pv_done[TcCfg::kStages];
+  uint64_t pv_done[3];
   uint64_t p_full[2];
   uint64_t q_full, q_empty, ml_full, o_free, mma_done;
   float2 ml[2][128];  // (m, l) of each warpgroup's rows; m = -inf: no unit of the segment was its own
+  short d[2][128];    // fp8: exponent of O
+  float scale[2][2];  // fp8: a stage's scales of K and V
   RunSmem run;
   uint32_t tmem_base;
   int abort_flag;
   uint32_t err;
 };
-constexpr size_t kTcSmemBytes = (TcCfg::kStages * 2 + 1) * TcCfg::kHalf + sizeof(TcSmem);
+constexpr size_t kTcSmemBytes = 7 * 32768 + sizeof(TcSmem);  // three stages and Q; or two, two of codes and Q
 static_assert(kTcSmemBytes <= 227 * 1024, "one CTA's shared memory");
 
 // Multiplies this thread's row of O (128 TMEM columns) by f.  Rare; out of line to leave the softmax its registers.
@@ -883,13 +896,45 @@ __device__ __forceinline__ void tmem_ld_wait_regs16(uint32_t (&r)[16]) {
                : "memory");
 }
 
-template <bool LOGITS>
-__global__ void __launch_bounds__(TcCfg::kThreads, 1)
+// 16-byte pieces of a unit's codes (rows of 128 bytes, TMA's 128-byte swizzle) to 16-bit values in the layout in which
+// TMA lands bf16 rows: K as bf16 (the queries' type), V as fp16 (the weights' type), both exact.  128 threads; eight
+// lanes read a row, and those of its second half write their pieces in the other order, so that eight lanes' stores
+// meet all banks.  Rows from `valid` on become zeros (V: 0 * NaN is NaN).
+template <bool BF16>
+__device__ __forceinline__ void widen(const uint8_t* codes, uint8_t* to, int thread, int valid) {
+  const int chunk = thread & 7, half = chunk >> 2;
+  const uint32_t flip = half;
+#pragma unroll 2
+  for (int row = thread >> 3; row < 128; row += 16) {
+    const int x = row & 7;
+    uint4 in = *reinterpret_cast<const uint4*>(codes + row * 128 + ((chunk ^ x) << 4));
+    if (row >= valid) in = make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {in.x, in.y, in.z, in.w};
+    uint32_t out[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      out[j] = e4m3x2_to_f16x2(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
+      if (BF16) {  // four significant bits: the upper half of the value in fp32
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&out[j]));
+        out[j] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+      }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(to + half * 16384 + row * 128);
+    const uint4 a = make_uint4(out[0], out[1], out[2], out[3]), b = make_uint4(out[4], out[5], out[6], out[7]);
+    const uint32_t at = 2 * (chunk & 3);
+    dst[(at + flip) ^ x] = flip ? b : a;
+    dst[(at + 1 - flip) ^ x] = flip ? a : b;
+  }
+}
+
+template <bool FP8, bool LOGITS>
+__global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
     dense_split_tc_kernel(const __grid_constant__ DenseMaps maps, DenseDecodeParams p) {
-  using C = TcCfg;
+  using C = TcCfg<FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* ring = smem;                                     // stages of K and V: two 64-dim halves of 128 rows each
-  uint8_t* q_buf = smem + C::kStages * 2 * C::kHalf;        // the same layout
+  uint8_t* codes = smem + C::kStages * 2 * C::kHalf;        // fp8: stages of K and V as they land
+  uint8_t* q_buf = smem + 6 * 32768;                        // as the ring
   TcSmem& sm = *reinterpret_cast<TcSmem*>(q_buf + C::kHalf);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int head = blockIdx.x % p.hkv, g = blockIdx.x / p.hkv;
@@ -902,7 +947,13 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
       mbar_init(&sm.pv_done[i], 1);
     }
     for (int i = 0; i < 6; ++i) mbar_init(&sm.s_done[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sm.p_full[i], 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.p_full[i], 4);
+      mbar_init(&sm.k_empty[i], 4);
+      mbar_init(&sm.v_empty[i], 4);
+      mbar_init(&sm.k_ready[i], 4);
+      mbar_init(&sm.v_ready[i], 4);
+    }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 1);
     mbar_init(&sm.ml_full, 8);
@@ -950,13 +1001,17 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
     // ------------------------------------------------------------ producers: K, V
     const CUtensorMap* map = warp == 0 ? &maps.k : &maps.v;
     uint64_t* full = warp == 0 ? sm.k_full : sm.v_full;
-    uint8_t* const dst0 = ring + (warp == 0 ? 0 : C::kHalf);
+    constexpr int kTileBytes = FP8 ? C::kCodes : C::kHalf;
+    uint8_t* const dst0 = (FP8 ? codes : ring) + (warp == 0 ? 0 : kTileBytes);
+    uint64_t* const empty = warp == 0 ? sm.k_empty : sm.v_empty;
+    const float* const scale = warp == 0 ? p.k_scale : p.v_scale;
     uint32_t fills = 0, issued = 0, bad = 0;
     const uint64_t policy = l2_evict_first();  // with logits: K and V pass through, the logits are to stay in L2
     bool stopped = false;
     while (!stopped && walk.next(sg)) {
       const int32_t* table = p.block_table + static_cast<long long>(sg.seq) * p.bt_stride + sg.off;
       int row = 0;
+      float s = 1.0f;
       for (int i = 0; i < sg.count; ++i) {
         if ((i & 31) == 0) {  // the next 32 pages' rows, one per lane
           row = 0;
@@ -967,25 +1022,29 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
               row = static_cast<int>(p.n_pages) * kBlock;  // past the cache: TMA reads zeros
             } else {
               row = e * kBlock;
+              if (FP8) s = scale[static_cast<long long>(e) * p.hkv + head];
             }
           }
         }
         const int r = __shfl_sync(0xFFFFFFFFu, row, i & 31);
+        const float sc = FP8 ? __shfl_sync(0xFFFFFFFFu, s, i & 31) : 1.0f;
         if (lane == 0) {
           const int st = fills % C::kStages;
           bool free = true;  // the stage's last unit is done with
           if (fills >= C::kStages) {
             const uint32_t u = fills - C::kStages;
-            free = warp == 0 ? mbar_wait(&sm.s_done[u % 6], (u / 6) & 1, abort_flag)
-                             : mbar_wait(&sm.pv_done[st], (u / C::kStages) & 1, abort_flag);
+            free = FP8         ? mbar_wait(&empty[st], (u / C::kStages) & 1, abort_flag)
+                   : warp == 0 ? mbar_wait(&sm.s_done[u % 6], (u / 6) & 1, abort_flag)
+                               : mbar_wait(&sm.pv_done[st], (u / C::kStages) & 1, abort_flag);
           }
           if (!free) {
             gave_up();
           } else {
-            uint8_t* dst = dst0 + st * 2 * C::kHalf;
-            mbar_arrive_expect_tx(&full[st], C::kHalf);
+            uint8_t* dst = dst0 + st * 2 * kTileBytes;
+            if (FP8) sm.scale[st][warp == 0 ? 0 : 1] = sc;
+            mbar_arrive_expect_tx(&full[st], kTileBytes);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
+            for (int half = 0; half < (FP8 ? 1 : 2); ++half) {
               if (LOGITS) tma_load_3d_policy(dst + half * 16384, map, &full[st], half * 64, head, r, policy);
               else tma_load_3d(dst + half * 16384, map, &full[st], half * 64, head, r);
             }
@@ -1021,7 +1080,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16(128, C::kKeys, false), idesc_o = idesc_bf16(128, kHeadDim, true);
+      const uint32_t idesc_s = idesc_bf16(128, C::kKeys, false), idesc_o = FP8 ? idesc_f16(128, kHeadDim, true) : idesc_bf16(128, kHeadDim, true);
       uint32_t fs = 0, fp = 0;          // units whose S, whose P V has been issued
       uint32_t segs = 0, pv_segs = 0;   // segments begun on either side
       uint32_t place = 0;               // a byte per warpgroup: its unit's place in the segment (0, 1, 2 and behind)
@@ -1033,7 +1092,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
         if (i == 0 && !mbar_wait(&sm.q_full, segs & 1, abort_flag)) return false;
         // S's columns are free once P V of unit fs - 2 has read its P
         if (fs >= 2 && !mbar_wait(&sm.pv_done[(fs - 2) % C::kStages], ((fs - 2) / C::kStages) & 1, abort_flag)) return false;
-        if (!mbar_wait(&sm.k_full[st], (fs / C::kStages) & 1, abort_flag)) return false;
+        if (!mbar_wait(FP8 ? &sm.k_ready[st] : &sm.k_full[st], (fs / C::kStages) & 1, abort_flag)) return false;
         tc_fence_after();
         const uint32_t qa = smem_u32(q_buf), ka = smem_u32(ring + st * 2 * C::kHalf);
 #pragma unroll
@@ -1060,15 +1119,15 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
         const uint32_t at = (place >> (8 * b)) & 0xFFu;
         if (at == 0) ++pv_segs;
         if (!mbar_wait(&sm.p_full[b], (fp >> 1) & 1, abort_flag) ||
-            !mbar_wait(&sm.v_full[st], (fp / C::kStages) & 1, abort_flag) ||
+            !mbar_wait(FP8 ? &sm.v_ready[st] : &sm.v_full[st], (fp / C::kStages) & 1, abort_flag) ||
             (at < 2 && pv_segs > 1 && !mbar_wait(&sm.o_free, (pv_segs - 2) & 1, abort_flag)))
           return false;
         tc_fence_after();
         const uint32_t va = smem_u32(ring + st * 2 * C::kHalf + C::kHalf);
         const uint32_t pc = tmem + C::kColS + b * 128, oc = tmem + C::kColO + b * 128;
-        // P of keys 32 c .. 32 c + 31: the values in columns 32 c .. + 15, the rests in 32 c + 16 .. + 31
+        // P of keys 32 c .. + 31: the values in columns 32 c .. + 15, the rests in 32 c + 16 .. + 31
 #pragma unroll
-        for (int part = 0; part < 2; ++part)
+        for (int part = 0; part < (FP8 ? 1 : 2); ++part)  // fp8: one value
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             umma_bf16_ts(oc, pc + (kk >> 1) * 32 + (kk & 1) * 8 + part * 16, sdesc_sw128(va + kk * 2048, 16384, 1024),
@@ -1093,7 +1152,6 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
     const bool busy = (warp & 3) * 32 < G;  // a warp whose rows are all past the group only keeps the barriers going
     const uint32_t la = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = la + C::kColS + b * 128, o_col = la + C::kColO + b * 128;
-    const float c = p.scale_log2;
     uint32_t f = 0, segs = 0;
     bool ok = true;
     int4 crossing = make_int4(-1, 0, 0, 0);  // the sequence that begins in this run and goes on
@@ -1102,19 +1160,50 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
+    // fp8: this warpgroup widens its units' codes; stages (of codes and of values) are its own.  K of its next unit, at
+    // once after a unit (whose S is done): a segment's output waits for P V, which is issued after the next S.  V,
+    // once P V of the unit before is done.
+    const uint32_t units = static_cast<uint32_t>(run.hi - run.lo);
+    float sk = 1.0f;
+    auto widen_k = [&](uint32_t n) {  // of unit n
+      if (n >= units) return true;
+      if (!mbar_wait_warp(&sm.k_full[b], n >> 1 & 1, abort_flag)) return false;
+      sk = sm.scale[b][0];
+      widen<true>(codes + b * 2 * C::kCodes, ring + b * 2 * C::kHalf, r, C::kKeys);
+      fence_proxy_async_smem();
+      warp_arrive(&sm.k_empty[b]);
+      warp_arrive(&sm.k_ready[b]);
+      return true;
+    };
+    if (FP8) ok = widen_k(b);
     for (; ok && walk.next(sg); ++segs) {
       float m = -INFINITY;
+      float d = 0.0f;  // fp8: O is relative to 2^(m + d - 11), d whole
       float2 l2 = make_float2(0.0f, 0.0f);
       for (int i = 0; i < sg.count; ++i, ++f) {
         if (static_cast<int>(f & 1) != b) continue;
+        const int valid = sg.len - (sg.off + i) * C::kKeys;
+        const bool tail = valid < C::kKeys;  // uniform: the sequence's last unit
+        float c = p.scale_log2, sv = 1.0f;
+        if (FP8) {
+          c *= sk;
+          if ((f >= 2 && !mbar_wait_warp(&sm.pv_done[b], (f >> 1 & 1) ^ 1, abort_flag)) ||
+              !mbar_wait_warp(&sm.v_full[b], f >> 1 & 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          sv = sm.scale[b][1];
+          widen<false>(codes + b * 2 * C::kCodes + C::kCodes, ring + b * 2 * C::kHalf + C::kHalf, r, valid);
+          fence_proxy_async_smem();
+          warp_arrive(&sm.v_empty[b]);
+          warp_arrive(&sm.v_ready[b]);
+        }
         if (!mbar_wait_warp(&sm.s_done[f % 6], (f / 6) & 1, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int valid = sg.len - (sg.off + i) * C::kKeys;
-        const bool tail = valid < C::kKeys;  // uniform: the sequence's last unit
-        if (tail) {
+        if (!FP8 && tail) {
           // Its V rows past the end hold anything, and 0 * NaN is NaN: zero them.  (The barrier is past the stage's
           // earlier fills: S of this unit came after P V of the unit before the last.)
           const int st = f % C::kStages;
@@ -1151,7 +1240,34 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
             x = fmax3(x, xa, xb);
           }
           x *= c;
-          if (i < 2) {  // this warpgroup's first unit of the segment
+          float to_fp16 = 1.0f;
+          if (FP8) {
+            // fp8: the weights times the page's scale are one fp16 value, O relative to an exponent of its own, d above
+            // m, which rises when a unit's largest would pass it by more than 2^4: at most 2^15, with fp16's full 11
+            // bits down to 2^-25 of the largest, whatever the pages' scales.
+            const float lv = log2f(sv);
+            if (i < 2) {
+              m = x == -INFINITY ? 0.0f : x;
+              d = fminf(fmaxf(ceilf(lv), -160.0f), 160.0f);
+            } else {
+              const float up = x - m > 8.0f ? ceilf(x - m) : 0.0f;
+              const float k = exp2_approx(-up);
+              l2.x *= k;
+              l2.y *= k;
+              m += up;
+              d -= up;
+              const float over = x - m + lv - d;
+              const bool need = over > 4.0f;
+              if (__any_sync(0xFFFFFFFFu, need)) {  // O is complete: its P V has been waited for
+                tc_fence_after();
+                const float raise = need ? ceilf(over) : 0.0f;
+                rescale_o(o_col, exp2_approx(-raise));
+                d += raise;
+              }
+            }
+            const float part = truncf(0.5f * (11.0f - d));  // in two steps: the exponent may pass fp32's
+            to_fp16 = sv * exp2_approx(part) * exp2_approx(11.0f - d - part);
+          } else if (i < 2) {  // this warpgroup's first unit of the segment
             m = x == -INFINITY ? 0.0f : x;
           } else {
             const bool need = x - m > 8.0f;
@@ -1173,7 +1289,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
           float* logits = nullptr;
           if (LOGITS && r < G)
             logits = p.logits + (((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) + r) * C::kKeys;
-          const float2 c2 = make_float2(c, c), nm = make_float2(-m, -m);
+          const float2 c2 = make_float2(c, c), nm = make_float2(-m, -m), s2 = make_float2(to_fp16, to_fp16);
           auto weights = [&](uint32_t (&v)[32], int q) {
             if (tail) {
 #pragma unroll
@@ -1197,10 +1313,15 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
                 const float2 z = ffma2(make_float2(__uint_as_float(v[h + 2 * j]), __uint_as_float(v[h + 2 * j + 1])), c2, nm);
                 const float2 w = make_float2(exp2_approx(z.x), exp2_approx(z.y));
                 l2 = fadd2(l2, w);
-                split_bf16(w.x, w.y, hi[j], lo[j]);
+                if (FP8) {
+                  const float2 v16 = fmul2(w, s2);
+                  hi[j] = pack_f16(v16.x, v16.y);
+                } else {
+                  split_bf16(w.x, w.y, hi[j], lo[j]);
+                }
               }
               tmem_st_8cols(s_col + 32 * q + h / 2, hi);
-              tmem_st_8cols(s_col + 32 * q + 16 + h / 2, lo);
+              if (!FP8) tmem_st_8cols(s_col + 32 * q + 16 + h / 2, lo);
             }
           };
           tmem_ld_32cols(s_col, va);
@@ -1221,6 +1342,10 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
         }
         tc_fence_before();
         warp_arrive(&sm.p_full[b]);
+        if (FP8 && !widen_k(f + 2)) {
+          ok = false;
+          break;
+        }
       }
       if (!ok) break;
 
@@ -1240,6 +1365,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
         break;
       }
       sm.ml[b][r] = make_float2(m, l);
+      if (FP8) sm.d[b][r] = static_cast<short>(d);
       warp_arrive(&sm.ml_full);
       if (!mbar_wait_warp(&sm.ml_full, segs & 1, abort_flag)) {
         ok = false;
@@ -1250,6 +1376,8 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
       const float top = fmaxf(m, other.x);
       const float k_own = exp2_diff(m, top), k_other = exp2_diff(other.x, top);
       l = b == 0 ? fmaf(l, k_own, other.y * k_other) : fmaf(other.y, k_other, l * k_own);  // the same in both warpgroups
+      const float e_own = FP8 ? exp2_diff(m + (d - 11.0f), top) : k_own;
+      const float e_other = FP8 ? exp2_diff(other.x + (sm.d[b ^ 1][r] - 11.0f), top) : k_other;
       m = top;
       const bool whole = sg.first && sg.last;
       const long long out_row0 = (static_cast<long long>(sg.seq) * p.hkv + head) * G;
@@ -1257,7 +1385,7 @@ __global__ void __launch_bounds__(TcCfg::kThreads, 1)
       if (busy) {
         const bool none_own = !some, none_other = other.x == -INFINITY;  // uniform: their O holds an older segment
         const float inv = whole ? inverse(l) : 1.0f;
-        const float f_own = k_own * inv, f_other = k_other * inv;
+        const float f_own = e_own * inv, f_other = e_other * inv;
         const uint32_t other_col = la + C::kColO + (b ^ 1) * 128;
         // Four lanes share a row: each loads two of every eight dims, and they trade until each has eight in a row, so
         // that a store writes 128 (or 64) bytes of 8 rows and not 32 (16) of 32 (34.1 -> 33.1 us at 128 heads, 200,000
@@ -1482,11 +1610,12 @@ __global__ void __launch_bounds__(kWeightThreads, 2) dense_weight_kernel(DenseDe
   }
 }
 
+template <bool FP8>
 cudaError_t launch_split_tc(const DenseMaps& maps, const DenseDecodeParams& p, cudaStream_t stream) {
-  auto* fn = p.logits ? dense_split_tc_kernel<true> : dense_split_tc_kernel<false>;
+  auto* fn = p.logits ? dense_split_tc_kernel<FP8, true> : dense_split_tc_kernel<FP8, false>;
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTcSmemBytes));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(fn, dim3(p.groups * p.hkv), dim3(TcCfg::kThreads), kTcSmemBytes, stream, maps, p);
+  e = launch_pdl(fn, dim3(p.groups * p.hkv), dim3(TcCfg<FP8>::kThreads), kTcSmemBytes, stream, maps, p);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }
@@ -1505,10 +1634,6 @@ cudaError_t launch_split(const DenseMaps& maps, const DenseDecodeParams& p, cuda
 template <bool FP8>
 cudaError_t launch_split_for(const DenseMaps& maps, const DenseDecodeParams& p, cudaStream_t stream) {
   if (p.group <= 16) return launch_split<1, FP8>(maps, p, stream);
-  if constexpr (FP8) {
-    if (p.group > 64) return launch_split<8, FP8>(maps, p, stream);
-    if (p.group > 32) return launch_split<4, FP8>(maps, p, stream);
-  }
   return launch_split<2, FP8>(maps, p, stream);
 }
 
@@ -1516,12 +1641,12 @@ cudaError_t launch_split_for(const DenseMaps& maps, const DenseDecodeParams& p, 
 
 int dense_decode_ctas_per_sm(int group) { return group <= 16 ? 2 : 1; }
 
-bool dense_decode_tc(int group, bool fp8) { return !fp8 && group > 32; }
+bool dense_decode_tc(int group) { return group > 32; }
 
 cudaError_t launch_dense_decode(const DenseMaps& maps, const DenseDecodeParams& p, bool fp8, cudaStream_t stream) {
-  cudaError_t e = dense_decode_tc(p.group, fp8) ? launch_split_tc(maps, p, stream)
-                  : fp8                         ? launch_split_for<true>(maps, p, stream)
-                                                : launch_split_for<false>(maps, p, stream);
+  cudaError_t e = dense_decode_tc(p.group) ? (fp8 ? launch_split_tc<true>(maps, p, stream) : launch_split_tc<false>(maps, p, stream))
+                  : fp8                    ? launch_split_for<true>(maps, p, stream)
+                                           : launch_split_for<false>(maps, p, stream);
   if (e != cudaSuccess) return e;
   const int entries = p.by_seq ? p.num_seqs : p.groups;
   int wpr = 1;  // warps to a row: one for every four partials that a sequence has on average, up to eight

@@ -307,8 +307,10 @@ struct DenseDecodeParams {
   float2* norm;                 // with weight: [num_seqs, hkv * group] (maximum, 1 / sum); else null
 };
 int dense_decode_ctas_per_sm(int group);
-// Whether the split runs on tcgen05 (units of 128 keys).
-bool dense_decode_tc(int group, bool fp8);
+// Whether the split runs on tcgen05 (units of 128 keys).  Its time hardly depends on the group (47 to 49 us for 160 MB of
+// bf16 pages at 64 to 128 heads, 42 to 44 us for 80 MB of E4M3); the other kernel, which repeats its work for every 16
+// heads, takes 36 us for either at 17 to 32 and 51 us for the E4M3 pages at 33 to 64.
+bool dense_decode_tc(int group);
 constexpr int kDenseTail = 16;  // rows of the boxes that a sequence's last unit is loaded by
 struct DenseMaps {
   CUtensorMap k, v;            // boxes of a unit's rows of one head (64 dims in bf16, 128 codes in fp8)

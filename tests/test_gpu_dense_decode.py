@@ -155,6 +155,26 @@ def test_fp8_scales_of_any_size(msa):
     b.check(msa)
 
 
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+@pytest.mark.parametrize("hq", [40, 64, 128])
+def test_fp8_scales_of_any_size_large_groups(msa, hq, order):
+    """The same where O's exponent moves at every page, never after the first, or now and then."""
+    b = Batch(msa, [2900, 130, 1], hq, 1, True, True, seed=10)
+    n = b.vs.shape[0]
+    grow = 2.0 ** torch.linspace(-60, 40, n, device="cuda")
+    at = torch.randperm(n, device="cuda")
+    if order != "mixed":
+        pages = b.host_table[0, :23].cuda().long()
+        rest = torch.tensor([p for p in range(n) if p not in set(pages.tolist())], device="cuda")
+        at[torch.cat([pages, rest])] = torch.arange(n, device="cuda")
+        if order == "down":
+            at = n - 1 - at
+    b.vs *= grow[at][:, None]
+    b.ks *= (2.0 ** torch.linspace(-12, 0, n, device="cuda"))[:, None]
+    b.q *= torch.tensor([2.0 ** -30, 2.0 ** 8, 1.0], device="cuda").to(torch.bfloat16).view(3, 1, 1)
+    b.check(msa)
+
+
 def test_zero_pages_and_queries_fp8(msa):
     b = Batch(msa, [300], 16, 1, True, False, seed=9)
     b.k[rows_of(b.host_table, 0, 128).cuda()] = 0
