@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
 // E4M3 pages: the codes land in a ring of their own (two stages) and each softmax
 // warpgroup widens its units' while it waits for its MMAs, K to bf16 (the queries'
 // type) and V to fp16, both exact; the weights times the page's V scale are one
-// fp16 value, so P V is one product.  Once widened a code meets all heads: 42 us
+// fp16 value, so P V is one product.  Once widened a code meets all heads: 41 us
 // for 80 MB of K and V where the small groups' kernel, which widens them for every
 // 16 heads, took 87 us at 128 heads and 51 us at 64.
 //
@@ -904,7 +904,7 @@ template <bool BF16>
 __device__ __forceinline__ void widen(const uint8_t* codes, uint8_t* to, int thread, int valid) {
   const int chunk = thread & 7, half = chunk >> 2;
   const uint32_t flip = half;
-#pragma unroll 2
+#pragma unroll 1  // two or more at once hold up the MMAs' reads of shared memory (2 to 8 % slower)
   for (int row = thread >> 3; row < 128; row += 16) {
     const int x = row & 7;
     uint4 in = *reinterpret_cast<const uint4*>(codes + row * 128 + ((chunk ^ x) << 4));
