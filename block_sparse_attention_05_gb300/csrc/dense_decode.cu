@@ -853,7 +853,7 @@ struct TcSmem {
   uint64_t pv_done[3];
   uint64_t p_full[2];
   uint64_t q_full, q_empty, ml_full, o_free, mma_done;
-  float2 ml[2][128];  // (m, l) of each warpgroup's rows; m = -inf: no unit of the segment was its own
+  float2 ml[2][128];  // (m, l) of each warpgroup's rows; m = -inf: no unit of the segment was its own, or no key counts
   short d[2][128];    // fp8: exponent of O
   float scale[2][2];  // fp8: a stage's scales of K and V
   RunSmem run;
@@ -1025,8 +1025,9 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
       int row = 0;
       float s = 1.0f;
       for (int i = 0; i < sg.count; ++i) {
-        if ((i & 31) == 0) {  // the next 32 pages' rows, one per lane
+        if ((i & 31) == 0) {  // the next 32 pages' rows and scales, one per lane
           row = 0;
+          s = 1.0f;
           if (i + lane < sg.count) {
             const int e = table[i + lane];
             if (e < 0 || e >= p.n_pages) {
@@ -1259,9 +1260,10 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
             // bits down to 2^-25 of the largest, whatever the pages' scales.
             const float lv = log2f(sv);
             if (i < 2) {
-              m = x == -INFINITY ? 0.0f : x;
+              m = x;
               d = fminf(fmaxf(ceilf(lv), -160.0f), 160.0f);
             } else {
+              if (m == -INFINITY) m = x;  // so far no key counts: O and l are 0
               const float up = x - m > 8.0f ? ceilf(x - m) : 0.0f;
               const float k = exp2_approx(-up);
               l2.x *= k;
@@ -1280,8 +1282,9 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
             const float part = truncf(0.5f * (11.0f - d));  // in two steps: the exponent may pass fp32's
             to_fp16 = sv * exp2_approx(part) * exp2_approx(11.0f - d - part);
           } else if (i < 2) {  // this warpgroup's first unit of the segment
-            m = x == -INFINITY ? 0.0f : x;
+            m = x;
           } else {
+            if (m == -INFINITY) m = x;  // so far no key counts: O and l are 0
             const bool need = x - m > 8.0f;
             if (__any_sync(0xFFFFFFFFu, need)) {
               // O is complete once P V of this warpgroup's unit before is done
@@ -1301,7 +1304,8 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
           float* logits = nullptr;
           if (LOGITS && r < G)
             logits = p.logits + (((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) + r) * C::kKeys;
-          const float2 c2 = make_float2(c, c), nm = make_float2(-m, -m), s2 = make_float2(to_fp16, to_fp16);
+          const float off = m == -INFINITY ? 0.0f : -m;  // -inf - -inf is NaN
+          const float2 c2 = make_float2(c, c), nm = make_float2(off, off), s2 = make_float2(to_fp16, to_fp16);
           auto weights = [&](uint32_t (&v)[32], int q) {
             if (tail) {
 #pragma unroll

@@ -145,6 +145,26 @@ def test_rising_and_falling_logits(msa):
         b.check(msa)
 
 
+@pytest.mark.parametrize("hq", [16, 32, 64, 128])
+def test_first_keys_without_weight(msa, hq):
+    """The first 300 keys' logits are -inf, the others' far below 0; in the second sequence no key counts."""
+    b = Batch(msa, [700, 200, 290], hq, 1, seed=11)
+    b.q[:, :, 0] = 16.0
+    for s, n in ((0, 300), (1, 200), (2, 10)):
+        rows = rows_of(b.host_table, s, b.lens[s]).cuda()
+        b.k[rows, :, 0] = -200.0
+        b.k[rows[:n], :, 0] = -math.inf
+    o, lse = b.call(msa)
+    assert (o[1] == 0).all() and (lse[1] == -math.inf).all()
+    k = b.k.clone()
+    k[k == -math.inf] = -1e5  # weight exp(-140000): 0 in 64 bits too, and bounds without infinities
+    ref_o, ref_lse, _, o_tol, lse_tol, _ = dense_reference(b.lens, b.table, b.q, k, b.v)
+    for s in (0, 2):
+        assert ((o[s].double() - ref_o[s]).abs() <= o_tol[s]).all()
+        # the bound on the largest logit is that of the keys that count
+        assert ((lse[s].double() - ref_lse[s]).abs() <= 2.0 ** -23 * (130 * 0.09 * (16 * 200 + 3000) + 720 + 8 * 300)).all()
+
+
 def test_fp8_scales_of_any_size(msa):
     """Pages whose K and V scales differ by many orders of magnitude."""
     b = Batch(msa, [1500, 400], 32, 2, True, True, seed=8)
