@@ -520,7 +520,13 @@ def msa_dense_attn_decode_paged_fp8(problem: Problem, q, k8_cache, v8_cache, k_s
     return _dense(problem, q, k8_cache, v8_cache, (k_scale, v_scale), block_table, weight, o, lse, ws)
 
 
+def _int32(x, name):
+    if not -2 ** 31 <= x < 2 ** 31:  # ctypes would cut it off
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+
+
 def msa_evict_workspace_size(problem: Problem, budget: int, num_pages: int) -> int:
+    _int32(budget, "budget")
     n = ctypes.c_size_t(0)
     _check(_lib.msa_evict_workspace_size(problem.c(), budget, num_pages, ctypes.byref(n)), "msa_evict_workspace_size")
     return int(n.value)
@@ -533,6 +539,8 @@ def evict_workspace(problem: Problem, budget: int, num_pages: int, device=None) 
 
 
 def _evict(problem, k, v, scales, block_table, weight, new_block_table, budget, recent, kept, new_weight, new_cu_k, ws):
+    _int32(budget, "budget")
+    _int32(recent, "recent")
     S, dev, c = _c_paged(problem)
     hkv = problem.hkv
     pages, caches = _pages(problem, dev, torch.uint8 if scales else torch.bfloat16, k, v, scales)

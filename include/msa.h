@@ -526,6 +526,8 @@ msa_status_t msa_evict_paged_fp8(const msa_problem_t *problem, void *k8_cache, v
  *   x, residual, sum, y  [rows, d_model] bf16, gamma [d_model] bf16, 16-byte
  *   aligned; sum may be NULL.  sum may be x or residual (in place), and y the
  *   other one; outputs must not overlap otherwise, nor in part.
+ *   mean(h^2) is an fp32 sum: it passes fp32 where a row has values of about
+ *   1e19 and more (y is then 0).
  * No workspace; rows = 0 is no work. */
 msa_status_t msa_add_rms_norm(const void *x, const void *residual, const void *gamma, int64_t rows, int32_t d_model,
                               float eps, void *sum, void *y, msa_stream_t stream);

@@ -162,3 +162,8 @@ def test_the_binding_checks_types_devices_and_shapes(msa):
         msa.msa_add_rms_norm(t(3, 64), t(64))
     with pytest.raises(TypeError):
         msa.msa_add_rms_norm_fp8(t(3, 64, d=torch.float32), t(64))
+    for budget, recent in ((2 ** 32 + 5, 0), (100, 2 ** 32), (-2 ** 31 - 1, 0)):  # would be cut off to 5, 0, 2^31 - 1
+        with pytest.raises(ValueError):
+            msa.msa_evict_paged(prob, cache, cache, table, t(2, 2, 200, d=torch.float32), table, budget, recent)
+    with pytest.raises(ValueError):
+        msa.msa_evict_workspace_size(prob, 2 ** 32 + 5, 3)
