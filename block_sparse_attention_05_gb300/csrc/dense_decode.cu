@@ -818,10 +818,10 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
 // each with its own S and O in TMEM (2 x (128 + 128) columns), m and l, merged at
 // the end of a segment: one computes P while the other's MMAs run.  What bounds it is
 // that chain: under each other's traffic S takes 0.45, the softmax 1.5, P V 1.2 and
-// the hand-offs 0.35 us, two chains in flight, a unit every 1.8 us.  No one link
-// carries it (P V without the rests 8 % faster, the softmax without its maximum 5 %,
-// four warpgroups with half the softmax each no faster), and TMEM has no columns for
-// a third S beside two O.  200,000 keys of 8 sequences, 128 heads: 33 us, and
+// the hand-offs 0.35 us, two chains in flight, a unit every 1.8 us (5.6 TB/s over the
+// SMs).  No one link carries it (P V without the rests 8 % faster, the softmax without
+// its maximum 5 %, four warpgroups with half the softmax each or P V begun at half of
+// P no faster), and TMEM has no columns for a third S beside two O.  200,000 keys of 8 sequences, 128 heads: 33 us, and
 // 5 for the join (bytes: 15).
 // Units of 64 keys ran at half this rate: an MMA with 64 columns takes as long as
 // one with 128, and issuing it and the commits (about 250 clocks each) held up the
