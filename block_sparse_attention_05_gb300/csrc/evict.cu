@@ -265,41 +265,47 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
     sync_all();  // nobody leaves before its words are read
   }
 
-  // Ordered compaction: keys above the threshold (the window's among them) and the first `want` equal to it.  A warp
-  // takes 32 kRows neighbours, a row of 32 at a time, so that what it keeps of a row is written in one piece; the
-  // warps' places come from one scan of their counts.
-  constexpr int kRows = 8;
-  for (int i0 = c0; i0 < c1; i0 += kRows * kSelThreads) {
-    const int i = i0 + 32 * kRows * warp + lane;
-    uint32_t sure[kRows], same[kRows];  // a bit per lane
-    uint32_t n_sure = 0, n_same = 0;
+  // Ordered compaction: keys above the threshold (the window's among them) and the first `want` equal to it.  A thread
+  // takes eight neighbours; the places come from a scan of the threads' counts, and the kept slots go through shared
+  // memory (the counts' place), so that they and their weights are written side by side: about 25 instructions for 32
+  // keys, where ballots over rows of 32 took 55.
+  constexpr int kPer = 8;
+  uint16_t* const stage = reinterpret_cast<uint16_t*>(hist);
+  static_assert(kPer * kSelThreads * 2 <= static_cast<int>(sizeof hist), "a turn's slots fit");
+  __syncthreads();  // the counts are read
+  for (int i0 = c0; i0 < c1; i0 += kPer * kSelThreads) {
+    const int i = i0 + kPer * t;
+    uint32_t sure = 0, same = 0;  // a bit per key
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const int at = i + 32 * j;
-      const bool in = at < c1;
-      uint32_t k = 0;
-      if (in) k = CACHED ? keys[at - c0] : at < end ? weight_key(w[at]) : kLate;
-      sure[j] = __ballot_sync(0xFFFFFFFFu, in && k > prefix);
-      same[j] = __ballot_sync(0xFFFFFFFFu, in && k == prefix);
-      n_sure += __popc(sure[j]);
-      n_same += __popc(same[j]);
+    for (int q = 0; q < kPer; q += 4) {
+      if (i + q >= c1) continue;
+      const uint4 k = CACHED ? *reinterpret_cast<const uint4*>(keys + (i + q - c0)) : load4(i + q);
+      const uint32_t ks[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (i + q + j >= c1) continue;
+        sure |= static_cast<uint32_t>(ks[j] > prefix) << (q + j);
+        same |= static_cast<uint32_t>(ks[j] == prefix) << (q + j);
+      }
     }
     uint32_t total;
-    const uint32_t x = block_exclusive(lane == 0 ? n_sure | (n_same << 16) : 0u, total, sm);
-    const uint32_t at0 = __shfl_sync(0xFFFFFFFFu, x, 0);
-    uint32_t na = base + (at0 & 0xFFFFu), ne = ties + (at0 >> 16);
-    const uint32_t below = (1u << lane) - 1u;
+    const uint32_t x = block_exclusive(__popc(sure) | (__popc(same) << 16), total, sm);
+    const uint32_t out0 = min(ties, want);  // ties that went before this turn
+    uint32_t to = (x & 0xFFFFu) + min(ties + (x >> 16), want) - out0, tie = ties + (x >> 16);
 #pragma unroll
-    for (int j = 0; j < kRows; ++j) {
-      const uint32_t e = ne + __popc(same[j] & below);
-      const bool a = (sure[j] >> lane) & 1u, tie = ((same[j] >> lane) & 1u) && e < want;
-      if (a || tie) {
-        const uint32_t to = na + __popc(sure[j] & below) + min(e, want);
-        kept[to] = i + 32 * j;
-        nw[to] = w[i + 32 * j];
-      }
-      na += __popc(sure[j]);
-      ne += __popc(same[j]);
+    for (int j = 0; j < kPer; ++j) {
+      const bool equal_kept = ((same >> j) & 1u) && tie < want;
+      if (((sure >> j) & 1u) || equal_kept) stage[to++] = static_cast<uint16_t>(i - i0 + j);
+      tie += (same >> j) & 1u;
+    }
+    __syncthreads();
+    const int count = static_cast<int>((total & 0xFFFFu) + min(ties + (total >> 16), want) - out0);
+    const uint32_t at = base + out0;
+#pragma unroll 4
+    for (int q = t; q < count; q += kSelThreads) {
+      const int slot = i0 + stage[q];
+      kept[at + q] = slot;
+      nw[at + q] = w[slot];
     }
     base += total & 0xFFFFu;
     ties += total >> 16;
