@@ -65,6 +65,32 @@ __device__ __forceinline__ uint32_t cluster_word(const uint32_t* p, uint32_t ran
   return v;
 }
 
+// The sum of a shared memory word over the cluster's other CTAs.
+__device__ __forceinline__ uint32_t others(const uint32_t* p, int cs, int rank) {
+  uint32_t v[7], sum = 0;  // all in flight at once
+#pragma unroll
+  for (int r = 1; r < 8; ++r) v[r - 1] = r < cs ? cluster_word(p, rank + r < cs ? rank + r : rank + r - cs) : 0u;
+#pragma unroll
+  for (int r = 0; r < 7; ++r) sum += v[r];
+  return sum;
+}
+
+// The lane in which the sum of n over the lanes so far reaches `want` (some lane's does), which becomes what is wanted
+// of that lane's n.  Called by a whole warp.
+__device__ __forceinline__ int crossing_lane(uint32_t n, uint32_t& want) {
+  const int lane = threadIdx.x & 31;
+  uint32_t incl = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  const uint32_t reached = __ballot_sync(0xFFFFFFFFu, incl >= want);
+  const int hit = reached ? __ffs(reached) - 1 : 31;
+  want -= __shfl_sync(0xFFFFFFFFu, incl - n, hit);
+  return hit;
+}
+
 // A cluster of `cs` CTAs per (sequence, KV head), each over its share of the
 // slots.  The threshold (the key of the last slot taken by weight) comes from
 // three digits of a radix select; the CTAs' digit counts are added through
@@ -82,8 +108,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
   extern __shared__ __align__(16) uint32_t keys[];  // CACHED: this CTA's share, in slot order
   __shared__ uint32_t hist[2 * 2048 + 1024];
   __shared__ uint32_t sm[33];
+  __shared__ uint32_t coarse[3][32];  // counts of a digit's 32 groups of bins, the highest first
   __shared__ uint32_t pick[3][2];
-  __shared__ uint32_t mine[2];  // kept for sure and equal to the threshold, in this CTA's share
+  __shared__ __align__(8) uint32_t mine[2];  // kept for sure and equal to the threshold, in this CTA's share
+  __shared__ uint32_t ahead[2];              // the same of the CTAs before this one
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int rank = cs > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int row = blockIdx.x / cs, s = row / p.hkv, g = row % p.hkv;
@@ -210,38 +238,61 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
 #pragma unroll 2
         for (int i = 4 * t; i < c1 - c0; i += 4 * kSelThreads) count4(*reinterpret_cast<const uint4*>(keys + i));
       }
-      sync_all();
-      // thread t takes the bins from the top: bins - 1 - (2 t) and the one below (one bin for 10 bits)
-      const int per = bins / kSelThreads;
-      const int top = bins - 1 - per * t;
-      const uint32_t own0 = counts[top], own1 = per > 1 ? counts[top - 1] : 0u;
-      uint32_t n0 = own0, n1 = own1;
-      if (cs > 1) {
-        uint32_t v0[7], v1[7];  // all in flight at once
-#pragma unroll
-        for (int r = 1; r < 8; ++r) {
-          v0[r - 1] = v1[r - 1] = 0;
-          if (r >= cs) continue;
-          const int from = rank + r < cs ? rank + r : rank + r - cs;
-          v0[r - 1] = cluster_word(&counts[top], from);
-          if (per > 1) v1[r - 1] = cluster_word(&counts[top - 1], from);
+      // The digit where the taken keys end, counted from the top.  One CTA or two: a thread for one or two bins.  More:
+      // first the digit's group of bins, then the bin, both found by warp 0 from the counts of all CTAs, a word or two
+      // per lane and CTA (reading every bin of seven other CTAs took 3.5 us a digit: 21 us for 65,536 slots on eight
+      // CTAs, now 15; on two CTAs the groups take 1 us longer than 28).
+      const bool by_group = cs > 2;
+      const int in_group = bins / 32;  // 64 or 32
+      uint32_t own0 = 0, own1 = 0;
+      int top = 0;
+      if (!by_group) {
+        sync_all();
+        const int per = bins / kSelThreads;
+        top = bins - 1 - per * t;
+        own0 = counts[top];
+        own1 = per > 1 ? counts[top - 1] : 0u;
+        uint32_t n0 = own0, n1 = own1;
+        if (cs > 1) {
+          n0 += cluster_word(&counts[top], rank ^ 1);
+          if (per > 1) n1 += cluster_word(&counts[top - 1], rank ^ 1);
         }
-#pragma unroll
-        for (int r = 0; r < 7; ++r) {
-          n0 += v0[r];
-          n1 += v1[r];
+        uint32_t total;
+        const uint32_t before = block_exclusive(n0 + n1, total, sm);
+        if (before < want && want <= before + n0 + n1) {
+          const bool second = want > before + n0;
+          pick[pass][0] = second ? top - 1 : top;
+          pick[pass][1] = want - before - (second ? n0 : 0u);
         }
+      } else {
+        __syncthreads();
+        const uint32_t* const b = counts + bins - (warp + 1) * in_group;
+        const uint32_t sum = __reduce_add_sync(0xFFFFFFFFu, b[lane] + (in_group > 32 ? b[32 + lane] : 0u));
+        if (lane == 0) coarse[pass][warp] = sum;
+        sync_all();
       }
-      uint32_t total;
-      const uint32_t before = block_exclusive(n0 + n1, total, sm);
-      if (before < want && want <= before + n0 + n1) {
-        const bool second = want > before + n0;
-        pick[pass][0] = second ? top - 1 : top;
-        pick[pass][1] = want - before - (second ? n0 : 0u);
+      if (by_group && warp == 0) {
+        const uint32_t own = coarse[pass][lane];
+        uint32_t at = want, all = own + others(&coarse[pass][lane], cs, rank);
+        const int group = crossing_lane(all, at);
+        above += lane < group ? own : 0u;
+        const int per = in_group / 32;  // bins of a lane, the highest first
+        top = bins - 1 - group * in_group - per * lane;
+        own0 = counts[top];
+        own1 = per > 1 ? counts[top - 1] : 0u;
+        uint32_t n0 = own0 + others(&counts[top], cs, rank), n1 = own1;
+        if (per > 1) n1 += others(&counts[top - 1], cs, rank);
+        all = n0 + n1;
+        const int hit = crossing_lane(all, at);
+        const bool second = at > n0;  // in lane `hit`
+        if (lane == hit) {
+          pick[pass][0] = second ? top - 1 : top;
+          pick[pass][1] = at - (second ? n0 : 0u);
+        }
       }
       __syncthreads();
       const int digit = static_cast<int>(pick[pass][0]);
-      above += (top > digit ? own0 : 0u) + (per > 1 && top - 1 > digit ? own1 : 0u);
+      above += (top > digit ? own0 : 0u) + (top - 1 > digit ? own1 : 0u);
       equal = counts[digit];
       prefix |= static_cast<uint32_t>(digit) << shift;
       mask |= static_cast<uint32_t>(bins - 1) << shift;
@@ -258,11 +309,19 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
       mine[1] = equal;
     }
     sync_all();
-    for (int r = 0; r < rank; ++r) {
-      base += cluster_word(&mine[0], r);
-      ties += cluster_word(&mine[1], r);
+    if (warp == 0) {
+      uint2 x = make_uint2(0, 0);
+      if (lane < rank) x = make_uint2(cluster_word(&mine[0], lane), cluster_word(&mine[1], lane));
+      x.x = __reduce_add_sync(0xFFFFFFFFu, x.x);
+      x.y = __reduce_add_sync(0xFFFFFFFFu, x.y);
+      if (lane == 0) {
+        ahead[0] = x.x;
+        ahead[1] = x.y;
+      }
     }
     sync_all();  // nobody leaves before its words are read
+    base = ahead[0];
+    ties = ahead[1];
   }
 
   // Ordered compaction: keys above the threshold (the window's among them) and the first `want` equal to it.  A thread
