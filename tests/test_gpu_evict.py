@@ -159,6 +159,32 @@ def test_weights_that_tie_or_are_no_numbers(msa, kind):
     c.check(msa)
 
 
+@pytest.mark.parametrize("kind", ["equal", "two_values", "few_values", "tail", "window_only", "uncached"])
+@pytest.mark.parametrize("lens,hkv", [([70001], 1), ([40000, 36001, 0, 8192, 32768], 2), ([17000] * 13, 2), ([33000] * 77, 1)])
+def test_ties_across_the_parts_of_a_long_row(msa, lens, hkv, kind):
+    """Rows that are shared out over eight, four, two and one parts: equal weights begin and end in any of them."""
+    if kind == "uncached" and len(lens) > 5:
+        pytest.skip("the same as for shorter rows")
+    if kind == "uncached":
+        lens = [n * 6 for n in lens]  # shares past what a part keeps in shared memory
+    budget, recent = max(lens) // 2 + 3, 0 if kind == "window_only" else 1001
+    if kind == "window_only":
+        budget = recent = 9000
+    c = Cache(msa, lens, hkv, budget, recent, seed=5)
+    w, i = c.weight, torch.arange(c.weight.shape[2], device="cuda")
+    if kind in ("equal", "uncached"):
+        w.fill_(0.25)
+        if kind == "uncached":
+            w[..., 5::7] = 0.5
+    elif kind == "two_values":
+        w.copy_(((i * 7) % 3 == 0).float())
+    elif kind == "few_values":
+        w.copy_((0x3F800000 + (i * 2654435761) % 4).to(torch.int32).view(torch.float32))
+    elif kind == "tail":  # the threshold's ties all in the last parts
+        w.copy_((i >= max(lens) * 3 // 4).float() - (i < 100).float())
+    c.check(msa)
+
+
 def test_shared_source_pages(msa):
     """A prefix that two sequences share stays as it is; each gets its own copy of what it keeps."""
     c = Cache(msa, [600, 700], 2, 200, 10, seed=4)
