@@ -10,9 +10,9 @@
 // header and page marks, the selection, which reads each weight once (4 bytes a
 // cached key), and the gather, which reads and writes each kept key's K and V
 // rows once (512 bytes in bf16) and bounds the call.  Measured: 12 sequences of
-// 65,536 keys to 32,768 (4 KV heads, bf16) 274 us, 6.0 TB/s, of which the gather
-// 240; 16 ragged ones of up to 9,001 to 4,096 in E4M3 42 us (13 for the bytes: the
-// gather, which rounds every code again, 27); one of 700 to 512 18 us, three
+// 65,536 keys to 32,768 (4 KV heads, bf16) 273 us, 6.0 TB/s, of which the gather
+// 241; 16 ragged ones of up to 9,001 to 4,096 in E4M3 41 us (13 for the bytes: the
+// gather, which rounds every code again, 27); one of 700 to 512 16 us, three
 // launches of dependent loads.
 #include <cuda_fp8.h>
 
@@ -98,8 +98,9 @@ __device__ __forceinline__ int crossing_lane(uint32_t n, uint32_t& want) {
 // the threshold in a CTA's share follows from its own counts, so the kept slots
 // are written in one more pass.  Each weight is read from L2 once: its key stays
 // in shared memory (CACHED, shares of up to kSelKeys slots; larger ones read the
-// weights again for each pass).  What bounds it is the instructions of four passes
-// over the keys, about 30 a key.
+// weights again for each pass).  What bounds it: 32,768 slots to a CTA take 5 us
+// to read and count, 4 for each further digit (2 of them the exchange) and 10 for
+// the compaction; 8,192 on each of eight CTAs 15 us in all.
 constexpr int kSelKeys = 48 * 1024;
 constexpr uint32_t kLate = 0xFFFFFFFFu;  // the key of a slot of the window: above every weight's
 
