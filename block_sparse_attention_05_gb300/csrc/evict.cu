@@ -96,8 +96,8 @@ __device__ __forceinline__ int crossing_lane(uint32_t n, uint32_t& want) {
 // three digits of a radix select; the CTAs' digit counts are added through
 // distributed shared memory, and each CTA finds the same digit.  What lies above
 // the threshold in a CTA's share follows from its own counts, so the kept slots
-// are written in one more pass.  Each weight is read from L2 once: its key stays
-// in shared memory (CACHED, shares of up to kSelKeys slots; larger ones read the
+// are written in one more pass.  Each weight is read once, a kept one again: its
+// key stays in shared memory (CACHED, shares of up to kSelKeys slots; larger ones read the
 // weights again for each pass).  What bounds it: 32,768 slots to a CTA take 5 us
 // to read and count, 4 for each further digit (2 of them the exchange) and 10 for
 // the compaction; 8,192 on each of eight CTAs 15 us in all.
