@@ -275,6 +275,31 @@ def test_outputs_given_by_the_caller_and_another_stream(msa):
     assert got[0] is mine[0] and torch.equal(o, mine[0]) and torch.equal(lse, mine[1])
 
 
+def test_two_streams_at_once(msa):
+    """Calls in flight on two streams, each with its own workspace, give what they give alone."""
+    batches = [Batch(msa, [9000, 700, 0, 4100], 128, 1, False, True, seed=21), Batch(msa, [12000, 77], 96, 2, True, seed=22),
+               Batch(msa, [5000] * 6, 64, 4, False, True, seed=23), Batch(msa, [300] * 50, 40, 8, True, seed=24)]
+    alone, spaces = [], []
+    for b in batches:
+        b.start = None if b.weight is None else b.weight.clone()
+        o, lse = b.call(msa)
+        alone.append((o, lse, None if b.weight is None else b.weight.clone()))
+        spaces.append((b.ws(msa), torch.empty_like(o), torch.empty_like(lse)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for turn in range(10):
+        for i, (b, (ws, o, lse)) in enumerate(zip(batches, spaces)):
+            with torch.cuda.stream(streams[i % 2]):
+                if b.weight is not None:
+                    b.weight.copy_(b.start)
+                b.call(msa, ws=ws, o=o, lse=lse)
+    torch.cuda.synchronize()
+    for b, (ws, o, lse), (want_o, want_lse, want_w) in zip(batches, spaces, alone):
+        assert msa.msa_read_device_status(ws) == 0
+        assert torch.equal(o, want_o) and torch.equal(lse, want_lse)
+        assert want_w is None or torch.equal(b.weight, want_w)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_graph_replays_follow_the_inputs(msa, fp8):
     b = Batch(msa, [3000, 500, 0], 64, 4, fp8, True, seed=13)
