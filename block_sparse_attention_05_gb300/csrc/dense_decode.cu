@@ -1401,7 +1401,9 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
       const long long out_row0 = (static_cast<long long>(sg.seq) * p.hkv + head) * G;
       const long long part_row0 = (static_cast<long long>(blockIdx.x) * 2 + (sg.first ? 1 : 0)) * G;
       if (busy) {
-        const bool none_own = !some, none_other = other.x == -INFINITY;  // uniform: their O holds an older segment
+        // A warpgroup that had no unit of the segment: its O holds an older one.  Uniform, from the segment alone: the
+        // rows of O that a lane sums below are other lanes'.  (A row of which no key counts has the factor 0.)
+        const bool none_own = !some, none_other = !(sg.count > 1 || static_cast<int>(last & 1) != b);
         const float inv = whole ? inverse(l) : 1.0f;
         const float f_own = e_own * inv, f_other = e_other * inv;
         const uint32_t other_col = la + C::kColO + (b ^ 1) * 128;
