@@ -1261,19 +1261,21 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
             // m, which rises when a unit's largest would pass it by more than 2^4: at most 2^15, with fp16's full 11
             // bits down to 2^-25 of the largest, whatever the pages' scales.
             const float lv = log2f(sv);
-            if (i < 2) {
+            // Per lane: the warpgroup's first unit of the segment, or so far no key counts (O and l are 0, whatever d was).
+            const bool fresh = i < 2 || m == -INFINITY;
+            if (fresh) {
               m = x;
               d = fminf(fmaxf(ceilf(lv), -160.0f), 160.0f);
-            } else {
-              if (m == -INFINITY) m = x;  // so far no key counts: O and l are 0
-              const float up = x - m > 8.0f ? ceilf(x - m) : 0.0f;
+            }
+            if (i >= 2) {  // uniform, as the vote and the rescale have to be
+              const float up = x - m > 8.0f ? ceilf(x - m) : 0.0f;  // fresh: 0, or x - m is NaN
               const float k = exp2_approx(-up);
               l2.x *= k;
               l2.y *= k;
               m += up;
               d -= up;
               const float over = x - m + lv - d;
-              const bool need = over > 4.0f;
+              const bool need = !fresh && over > 4.0f;
               if (__any_sync(0xFFFFFFFFu, need)) {  // O is complete: its P V has been waited for
                 tc_fence_after();
                 const float raise = need ? ceilf(over) : 0.0f;
