@@ -38,6 +38,10 @@ namespace {
 
 constexpr int kTile = kDenseTile;  // keys of a unit and of a ring stage (small groups)
 constexpr float kLn2 = 0.6931471805599453f;
+// A weight is 2^(s c - m) of an exact product and a maximum that is rounded, off by half the maximum's last place: 2^-14
+// below this size of a logit in log2 units (710 nats), but without bound above it (2^127 from logits of 2^31).  Rows at or
+// above it round their logits first: an fp32 softmax of fp32 logits, like that of the weights kernel, which reads them.
+constexpr float kRoundLogits = 1024.0f;
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -298,7 +302,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
   float2* ml = reinterpret_cast<float2*>(smem + C::kStages * C::kStage + C::kExchange);  // [warp][16] (m, l)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kStages * C::kStage + C::kExchange + C::kMl);
   uint64_t* empty = full + C::kStages;
-  float2* scales = reinterpret_cast<float2*>(empty + C::kStages);  // fp8: the stage's (K, V) scales
+  float2* scales = reinterpret_cast<float2*>(empty + C::kStages);  // fp8: the stage's K scale and log2 of its V scale
   int* abort_flag = reinterpret_cast<int*>(scales + C::kStages);
   uint32_t* err = reinterpret_cast<uint32_t*>(abort_flag + 1);
   RunSmem& run_sm = *reinterpret_cast<RunSmem*>(err + 1);
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
           } else {
             uint8_t* dk = ring + st * C::kStage;
             uint8_t* dv = dk + C::kHalf;
-            if (FP8) scales[st] = make_float2(tk, tv);
+            if (FP8) scales[st] = make_float2(tk, fmaxf(log2f(tv), -160.0f));
             auto load = [&](uint8_t* dst, const CUtensorMap* map, int dim, int row) {
               if (LOGITS) tma_load_3d_policy(dst, map, &full[st], dim, head, row, policy);
               else tma_load_3d(dst, map, &full[st], dim, head, row);
@@ -480,7 +484,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[j][i] = 0.0f;
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-      float ref0 = -INFINITY, ref1 = -INFINITY;  // fp8: O's own reference (see below)
+      float ref0 = -INFINITY, ref1 = -INFINITY;  // fp8: O's own reference, less m (see below)
 
       for (int u = sg.off; u < sg.off + sg.count; ++u, ++fills) {
         if (C::kTeams > 1 && static_cast<int>(fills % C::kTeams) != team) continue;
@@ -502,7 +506,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
             const float2 sc = scales[st];
             c0 *= sc.x;
             c1 *= sc.x;
-            lv = log2f(sc.y);
+            lv = sc.y;
           }
           // s[j]: keys key0 + 8 j + 2 t4 (+ 1) of rows r0 and r1
           float s[2 * NS][4];
@@ -542,13 +546,34 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
               for (int i = 0; i < 2; ++i)
                 if (8 * j + 2 * t4 + i >= valid) s[j][i] = s[j][2 + i] = -INFINITY;
           }
+          auto round_logits = [&](float f0, float f1) {
+#pragma unroll
+            for (int j = 0; j < 2 * NS; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                s[j][i] = __fmul_rn(s[j][i], f0);
+                s[j][2 + i] = __fmul_rn(s[j][2 + i], f1);
+              }
+          };
           if (LOGITS) {
+            round_logits(c0, c1);
+            c0 = c1 = 1.0f;
             float* w = p.logits + ((sg.unit + (u - sg.off)) * p.hkv + head) * static_cast<long long>(G) * kTile +
                        key0 + 2 * t4;
 #pragma unroll
             for (int j = 0; j < 2 * NS; ++j) {
-              if (r0 < G) *reinterpret_cast<float2*>(w + r0 * kTile + 8 * j) = make_float2(s[j][0] * c0, s[j][1] * c0);
-              if (r1 < G) *reinterpret_cast<float2*>(w + r1 * kTile + 8 * j) = make_float2(s[j][2] * c1, s[j][3] * c1);
+              if (r0 < G) *reinterpret_cast<float2*>(w + r0 * kTile + 8 * j) = make_float2(s[j][0], s[j][1]);
+              if (r1 < G) *reinterpret_cast<float2*>(w + r1 * kTile + 8 * j) = make_float2(s[j][2], s[j][3]);
+            }
+          } else if (FP8) {
+            // Products of a query of less than 2 and a code are below 2^17, logits below 2^16 with a factor under a half
+            // (off by 2^-8 at most, which the fp16 weights have room for).  The factor is known ahead of the products; a
+            // look at the maximum behind them holds up the exponentials (24 sequences of up to 65,521: 125.1 -> 126.6 us).
+            const bool large0 = c0 >= 0.5f, large1 = c1 >= 0.5f;
+            if (__any_sync(0xFFFFFFFFu, large0 || large1)) {
+              round_logits(large0 ? c0 : 1.0f, large1 ? c1 : 1.0f);
+              if (large0) c0 = 1.0f;
+              if (large1) c1 = 1.0f;
             }
           }
           float x0 = -INFINITY, x1 = -INFINITY;
@@ -563,32 +588,44 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
             x1 = fmaxf(x1, __shfl_xor_sync(0xFFFFFFFFu, x1, of));
           }
           const float n0 = fmaxf(m0, x0 * c0), n1 = fmaxf(m1, x1 * c1);  // the factors are positive
-          float a0 = exp2_diff(m0, n0), a1 = exp2_diff(m1, n1);
+          const float e0 = n0 == -INFINITY ? 0.0f : n0, e1 = n1 == -INFINITY ? 0.0f : n1;
+          const float d0 = m0 - e0, d1 = m1 - e1;  // -inf while no key counts
+          float a0 = exp2_approx(d0), a1 = exp2_approx(d1);
           l0 *= a0;
           l1 *= a1;
           m0 = n0;
           m1 = n1;
-          // fp8: O is kept relative to its own reference, the running maximum of
-          // m + log2(V scale), so that the weights of the codes fit fp16 whatever
+          // fp8: O is kept relative to a reference of its own, the running maximum
+          // of m + log2(V scale), so that the weights of the codes fit fp16 whatever
           // the pages' scales: at most 2^14, with fp16's full 11 bits down to
-          // 2^-28 of the largest.
+          // 2^-28 of the largest.  It is held as its distance from m, a small
+          // number that a large m does not round (-inf again after units without
+          // a key that counts).
           float f0 = 1.0f, f1 = 1.0f;
           if (FP8) {
-            const float y0 = fmaxf(ref0, n0 + lv), y1 = fmaxf(ref1, n1 + lv);
-            a0 = exp2_diff(ref0, y0);
-            a1 = exp2_diff(ref1, y1);
+            ref0 += d0;
+            ref1 += d1;
+            const float y0 = fmaxf(ref0, lv), y1 = fmaxf(ref1, lv);
+            a0 = exp2_approx(ref0 - y0);
+            a1 = exp2_approx(ref1 - y1);
             ref0 = y0;
             ref1 = y1;
-            f0 = exp2_diff(n0 + lv + 14.0f, y0);
-            f1 = exp2_diff(n1 + lv + 14.0f, y1);
+            f0 = exp2_approx(lv + 14.0f - y0);
+            f1 = exp2_approx(lv + 14.0f - y1);
           }
-          if (__any_sync(0xFFFFFFFFu, a0 != 1.0f || a1 != 1.0f)) {
+          const bool look = !LOGITS && !FP8;
+          const bool big0 = look && fabsf(n0) >= kRoundLogits, big1 = look && fabsf(n1) >= kRoundLogits;
+          if (__any_sync(0xFFFFFFFFu, a0 != 1.0f || a1 != 1.0f || big0 || big1)) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               o[j][0] *= a0; o[j][1] *= a0; o[j][2] *= a1; o[j][3] *= a1;
             }
+            if (look && __any_sync(0xFFFFFFFFu, big0 || big1)) {  // rare; each row for itself
+              round_logits(big0 ? c0 : 1.0f, big1 ? c1 : 1.0f);
+              if (big0) c0 = 1.0f;
+              if (big1) c1 = 1.0f;
+            }
           }
-          const float e0 = n0 == -INFINITY ? 0.0f : n0, e1 = n1 == -INFINITY ? 0.0f : n1;
 #pragma unroll
           for (int j = 0; j < 2 * NS; ++j) {
 #pragma unroll
@@ -667,8 +704,8 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
       }
       float b0 = 1.0f, b1 = 1.0f;  // factor of this warp's O
       if (FP8) {
-        b0 = exp2_diff(ref0, m0 + 14.0f);
-        b1 = exp2_diff(ref1, m1 + 14.0f);
+        b0 = exp2_approx(ref0 - 14.0f);
+        b1 = exp2_approx(ref1 - 14.0f);
       }
       if (KG > 1) {
         if (t4 == 0) {
@@ -810,7 +847,8 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
 //   P = 2^(S c - m)   one row per thread; written over S in TMEM as a bf16 value
 //                and the bf16 rest (16 significant bits), the A operand of
 //   O += P V     128 x 128 x 128, twice (value and rest), accumulated in TMEM
-// m is a row's reference, not its maximum: O and l are rescaled only when a unit's
+// m is a row's reference, not its maximum: a whole number, the first unit's maximum
+// rounded up, and O and l are rescaled, by an exact power of two, only when a unit's
 // maximum passes it by more than 2^8.
 //
 // Per unit (64 KB of K and V, 1.4 us of an SM's share of HBM) the MMAs take 0.8 us
@@ -866,8 +904,8 @@ struct TcSmem {
 constexpr size_t kTcSmemBytes = 7 * 32768 + sizeof(TcSmem);  // three stages and Q; or two, two of codes and Q
 static_assert(kTcSmemBytes <= 227 * 1024, "one CTA's shared memory");
 
-// Multiplies this thread's row of O (128 TMEM columns) by f.  Rare; out of line to leave the softmax its registers.
-__device__ __noinline__ void rescale_o(uint32_t addr, float f) {
+// Multiplies this thread's row of O or S (128 TMEM columns) by f.  Rare; out of line to leave the softmax its registers.
+__device__ __noinline__ void scale_row(uint32_t addr, float f) {
   for (int c = 0; c < 128; c += 8) {
     uint32_t w[8];
     tmem_ld_8cols(addr + c, w);
@@ -1256,55 +1294,50 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
           }
           x *= c;
           float to_fp16 = 1.0f;
+          // Per lane: the warpgroup's first unit of the segment, or so far no key counts (O and l are 0).
+          const bool fresh = i < 2 || m == -INFINITY;
+          const float top = ceilf(x);
+          if (fresh) m = top;
+          const bool rise = x - m > 8.0f;  // not where it is fresh
+          const float up = rise ? top - m : 0.0f, k = exp2_approx(-up);
+          if (rise) m = top;
+          const bool big = fabsf(m) >= kRoundLogits;
           if (FP8) {
             // fp8: the weights times the page's scale are one fp16 value, O relative to an exponent of its own, d above
             // m, which rises when a unit's largest would pass it by more than 2^4: at most 2^15, with fp16's full 11
             // bits down to 2^-25 of the largest, whatever the pages' scales.
-            const float lv = log2f(sv);
-            // Per lane: the warpgroup's first unit of the segment, or so far no key counts (O and l are 0, whatever d was).
-            const bool fresh = i < 2 || m == -INFINITY;
-            if (fresh) {
-              m = x;
-              d = fminf(fmaxf(ceilf(lv), -160.0f), 160.0f);
-            }
-            if (i >= 2) {  // uniform, as the vote and the rescale have to be
-              const float up = x - m > 8.0f ? ceilf(x - m) : 0.0f;  // fresh: 0, or x - m is NaN
-              const float k = exp2_approx(-up);
-              l2.x *= k;
-              l2.y *= k;
-              m += up;
-              d -= up;
-              const float over = x - m + lv - d;
-              const bool need = !fresh && over > 4.0f;
-              if (__any_sync(0xFFFFFFFFu, need)) {  // O is complete: its P V has been waited for
+            const float lv = log2f(sv), d_new = fminf(fmaxf(ceilf(lv), -160.0f), 160.0f);
+            l2.x *= k;
+            l2.y *= k;
+            d = fresh ? d_new : d - up;
+            const float over = x - m + lv - d;
+            const bool need = !fresh && over > 4.0f;
+            if (__any_sync(0xFFFFFFFFu, need || big)) {  // uniform, as the votes and the rescaling have to be
+              if (__any_sync(0xFFFFFFFFu, need)) {  // not a segment's first units; O is complete: its P V has been waited for
                 tc_fence_after();
                 const float raise = need ? ceilf(over) : 0.0f;
-                rescale_o(o_col, exp2_approx(-raise));
-                d += raise;
+                scale_row(o_col, exp2_approx(-raise));
+                d = raise > 150.0f ? d_new : d + raise;  // O is 0 then, and a sum of numbers of that size not exact
               }
+              if (__any_sync(0xFFFFFFFFu, big)) scale_row(s_col, big ? c : 1.0f);
             }
             const float part = truncf(0.5f * (11.0f - d));  // in two steps: the exponent may pass fp32's
             to_fp16 = sv * exp2_approx(part) * exp2_approx(11.0f - d - part);
-          } else if (i < 2) {  // this warpgroup's first unit of the segment
-            m = x;
-          } else {
-            if (m == -INFINITY) m = x;  // so far no key counts: O and l are 0
-            const bool need = x - m > 8.0f;
-            if (__any_sync(0xFFFFFFFFu, need)) {
+          } else if (__any_sync(0xFFFFFFFFu, rise || big)) {
+            if (__any_sync(0xFFFFFFFFu, rise)) {  // not a segment's first units
               // O is complete once P V of this warpgroup's unit before is done
               if (!mbar_wait_warp(&sm.pv_done[(f - 2) % C::kStages], ((f - 2) / C::kStages) & 1, abort_flag)) {
                 ok = false;
                 break;
               }
               tc_fence_after();
-              const float up = need ? ceilf(x - m) : 0.0f;
-              const float k = exp2_approx(-up);
-              rescale_o(o_col, k);
+              scale_row(o_col, k);
               l2.x *= k;
               l2.y *= k;
-              m += up;
             }
+            if (__any_sync(0xFFFFFFFFu, big)) scale_row(s_col, big ? c : 1.0f);
           }
+          if (big) c = 1.0f;  // S holds the row's logits
           float* logits = nullptr;
           if (LOGITS && r < G)
             logits = p.logits + (((sg.unit + i) * p.hkv + head) * static_cast<long long>(G) + r) * C::kKeys;
@@ -1396,8 +1429,10 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
       const float top = fmaxf(m, other.x);
       const float k_own = exp2_diff(m, top), k_other = exp2_diff(other.x, top);
       l = b == 0 ? fmaf(l, k_own, other.y * k_other) : fmaf(other.y, k_other, l * k_own);  // the same in both warpgroups
-      const float e_own = FP8 ? exp2_diff(m + (d - 11.0f), top) : k_own;
-      const float e_other = FP8 ? exp2_diff(other.x + (sm.d[b ^ 1][r] - 11.0f), top) : k_other;
+      // fp8: 2^(m + d - 11 - top), the small numbers by themselves
+      auto from_d = [&](float m, float d) { return m == -INFINITY ? 0.0f : exp2_approx((m - top) + (d - 11.0f)); };
+      const float e_own = FP8 ? from_d(m, d) : k_own;
+      const float e_other = FP8 ? from_d(other.x, sm.d[b ^ 1][r]) : k_other;
       m = top;
       const bool whole = sg.first && sg.last;
       const long long out_row0 = (static_cast<long long>(sg.seq) * p.hkv + head) * G;

@@ -153,6 +153,64 @@ def test_first_units_without_weight(msa, group, fp8):
             assert ((lse[s, hs].double() - top).abs() <= lse_tol).all(), (s, g)
 
 
+@pytest.mark.parametrize("power", [8, 12, 16, 19, 20, 21, 24, 26, 31, 40, 60, 100])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", GROUPS)
+def test_large_logits(msa, group, fp8, power):
+    """All keys of one large logit, 3 * 2^power (exact in every step but the last product), and then a second level of
+    keys at half of it: the weights are 1 / (number of the upper level's keys), whatever the size.
+
+    Bounds: the weights' rounding 2^-16 (E4M3 2^-11), a sum over n keys (n + 16) 2^-23, the output's 2^-8; lse and the
+    logits in log2 units are three fp32 roundings of the logit; the weights that are added up, G of them, each off
+    by 2^-23 (16 + the rounding of logit and maximum, which are the same number)."""
+    hkv = one_run_heads(group)
+    lens = [1000, 300]
+    b = Batch(msa, lens, group * hkv, hkv, False, True, seed=group, scale=1.0)
+    b.q.zero_()
+    b.q[:, :, 0] = 2.0 ** (power // 2)
+    b.q[:, 1::2, 0] = 2.0 ** (power // 2) * 1.5   # heads of two sizes beside one another
+    upper = [torch.ones(n, dtype=torch.bool) for n in lens]
+    upper[0] = (torch.arange(lens[0]) * 7) % 3 != 1
+    upper[0][:200] = False   # the upper level begins inside the run
+    for s, n in enumerate(lens):
+        rows = rows_of(b.host_table, s, n).cuda()
+        b.k[rows] = 0
+        b.k[rows, :, 0] = torch.where(upper[s], 3.0, 1.5).cuda().to(torch.bfloat16)[:, None] * 2.0 ** (power - power // 2)
+    if fp8:
+        to_fp8(b)
+        pages = b.host_table.flatten()
+        pages = pages[pages >= 0].cuda().long()
+        b.ks[pages] = 2.0 ** (power - power // 2 - 7)   # codes 384 and 192 in every page
+        for s, n in enumerate(lens):
+            rows = rows_of(b.host_table, s, n).cuda()
+            b.k[rows, :, 0] = torch.where(upper[s], 384.0, 192.0).cuda().to(torch.float8_e4m3fn).view(torch.uint8)[:, None]
+        b.vs[pages] *= torch.rand(len(pages), 1, device="cuda") + 0.5
+    assert units_per_run(lens, group, hkv) >= 8
+    before = b.weight.clone()
+    ws = b.ws(msa)
+    o, lse = b.call(msa, ws=ws)
+    assert msa.msa_read_device_status(ws) == 0
+    logit = b.q[..., 0].double() * 3.0 * 2.0 ** (power - power // 2)
+    u2 = 2.0 ** -23
+    for s, n in enumerate(lens):
+        rows, count = rows_of(b.host_table, s, n)[upper[s]].cuda(), int(upper[s].sum())
+        v = b.v[rows]
+        v = v.view(torch.float8_e4m3fn).double() * b.vs[rows // PAGE].double()[..., None] if fp8 else v.double()
+        want = v.mean(0)[:, None]                                     # [hkv, 1, 128]
+        size = v.abs().mean(0)[:, None]
+        small = 2.0 ** -24 * n / count * v.abs().amax(0)[:, None] if fp8 else 0.0
+        tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 if fp8 else 2.0 ** -16) * size + (n + 16) * u2 * size + small
+        got = o[s].double().view(hkv, group, DIM)
+        assert torch.isfinite(got).all() and ((got - want).abs() <= tol).all(), float((got - want).abs().max())
+        exact = logit[s] + math.log(count)
+        assert ((lse[s].double() - exact).abs() <= 3 * u2 * exact.abs() + (n + 16) * u2).all()
+        added = (b.weight[s, :, :n].double() - before[s, :, :n].double()).cpu()
+        each = torch.where(upper[s], group / count, 0.0).double()
+        wtol = each * (n + 32) * u2 + u2 * (before[s, :, :n].double().cpu() + each)
+        # logits below 2^10 in log2 units are not rounded before the sum: the maximum's rounding, 2^-14, is in the weights
+        assert ((added - each).abs() <= wtol + each * 2.0 ** -14).all()
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("hq,hkv", [(40, 1), (128, 1), (96, 2)])
 @pytest.mark.parametrize("lens", ["127", "128", "129", "ragged", "trailing_empty", "all_empty", "long_and_short", "many_short"])
