@@ -42,6 +42,11 @@ constexpr float kLn2 = 0.6931471805599453f;
 // below this size of a logit in log2 units (710 nats), but without bound above it (2^127 from logits of 2^31).  Rows at or
 // above it round their logits first: an fp32 softmax of fp32 logits, like that of the weights kernel, which reads them.
 constexpr float kRoundLogits = 1024.0f;
+// A product's factor with a page's scale in it, kept a normal number: 0 times a masked -inf, or inf times a product of 0,
+// would be NaN.  A scale that is NaN stays it.
+__device__ __forceinline__ float normal_factor(float c) {
+  return c < 1.17549435e-38f ? 1.17549435e-38f : c > 3.40282347e38f ? 3.40282347e38f : c;
+}
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -381,7 +386,7 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
           } else {
             uint8_t* dk = ring + st * C::kStage;
             uint8_t* dv = dk + C::kHalf;
-            if (FP8) scales[st] = make_float2(tk, fmaxf(log2f(tv), -160.0f));
+            if (FP8) scales[st] = make_float2(tk, tv == 0.0f ? -160.0f : log2f(tv));
             auto load = [&](uint8_t* dst, const CUtensorMap* map, int dim, int row) {
               if (LOGITS) tma_load_3d_policy(dst, map, &full[st], dim, head, row, policy);
               else tma_load_3d(dst, map, &full[st], dim, head, row);
@@ -504,8 +509,8 @@ __global__ void __launch_bounds__(SplitCfg<MG, FP8>::kThreads, SplitCfg<MG, FP8>
           float c0 = qs0, c1 = qs1, lv = 0.0f;
           if (FP8) {
             const float2 sc = scales[st];
-            c0 *= sc.x;
-            c1 *= sc.x;
+            c0 = normal_factor(c0 * sc.x);
+            c1 = normal_factor(c1 * sc.x);
             lv = sc.y;
           }
           // s[j]: keys key0 + 8 j + 2 t4 (+ 1) of rows r0 and r1
@@ -1239,7 +1244,7 @@ __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
         const bool tail = valid < C::kKeys;  // uniform: the sequence's last unit
         float c = p.scale_log2, sv = 1.0f;
         if (FP8) {
-          c *= sk;
+          c = normal_factor(c * sk);
           if ((f >= 2 && !mbar_wait_warp(&sm.pv_done[b], (f >> 1 & 1) ^ 1, abort_flag)) ||
               !mbar_wait_warp(&sm.v_full[b], f >> 1 & 1, abort_flag)) {
             ok = false;

@@ -211,6 +211,45 @@ def test_large_logits(msa, group, fp8, power):
         assert ((added - each).abs() <= wtol + each * 2.0 ** -14).all()
 
 
+@pytest.mark.parametrize("scale", [2e29, 1e-30, 1e-44])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("group", [8, 128])
+def test_softmax_scales_at_the_ends_of_the_range(msa, group, fp8, scale):
+    """A query of zeros, or logits of next to nothing: uniform weights whatever the factor in front of the product."""
+    b = Batch(msa, [300, 70], group, 1, fp8, True, seed=5, scale=scale)
+    if scale > 1:
+        b.q.zero_()
+        b.q[0, :, 0] = 2.0 ** 100  # a factor past fp32 on products of zero
+        b.k[rows_of(b.host_table, 0, 300).cuda()] = 0
+    elif fp8:
+        b.ks *= 1e-30
+    b.weight.zero_()
+    o, lse = b.call(msa)
+    for s, n in enumerate(b.lens):
+        v = b.v[rows_of(b.host_table, s, n).cuda(), 0]
+        if fp8:
+            v = v.view(torch.float8_e4m3fn).double() * b.vs[rows_of(b.host_table, s, n).cuda() // PAGE, 0].double()[:, None]
+        v = v.double()
+        tol = 2.0 ** -8 * v.mean(0).abs() + (2.0 ** -11 + (n + 16) * 2.0 ** -23) * v.abs().mean(0)
+        tol = tol + (2.0 ** -24 * v.abs().amax(0) if fp8 else 0)
+        assert ((o[s].double() - v.mean(0)).abs() <= tol).all()
+        assert ((lse[s].double() - math.log(n)).abs() <= (n + 16) * 2.0 ** -23).all()
+        assert ((b.weight[s, 0, :n].double() - group / n).abs() <= group / n * (n + 32) * 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("group", [8, 24, 128])
+def test_a_scale_that_is_nan_shows(msa, group, which):
+    """In its own sequence and KV head, and nowhere else."""
+    b = Batch(msa, [700, 130], group * 2, 2, True, False, seed=6)
+    clean_o, clean_lse = b.call(msa)
+    getattr(b, which)[b.host_table[0, 3].item(), 1] = math.nan
+    o, lse = b.call(msa)
+    assert o[0, group:].isnan().all() and (which == "vs" or lse[0, group:].isnan().all())
+    assert torch.equal(o[0, :group], clean_o[0, :group]) and torch.equal(o[1], clean_o[1])
+    assert torch.equal(lse[0, :group], clean_lse[0, :group]) and torch.equal(lse[1], clean_lse[1])
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("hq,hkv", [(40, 1), (128, 1), (96, 2)])
 @pytest.mark.parametrize("lens", ["127", "128", "129", "ragged", "trailing_empty", "all_empty", "long_and_short", "many_short"])
