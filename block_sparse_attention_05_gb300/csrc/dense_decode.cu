@@ -1548,6 +1548,9 @@ __global__ void __launch_bounds__(kJoinThreads) dense_join_kernel(DenseDecodePar
     if (threadIdx.x == 0) p.hdr->status = all_flags;
   }
   if (meta.x < 0) return;
+  // A CTA of the split that gave up a wait leaves the entries of its later sequences as the workspace held them: whatever
+  // they say, nothing outside the buffers is touched (the call is flagged).
+  if (meta.x >= p.num_seqs || meta.y < 0 || meta.y > meta.z || meta.z >= p.groups) return;
   const int head = blockIdx.x % p.hkv, G = p.group;
   const int row = blockIdx.y * (8 / wpr) + warp / wpr, sub = warp % wpr;
   const int n = meta.z - meta.y + 1;
