@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(EvictParams p
   const float* w = p.weight + static_cast<long long>(row) * p.weight_stride;
   float* nw = p.new_weight + static_cast<long long>(row) * p.new_weight_stride;
   int32_t* kept = p.kept + static_cast<long long>(row) * p.budget;
-  for (int i = m + rank * kSelThreads + t; i < p.budget; i += cs * kSelThreads) kept[i] = -1;
+  for (uint32_t i = m + rank * kSelThreads + t; i < static_cast<uint32_t>(p.budget); i += cs * kSelThreads)
+    kept[i] = -1;  // unsigned: the index passes 2^31 on the way out when the budget is near it
   if (n <= p.budget) {  // uniform in the cluster
     for (int i = rank * kSelThreads + t; i < n; i += cs * kSelThreads) {
       kept[i] = i;
