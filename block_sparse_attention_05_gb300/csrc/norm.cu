@@ -3,7 +3,7 @@
 //   h = x + residual,  sum = bf16(h),  y = h / sqrt(mean(h^2) + eps) * gamma.
 // The norm is taken from the fp32 h, before its rounding to the residual
 // stream.  E4M3 output: one fp32 scale per row, max |y| / 448 (1 when that is
-// below 2^-120), code = round-to-nearest-even(y * (1 / scale)).
+// below 2^-120), code = round-to-nearest-even(y / scale), as of an fp32 division.
 //
 // Bound by HBM: x and residual are read and sum and y written once (8 bytes an
 // element, 7 with codes).  The row stays in registers between the reductions, so
@@ -63,6 +63,14 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 // neighbours in the first and last chunk count as 0 and are not written, and the
 // tensor's last, partial chunk is read by element.
 constexpr int kWarpThreads = 256;
+
+// a / b, rounded to nearest, from 1 / b, rounded to nearest: the product, and the product's remainder times the reciprocal
+// added once (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  The product
+// alone is off by 2^-24 in rows at a time, which moves values that lie between two codes.
+__device__ __forceinline__ float2 quotients(float2 a, float b, float inv) {
+  const float2 i2 = make_float2(inv, inv), q = fmul2(a, i2);
+  return ffma2(ffma2(q, make_float2(-b, -b), a), i2, q);
+}
 
 template <int CH, bool FP8, bool ODD, bool WARP>
 __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) add_rms_norm_kernel(NormParams p, int lanes) {
@@ -179,7 +187,7 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) add_rms_norm_kerne
   float scale = __fdiv_rn(top, 448.0f);
   if (!(scale >= 0x1p-120f)) scale = 1.0f;  // a row of (next to) nothing: codes 0
   if (t == 0 && n > 0) p.scale[row] = scale;
-  const float inv = __frcp_rn(scale);  // one division a row, not one an element
+  const float inv = __frcp_rn(scale);
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int i = c * T + t;
@@ -188,7 +196,7 @@ __global__ void __launch_bounds__(WARP ? kWarpThreads : 1024) add_rms_norm_kerne
     uint32_t q[2] = {0, 0};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = make_float2(h[c][2 * j] * inv, h[c][2 * j + 1] * inv);
+      const float2 f = quotients(make_float2(h[c][2 * j], h[c][2 * j + 1]), scale, inv);
       q[j >> 1] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3)) << (16 * (j & 1));
     }
     if (inner(i)) {

@@ -534,7 +534,7 @@ msa_status_t msa_add_rms_norm(const void *x, const void *residual, const void *g
 
 /* The same with y as E4M3 codes y8 [rows, d_model] (16-byte aligned) and one
  * scale per row y_scale [rows] (4-byte aligned): scale = max |y| / 448 (1 when
- * that is below 2^-120), code = round-to-nearest-even(y * (1 / scale)) in fp32,
+ * that is below 2^-120), code = round-to-nearest-even(y / scale) in fp32,
  * saturated. */
 msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const void *gamma, int64_t rows,
                                   int32_t d_model, float eps, void *sum, void *y8, float *y_scale,
