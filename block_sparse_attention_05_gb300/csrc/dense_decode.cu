@@ -7,15 +7,20 @@
 //   o_h = sum_j 2^(s - m) v_j / l_h,  lse_h = (m + log2 l) ln 2,
 //   weight[g,j] += sum over the group's heads of 2^(s[h,j] - m_h) / l_h.
 //
-// Bound: K and V are read once and each value meets G query heads (2 G flops a
-// byte in bf16, 32 at G = 16), so HBM bounds the call until G nears 128.
+// Bound: K and V are read once; a key costs 4 * 128 G flops over 512 bytes in
+// bf16, G flops a byte (2 G in E4M3).  HBM bounds groups of up to 16 heads.
+// Larger ones are bound by what a unit costs its SM: those of 17 to 32 load, and in
+// E4M3 widen, every fragment of K and V once per 16 heads (160 MB in bf16 36 us,
+// 24 for the bytes; 80 MB in E4M3 34 to 36, 12 for the bytes), those above have the chain
+// described at their kernel.
 // Measured (16 heads to each of 4 KV heads): one sequence of 1,048,576 keys in
-// bf16 314 us (6.8 TB/s), 24 ragged sequences of up to 65,521 in E4M3 124 us
+// bf16 314 us (6.8 TB/s), 24 ragged sequences of up to 65,521 in E4M3 123 us
 // (5.9 TB/s; issuing the widening and the MMAs of 16 keys at a time is the rest),
 // 200 short ones of up to 700 keys (40 heads to 8) 50 us (5.1 TB/s, with about
-// 10 us of start, last units and join); 32 sequences of up to 16,384 with weights
-// 103 us against 72 for the bytes of K, V and weights: the logits, 64 bytes a key
-// and KV head, are written and read besides.
+// 10 us of start, last units and join); 32 sequences of up to 16,384, calls back to
+// back in a graph: 79 us, with weights 100 (72 for the bytes of K, V and weights), in
+// E4M3 52 and 67: the logits, 64 bytes a key and KV head, are written beside K and V
+// and read by a kernel behind the join.
 //
 // Work split: a unit is 64 keys of one sequence (128 in groups of more than 32
 // heads).  All units of the batch, in

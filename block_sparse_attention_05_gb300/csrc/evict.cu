@@ -11,9 +11,9 @@
 // cached key), and the gather, which reads and writes each kept key's K and V
 // rows once (512 bytes in bf16) and bounds the call.  Measured: 12 sequences of
 // 65,536 keys to 32,768 (4 KV heads, bf16) 273 us, 6.0 TB/s, of which the gather
-// 241; 16 ragged ones of up to 9,001 to 4,096 in E4M3 41 us (13 for the bytes: the
-// gather, which rounds every code again, 27); one of 700 to 512 16 us, three
-// launches of dependent loads.
+// 241; the 12 in E4M3 226 us (123 for the bytes), 16 ragged ones of up to 9,001 to
+// 4,096 in E4M3 39 to 41 us (13 for the bytes: the gather, which rounds every code
+// again, 27); one of 700 to 512 16 us, three launches of dependent loads.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -475,7 +475,8 @@ __global__ void __launch_bounds__(kGatherThreads) evict_gather_kernel(EvictParam
 // its old page, the new code the rounding of code * ratio with ratio = old scale
 // * 448 / max.  Codes and scales of few significant bits meet midpoints of
 // E4M3 exactly, so the product is rounded once and from more bits than fp32's;
-// a page that keeps its largest value keeps its codes.
+// a page that keeps its largest value keeps its codes when that one's code is 448
+// (as the quantizers' pages have it).
 __device__ __forceinline__ float2 e4m3_values(uint32_t codes) {  // of two codes
   return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes), __NV_E4M3)));
 }

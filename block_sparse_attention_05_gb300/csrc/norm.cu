@@ -6,10 +6,14 @@
 // below 2^-120), code = round-to-nearest-even(y / scale), as of an fp32 division.
 //
 // Bound by HBM: x and residual are read and sum and y written once (8 bytes an
-// element, 7 with codes).  The row stays in registers between the reductions, so
-// nothing is read twice.  Measured at 16,384 x 8,192: bf16 156 us (6.9 TB/s), codes
-// 145 us (6.5 TB/s); with the warps' sums of a row added one after another
-// instead of by shuffles the codes took 210 us (two reductions a row).
+// element, 7 with codes).  Rows of up to 32,768 stay in registers between the
+// reductions, so nothing is read twice; of wider ones, 72 elements a thread in 64
+// registers, 112 to 144 bytes a thread go to local memory.  Measured at 16,384 x
+// 8,192: bf16 154 us (7.0 TB/s), codes 142 us (6.6 TB/s); with the warps' sums of a
+// row added one after another instead of by shuffles the codes took 210 us (two
+// reductions a row).  Wide rows leave an SM one CTA, whose loads and stores take
+// turns: 4,096 x 32,768 207 and 203 us, 2,048 x 65,536 245 and 270 us (the same
+// elements).
 #include <cuda_fp8.h>
 
 #include "common.cuh"

@@ -447,6 +447,17 @@ msa_status_t msa_forward_decode_paged_fp8_index(const msa_problem_t *problem, co
  *   o, lse      written for every sequence.
  * Workspace: op MSA_OP_DENSE_ATTN_DECODE, or MSA_OP_DENSE_ATTN_DECODE_WEIGHT
  * with a weight (it then holds the logits: 4 bytes per query head and key).
+ * Numbers.  A logit is an fp32 sum of the 128 products, times the factor; any
+ * finite logit gives finite results (rows with logits of 710 and more round them
+ * to fp32 before the maximum is taken off, and with a weight every row does).  A
+ * logit of +inf gives NaN; keys of -inf do not count, and a head with no key that
+ * counts has o = 0, lse = -inf.  What one head's query holds does not change
+ * another head's results.  Exponentials are the hardware's 2^x (2^-22 of the
+ * value).  Maximum, sum, O, lse and weight are fp32; a weight that meets V has 16
+ * significant bits (bf16 V) or 11 (E4M3 V: fp16, full down to 2^-25 of the largest
+ * weight times page scale).  E4M3 pages, groups of up to 32 heads: the query goes
+ * to fp16 with a power of two per head, exact but for values 2^-24 below its
+ * largest.  An inf or NaN in a key's row shows in the heads that meet the key.
  * Lengths that contradict the host sizes make the kernels skip the call
  * (MSA_DEVICE_BAD_SEQLENS); a page outside the cache reads as zeros
  * (MSA_DEVICE_BAD_INDEX).
@@ -510,7 +521,7 @@ msa_status_t msa_evict_paged(const msa_problem_t *problem, void *k_cache, void *
  * = fp32(max |value| / 448) over the new page's rows (1, and codes 0, when the
  * largest is below 2^-118), code =
  * round-to-nearest-even of the exact value * 448 / max |value| (so a page that
- * keeps its largest value keeps its codes). */
+ * keeps its largest value keeps its codes when that one's code is 448). */
 msa_status_t msa_evict_paged_fp8(const msa_problem_t *problem, void *k8_cache, void *v8_cache, float *k_scale,
                                  float *v_scale, const int32_t *block_table, int32_t max_blocks_per_seq,
                                  int64_t num_pages, const float *weight, int64_t weight_stride, int32_t budget,

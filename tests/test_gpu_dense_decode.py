@@ -118,8 +118,8 @@ def test_long(msa, hq, hkv, fp8):
 
 
 @pytest.mark.parametrize("lens,hq,hkv", [
-    ([(i * 97) % 800 for i in range(700)], 10, 2),      # many sequences, the last units claimed by who comes first
-    ([1, 200000, 0, 70000, 3], 16, 1),                  # long ones, claimed pieces inside a sequence
+    ([(i * 97) % 800 for i in range(700)], 10, 2),      # many sequences, several to a run
+    ([1, 200000, 0, 70000, 3], 16, 1),                  # long ones, cut into many runs
     ([(i * 13) % 61 for i in range(5000)], 3, 1),       # more sequences than a warp looks through
     ([90000] + [(i * 31) % 50 for i in range(4500)], 6, 3),
 ])
