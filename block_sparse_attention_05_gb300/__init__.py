@@ -18,6 +18,9 @@ Entry points (same names as the C functions):
   msa_dense_attn_decode_paged, msa_dense_attn_decode_paged_fp8,
   msa_evict_paged, msa_evict_paged_fp8, msa_evict_workspace_size,
   msa_add_rms_norm, msa_add_rms_norm_fp8,
+  msa_dense_attn_prefill, msa_dense_attn_prefill_paged, msa_dense_attn_prefill_paged_fp8,
+  msa_tree_attn_paged, msa_tree_attn_paged_fp8,
+  msa_extend_block_table, msa_extend_workspace_size, msa_append_paged, msa_append_paged_fp8, msa_append_workspace_size,
   msa_workspace_size, msa_read_device_status.
 """
 from __future__ import annotations
@@ -63,6 +66,8 @@ class Op(enum.IntEnum):
     QUANTIZE_INDEX_FP8 = 12
     DENSE_ATTN_DECODE = 13
     DENSE_ATTN_DECODE_WEIGHT = 14
+    DENSE_ATTN_PREFILL = 16
+    TREE_ATTN = 17
 
 
 DEVICE_TIMEOUT = 1
@@ -167,6 +172,36 @@ _lib.msa_add_rms_norm.restype = ctypes.c_int
 _lib.msa_add_rms_norm.argtypes = [_vp, _vp, _vp, _i64, _i32, _f32, _vp, _vp, _vp]
 _lib.msa_add_rms_norm_fp8.restype = ctypes.c_int
 _lib.msa_add_rms_norm_fp8.argtypes = [_vp, _vp, _vp, _i64, _i32, _f32, _vp, _vp, _vp, _vp]
+# problem, q, k, v, o, lse, ws, bytes, stream
+_lib.msa_dense_attn_prefill.restype = ctypes.c_int
+_lib.msa_dense_attn_prefill.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+# problem, q, caches (, scales), block table, stride, pages (, visible, words), o, lse, ws, bytes, stream
+_lib.msa_dense_attn_prefill_paged.restype = ctypes.c_int
+_lib.msa_dense_attn_prefill_paged.argtypes = [_P, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _sz, _vp]
+_lib.msa_dense_attn_prefill_paged_fp8.restype = ctypes.c_int
+_lib.msa_dense_attn_prefill_paged_fp8.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _vp, _vp, _sz, _vp]
+_lib.msa_tree_attn_paged.restype = ctypes.c_int
+_lib.msa_tree_attn_paged.argtypes = [_P, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _i32, _vp, _vp, _vp, _sz, _vp]
+_lib.msa_tree_attn_paged_fp8.restype = ctypes.c_int
+_lib.msa_tree_attn_paged_fp8.argtypes = [_P, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _vp, _i32, _vp, _vp, _vp, _sz,
+                                         _vp]
+_lib.msa_extend_workspace_size.restype = ctypes.c_int
+_lib.msa_extend_workspace_size.argtypes = [_i32, ctypes.POINTER(ctypes.c_size_t)]
+# seqs, lengths, new tokens, capacity, free pages, their number, taken, pages, block table, stride, new lengths,
+# cu_seqlens_q, cu_seqlens_k, slots, positions, taken_out, ws, bytes, stream
+_lib.msa_extend_block_table.restype = ctypes.c_int
+_lib.msa_extend_block_table.argtypes = [_i32, _vp, _vp, _i64, _vp, _i32, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                                        _vp, _vp, _sz, _vp]
+_lib.msa_append_workspace_size.restype = ctypes.c_int
+_lib.msa_append_workspace_size.argtypes = [_i64, ctypes.POINTER(ctypes.c_size_t)]
+# k, stride, v, stride, k_idx, stride, slots, tokens, heads, index_dim, caches, pages, ws, bytes, stream
+_lib.msa_append_paged.restype = ctypes.c_int
+_lib.msa_append_paged.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _sz,
+                                  _vp]
+# k, stride, v, stride, k_idx, stride, slots, tokens, heads, k, v, scales, k_idx, scale, pages, ws, bytes, stream
+_lib.msa_append_paged_fp8.restype = ctypes.c_int
+_lib.msa_append_paged_fp8.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _vp,
+                                      _i64, _vp, _sz, _vp]
 _lib.msa_read_device_status.restype = ctypes.c_int
 _lib.msa_read_device_status.argtypes = [_vp, ctypes.POINTER(ctypes.c_uint32), _vp]
 _lib.msa_set_stage_events.restype = ctypes.c_int
@@ -183,7 +218,10 @@ EXPORTED = ("msa_workspace_size", "msa_index_pool", "msa_topk_pooled", "msa_inde
             "msa_forward_decode_paged_fp8", "msa_quantize_index_fp8", "msa_index_pool_fp8", "msa_index_topk_fp8",
             "msa_forward_fp8_index", "msa_forward_decode_paged_fp8_index",
             "msa_dense_attn_decode_paged", "msa_dense_attn_decode_paged_fp8", "msa_evict_workspace_size",
-            "msa_evict_paged", "msa_evict_paged_fp8", "msa_add_rms_norm", "msa_add_rms_norm_fp8")
+            "msa_evict_paged", "msa_evict_paged_fp8", "msa_add_rms_norm", "msa_add_rms_norm_fp8",
+            "msa_dense_attn_prefill", "msa_dense_attn_prefill_paged", "msa_dense_attn_prefill_paged_fp8",
+            "msa_tree_attn_paged", "msa_tree_attn_paged_fp8", "msa_extend_workspace_size", "msa_extend_block_table",
+            "msa_append_workspace_size", "msa_append_paged", "msa_append_paged_fp8")
 
 STAGES = ("plan", "index", "topk", "schedule", "attn", "combine")
 
@@ -642,6 +680,209 @@ def msa_add_rms_norm_fp8(x, gamma, residual=None, eps: float = 1e-6, sum_out=Non
     if status:
         raise MsaError(status, "msa_add_rms_norm_fp8")
     return sum_out, y8, y_scale
+
+
+# ---------------------------------------------------------------- prompts, drafted trees, cache tables and rows
+def _prompt(where, op, problem, q, k, v, scales, block_table, visible, o, lse, ws):
+    S, dev, c = _c_paged(problem)
+    T, hq = problem.total_q, problem.hq
+    args = ()
+    if block_table is None:
+        shape = (problem.total_k, problem.hkv, 128)
+        caches = (_is(k, torch.bfloat16, shape, dev, "k"), _is(v, torch.bfloat16, shape, dev, "v"))
+    else:
+        pages, caches = _pages(problem, dev, torch.uint8 if scales else torch.bfloat16, k, v, scales)
+        args = (_table(block_table, S, dev, "block_table"), block_table.shape[1], pages)
+    if op is Op.TREE_ATTN:
+        if visible.dim() != 2:
+            raise ValueError(f"visible: expected [total_q, words], got {list(visible.shape)}")
+        args += (_is(visible, torch.int32, (T, visible.shape[1]), dev, "visible"), visible.shape[1])
+    at_q = _is(q, torch.bfloat16, (T, hq, 128), dev, "q")
+    if o is None:
+        o = torch.empty_like(q)
+        at_o = o.data_ptr()
+    else:
+        at_o = _is(o, torch.bfloat16, (T, hq, 128), dev, "o")
+    if lse is None:
+        lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+        at_lse = lse.data_ptr()
+    else:
+        at_lse = _is(lse, torch.float32, (T, hq), dev, "lse")
+    ws, at_ws, nws = _space(ws, lambda: msa_workspace_size(problem, op), dev)
+    status = getattr(_lib, where)(c, at_q, *caches, *args, at_o, at_lse, at_ws, nws, _raw_stream(dev))
+    if status:
+        raise MsaError(status, where)
+    return o, lse
+
+
+def msa_dense_attn_prefill(problem: Problem, q, k, v, o=None, lse=None, ws=None):
+    """Causal attention of prompts and prompt chunks over every key: packed q [total_q, Hq, 128] and k, v [total_k, Hkv,
+    128], the queries the last q_len positions of their sequences; any group size up to 128, lengths from 0.  Returns (o
+    [total_q, Hq, 128] bf16, lse [total_q, Hq] fp32).  Workspace: op DENSE_ATTN_PREFILL."""
+    return _prompt("msa_dense_attn_prefill", Op.DENSE_ATTN_PREFILL, problem, q, k, v, None, None, None, o, lse, ws)
+
+
+def msa_dense_attn_prefill_paged(problem: Problem, q, k_cache, v_cache, block_table, o=None, lse=None, ws=None):
+    """msa_dense_attn_prefill over a paged cache ([num_pages * 128, Hkv, 128] rows, block_table int32 [num_seqs,
+    max_blocks]) that holds the new tokens' rows already."""
+    return _prompt("msa_dense_attn_prefill_paged", Op.DENSE_ATTN_PREFILL, problem, q, k_cache, v_cache, None,
+                   block_table, None, o, lse, ws)
+
+
+def msa_dense_attn_prefill_paged_fp8(problem: Problem, q, k8_cache, v8_cache, k_scale, v_scale, block_table, o=None,
+                                     lse=None, ws=None):
+    """msa_dense_attn_prefill_paged over E4M3 pages (uint8 codes) with k_scale / v_scale [num_pages, Hkv]."""
+    return _prompt("msa_dense_attn_prefill_paged_fp8", Op.DENSE_ATTN_PREFILL, problem, q, k8_cache, v8_cache,
+                   (k_scale, v_scale), block_table, None, o, lse, ws)
+
+
+def msa_tree_attn_paged(problem: Problem, q, k_cache, v_cache, block_table, visible, o=None, lse=None, ws=None):
+    """Attention of a tree of drafted tokens: the q_len new tokens of each sequence (in the cache's last q_len slots) see
+    every cached key before them and the drafts whose bit is set in their row of ``visible`` (int32 [total_q, words], bit
+    d % 32 of word d / 32 for draft d of the sequence).  Returns (o, lse) as msa_dense_attn_prefill; a draft that sees no
+    key has o = 0, lse = -inf.  Workspace: op TREE_ATTN."""
+    return _prompt("msa_tree_attn_paged", Op.TREE_ATTN, problem, q, k_cache, v_cache, None, block_table, visible, o, lse,
+                   ws)
+
+
+def msa_tree_attn_paged_fp8(problem: Problem, q, k8_cache, v8_cache, k_scale, v_scale, block_table, visible, o=None,
+                            lse=None, ws=None):
+    """msa_tree_attn_paged over E4M3 pages (uint8 codes) with k_scale / v_scale [num_pages, Hkv]."""
+    return _prompt("msa_tree_attn_paged_fp8", Op.TREE_ATTN, problem, q, k8_cache, v8_cache, (k_scale, v_scale),
+                   block_table, visible, o, lse, ws)
+
+
+def msa_extend_workspace_size(num_seqs: int) -> int:
+    _int32(num_seqs, "num_seqs")
+    n = ctypes.c_size_t(0)
+    _check(_lib.msa_extend_workspace_size(num_seqs, ctypes.byref(n)), "msa_extend_workspace_size")
+    return int(n.value)
+
+
+def extend_workspace(num_seqs: int, device="cuda") -> torch.Tensor:
+    """A device buffer for msa_extend_block_table over batches of ``num_seqs`` sequences."""
+    return torch.empty(msa_extend_workspace_size(num_seqs), dtype=torch.uint8, device=device)
+
+
+def _out(t, dtype, shape, dev, name):
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        return t, t.data_ptr()
+    return t, _is(t, dtype, shape, dev, name)
+
+
+def msa_extend_block_table(lengths, new_tokens, free_pages, block_table, capacity: int, taken=None, new_lengths=None,
+                           num_pages: int = (1 << 24) - 1, cu_q=None, cu_k=None, slots=None, positions=None,
+                           taken_out=None, ws=None):
+    """Pages for the new tokens of a batch: ``lengths`` and ``new_tokens`` int32 [num_seqs], ``free_pages`` int32 (the
+    first ``taken`` [1] of which are gone), ``block_table`` int32 [num_seqs, max_blocks], whose entries of the new blocks
+    are written.  Returns (cu_q, cu_k, slots int64 [capacity], positions int32 [capacity], taken_out int32 [1]): the grown
+    batch's prefix sums, and each new token's cache row (-1 past the last token) and place in its sequence.
+    ``new_lengths`` (may be ``lengths``) and ``taken_out`` (may be ``taken``) let a captured step advance by itself.
+    Workspace: extend_workspace."""
+    _int32(capacity, "capacity")
+    if not lengths.is_cuda:
+        _need(lengths, torch.int32, "lengths")
+    dev = _current_device()
+    S = lengths.numel()
+    at_len, at_new = _is(lengths, torch.int32, (S,), dev, "lengths"), _is(new_tokens, torch.int32, (S,), dev, "new_tokens")
+    at_free = _is(free_pages, torch.int32, (free_pages.numel(),), dev, "free_pages")
+    at_table = _table(block_table, S, dev, "block_table")
+    at_taken = None if taken is None else _is(taken, torch.int32, (1,), dev, "taken")
+    at_grown = None if new_lengths is None else _is(new_lengths, torch.int32, (S,), dev, "new_lengths")
+    room = max(capacity, 0)
+    cu_q, at_q = _out(cu_q, torch.int32, (S + 1,), dev, "cu_q")
+    cu_k, at_k = _out(cu_k, torch.int32, (S + 1,), dev, "cu_k")
+    slots, at_slots = _out(slots, torch.int64, (room,), dev, "slots")
+    positions, at_pos = _out(positions, torch.int32, (room,), dev, "positions")
+    taken_out, at_out = _out(taken_out, torch.int32, (1,), dev, "taken_out")
+    ws, at_ws, nws = _space(ws, lambda: msa_extend_workspace_size(S), dev)
+    status = _lib.msa_extend_block_table(S, at_len, at_new, capacity, at_free, free_pages.numel(), at_taken, num_pages,
+                                         at_table, block_table.shape[1], at_grown, at_q, at_k, at_slots, at_pos, at_out,
+                                         at_ws, nws, _raw_stream(dev))
+    if status:
+        raise MsaError(status, "msa_extend_block_table")
+    return cu_q, cu_k, slots, positions, taken_out
+
+
+def msa_append_workspace_size(num_pages: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(_lib.msa_append_workspace_size(num_pages, ctypes.byref(n)), "msa_append_workspace_size")
+    return int(n.value)
+
+
+def append_workspace(num_pages: int, device="cuda") -> torch.Tensor:
+    """A device buffer for msa_append_paged_fp8 (and msa_append_paged, which needs none) over caches of ``num_pages``."""
+    return torch.empty(msa_append_workspace_size(num_pages), dtype=torch.uint8, device=device)
+
+
+def _rows(t, tokens, inner, dev, name):
+    """The address and token stride of new rows: contiguous but for the distance between tokens."""
+    if t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (tokens, *inner):
+        strides, n = t.stride(), 1
+        for size, stride in zip(inner[::-1], strides[:0:-1]):
+            if stride != n and size != 1:
+                raise ValueError(f"{name}: a token's row must be contiguous, got strides {list(strides)}")
+            n *= size
+        return t.data_ptr(), n if tokens <= 1 else strides[0]
+    if t.dtype is not torch.bfloat16 or not t.is_cuda:
+        _need(t, torch.bfloat16, name)
+    _refuse(t.contiguous(), torch.bfloat16, (tokens, *inner), dev, name)
+
+
+def _append(where, k, v, slots, k_cache, v_cache, scales, k_idx, k_idx_cache, k_idx_scale, ws):
+    if not slots.is_cuda:
+        _need(slots, torch.int64, "slots")
+    dev = _current_device()
+    dtype = torch.uint8 if scales else torch.bfloat16
+    N = slots.numel()
+    at_slots = _is(slots, torch.int64, (N,), dev, "slots")
+    if k_cache.dim() != 3 or k_cache.shape[0] % 128:
+        raise ValueError("the caches must be whole pages of 128 rows, [num_pages * 128, num_kv_heads, 128]")
+    rows, hkv = k_cache.shape[0], k_cache.shape[1]
+    at_k, stride_k = _rows(k, N, (hkv, 128), dev, "k")
+    at_v, stride_v = _rows(v, N, (hkv, 128), dev, "v")
+    caches = (_is(k_cache, dtype, (rows, hkv, 128), dev, "k_cache"), _is(v_cache, dtype, (rows, hkv, 128), dev, "v_cache"))
+    at_i, stride_i, at_ic, at_is, d = None, 0, None, None, 128
+    if (k_idx is None) != (k_idx_cache is None):
+        raise ValueError("k_idx and its cache come together")
+    if k_idx is not None:
+        d = k_idx_cache.shape[-1]
+        at_i, stride_i = _rows(k_idx, N, (d,), dev, "k_idx")
+        at_ic = _is(k_idx_cache, dtype, (rows, 128 if scales else d), dev, "k_idx_cache")
+    at_ws, nws = None, 0
+    if scales:
+        shape = (rows // 128, hkv)
+        at_scales = (_is(scales[0], torch.float32, shape, dev, "k_scale"), _is(scales[1], torch.float32, shape, dev, "v_scale"))
+        if k_idx is not None:
+            if k_idx_scale is None:
+                raise ValueError("k_idx_scale: needed with k_idx")
+            at_is = _is(k_idx_scale, torch.float32, (rows // 128,), dev, "k_idx_scale")
+        ws, at_ws, nws = _space(ws, lambda: msa_append_workspace_size(rows // 128), dev)
+        status = _lib.msa_append_paged_fp8(at_k, stride_k, at_v, stride_v, at_i, stride_i, at_slots, N, hkv, *caches,
+                                           *at_scales, at_ic, at_is, rows // 128, at_ws, nws, _raw_stream(dev))
+    else:
+        if ws is not None:
+            ws, at_ws, nws = _space(ws, None, dev)
+        status = _lib.msa_append_paged(at_k, stride_k, at_v, stride_v, at_i, stride_i, at_slots, N, hkv, d, *caches, at_ic,
+                                       rows // 128, at_ws, nws, _raw_stream(dev))
+    if status:
+        raise MsaError(status, where)
+
+
+def msa_append_paged(k, v, slots, k_cache, v_cache, k_idx=None, k_idx_cache=None, ws=None):
+    """Writes new tokens' rows k, v [tokens, Hkv, 128] (and k_idx [tokens, d_idx]), which may be slices of wider rows, to
+    rows ``slots`` (int64, distinct, -1: none) of the caches.  ``ws`` (256 bytes) is for device flags only."""
+    _append("msa_append_paged", k, v, slots, k_cache, v_cache, None, k_idx, k_idx_cache, None, ws)
+
+
+def msa_append_paged_fp8(k, v, slots, k8_cache, v8_cache, k_scale, v_scale, k_idx=None, k_idx8_cache=None,
+                         k_idx_scale=None, ws=None):
+    """msa_append_paged into E4M3 pages: k_scale / v_scale [num_pages, Hkv] (k_idx_scale [num_pages]) grow where the new
+    rows need it, and the rows that a page holds already are then rounded again.  A page's tokens follow one another in
+    ``slots``.  Workspace: append_workspace."""
+    _append("msa_append_paged_fp8", k, v, slots, k8_cache, v8_cache, (k_scale, v_scale), k_idx, k_idx8_cache, k_idx_scale,
+            ws)
 
 
 # ---------------------------------------------------------------- fp8 K/V

@@ -819,6 +819,200 @@ msa_status_t evict(const msa_problem_t* problem, void* k, void* v, float* k_scal
   return cuda_status(launch_evict(p, fp8, dev.sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------- dense attention of prompts and drafted trees
+struct PromptShape {
+  int S, T, N, hq, hkv, G, max_q, max_k, max_nb, tile_tokens;
+  long long max_items;
+  float scale;
+};
+
+msa_status_t derive_prompt(const msa_problem_t* p, PromptShape& d) {
+  if (!p) return MSA_ERR_INVALID_ARG;
+  if (p->num_seqs < 1 || !p->cu_seqlens_q || !p->cu_seqlens_k) return MSA_ERR_INVALID_ARG;
+  if (p->total_q < 0 || p->total_k < 0 || p->max_seqlen_q < 0 || p->max_seqlen_k < 0) return MSA_ERR_INVALID_ARG;
+  if (p->max_seqlen_q > p->total_q || p->max_seqlen_k > p->total_k) return MSA_ERR_INVALID_ARG;
+  if (p->num_q_heads <= 0 || p->num_kv_heads <= 0 || p->num_q_heads % p->num_kv_heads) return MSA_ERR_INVALID_ARG;
+  if (p->head_dim <= 0 || p->block_size <= 0) return MSA_ERR_INVALID_ARG;
+  if (!(p->softmax_scale < 1e30f)) return MSA_ERR_INVALID_ARG;  // NaN, inf, or inf in log2 units
+  if (p->head_dim != 128 || p->block_size != 128) return MSA_ERR_UNSUPPORTED;
+  d.S = p->num_seqs;
+  d.T = p->total_q;
+  d.N = p->total_k;
+  d.hq = p->num_q_heads;
+  d.hkv = p->num_kv_heads;
+  d.G = d.hq / d.hkv;
+  if (d.G > 128 || d.hkv > 1024 || d.S > (1 << 20) || d.T >= (1 << 25) || p->max_seqlen_k > (1 << 30))
+    return MSA_ERR_UNSUPPORTED;
+  d.max_q = p->max_seqlen_q;
+  d.max_k = p->max_seqlen_k;
+  d.max_nb = (d.max_k + 127) / 128;
+  d.tile_tokens = 128 / d.G;
+  d.max_items = static_cast<long long>(d.T) / (2 * d.tile_tokens) + d.S;
+  d.scale = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(static_cast<float>(p->head_dim));
+  return MSA_OK;
+}
+
+struct PromptLayout {
+  size_t hdr, plan, seq, item_base, items, block_base, part_o, part_ml, total;
+};
+
+PromptLayout prompt_layout(const PromptShape& d) {
+  PromptLayout L{};
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes);
+    return at;
+  };
+  L.hdr = take(sizeof(WsHeader));
+  L.plan = take(sizeof(PromptPlan));
+  L.seq = take(sizeof(SeqInfo) * d.S);
+  L.item_base = take(sizeof(int32_t) * d.S);
+  L.items = take(sizeof(int2) * d.max_items);
+  L.block_base = take(sizeof(int32_t) * d.max_items);
+  if (prompt_may_split(d.max_nb)) {
+    L.part_o = take(sizeof(float) * kPromptMaxCtas * 2 * 256 * kHeadDim);
+    L.part_ml = take(sizeof(float2) * kPromptMaxCtas * 2 * 256);
+  }
+  L.total = off;
+  return L;
+}
+
+struct PromptCall {
+  const void *q, *k, *v;
+  const float *k_scale, *v_scale;
+  bool fp8, paged, tree;
+  const int32_t* block_table;
+  int32_t max_blocks_per_seq;
+  int64_t num_pages;
+  const int32_t* visible;
+  int32_t mask_words;
+  void* o;
+  float* lse;
+};
+
+msa_status_t prompt_attn(const msa_problem_t* problem, const PromptCall& c, void* ws, size_t ws_bytes,
+                         msa_stream_t stream) {
+  t_stage = -1;
+  t_error_detail[0] = 0;
+  PromptShape d;
+  msa_status_t st = derive_prompt(problem, d);
+  if (st != MSA_OK) return st;
+  const bool rows = d.T > 0;  // without query rows only the lengths are checked
+  if (rows && (!c.q || !c.o || !c.lse || !c.k || !c.v)) return MSA_ERR_INVALID_ARG;
+  if (!aligned16(c.q) || !aligned16(c.o) || !aligned16(c.lse) || !aligned16(c.k) || !aligned16(c.v))
+    return MSA_ERR_ALIGNMENT;
+  if (c.paged) {
+    if (!c.block_table) return MSA_ERR_INVALID_ARG;
+    if (!aligned4(c.block_table)) return MSA_ERR_ALIGNMENT;
+    if (c.num_pages < 1 || c.num_pages * 128 >= (1LL << 31)) return MSA_ERR_INVALID_ARG;
+    if (c.max_blocks_per_seq < d.max_nb) return MSA_ERR_INVALID_ARG;
+  }
+  if (c.fp8) {
+    if (!c.k_scale || !c.v_scale) return MSA_ERR_INVALID_ARG;
+    if (!aligned4(c.k_scale) || !aligned4(c.v_scale)) return MSA_ERR_ALIGNMENT;
+  }
+  if (c.tree) {
+    if (c.mask_words < (d.max_q + 31) / 32) return MSA_ERR_INVALID_ARG;
+    if (rows && !c.visible) return MSA_ERR_INVALID_ARG;
+    if (!aligned4(c.visible)) return MSA_ERR_ALIGNMENT;
+  }
+  const PromptLayout L = prompt_layout(d);
+  if (!ws || ws_bytes < L.total) return MSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
+  DeviceFacts dev;
+  if ((st = device_facts(dev)) != MSA_OK) return st;
+  PromptMaps maps{};
+  if (rows) {
+    const long long n = c.paged ? c.num_pages * 128 : d.N;
+    auto map = [&](CUtensorMap& m, const void* x) {
+      return c.fp8 ? map_3d_u8(m, x, n, d.hkv) : map_3d(m, x, n, d.hkv, 1, 128);
+    };
+    if (!map_3d(maps.q, c.q, d.T, d.hq, d.G, d.tile_tokens) || !map(maps.k, c.k) || !map(maps.v, c.v))
+      return MSA_ERR_CUDA;
+  }
+  PromptParams p{};
+  p.num_seqs = d.S;
+  p.hq = d.hq;
+  p.hkv = d.hkv;
+  p.group = d.G;
+  p.total_q = d.T;
+  p.total_k = d.N;
+  p.max_q = d.max_q;
+  p.max_k = d.max_k;
+  p.max_nb = d.max_nb;
+  p.tile_tokens = d.tile_tokens;
+  p.ctas = dev.sms < kPromptMaxCtas ? dev.sms : kPromptMaxCtas;
+  p.max_items = d.max_items;
+  p.cu_q = problem->cu_seqlens_q;
+  p.cu_k = problem->cu_seqlens_k;
+  p.block_table = c.paged ? c.block_table : nullptr;
+  p.bt_stride = c.max_blocks_per_seq;
+  p.n_pages = c.num_pages;
+  p.k_scale = c.k_scale;
+  p.v_scale = c.v_scale;
+  p.visible = c.tree ? c.visible : nullptr;
+  p.mask_words = c.mask_words;
+  p.o = static_cast<__nv_bfloat16*>(c.o);
+  p.lse = c.lse;
+  p.scale_log2 = d.scale * 1.4426950408889634f;
+  p.hdr = at<WsHeader>(ws, L.hdr);
+  p.plan = at<PromptPlan>(ws, L.plan);
+  p.seq = at<SeqInfo>(ws, L.seq);
+  p.item_base = at<int32_t>(ws, L.item_base);
+  p.items = at<int2>(ws, L.items);
+  p.block_base = at<int32_t>(ws, L.block_base);
+  p.part_o = prompt_may_split(d.max_nb) ? at<float>(ws, L.part_o) : nullptr;
+  p.part_ml = prompt_may_split(d.max_nb) ? at<float2>(ws, L.part_ml) : nullptr;
+  StageScope scope(MSA_STAGE_ATTN, reinterpret_cast<cudaStream_t>(stream));
+  return cuda_status(launch_prompt_attn(maps, p, c.fp8, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------- filling a paged cache
+bool aligned8(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+
+size_t extend_bytes(int32_t num_seqs) { return align_up(sizeof(WsHeader)) + align_up(sizeof(int32_t) * num_seqs); }
+size_t append_bytes(int64_t num_pages) { return align_up(sizeof(WsHeader)) + align_up(sizeof(uint32_t) * num_pages); }
+
+struct AppendRows {
+  const void* x;
+  int64_t stride;
+  int width;
+  void* cache;
+  float* scale;
+};
+
+msa_status_t append_rows(const AppendRows* rows, int planes, const int64_t* slots, int64_t tokens, int64_t num_pages,
+                         bool fp8, void* ws, size_t ws_bytes, msa_stream_t stream) {
+  t_stage = -1;
+  t_error_detail[0] = 0;
+  if (tokens < 0 || tokens > (1LL << 31) || num_pages < 1 || num_pages * 128 >= (1LL << 31)) return MSA_ERR_INVALID_ARG;
+  if (tokens > 0 && !slots) return MSA_ERR_INVALID_ARG;
+  if (!aligned8(slots)) return MSA_ERR_ALIGNMENT;
+  AppendParams p{};
+  for (int i = 0; i < planes; ++i) {
+    const AppendRows& r = rows[i];
+    if ((tokens > 0 && !r.x) || !r.cache || (fp8 && !r.scale)) return MSA_ERR_INVALID_ARG;
+    if (r.stride < r.width) return MSA_ERR_INVALID_ARG;
+    if (!aligned16(r.x) || !aligned16(r.cache) || !aligned4(r.scale) || r.stride % 8) return MSA_ERR_ALIGNMENT;
+    p.plane[i] = {static_cast<const __nv_bfloat16*>(r.x), r.stride, r.width, r.cache, r.scale};
+  }
+  p.planes = planes;
+  p.slots = reinterpret_cast<const long long*>(slots);
+  p.tokens = tokens;
+  p.n_pages = num_pages;
+  const size_t need = fp8 ? append_bytes(num_pages) : ws ? align_up(sizeof(WsHeader)) : 0;
+  if (need > 0 && (!ws || ws_bytes < need)) return MSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
+  p.hdr = static_cast<WsHeader*>(ws);
+  p.marks = fp8 ? at<uint32_t>(ws, align_up(sizeof(WsHeader))) : nullptr;
+  DeviceFacts dev;
+  const msa_status_t st = device_facts(dev);
+  if (st != MSA_OK) return st;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return cuda_status(fp8 ? launch_append_fp8(p, need, s) : launch_append(p, dev.sms, s));
+}
+
 msa_status_t add_rms_norm(const void* x, const void* residual, const void* gamma, int64_t rows, int32_t d_model,
                           float eps, void* sum, void* y, void* y8, float* y_scale, bool fp8, msa_stream_t stream) {
   t_stage = -1;
@@ -956,6 +1150,12 @@ const char* msa_status_string(msa_status_t s) {
 
 msa_status_t msa_workspace_size(const msa_problem_t* problem, msa_op_t op, size_t* bytes) {
   if (!bytes) return MSA_ERR_INVALID_ARG;
+  if (op == MSA_OP_DENSE_ATTN_PREFILL || op == MSA_OP_TREE_ATTN) {
+    PromptShape d;
+    const msa_status_t st = derive_prompt(problem, d);
+    if (st == MSA_OK) *bytes = prompt_layout(d).total;
+    return st;
+  }
   if (op < MSA_OP_INDEX_POOL || op > MSA_OP_DENSE_ATTN_DECODE_WEIGHT) return MSA_ERR_INVALID_ARG;
   if (op == MSA_OP_DENSE_ATTN_DECODE || op == MSA_OP_DENSE_ATTN_DECODE_WEIGHT) {
     PagedDecode pd;
@@ -1502,6 +1702,137 @@ msa_status_t msa_add_rms_norm_fp8(const void* x, const void* residual, const voi
                                   int32_t d_model, float eps, void* sum, void* y8, float* y_scale,
                                   msa_stream_t stream) {
   return add_rms_norm(x, residual, gamma, rows, d_model, eps, sum, nullptr, y8, y_scale, true, stream);
+}
+
+msa_status_t msa_dense_attn_prefill(const msa_problem_t* problem, const void* q, const void* k, const void* v, void* o,
+                                    float* lse, void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  const PromptCall c{q, k, v, nullptr, nullptr, false, false, false, nullptr, 0, 0, nullptr, 0, o, lse};
+  return prompt_attn(problem, c, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_dense_attn_prefill_paged(const msa_problem_t* problem, const void* q, const void* k_cache,
+                                          const void* v_cache, const int32_t* block_table, int32_t max_blocks_per_seq,
+                                          int64_t num_pages, void* o, float* lse, void* workspace,
+                                          size_t workspace_bytes, msa_stream_t stream) {
+  const PromptCall c{q,           k_cache,            v_cache,   nullptr, nullptr, false, true, false,
+                     block_table, max_blocks_per_seq, num_pages, nullptr, 0,       o,     lse};
+  return prompt_attn(problem, c, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_dense_attn_prefill_paged_fp8(const msa_problem_t* problem, const void* q, const void* k8_cache,
+                                              const void* v8_cache, const float* k_scale, const float* v_scale,
+                                              const int32_t* block_table, int32_t max_blocks_per_seq,
+                                              int64_t num_pages, void* o, float* lse, void* workspace,
+                                              size_t workspace_bytes, msa_stream_t stream) {
+  const PromptCall c{q,           k8_cache,           v8_cache,  k_scale, v_scale, true, true, false,
+                     block_table, max_blocks_per_seq, num_pages, nullptr, 0,       o,    lse};
+  return prompt_attn(problem, c, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_tree_attn_paged(const msa_problem_t* problem, const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* block_table, int32_t max_blocks_per_seq, int64_t num_pages,
+                                 const int32_t* visible, int32_t mask_words, void* o, float* lse, void* workspace,
+                                 size_t workspace_bytes, msa_stream_t stream) {
+  const PromptCall c{q,           k_cache,            v_cache,   nullptr, nullptr,    false, true, true,
+                     block_table, max_blocks_per_seq, num_pages, visible, mask_words, o,     lse};
+  return prompt_attn(problem, c, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_tree_attn_paged_fp8(const msa_problem_t* problem, const void* q, const void* k8_cache,
+                                     const void* v8_cache, const float* k_scale, const float* v_scale,
+                                     const int32_t* block_table, int32_t max_blocks_per_seq, int64_t num_pages,
+                                     const int32_t* visible, int32_t mask_words, void* o, float* lse, void* workspace,
+                                     size_t workspace_bytes, msa_stream_t stream) {
+  const PromptCall c{q,           k8_cache,           v8_cache,  k_scale, v_scale,    true, true, true,
+                     block_table, max_blocks_per_seq, num_pages, visible, mask_words, o,    lse};
+  return prompt_attn(problem, c, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_extend_workspace_size(int32_t num_seqs, size_t* bytes) {
+  if (!bytes || num_seqs < 1) return MSA_ERR_INVALID_ARG;
+  if (num_seqs > (1 << 20)) return MSA_ERR_UNSUPPORTED;
+  *bytes = extend_bytes(num_seqs);
+  return MSA_OK;
+}
+
+msa_status_t msa_extend_block_table(int32_t num_seqs, const int32_t* lengths, const int32_t* new_tokens,
+                                    int64_t capacity, const int32_t* free_pages, int32_t num_free,
+                                    const int32_t* taken, int64_t num_pages, int32_t* block_table,
+                                    int32_t max_blocks_per_seq, int32_t* new_lengths, int32_t* cu_seqlens_q,
+                                    int32_t* cu_seqlens_k, int64_t* slots, int32_t* positions, int32_t* taken_out,
+                                    void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  t_stage = -1;
+  t_error_detail[0] = 0;
+  if (num_seqs < 1 || !lengths || !new_tokens || !block_table || !cu_seqlens_q || !cu_seqlens_k || !taken_out)
+    return MSA_ERR_INVALID_ARG;
+  if (capacity < 0 || capacity > 0x7FFFFFFFLL || (capacity > 0 && (!slots || !positions))) return MSA_ERR_INVALID_ARG;
+  if (num_free < 0 || (num_free > 0 && !free_pages) || max_blocks_per_seq < 1) return MSA_ERR_INVALID_ARG;
+  if (num_pages < 1 || num_pages * 128 >= (1LL << 31)) return MSA_ERR_INVALID_ARG;
+  if (num_seqs > (1 << 20)) return MSA_ERR_UNSUPPORTED;
+  if (!aligned4(lengths) || !aligned4(new_tokens) || !aligned4(free_pages) || !aligned4(taken) ||
+      !aligned4(block_table) || !aligned4(new_lengths) || !aligned4(cu_seqlens_q) || !aligned4(cu_seqlens_k) ||
+      !aligned8(slots) || !aligned4(positions) || !aligned4(taken_out))
+    return MSA_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < extend_bytes(num_seqs)) return MSA_ERR_WORKSPACE;
+  if (reinterpret_cast<uintptr_t>(workspace) % kAlign) return MSA_ERR_ALIGNMENT;
+  DeviceFacts dev;
+  const msa_status_t st = device_facts(dev);
+  if (st != MSA_OK) return st;
+  ExtendParams p{};
+  p.num_seqs = num_seqs;
+  p.lengths = lengths;
+  p.new_tokens = new_tokens;
+  p.capacity = capacity;
+  p.max_len = static_cast<long long>(max_blocks_per_seq) * 128;
+  if (p.max_len > (1LL << 30)) p.max_len = 1LL << 30;
+  p.free_pages = free_pages;
+  p.num_free = num_free;
+  p.n_pages = num_pages;
+  p.taken = taken;
+  p.taken_out = taken_out;
+  p.block_table = block_table;
+  p.bt_stride = max_blocks_per_seq;
+  p.new_lengths = new_lengths;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.slots = reinterpret_cast<long long*>(slots);
+  p.positions = positions;
+  p.hdr = static_cast<WsHeader*>(workspace);
+  p.page_base = at<int32_t>(workspace, align_up(sizeof(WsHeader)));
+  return cuda_status(launch_extend(p, dev.sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+msa_status_t msa_append_workspace_size(int64_t num_pages, size_t* bytes) {
+  if (!bytes || num_pages < 1 || num_pages * 128 >= (1LL << 31)) return MSA_ERR_INVALID_ARG;
+  *bytes = append_bytes(num_pages);
+  return MSA_OK;
+}
+
+msa_status_t msa_append_paged(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                              int64_t k_idx_stride, const int64_t* slots, int64_t tokens, int32_t num_kv_heads,
+                              int32_t index_dim, void* k_cache, void* v_cache, void* k_idx_cache, int64_t num_pages,
+                              void* workspace, size_t workspace_bytes, msa_stream_t stream) {
+  if (num_kv_heads < 1) return MSA_ERR_INVALID_ARG;
+  if (num_kv_heads > 1024 || (k_idx_cache && index_dim != 64 && index_dim != 128)) return MSA_ERR_UNSUPPORTED;
+  if (!k_idx_cache && k_idx) return MSA_ERR_INVALID_ARG;
+  const AppendRows rows[3] = {{k, k_stride, num_kv_heads * 128, k_cache, nullptr},
+                              {v, v_stride, num_kv_heads * 128, v_cache, nullptr},
+                              {k_idx, k_idx_stride, index_dim, k_idx_cache, nullptr}};
+  return append_rows(rows, k_idx_cache ? 3 : 2, slots, tokens, num_pages, false, workspace, workspace_bytes, stream);
+}
+
+msa_status_t msa_append_paged_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const void* k_idx,
+                                  int64_t k_idx_stride, const int64_t* slots, int64_t tokens, int32_t num_kv_heads,
+                                  void* k8_cache, void* v8_cache, float* k_scale, float* v_scale, void* k_idx8_cache,
+                                  float* k_idx_scale, int64_t num_pages, void* workspace, size_t workspace_bytes,
+                                  msa_stream_t stream) {
+  if (num_kv_heads < 1) return MSA_ERR_INVALID_ARG;
+  if (num_kv_heads > 1024) return MSA_ERR_UNSUPPORTED;
+  if (!k_idx8_cache && (k_idx || k_idx_scale)) return MSA_ERR_INVALID_ARG;
+  const AppendRows rows[3] = {{k, k_stride, num_kv_heads * 128, k8_cache, k_scale},
+                              {v, v_stride, num_kv_heads * 128, v8_cache, v_scale},
+                              {k_idx, k_idx_stride, 128, k_idx8_cache, k_idx_scale}};
+  return append_rows(rows, k_idx8_cache ? 3 : 2, slots, tokens, num_pages, true, workspace, workspace_bytes, stream);
 }
 
 msa_status_t msa_read_device_status(const void* workspace, uint32_t* flags, msa_stream_t stream) {

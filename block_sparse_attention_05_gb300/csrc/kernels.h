@@ -319,6 +319,92 @@ struct DenseMaps {
 };
 cudaError_t launch_dense_decode(const DenseMaps& maps, const DenseDecodeParams& p, bool fp8, cudaStream_t stream);
 
+// ---------------------------------------------------------------- dense attention of prompts and drafted trees
+constexpr int kPromptMaxCtas = 160;  // CTAs of the attention kernel at most (one per SM)
+// What the plan kernel leaves for the others.
+struct PromptPlan {
+  long long total;  // blocks of all items and KV heads
+  int n_items;
+  int runs;         // > 0: all blocks are cut into so many runs; 0: items are taken whole
+};
+struct PromptParams {
+  int num_seqs, hq, hkv, group, total_q, total_k, max_q, max_k, max_nb;
+  int tile_tokens;              // 128 / group: tokens of a tile; an item has two tiles
+  int ctas;                     // grid of the attention kernel
+  long long max_items;          // bound of the item buffers
+  const int32_t* cu_q;
+  const int32_t* cu_k;
+  const int32_t* block_table;   // [num_seqs, bt_stride], or null: packed keys
+  int bt_stride;
+  long long n_pages;
+  const float* k_scale;         // fp8: [n_pages, hkv]
+  const float* v_scale;
+  const int32_t* visible;       // [total_q, mask_words] bits of the new tokens that a new token sees, or null: causal
+  int mask_words;
+  __nv_bfloat16* o;             // [total_q, hq, 128]
+  float* lse;                   // [total_q, hq]
+  float scale_log2;             // softmax scale * log2(e)
+  // workspace
+  WsHeader* hdr;
+  PromptPlan* plan;
+  SeqInfo* seq;                 // [num_seqs]
+  int32_t* item_base;           // [num_seqs] items before a sequence's
+  int2* items;                  // [max_items] (sequence, first token)
+  int32_t* block_base;          // [max_items] with runs: blocks of one KV head before an item's
+  float* part_o;                // [ctas, 2, 256, 128]: slot 1 the item that goes on behind the run; null: never runs
+  float2* part_ml;              // [ctas, 2, 256] (reference, sum)
+};
+bool prompt_may_split(int max_nb);  // whether a call with so many key blocks can be cut into runs
+struct PromptMaps {
+  CUtensorMap q;     // boxes of 64 dims of a group's heads of tile_tokens tokens
+  CUtensorMap k, v;  // boxes of 128 rows of a head (64 dims in bf16, 128 codes in fp8)
+};
+cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bool fp8, cudaStream_t stream);
+
+// ---------------------------------------------------------------- filling a paged cache
+struct ExtendParams {
+  int num_seqs;
+  const int32_t* lengths;       // [num_seqs] cached tokens
+  const int32_t* new_tokens;    // [num_seqs]
+  long long capacity;           // entries of slots and positions
+  long long max_len;            // tokens that a row of the table can hold
+  const int32_t* free_pages;    // [num_free]
+  int num_free;
+  long long n_pages;
+  const int32_t* taken;         // free pages handed out before, or null: none
+  int32_t* taken_out;
+  int32_t* block_table;         // [num_seqs, bt_stride]
+  int bt_stride;
+  int32_t* new_lengths;         // [num_seqs] or null
+  int32_t* cu_q;                // [num_seqs + 1]
+  int32_t* cu_k;                // [num_seqs + 1]
+  long long* slots;             // [capacity]
+  int32_t* positions;           // [capacity]
+  WsHeader* hdr;
+  int32_t* page_base;           // [num_seqs] workspace: place in the free list of a sequence's first new page
+};
+cudaError_t launch_extend(const ExtendParams& p, int sms, cudaStream_t stream);
+
+// One tensor of new rows and its cache.
+struct AppendPlane {
+  const __nv_bfloat16* x;  // [tokens] rows of `width`, `stride` elements apart
+  long long stride;
+  int width;
+  void* cache;             // [n_pages * 128, width] bf16, or E4M3 codes with
+  float* scale;            // [n_pages, width / 128]
+};
+struct AppendParams {
+  AppendPlane plane[3];
+  int planes;
+  const long long* slots;  // [tokens], -1: no row
+  long long tokens;
+  long long n_pages;
+  WsHeader* hdr;           // null (bf16): no flags
+  uint32_t* marks;         // fp8: [n_pages] behind the header
+};
+cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_append_fp8(const AppendParams& p, size_t clear_bytes, cudaStream_t stream);
+
 // ---------------------------------------------------------------- eviction
 struct EvictParams {
   int num_seqs, hkv, max_k, total_k, budget, recent;

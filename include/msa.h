@@ -134,7 +134,10 @@ typedef enum msa_op {
   MSA_OP_INDEX_PROLOGUE = 11,    /* msa_index_prologue */
   MSA_OP_QUANTIZE_INDEX_FP8 = 12,/* msa_quantize_index_fp8 */
   MSA_OP_DENSE_ATTN_DECODE = 13, /* msa_dense_attn_decode_paged(_fp8), weight = NULL */
-  MSA_OP_DENSE_ATTN_DECODE_WEIGHT = 14 /* the same with a weight */
+  MSA_OP_DENSE_ATTN_DECODE_WEIGHT = 14, /* the same with a weight */
+  /* 15 is no operation */
+  MSA_OP_DENSE_ATTN_PREFILL = 16, /* msa_dense_attn_prefill, msa_dense_attn_prefill_paged(_fp8) */
+  MSA_OP_TREE_ATTN = 17          /* msa_tree_attn_paged(_fp8) */
 } msa_op_t;
 
 /* Workspace bytes that `op` needs for `problem` (host-only; no CUDA call).
@@ -550,6 +553,142 @@ msa_status_t msa_add_rms_norm(const void *x, const void *residual, const void *g
 msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const void *gamma, int64_t rows,
                                   int32_t d_model, float eps, void *sum, void *y8, float *y_scale,
                                   msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Many new tokens at once, in the full-attention layers: prompts and chunks of
+ * prompts, and trees of drafted tokens.
+ *
+ * msa_dense_attn_prefill: exact causal softmax attention.  For new token t of a
+ * sequence (query row t, at position kv_len - q_len + t) and query head h of
+ * group g, over the keys j <= kv_len - q_len + t:
+ *   s[t,h,j] = softmax_scale * q_t,h . k_j,g,   lse = ln sum_j exp(s),
+ *   o = sum_j exp(s - lse) v_j,g.
+ *   problem     any packed batch: q_len <= kv_len per sequence, either may be 0;
+ *               index_dim and topk are not looked at.  head_dim = block_size =
+ *               128; any group size num_q_heads / num_kv_heads from 1 to 128,
+ *               num_kv_heads <= 1024, num_seqs <= 2^20, total_q < 2^25,
+ *               max_seqlen_k <= 2^30, softmax_scale < 1e30.
+ *   q, k, v     packed, as in the conventions above.
+ *   o, lse      written for every query row.
+ * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (about 42 MB, whatever the lengths, plus 12
+ * bytes per pair of tiles of 128 / group tokens).
+ * Numbers.  Logits, references, sums, O and lse are fp32; a weight that meets V is
+ * rounded to bf16 (2^-8 of the weight), the sum takes it unrounded.  Exponentials
+ * are the hardware's 2^x (2^-22 of the value).  Any finite logit gives finite
+ * results; a logit of +inf gives NaN, keys of -inf do not count.  A key that a
+ * query does not see does not count whatever its K holds; an inf or NaN in V shows
+ * in the queries that see a key of its block of 128.  What lies past a sequence's
+ * last key does not matter.  The same inputs give the same bits.
+ * Lengths that contradict the host sizes make the kernels skip the call
+ * (MSA_DEVICE_BAD_SEQLENS).
+ * ------------------------------------------------------------------------ */
+msa_status_t msa_dense_attn_prefill(const msa_problem_t *problem, const void *q, const void *k, const void *v,
+                                    void *o, float *lse, void *workspace, size_t workspace_bytes,
+                                    msa_stream_t stream);
+
+/* The same over paged keys (the new tokens' rows are in the cache already, see
+ * msa_append_paged): k_cache, v_cache, block_table, max_blocks_per_seq and
+ * num_pages as for msa_dense_attn_decode_paged; a page outside the cache reads as
+ * zeros (MSA_DEVICE_BAD_INDEX). */
+msa_status_t msa_dense_attn_prefill_paged(const msa_problem_t *problem, const void *q, const void *k_cache,
+                                          const void *v_cache, const int32_t *block_table,
+                                          int32_t max_blocks_per_seq, int64_t num_pages, void *o, float *lse,
+                                          void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* The same over E4M3 pages with one scale per (page, KV head): the attention over
+ * the dequantized values.  Scales from 2^-100 to 2^100. */
+msa_status_t msa_dense_attn_prefill_paged_fp8(const msa_problem_t *problem, const void *q, const void *k8_cache,
+                                              const void *v8_cache, const float *k_scale, const float *v_scale,
+                                              const int32_t *block_table, int32_t max_blocks_per_seq,
+                                              int64_t num_pages, void *o, float *lse, void *workspace,
+                                              size_t workspace_bytes, msa_stream_t stream);
+
+/* Attention of a tree of drafted tokens: the q_len new tokens of a sequence (the
+ * drafts, in the cache's last q_len slots) see every cached key before them and,
+ * of one another, what a mask says.
+ *   visible     int32 [total_q, mask_words], mask_words >= ceil(max_seqlen_q /
+ *               32), 4-byte aligned: bit d % 32 of word d / 32 of draft t's row is
+ *               set when draft t sees draft d of its sequence (its ancestors and
+ *               itself).  Bits from q_len on do not count.  A draft that sees no
+ *               key at all has o = 0, lse = -inf.
+ * Everything else as for msa_dense_attn_prefill_paged; workspace: op
+ * MSA_OP_TREE_ATTN. */
+msa_status_t msa_tree_attn_paged(const msa_problem_t *problem, const void *q, const void *k_cache,
+                                 const void *v_cache, const int32_t *block_table, int32_t max_blocks_per_seq,
+                                 int64_t num_pages, const int32_t *visible, int32_t mask_words, void *o, float *lse,
+                                 void *workspace, size_t workspace_bytes, msa_stream_t stream);
+msa_status_t msa_tree_attn_paged_fp8(const msa_problem_t *problem, const void *q, const void *k8_cache,
+                                     const void *v8_cache, const float *k_scale, const float *v_scale,
+                                     const int32_t *block_table, int32_t max_blocks_per_seq, int64_t num_pages,
+                                     const int32_t *visible, int32_t mask_words, void *o, float *lse,
+                                     void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Filling a paged cache: tables from lengths, and the new tokens' rows.
+ *
+ * msa_extend_block_table: sequence s, of lengths[s] cached tokens, gets
+ * new_tokens[s] more.  Its ceil((lengths + new) / 128) - ceil(lengths / 128) new
+ * blocks take the next free pages, sequence by sequence:
+ *   free_pages   int32 [num_free], the first *taken of which are gone (taken =
+ *                NULL: none); *taken_out (may be taken) is what is gone behind the
+ *                call.
+ *   block_table  int32 [num_seqs, max_blocks_per_seq]: the new blocks' entries are
+ *                written, the others left as they were.
+ *   new_lengths  int32 [num_seqs] (may be lengths, or NULL): lengths + new.
+ *   cu_seqlens_q, cu_seqlens_k  int32 [num_seqs + 1]: prefix sums of new_tokens and
+ *                of lengths + new_tokens, as a problem of the grown cache has them.
+ *   slots        int64 [capacity], 8-byte aligned: the cache row of each new token,
+ *                sequence by sequence; -1 past the last one.
+ *   positions    int32 [capacity]: its place in its sequence; 0 past the last one.
+ *   num_pages    pages of the cache; a page outside it (in the table's last old
+ *                block or the free list), and a block that the list has no page
+ *                for, becomes -1 in the table and its tokens' slots -1
+ *                (MSA_DEVICE_BAD_INDEX).
+ * Negative lengths, sequences that the table has no room for, *taken past the list
+ * and more new tokens than `capacity` (or 2^31 keys) make the call do nothing but
+ * fill slots with -1 and positions and prefix sums with 0
+ * (MSA_DEVICE_BAD_SEQLENS).  num_seqs <= 2^20.  Workspace:
+ * msa_extend_workspace_size. */
+msa_status_t msa_extend_workspace_size(int32_t num_seqs, size_t *bytes);
+msa_status_t msa_extend_block_table(int32_t num_seqs, const int32_t *lengths, const int32_t *new_tokens,
+                                    int64_t capacity, const int32_t *free_pages, int32_t num_free,
+                                    const int32_t *taken, int64_t num_pages, int32_t *block_table,
+                                    int32_t max_blocks_per_seq, int32_t *new_lengths, int32_t *cu_seqlens_q,
+                                    int32_t *cu_seqlens_k, int64_t *slots, int32_t *positions, int32_t *taken_out,
+                                    void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* New tokens' rows into their slots: k_cache[slots[i]] = k[i] and so on.
+ *   k, v       bf16 [tokens, num_kv_heads, 128], tokens k_stride (v_stride)
+ *              elements apart: slices of a wider projection's output, say.
+ *   k_idx      bf16 [tokens, index_dim] (k_idx_stride apart) with k_idx_cache, or
+ *              NULL for both.  index_dim 64 or 128.
+ *   slots      int64 [tokens], 8-byte aligned, distinct; -1: the token has no row.
+ *              Others outside the cache are skipped (MSA_DEVICE_BAD_INDEX).
+ * Strides are multiples of 8 and at least a row; pointers 16-byte aligned.  workspace
+ * may be NULL (no device flags) or has 256 bytes.  num_kv_heads <= 1024. */
+msa_status_t msa_append_paged(const void *k, int64_t k_stride, const void *v, int64_t v_stride, const void *k_idx,
+                              int64_t k_idx_stride, const int64_t *slots, int64_t tokens, int32_t num_kv_heads,
+                              int32_t index_dim, void *k_cache, void *v_cache, void *k_idx_cache, int64_t num_pages,
+                              void *workspace, size_t workspace_bytes, msa_stream_t stream);
+
+/* The same into E4M3 pages with one scale per (page, head) (k_idx8_cache with
+ * k_idx_scale [num_pages], index_dim 128).  The tokens that follow one another into
+ * one page -- a page's tokens have to, 128 at most -- are taken together: with L the
+ * smallest row among them, the page's rows below L hold values already;
+ *   scale' = max(scale if L > 0, fp32(max |new| / 448))   (1 when that is 0; a max
+ *            |new| below 2^-118 counts as 0, inf and NaN do not count)
+ *   code   = round-to-nearest-even, saturated, of the exact x * 448 / max |new| where
+ *            the new rows set the scale, else of fp32(x / scale),
+ * and where scale' > scale the codes of the rows below L become those of code * scale *
+ * 448 / max |new| (two fp32 roundings).  Other rows are left as they
+ * were.  A page that comes twice raises MSA_DEVICE_BAD_INDEX and its contents are
+ * undefined.  Workspace: msa_append_workspace_size. */
+msa_status_t msa_append_workspace_size(int64_t num_pages, size_t *bytes);
+msa_status_t msa_append_paged_fp8(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                  const void *k_idx, int64_t k_idx_stride, const int64_t *slots, int64_t tokens,
+                                  int32_t num_kv_heads, void *k8_cache, void *v8_cache, float *k_scale,
+                                  float *v_scale, void *k_idx8_cache, float *k_idx_scale, int64_t num_pages,
+                                  void *workspace, size_t workspace_bytes, msa_stream_t stream);
 
 /* Waits for `stream`, then returns in *flags the MSA_DEVICE_* bits that the
  * last call on this workspace raised (0 = none).  workspace = NULL reads the
