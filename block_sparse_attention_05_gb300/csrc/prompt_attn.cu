@@ -256,7 +256,7 @@ struct PartWalker {
 };
 
 // ---------------------------------------------------------------- attention kernel
-// Warps 0..3 and 4..7: softmax and output of a tile each; 8: MMAs; 9: loads; fp8: 12..15 widen codes.
+// Warps 0..3 and 4..7: softmax and output of a tile each; 8 and 10: the MMAs of each; 9: loads; fp8: 12..15 widen codes.
 template <bool FP8>
 struct PromptCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
@@ -272,7 +272,7 @@ struct PromptSmem {
   uint64_t full[5], empty[5];            // a stage holds a tile / its MMAs are done
   uint64_t code_full[4], code_empty[4];  // fp8
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], o_full[2];  // by warpgroup
+  uint64_t s_full[2], p_full[2], o_full[2], turn[2];  // by warpgroup
   uint64_t ml_full, o_free, mma_done;
   float2 ml[2][128];
   float scale[8];       // fp8: scales of the last tiles (no more than 3 behind the one that a warpgroup is at)
@@ -291,6 +291,13 @@ __device__ __forceinline__ void tmem_st_16cols(uint32_t taddr, const uint32_t (&
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// True in one lane of the (converged) warp, the same one each time: MMAs and their commits come from one thread.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // Bits of the keys j0 .. j0 + 31 that a new token sees: every key below `past`, and of the `n` new ones behind it those
@@ -327,22 +334,24 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(&sm.full[i], FP8 ? 4 : 1);
-      mbar_init(&sm.empty[i], 1);
+      mbar_init(&sm.empty[i], 2);
     }
     for (int i = 0; i < C::kCodeStages; ++i) {
       mbar_init(&sm.code_full[i], 1);
       mbar_init(&sm.code_empty[i], 4);
     }
     mbar_init(&sm.q_full, 1);
-    mbar_init(&sm.q_empty, 1);
+    mbar_init(&sm.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 4);
       mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.turn[i], 1);
     }
     mbar_init(&sm.ml_full, 8);
     mbar_init(&sm.o_free, 8);
-    mbar_init(&sm.mma_done, 1);
+    mbar_init(&sm.mma_done, 2);
+    mbar_arrive(&sm.turn[0]);
     sm.abort_flag = 0;
     sm.err = 0;
     fence_mbar_init();
@@ -439,62 +448,104 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         mbar_wait(&full[f % kLanding], (f / kLanding) & 1, nullptr);
       if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, nullptr);
     }
-  } else if (warp == 8) {
+  } else if (warp == 8 || warp == 10) {
     // ------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      const uint32_t idesc_s = idesc_bf16(128, 128, false), idesc_o = idesc_bf16(128, kHeadDim, true);
-      uint32_t tiles = 0, parts = 0;  // tiles before the part's, parts before it
-      uint32_t ps[2] = {0, 0};        // P taken, by warpgroup
-      bool ok = true;
-      while (ok && walk.next(g)) {
-        // step n: warpgroup n & 1, S (then P V) of its next block
-        const int steps = g.one ? g.count : 2 * g.count;
-        auto issue_s = [&](int n) {
-          const int b = n & 1, blk = g.one ? n : n >> 1;
-          const uint32_t tile = tiles + 2 * blk, st = tile % C::kStages;
-          if (n == 0 && !mbar_wait(&sm.q_full, parts & 1, abort_flag)) return false;
-          if ((g.one || b == 0) && !mbar_wait(&sm.full[st], (tile / C::kStages) & 1, abort_flag)) return false;
-          tc_fence_after();
-          const uint32_t qa = smem_u32(q_buf + (g.one ? 0 : b * 32768)), ka = smem_u32(ring + st * C::kTile);
+    // A warp for the MMAs of each warpgroup.  They read shared memory at nearly its full rate, under which a look at a
+    // barrier takes 160 clocks, and only one or two MMAs (of 64 clocks) wait in the tensor core's queue: one warp that
+    // waits and issues leaves it idle for a third of the time.  So one warp waits for its operands while the other issues,
+    // and they take turns (without turns their MMAs mix, and both warpgroups wait for both).  The turn is passed on while
+    // three MMAs are still to be issued, which covers its way.
+    const int b = warp == 8 ? 0 : 1;
+    const uint32_t idesc_s = idesc_bf16(128, 128, false), idesc_o = idesc_bf16(128, kHeadDim, true);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(q_buf), 16, 1024), k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(ring), 16384, 1024);
+    const uint32_t s_col = tmem + C::kColS + b * 128, o_col = tmem + C::kColO + b * 128;
+    uint32_t tiles = 0, parts = 0;  // tiles before the part's, parts before it
+    uint32_t p_ph = 0, turn_ph = 0;
+    bool ok = true;
+    while (ok && walk.next(g)) {
+      // step i: P V of the warpgroup's block i, S of its block i + 1
+      const int every = g.one ? 2 : 1, first = g.one ? b : 0;          // its blocks: first, first + every, ...
+      const int steps = g.one ? (g.count + 1) / 2 : g.count;           // of both warps; the second may have one block less
+      const int blocks = g.one ? (g.count + 1 - b) / 2 : g.count;
+      const uint64_t qa = q_desc + (g.one ? 0 : b * 2048);
+      ok = mbar_wait_warp(&sm.q_full, parts & 1, abort_flag);
+      for (int i = -1; ok && i < steps; ++i) {
+        const bool pv = i >= 0 && i < blocks, s = i + 1 < blocks;
+        const uint32_t v_tile = tiles + 2 * (first + i * every) + 1, k_tile = v_tile - 1 + 2 * every;
+        const uint32_t v_st = v_tile % C::kStages, k_st = k_tile % C::kStages;
+        // With three stages, K of a warpgroup's next block may land only where V of this one has been.
+        const bool apart = C::kStages < 5 && g.one && pv;
+        if (s && !apart) ok = mbar_wait_warp(&sm.full[k_st], (k_tile / C::kStages) & 1, abort_flag);
+        if (pv) {
+          ok = ok && mbar_wait_warp(&sm.full[v_st], (v_tile / C::kStages) & 1, abort_flag);
+          // O of the part before has been read
+          if (i == 0 && parts > 0) ok = ok && mbar_wait_warp(&sm.o_free, (parts - 1) & 1, abort_flag);
+          ok = ok && mbar_wait_warp(&sm.p_full[b], p_ph, abort_flag);
+          p_ph ^= 1;
+        }
+        ok = ok && mbar_wait_warp(&sm.turn[b], turn_ph, abort_flag);
+        turn_ph ^= 1;
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t ka = k_desc + k_st * 2048, va = v_desc + v_st * 2048;
+        const uint32_t more = i > 0 ? 1u : 0u;
+        auto issue_pv = [&](bool pass) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-            umma_bf16(tmem + C::kColS + b * 128, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), idesc_s,
-                      kk ? 1u : 0u);
+            umma_bf16_ts(o_col, s_col + kk * 8, va + kk * 128, idesc_o, kk ? 1u : more);
+            if (kk == 4 && pass) mbar_arrive(&sm.turn[b ^ 1]);
+          }
+        };
+        // S follows P V of the block before: in order on the tensor cores, so S's columns are free
+        auto issue_s = [&] {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
+            umma_bf16(s_col, qa + off, ka + off, idesc_s, kk ? 1u : 0u);
+            if (kk == 4) mbar_arrive(&sm.turn[b ^ 1]);
           }
           umma_commit(&sm.s_full[b]);
-          if (g.one || b == 1) umma_commit(&sm.empty[st]);
-          if (n == steps - 1) umma_commit(&sm.q_empty);
-          return true;
         };
-        auto issue_pv = [&](int n) {
-          const int b = n & 1, blk = g.one ? n : n >> 1;
-          const uint32_t tile = tiles + 2 * blk + 1, st = tile % C::kStages;
-          if (!mbar_wait(&sm.p_full[b], ps[b] & 1, abort_flag)) return false;
-          ++ps[b];
-          if ((g.one || b == 0) && !mbar_wait(&sm.full[st], (tile / C::kStages) & 1, abort_flag)) return false;
-          // O of the part before has been read
-          if (n == 0 && parts > 0 && !mbar_wait(&sm.o_free, (parts - 1) & 1, abort_flag)) return false;
+        // Every stage and the queries are given back by both warps (by the one that used it, for both, where one did).
+        auto give = [&](uint64_t* bar) {
+          umma_commit(bar);
+          if (g.one) umma_commit(bar);
+        };
+        if (elect_one()) {
+          if (pv) issue_pv(!s);
+          if (s && !apart) issue_s();
+          if (!pv && !s) mbar_arrive(&sm.turn[b ^ 1]);
+          if (pv) {
+            if (!s) umma_commit(&sm.o_full[b]);
+            give(&sm.empty[v_st]);
+          }
+          if (s && !apart) give(&sm.empty[k_st]);
+        }
+        __syncwarp();
+        if (s && apart) {
+          ok = mbar_wait_warp(&sm.full[k_st], (k_tile / C::kStages) & 1, abort_flag);
+          if (!ok) break;
           tc_fence_after();
-          const uint32_t va = smem_u32(ring + st * C::kTile);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            umma_bf16_ts(tmem + C::kColO + b * 128, tmem + C::kColS + b * 128 + kk * 8, sdesc_sw128(va + kk * 2048, 16384, 1024),
-                         idesc_o, (n < 2 && kk == 0) ? 0u : 1u);
-          if (g.one || b == 1) umma_commit(&sm.empty[st]);
-          if (n >= steps - 2) umma_commit(&sm.o_full[b]);
-          return true;
-        };
-        // S of a warpgroup's next block follows its P V: in order on the tensor cores, so S's columns are free
-        ok = issue_s(0) && (steps < 2 || issue_s(1));
-        for (int n = 0; ok && n < steps; ++n) ok = issue_pv(n) && (n + 2 >= steps || issue_s(n + 2));
-        tiles += 2 * g.count;
-        ++parts;
+          if (elect_one()) {
+            issue_s();
+            give(&sm.empty[k_st]);
+          }
+          __syncwarp();
+        }
+        if (i + 1 == (blocks > 0 ? blocks - 1 : 0)) {  // its last S of the part (or the first step, if it has none)
+          if (elect_one()) umma_commit(&sm.q_empty);
+          __syncwarp();
+        }
       }
-      if (!ok) gave_up();
-      umma_commit(&sm.mma_done);
-      mbar_wait(&sm.mma_done, 0, nullptr);
+      tiles += 2 * g.count;
+      ++parts;
     }
+    if (!ok && lane == 0) gave_up();
+    // every MMA done before the tensor memory is given back
+    if (elect_one()) umma_commit(&sm.mma_done);
+    __syncwarp();
+    mbar_wait_warp(&sm.mma_done, 0, nullptr);
   } else if (warp < 8) {
     // ------------------------------------------------------------ softmax and output
     regs_claim<C::kSoftmaxRegs>();
