@@ -853,7 +853,7 @@ msa_status_t derive_prompt(const msa_problem_t* p, PromptShape& d) {
 }
 
 struct PromptLayout {
-  size_t hdr, plan, seq, item_base, items, block_base, part_o, part_ml, total;
+  size_t hdr, plan, seq, item_base, items, run_item, part_o, part_ml, total;
 };
 
 PromptLayout prompt_layout(const PromptShape& d) {
@@ -868,8 +868,8 @@ PromptLayout prompt_layout(const PromptShape& d) {
   L.plan = take(sizeof(PromptPlan));
   L.seq = take(sizeof(SeqInfo) * d.S);
   L.item_base = take(sizeof(int32_t) * d.S);
-  L.items = take(sizeof(int2) * d.max_items);
-  L.block_base = take(sizeof(int32_t) * d.max_items);
+  L.items = take(sizeof(PromptItem) * d.max_items);
+  L.run_item = take(sizeof(int32_t) * kPromptMaxCtas);
   if (prompt_may_split(d.max_nb)) {
     L.part_o = take(sizeof(float) * kPromptMaxCtas * 2 * 256 * kHeadDim);
     L.part_ml = take(sizeof(float2) * kPromptMaxCtas * 2 * 256);
@@ -960,8 +960,8 @@ msa_status_t prompt_attn(const msa_problem_t* problem, const PromptCall& c, void
   p.plan = at<PromptPlan>(ws, L.plan);
   p.seq = at<SeqInfo>(ws, L.seq);
   p.item_base = at<int32_t>(ws, L.item_base);
-  p.items = at<int2>(ws, L.items);
-  p.block_base = at<int32_t>(ws, L.block_base);
+  p.items = at<PromptItem>(ws, L.items);
+  p.run_item = at<int32_t>(ws, L.run_item);
   p.part_o = prompt_may_split(d.max_nb) ? at<float>(ws, L.part_o) : nullptr;
   p.part_ml = prompt_may_split(d.max_nb) ? at<float2>(ws, L.part_ml) : nullptr;
   StageScope scope(MSA_STAGE_ATTN, reinterpret_cast<cudaStream_t>(stream));

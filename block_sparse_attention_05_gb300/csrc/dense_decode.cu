@@ -879,37 +879,6 @@ struct TcSmem {
 constexpr size_t kTcSmemBytes = 7 * 32768 + sizeof(TcSmem);  // three stages and Q; or two, two of codes and Q
 static_assert(kTcSmemBytes <= 227 * 1024, "one CTA's shared memory");
 
-// Element i of lane t4 of four goes to element t4 of lane i.
-__device__ __forceinline__ void quad_transpose(uint32_t (&x)[4], int t4) {
-#pragma unroll
-  for (int d = 1; d <= 2; d <<= 1)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i & d) continue;
-      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, t4 & d ? x[i] : x[i | d], d);
-      if (t4 & d) x[i] = got;
-      else x[i | d] = got;
-    }
-}
-
-// 16 rows (TMEM lanes, from a multiple of 16) of 32 columns: registers 4 i + {0, 1} hold columns 8 i + 2 (lane % 4) +
-// {0, 1} of row lane / 4, registers 4 i + {2, 3} those of row lane / 4 + 8.
-__device__ __forceinline__ void tmem_ld_16rows_32cols(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_ld_wait_regs16(uint32_t (&r)[16]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-               :
-               : "memory");
-}
-
 template <bool FP8, bool LOGITS>
 __global__ void __launch_bounds__(TcCfg<FP8>::kThreads, 1)
     dense_split_tc_kernel(const __grid_constant__ DenseMaps maps, DenseDecodeParams p) {

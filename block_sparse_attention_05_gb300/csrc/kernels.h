@@ -327,6 +327,13 @@ struct PromptPlan {
   int n_items;
   int runs;         // > 0: all blocks are cut into so many runs; 0: items are taken whole
 };
+// Up to two tiles of new tokens of a sequence, for every KV head.
+struct PromptItem {
+  int seq, t0;                     // its first token
+  int q_start, q_len, k_start, past;  // the sequence: first query row, new tokens, first key row, cached keys
+  int blocks;                      // key blocks of the item
+  int base;                        // with runs: blocks of one KV head before it
+};
 struct PromptParams {
   int num_seqs, hq, hkv, group, total_q, total_k, max_q, max_k, max_nb;
   int tile_tokens;              // 128 / group: tokens of a tile; an item has two tiles
@@ -349,10 +356,11 @@ struct PromptParams {
   PromptPlan* plan;
   SeqInfo* seq;                 // [num_seqs]
   int32_t* item_base;           // [num_seqs] items before a sequence's
-  int2* items;                  // [max_items] (sequence, first token)
-  int32_t* block_base;          // [max_items] with runs: blocks of one KV head before an item's
-  float* part_o;                // [ctas, 2, 256, 128]: slot 1 the item that goes on behind the run; null: never runs
-  float2* part_ml;              // [ctas, 2, 256] (reference, sum)
+  PromptItem* items;            // [max_items]
+  int32_t* run_item;            // [kPromptMaxCtas] with runs: the item that each begins in
+  // [ctas, 2, 2 tiles, 32, 128, 4] four dims of 128 rows each: slot 1 the item that goes on behind the run; null: never runs
+  float* part_o;
+  float2* part_ml;              // [ctas, 2, 2, 128] (reference, sum)
 };
 bool prompt_may_split(int max_nb);  // whether a call with so many key blocks can be cut into runs
 struct PromptMaps {

@@ -141,20 +141,31 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     plan->runs = split ? static_cast<int>(min(total, static_cast<long long>(p.ctas))) : 0;
     plan->total = total;
   }
+  auto item = [&](int j, int base) {
+    const int s = find_seq(p.item_base, p.num_seqs, j), t0 = (j - p.item_base[s]) * per_item;
+    const SeqInfo si = p.seq[s];
+    return PromptItem{s, t0, si.q_start, si.q_len, si.k_start, si.kv_len - si.q_len, item_blocks(p, si, t0), base};
+  };
   if (split) {
-    // the items in order, with the blocks before each (of one KV head)
+    // the items in order, with the blocks before each (of one KV head), and the item that each run begins in
+    const int runs = static_cast<int>(min(total, static_cast<long long>(p.ctas)));
     long long carry = 0;
     for (int base = 0; base < items; base += kPlanThreads) {
       const int j = base + threadIdx.x;
-      int n = 0;
-      if (j < items) {
-        const int s = find_seq(p.item_base, p.num_seqs, j), t0 = (j - p.item_base[s]) * per_item;
-        n = item_blocks(p, p.seq[s], t0);
-        p.items[j] = make_int2(s, t0);
-      }
+      PromptItem it{};
+      if (j < items) it = item(j, 0);
       long long t;
-      const long long before = plan_scan(n, sh, &t);
-      if (j < items) p.block_base[j] = static_cast<int>(carry + before);  // total < ctas * max_nb: fits
+      const long long before = carry + plan_scan(it.blocks, sh, &t);
+      if (j < items) {
+        it.base = static_cast<int>(before);  // total < ctas * (max_nb + slack): fits
+        p.items[j] = it;
+        const long long lo = before * p.hkv, hi = lo + static_cast<long long>(it.blocks) * p.hkv;
+        for (int r = static_cast<int>((lo * runs + total - 1) / total); r < runs; ++r) {
+          const long long at = total * r / runs;
+          if (at >= hi) break;
+          if (at >= lo) p.run_item[r] = j;
+        }
+      }
       carry += t;
     }
     return;
@@ -170,8 +181,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   }
   __syncthreads();
   for (int j = threadIdx.x; j < items; j += kPlanThreads) {
-    const int s = find_seq(p.item_base, p.num_seqs, j), t0 = (j - p.item_base[s]) * per_item;
-    p.items[atomicAdd(&bins[item_blocks(p, p.seq[s], t0) >> shift], 1)] = make_int2(s, t0);
+    const PromptItem it = item(j, 0);
+    p.items[atomicAdd(&bins[it.blocks >> shift], 1)] = it;
   }
 }
 
@@ -184,33 +195,23 @@ struct Part {
   bool one;          // one tile of rows: its blocks go to the warpgroups in turn
 };
 
-// The item (of `items`) that holds unit u of a call that is cut into runs.
-__device__ __forceinline__ int item_of(const PromptParams& p, int items, long long u) {
-  int lo = 0, hi = items - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (static_cast<long long>(p.block_base[mid]) * p.hkv <= u) lo = mid;
-    else hi = mid - 1;
-  }
-  return lo;
-}
-
 // Every warp walks the same parts.
 struct PartWalker {
   const PromptParams& p;
   int items, runs, item, round;
   long long at, hi;
   __device__ explicit PartWalker(const PromptParams& params) : p(params) {
+    const int start = p.run_item[blockIdx.x];  // (without runs: not a value, and not used)
     items = p.plan->n_items;
     runs = p.plan->runs;
+    const long long total = p.plan->total;
     round = 0;
     item = 0;
     at = hi = 0;
-    if (runs > 0 && static_cast<int>(blockIdx.x) < runs) {
-      const long long total = p.plan->total;
+    if (static_cast<int>(blockIdx.x) < runs) {
       at = total * blockIdx.x / runs;
       hi = total * (blockIdx.x + 1) / runs;
-      item = item_of(p, items, at);
+      item = start;
     }
   }
   __device__ bool next(Part& g) {
@@ -228,29 +229,27 @@ struct PartWalker {
       j = static_cast<int>(i / p.hkv);
       g.head = static_cast<int>(i - static_cast<long long>(j) * p.hkv);
     }
-    const int2 it = p.items[j];
-    const SeqInfo si = p.seq[it.x];
-    const int n = item_blocks(p, si, it.y);
-    g.seq = it.x;
-    g.t0 = it.y;
-    g.q_start = si.q_start;
-    g.q_len = si.q_len;
-    g.k_start = si.k_start;
-    g.past = si.kv_len - si.q_len;
-    g.one = si.q_len - it.y <= p.tile_tokens;
+    const PromptItem it = p.items[j];
+    g.seq = it.seq;
+    g.t0 = it.t0;
+    g.q_start = it.q_start;
+    g.q_len = it.q_len;
+    g.k_start = it.k_start;
+    g.past = it.past;
+    g.one = it.q_len - it.t0 <= p.tile_tokens;
     if (runs > 0) {
-      const long long off = at - static_cast<long long>(p.block_base[j]) * p.hkv;
-      g.head = static_cast<int>(off / n);
-      blk = static_cast<int>(off - static_cast<long long>(g.head) * n);
-      g.count = static_cast<int>(min(static_cast<long long>(n - blk), hi - at));
+      const long long off = at - static_cast<long long>(it.base) * p.hkv;
+      g.head = static_cast<int>(off / it.blocks);
+      blk = static_cast<int>(off - static_cast<long long>(g.head) * it.blocks);
+      g.count = static_cast<int>(min(static_cast<long long>(it.blocks - blk), hi - at));
       at += g.count;
-      if (blk + g.count == n && g.head == p.hkv - 1) ++item;
+      if (blk + g.count == it.blocks && g.head == p.hkv - 1) ++item;
     } else {
-      g.count = n;
+      g.count = it.blocks;
     }
     g.block = blk;
     g.first = blk == 0;
-    g.last = blk + g.count == n;
+    g.last = blk + g.count == it.blocks;
     return true;
   }
 };
@@ -262,18 +261,20 @@ struct PromptCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
   // a warpgroup's registers per thread; the launch has 65,536 for all
   static constexpr int kSoftmaxRegs = FP8 ? 184 : 208, kOtherRegs = FP8 ? 72 : 88;
-  static constexpr int kStages = FP8 ? 3 : 5;      // tiles of 128 keys as the MMAs read them, K and V by turns
+  // Stages of tiles of 128 keys as the MMAs read them.  A part of one tile of rows has the second tile's room as one more.
+  static constexpr int kStages = FP8 ? 3 : 5;
+  static constexpr int kOutStage = kStages - 2;  // a part's output passes through this and the next one
   static constexpr int kCodeStages = FP8 ? 4 : 0;  // tiles as they land
   static_assert(!FP8 || kCodeStages == 4, "as the widening warps count them");
   static constexpr int kTile = 32768, kCodes = 16384;
   static constexpr uint32_t kColS = 0, kColO = 256;
 };
 struct PromptSmem {
-  uint64_t full[5], empty[5];            // a stage holds a tile / its MMAs are done
+  uint64_t full[6], empty[6];            // a stage holds a tile / its MMAs are done
   uint64_t code_full[4], code_empty[4];  // fp8
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_full[2], turn[2];  // by warpgroup
-  uint64_t ml_full, o_free, mma_done;
+  uint64_t ml_full, o_free, out_free, mma_done;
   float2 ml[2][128];
   float scale[8];       // fp8: scales of the last tiles (no more than 3 behind the one that a warpgroup is at)
   float code_scale[4];  // and a code stage's
@@ -319,20 +320,100 @@ __device__ __forceinline__ uint32_t tree_bits(const int32_t* mask, int words, in
   return left >= 32 ? bits : bits & ((1u << left) - 1u);
 }
 
+// The tiles of a part in the order in which they are loaded.  Two tiles of rows: K and V of a block by turns.  One: K of two
+// blocks (one per warpgroup), then their V, so that stages come free in the order in which they are wanted.
+template <int STAGES>
+struct Tiles {
+  int total;     // tiles of the part
+  bool one;      // one tile of rows: a stage more
+  uint32_t ph;   // a bit per stage: parity of its next fill
+  __device__ __forceinline__ void part(const Part& g) {
+    one = g.one;
+    total = 2 * g.count;
+  }
+  __device__ __forceinline__ int k_tile(int block) const {
+    return one ? 4 * (block >> 1) + (block & 1) : 2 * block;
+  }
+  __device__ __forceinline__ int v_tile(int block) const {
+    // the last of an odd number has no other's K before its V
+    return one ? 4 * (block >> 1) + ((block | 1) < total / 2 ? 2 + (block & 1) : 1) : 2 * block + 1;
+  }
+  __device__ __forceinline__ int block(int tile, bool& v) const {
+    if (!one) {
+      v = tile & 1;
+      return tile >> 1;
+    }
+    const int first = tile >> 2 << 1, w = tile & 3;
+    const bool pair = first + 1 < total / 2;
+    v = pair ? w >= 2 : w == 1;
+    return first + (pair ? w & 1 : 0);
+  }
+  // Every part begins with stage 0.
+  __device__ __forceinline__ int stage(int tile) const {
+    const uint32_t t = tile;
+    return one ? t % (STAGES + 1) : t % STAGES;
+  }
+  __device__ __forceinline__ uint32_t parity(int tile) const {
+    const uint32_t t = tile;
+    return (ph >> stage(tile) ^ (one ? t / (STAGES + 1) : t / STAGES)) & 1u;
+  }
+  __device__ __forceinline__ void done() {
+    const int n = STAGES + (one ? 1 : 0);
+    const int q = total / n, r = total - q * n;
+    ph ^= ((q & 1) ? (1u << n) - 1u : 0u) ^ ((1u << r) - 1u);
+  }
+};
+
+// E4M3 codes of a tile (rows of 128 bytes, TMA's 128-byte swizzle) to bf16 in the layout in which TMA lands bf16 rows; exact.
+// 128 threads, 16 codes at a time, four pieces in flight: shared memory answers in 150 clocks beside the MMAs.  Eight lanes
+// read a row, and those of its second half write their pieces in the other order, so that eight lanes' stores meet all
+// banks.  Rows from `valid` on become zeros (V: 0 * NaN is NaN).
+__device__ __forceinline__ void widen_tile(const uint8_t* codes, uint8_t* to, int thread, int valid) {
+  const int chunk = thread & 7, half = chunk >> 2, x = (thread >> 3) & 7;  // x: the row mod 8, the same in every pass
+  const uint32_t flip = half;
+  const uint4* from = reinterpret_cast<const uint4*>(codes + (thread >> 3) * 128 + ((chunk ^ x) << 4));
+  uint4* dst = reinterpret_cast<uint4*>(to + half * 16384 + (thread >> 3) * 128);
+  const uint32_t at = 2 * (chunk & 3);
+#pragma unroll 1
+  for (int pass = 0; pass < 8; pass += 4) {
+    uint4 in[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      in[k] = from[(pass + k) * 128];
+      if ((thread >> 3) + (pass + k) * 16 >= valid) in[k] = make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
+      uint32_t out[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {  // four significant bits: the upper half of the value in fp32
+        const uint32_t h = e4m3x2_to_f16x2(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        out[j] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
+      }
+      const uint4 a = make_uint4(out[0], out[1], out[2], out[3]), b = make_uint4(out[4], out[5], out[6], out[7]);
+      uint4* d = dst + (pass + k) * 128;
+      d[(at + flip) ^ x] = flip ? b : a;
+      d[(at + 1 - flip) ^ x] = flip ? a : b;
+    }
+  }
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ PromptMaps maps, PromptParams p) {
   using C = PromptCfg<FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* const q_buf = smem;             // two tiles, each two 64-dim halves of 128 rows
-  uint8_t* const ring = smem + 2 * 32768;  // stages, as the queries' tiles
+  uint8_t* const ring = smem + 2 * 32768;  // stages, as the queries' tiles; the last one is the second tile of queries
   uint8_t* const codes = ring + C::kStages * C::kTile;
   PromptSmem& sm = *reinterpret_cast<PromptSmem*>(smem + 7 * 32768);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, T = p.tile_tokens;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < C::kStages; ++i) {
+    for (int i = 0; i <= C::kStages; ++i) {
       mbar_init(&sm.full[i], FP8 ? 4 : 1);
       mbar_init(&sm.empty[i], 2);
     }
@@ -350,6 +431,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     }
     mbar_init(&sm.ml_full, 8);
     mbar_init(&sm.o_free, 8);
+    mbar_init(&sm.out_free, 8);
     mbar_init(&sm.mma_done, 2);
     mbar_arrive(&sm.turn[0]);
     sm.abort_flag = 0;
@@ -359,9 +441,6 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     tma_prefetch_desc(&maps.k);
     tma_prefetch_desc(&maps.v);
   }
-  // query rows that no load writes (the group does not divide 128, a second tile that no part had) are zero
-  for (int i = threadIdx.x; i < 2 * 32768 / 16; i += C::kThreads) reinterpret_cast<uint4*>(q_buf)[i] = make_uint4(0, 0, 0, 0);
-  fence_proxy_async_smem();
   if (warp == 8) {
     tmem_alloc(&sm.tmem_base, 512);
     tmem_relinquish();
@@ -378,74 +457,122 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
   };
   if (warp >= 8) regs_release<C::kOtherRegs>();
 
+  auto stage_at = [&](int st) { return st < C::kStages ? ring + st * C::kTile : q_buf + 32768; };
   PartWalker walk(p);
   Part g{};
+  Tiles<C::kStages> tl{};
   if (warp == 9) {
-    // ------------------------------------------------------------ loads: Q of a part, its tiles of K and V by turns
-    constexpr int kLanding = FP8 ? C::kCodeStages : C::kStages;
-    constexpr int kBytes = FP8 ? C::kCodes : C::kTile;
-    uint8_t* const to = FP8 ? codes : ring;
-    uint64_t* const full = FP8 ? sm.code_full : sm.full;
-    uint64_t* const empty = FP8 ? sm.code_empty : sm.empty;
-    uint32_t tiles = 0, queries = 0, bad = 0;
-    bool ok = true;
-    auto load_q = [&] {  // lane 0
-      if (queries > 0 && !mbar_wait(&sm.q_empty, (queries - 1) & 1, abort_flag)) return false;
-      ++queries;
-      const int n = g.one ? 1 : 2;
-      mbar_arrive_expect_tx(&sm.q_full, n * T * G * 256);
-      for (int b = 0; b < n; ++b)
-        for (int half = 0; half < 2; ++half)
-          tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * 64, g.head * G,
-                      g.q_start + g.t0 + b * T);
-      return true;
+    // ------------------------------------------------------------ loads: Q of a part, its tiles
+    uint32_t landed = 0, parts = 0, queries = 0, bad = 0;  // landed: fp8, code tiles
+    uint32_t used = 0, filled = 0;  // bf16: a bit per stage that has been filled; its last fill's parity
+    bool ok = true, lent = false;   // lent: the second tile of queries has been a stage since it was loaded last
+    uint32_t lent_parity = 0;
+    // Rows of a part's blocks, 32 at a time, one per lane, and their scales; the next 32 are on their way while these load.
+    struct Rows {
+      int row;
+      float sk, sv;
     };
-    while (ok && walk.next(g)) {
-      int row = 0;
-      float sk = 1.0f, sv = 1.0f;
-      for (int i = 0; i < g.count; ++i) {
-        if ((i & 31) == 0) {  // the next 32 blocks' rows and scales, one per lane
-          const int b = g.block + i + lane;
-          row = g.k_start + b * kBlock;
-          if (p.block_table && i + lane < g.count) {
-            const int e = p.block_table[static_cast<long long>(g.seq) * p.bt_stride + b];
-            const bool there = e >= 0 && e < p.n_pages;
-            if (!there) bad = 1;
-            row = (there ? e : static_cast<int>(p.n_pages)) * kBlock;  // past the cache: TMA reads zeros
-            if (FP8) {
-              sk = there ? p.k_scale[static_cast<long long>(e) * p.hkv + g.head] : 1.0f;
-              sv = there ? p.v_scale[static_cast<long long>(e) * p.hkv + g.head] : 1.0f;
-            }
-          }
+    auto look_up = [&](int from) {
+      Rows x{0, 1.0f, 1.0f};
+      const int b = g.block + from + lane;
+      x.row = g.k_start + b * kBlock;
+      if (p.block_table && from + lane < g.count) {
+        const int e = p.block_table[static_cast<long long>(g.seq) * p.bt_stride + b];
+        const bool there = e >= 0 && e < p.n_pages;
+        if (!there) bad = 1;
+        x.row = (there ? e : static_cast<int>(p.n_pages)) * kBlock;  // past the cache: TMA reads zeros
+        if (FP8) {
+          x.sk = there ? p.k_scale[static_cast<long long>(e) * p.hkv + g.head] : 1.0f;
+          x.sv = there ? p.v_scale[static_cast<long long>(e) * p.hkv + g.head] : 1.0f;
         }
-        const int r = __shfl_sync(0xFFFFFFFFu, row, i & 31);
-        const float k_sc = FP8 ? __shfl_sync(0xFFFFFFFFu, sk, i & 31) : 1.0f;
-        const float v_sc = FP8 ? __shfl_sync(0xFFFFFFFFu, sv, i & 31) : 1.0f;
-        if (lane == 0) {
-          for (int h = 0; ok && h < 2; ++h, ++tiles) {
-            const int st = tiles % kLanding;
-            if (tiles >= kLanding && !mbar_wait(&empty[st], (tiles / kLanding - 1) & 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (FP8) sm.code_scale[st] = h ? v_sc : k_sc;
-            mbar_arrive_expect_tx(&full[st], kBytes);
-            uint8_t* const dst = to + st * kBytes;
-            const CUtensorMap* map = h ? &maps.v : &maps.k;
-            tma_load_3d(dst, map, &full[st], 0, g.head, r);
-            if (!FP8) tma_load_3d(dst + 16384, map, &full[st], 64, g.head, r);
-          }
-          if (ok && i == 0) ok = load_q();  // behind the first block: it waits for the part before
-          if (!ok) gave_up();
-        }
-        ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
-        if (!ok) break;
       }
+      return x;
+    };
+    // Every wait and shuffle takes 150 clocks beside the MMAs, and a tile has 1,000: the whole warp waits, and a tile's row
+    // is fetched from its lane while the tile before it is waited for.
+    while (ok && walk.next(g)) {
+      tl.part(g);
+      Rows now = look_up(0), then = look_up(32);
+      bool v = false, next_v;
+      int row = __shfl_sync(0xFFFFFFFFu, now.row, 0);
+      float sc = FP8 ? __shfl_sync(0xFFFFFFFFu, now.sk, 0) : 1.0f;
+      bool out_read = parts == 0;  // the part before has read its output's stages
+      for (int t = 0; t < tl.total; ++t, v = next_v) {
+        if (((t + 1) & 63) == 0) {  // 32 blocks in either order
+          now = then;
+          then = look_up(((t + 1) >> 1) + 32);
+        }
+        const int next = tl.block(t + 1, next_v) & 31;
+        const int next_row = __shfl_sync(0xFFFFFFFFu, now.row, next);
+        const float next_sc = FP8 ? __shfl_sync(0xFFFFFFFFu, next_v ? now.sv : now.sk, next) : 1.0f;
+        const CUtensorMap* map = v ? &maps.v : &maps.k;
+        if (FP8) {
+          const int st = landed & 3;
+          ok = landed < 4 || mbar_wait_warp(&sm.code_empty[st], (landed / 4 - 1) & 1, abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            sm.code_scale[st] = sc;
+            mbar_arrive_expect_tx(&sm.code_full[st], C::kCodes);
+            tma_load_3d(codes + st * C::kCodes, map, &sm.code_full[st], 0, g.head, row);
+          }
+          __syncwarp();
+          ++landed;
+        } else {
+          const int st = tl.stage(t);
+          if (st >= C::kOutStage && !out_read) {
+            ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+            if (!ok) break;
+            out_read = true;
+          }
+          // its last fill, if any, has been given back
+          ok = !(used >> st & 1) || mbar_wait_warp(&sm.empty[st], tl.parity(t) ^ 1, abort_flag);
+          if (!ok) break;
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.full[st], C::kTile);
+            uint8_t* const dst = stage_at(st);
+            tma_load_3d(dst, map, &sm.full[st], 0, g.head, row);
+            tma_load_3d(dst + 16384, map, &sm.full[st], 64, g.head, row);
+          }
+          __syncwarp();
+          used |= 1u << st;
+          filled = (filled & ~(1u << st)) | tl.parity(t) << st;
+        }
+        row = next_row;
+        sc = next_sc;
+        if (t == 1) {  // Q behind two tiles: it waits for the part before
+          ok = (parts == 0 || mbar_wait_warp(&sm.q_empty, (parts - 1) & 1, abort_flag)) &&
+               (g.one || !lent || mbar_wait_warp(&sm.empty[C::kStages], lent_parity, abort_flag));
+          if (!ok) break;
+          if (!g.one) lent = false;
+          if (lane == 0) {
+            const int n = g.one ? 1 : 2;
+            mbar_arrive_expect_tx(&sm.q_full, n * T * G * 256);
+            for (int b = 0; b < n; ++b)
+              for (int half = 0; half < 2; ++half)
+                tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * 64, g.head * G,
+                            g.q_start + g.t0 + b * T);
+          }
+          __syncwarp();
+          ++queries;
+        }
+      }
+      if (!FP8 && ok && !out_read) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+      if (g.one && tl.total > C::kStages) {  // the lent stage's last fill in this part
+        const int n = C::kStages + 1;
+        lent = true;
+        lent_parity = tl.parity(C::kStages + (tl.total - n) / n * n);
+      }
+      tl.done();
+      ++parts;
     }
+    if (!ok && lane == 0) gave_up();
     if (bad) atomicOr(&sm.err, kFlagBadIndex);
     if (lane == 0) {  // no copy may land after this CTA has left (all have, but after a wait that gave up)
-      for (uint32_t f = tiles > kLanding ? tiles - kLanding : 0; f < tiles; ++f)
-        mbar_wait(&full[f % kLanding], (f / kLanding) & 1, nullptr);
+      if (FP8)
+        for (uint32_t f = landed > 4 ? landed - 4 : 0; f < landed; ++f) mbar_wait(&sm.code_full[f & 3], (f / 4) & 1, nullptr);
+      else
+        for (int st = 0; st <= C::kStages; ++st)
+          if (used >> st & 1) mbar_wait(&sm.full[st], filled >> st & 1, nullptr);
       if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, nullptr);
     }
   } else if (warp == 8 || warp == 10) {
@@ -460,7 +587,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     const uint64_t q_desc = sdesc_sw128(smem_u32(q_buf), 16, 1024), k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
     const uint64_t v_desc = sdesc_sw128(smem_u32(ring), 16384, 1024);
     const uint32_t s_col = tmem + C::kColS + b * 128, o_col = tmem + C::kColO + b * 128;
-    uint32_t tiles = 0, parts = 0;  // tiles before the part's, parts before it
+    uint32_t parts = 0;  // parts before this one
     uint32_t p_ph = 0, turn_ph = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
@@ -469,16 +596,15 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       const int steps = g.one ? (g.count + 1) / 2 : g.count;           // of both warps; the second may have one block less
       const int blocks = g.one ? (g.count + 1 - b) / 2 : g.count;
       const uint64_t qa = q_desc + (g.one ? 0 : b * 2048);
+      tl.part(g);
       ok = mbar_wait_warp(&sm.q_full, parts & 1, abort_flag);
       for (int i = -1; ok && i < steps; ++i) {
         const bool pv = i >= 0 && i < blocks, s = i + 1 < blocks;
-        const uint32_t v_tile = tiles + 2 * (first + i * every) + 1, k_tile = v_tile - 1 + 2 * every;
-        const uint32_t v_st = v_tile % C::kStages, k_st = k_tile % C::kStages;
-        // With three stages, K of a warpgroup's next block may land only where V of this one has been.
-        const bool apart = C::kStages < 5 && g.one && pv;
-        if (s && !apart) ok = mbar_wait_warp(&sm.full[k_st], (k_tile / C::kStages) & 1, abort_flag);
+        const int v_tile = tl.v_tile(pv ? first + i * every : 0), k_tile = tl.k_tile(s ? first + (i + 1) * every : 0);
+        const int v_st = tl.stage(v_tile), k_st = tl.stage(k_tile);
+        if (s) ok = mbar_wait_warp(&sm.full[k_st], tl.parity(k_tile), abort_flag);
         if (pv) {
-          ok = ok && mbar_wait_warp(&sm.full[v_st], (v_tile / C::kStages) & 1, abort_flag);
+          ok = ok && mbar_wait_warp(&sm.full[v_st], tl.parity(v_tile), abort_flag);
           // O of the part before has been read
           if (i == 0 && parts > 0) ok = ok && mbar_wait_warp(&sm.o_free, (parts - 1) & 1, abort_flag);
           ok = ok && mbar_wait_warp(&sm.p_full[b], p_ph, abort_flag);
@@ -488,7 +614,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         turn_ph ^= 1;
         if (!ok) break;
         tc_fence_after();
-        const uint64_t ka = k_desc + k_st * 2048, va = v_desc + v_st * 2048;
+        // (the lent stage lies one tile before the first)
+        const uint64_t ka = k_desc + (k_st < C::kStages ? k_st : -1) * 2048, va = v_desc + (v_st < C::kStages ? v_st : -1) * 2048;
         const uint32_t more = i > 0 ? 1u : 0u;
         auto issue_pv = [&](bool pass) {
 #pragma unroll
@@ -514,31 +641,21 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         };
         if (elect_one()) {
           if (pv) issue_pv(!s);
-          if (s && !apart) issue_s();
+          if (s) issue_s();
           if (!pv && !s) mbar_arrive(&sm.turn[b ^ 1]);
           if (pv) {
             if (!s) umma_commit(&sm.o_full[b]);
             give(&sm.empty[v_st]);
           }
-          if (s && !apart) give(&sm.empty[k_st]);
+          if (s) give(&sm.empty[k_st]);
         }
         __syncwarp();
-        if (s && apart) {
-          ok = mbar_wait_warp(&sm.full[k_st], (k_tile / C::kStages) & 1, abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            issue_s();
-            give(&sm.empty[k_st]);
-          }
-          __syncwarp();
-        }
         if (i + 1 == (blocks > 0 ? blocks - 1 : 0)) {  // its last S of the part (or the first step, if it has none)
           if (elect_one()) umma_commit(&sm.q_empty);
           __syncwarp();
         }
       }
-      tiles += 2 * g.count;
+      tl.done();
       ++parts;
     }
     if (!ok && lane == 0) gave_up();
@@ -552,6 +669,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     const int b = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // TMEM lane: row of the tile
     const int my_t = r / G, my_h = r - my_t * G;
+    const uint32_t group_inv = 65536u / G + 1;  // row * group_inv >> 16 = row / G for rows below 128
     const uint32_t la = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = la + C::kColS + b * 128, o_col = la + C::kColO + b * 128;
     uint32_t tiles = 0, parts = 0, steps = 0, outs = 0, merges = 0;
@@ -566,6 +684,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       const bool mine = my_t < T && tok < g.q_len;
       const int sees = p.visible ? g.past : g.past + t_tile + 1;  // keys that every row of the tile sees
       const int32_t* mask = p.visible && mine ? p.visible + static_cast<long long>(g.q_start + tok) * p.mask_words : nullptr;
+      tl.part(g);
       float m = -INFINITY;
       float2 l2 = make_float2(0.0f, 0.0f);
       int blk = g.one ? b : 0;
@@ -578,23 +697,23 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint32_t v_tile = tiles + 2 * blk + 1, v_st = v_tile % C::kStages;
+        const int v_tile = tl.v_tile(blk), v_st = tl.stage(v_tile);
         float c = p.scale_log2, sv = 1.0f;
         if (FP8) {
           // the scales come with their tiles, K's before V's (every earlier fill of the stage is past: its P V came before S of this step)
-          if (!mbar_wait_warp(&sm.full[v_st], (v_tile / C::kStages) & 1, abort_flag)) {
+          if (!mbar_wait_warp(&sm.full[v_st], tl.parity(v_tile), abort_flag)) {
             ok = false;
             break;
           }
-          c = normal_factor(c * sm.scale[(v_tile - 1) & 7]);
-          sv = sm.scale[v_tile & 7];
+          c = normal_factor(c * sm.scale[(tiles + tl.k_tile(blk)) & 7]);
+          sv = sm.scale[(tiles + v_tile) & 7];
         } else if (edge && j0 + kBlock > g.past + g.q_len && (g.one || b == 0)) {
           // V rows past the sequence's end hold anything, and 0 * NaN is NaN: zero them
-          if (!mbar_wait_warp(&sm.full[v_st], (v_tile / C::kStages) & 1, abort_flag)) {
+          if (!mbar_wait_warp(&sm.full[v_st], tl.parity(v_tile), abort_flag)) {
             ok = false;
             break;
           }
-          uint4* v = reinterpret_cast<uint4*>(ring + v_st * C::kTile);
+          uint4* v = reinterpret_cast<uint4*>(stage_at(v_st));
           for (int i = (g.past + g.q_len - j0) * 8 + r; i < kBlock * 8; i += 128) {
             v[i] = make_uint4(0, 0, 0, 0);
             v[1024 + i] = make_uint4(0, 0, 0, 0);
@@ -632,7 +751,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         load();
         const float x = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
         const bool fresh = m == -INFINITY;  // no key counts so far: O and l are 0, or not there yet
-        const bool rise = !fresh && x - m > 8.0f;
+        // (rows of nobody hold what the stages held before: they neither rescale nor round)
+        const bool rise = mine && !fresh && x - m > 8.0f;
         if (__any_sync(0xFFFFFFFFu, rise)) {  // O is complete: its P V came before this S
           const float k = rise ? exp2_approx(m - x) : 1.0f;
           l2.x *= k;
@@ -641,7 +761,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           load();
         }
         if (fresh || rise) m = x;
-        if (__any_sync(0xFFFFFFFFu, fabsf(m) >= kRoundLogits && m != -INFINITY)) {
+        if (__any_sync(0xFFFFFFFFu, mine && fabsf(m) >= kRoundLogits && m != -INFINITY)) {
           // products rounded to fp32 logits before the reference is taken off: see kRoundLogits
           const float k = fabsf(m) >= kRoundLogits ? c : 1.0f;
 #pragma unroll
@@ -670,7 +790,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         warp_arrive(&sm.p_full[b]);
       }
       if (!ok) break;
-      tiles += 2 * g.count;
+      tiles += tl.total;
+      tl.done();
 
       // ---- output
       const bool some = had < g.count;
@@ -684,11 +805,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       }
       float l = l2.x + l2.y;
       const bool whole = g.first && g.last;
-      const long long out_row = (static_cast<long long>(g.q_start) + tok) * p.hq + g.head * G + my_h;
-      const long long part_row =
-          (static_cast<long long>(blockIdx.x) * 2 + (g.first ? 1 : 0)) * 256 + (g.one ? 0 : b * 128) + r;
-      if (g.one) {
-        // both warpgroups' sums of a row, each writes half of the dims
+      const long long part_at = static_cast<long long>(blockIdx.x) * 4 + (g.first ? 2 : 0) + (g.one ? 0 : b);  // a tile's
+      float f_own = 1.0f, f_other = 0.0f;  // what this warpgroup's and the other's O count with
+      if (g.one) {  // both warpgroups' sums of a row; each writes half of the dims
         if (parts > 0 && !mbar_wait_warp(&sm.o_free, (parts - 1) & 1, abort_flag)) {  // the part before's are read
           ok = false;
           break;
@@ -703,99 +822,117 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         tc_fence_after();
         const float2 other = sm.ml[b ^ 1][r];
         const float top = fmaxf(m, other.x);
-        const float k_own = exp2_diff(m, top), k_other = exp2_diff(other.x, top);
-        l = b == 0 ? fmaf(l, k_own, other.y * k_other) : fmaf(other.y, k_other, l * k_own);  // the same in both
+        f_own = exp2_diff(m, top);
+        f_other = exp2_diff(other.x, top);
+        l = b == 0 ? fmaf(l, f_own, other.y * f_other) : fmaf(other.y, f_other, l * f_own);  // the same in both
         m = top;
-        const bool both = g.count > 1;  // else O of warpgroup 1 holds an older part's
-        const float inv = whole ? inverse(l) : 1.0f;
-        const float f0 = (b == 0 ? k_own : k_other) * inv, f1 = (b == 0 ? k_other : k_own) * inv;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const int dim = b * 64 + q * 32;
-          uint32_t x[32], y[32];
-          tmem_ld_32cols(la + C::kColO + dim, x);
-          tmem_ld_32cols(la + C::kColO + 128 + dim, y);
-          tmem_ld_wait_regs(x);
-          float unused = 0.0f;
-          tmem_regs_written(y, unused);
-          float o[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            o[j] = (l > 0.0f || !(l == 0.0f))
-                       ? (f0 == 0.0f ? 0.0f : __uint_as_float(x[j]) * f0) + (both && f1 != 0.0f ? __uint_as_float(y[j]) * f1 : 0.0f)
-                       : 0.0f;
-          if (mine) {
-            if (whole) {
-              __nv_bfloat16* to = p.o + out_row * kHeadDim + dim;
-#pragma unroll
-              for (int j = 0; j < 32; j += 16) {
-                uint32_t h[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[i] = pack_bf16(o[j + 2 * i], o[j + 2 * i + 1]);
-                *reinterpret_cast<uint4*>(to + j) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(to + j + 8) = make_uint4(h[4], h[5], h[6], h[7]);
-              }
-            } else {
-              float* to = p.part_o + part_row * kHeadDim + dim;
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-            }
-          }
-        }
-      } else {
-        const float inv = whole ? inverse(l) : 1.0f;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t x[32];
-          tmem_ld_32cols(o_col + 32 * q, x);
-          tmem_ld_wait_regs(x);
-          if (mine) {
-            if (whole) {
-              __nv_bfloat16* to = p.o + out_row * kHeadDim + 32 * q;
-#pragma unroll
-              for (int j = 0; j < 32; j += 16) {
-                uint32_t h[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  h[i] = pack_bf16(__uint_as_float(x[j + 2 * i]) * inv, __uint_as_float(x[j + 2 * i + 1]) * inv);
-                *reinterpret_cast<uint4*>(to + j) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(to + j + 8) = make_uint4(h[4], h[5], h[6], h[7]);
-              }
-            } else {
-              float* to = p.part_o + part_row * kHeadDim + 32 * q;
-#pragma unroll
-              for (int j = 0; j < 32; j += 4)
-                *reinterpret_cast<uint4*>(to + j) = make_uint4(x[j], x[j + 1], x[j + 2], x[j + 3]);
-            }
-          }
-        }
       }
-      if (mine && (!g.one || b == 0)) {
-        if (whole) p.lse[out_row] = (m + log2f(l)) * kLn2;
-        else p.part_ml[part_row] = make_float2(m, l);
+      // A row without a key that counts has O = 0.
+      const float inv = l == 0.0f ? 0.0f : whole ? 1.0f / l : 1.0f;
+      f_own *= inv;
+      f_other *= inv;
+      // Where a warpgroup had no block of the part its O holds an older one's (uniform: by the part alone).
+      const bool own_there = some, other_there = g.one && (b == 0 ? g.count > 1 : true);
+      const uint32_t other_col = la + C::kColO + (b ^ 1) * 128;
+      const int dim0 = g.one ? b * 64 : 0, chunks = g.one ? 2 : 4;
+      // The output goes through a stage of the ring (whose last tile has been multiplied), each warp's rows by the warp
+      // itself, so that a store writes whole rows: with 16 bytes of 32 rows to a store the output took 7,200 clocks of every
+      // part, through shuffles (150 clocks each beside the MMAs) more.
+      const int out_st = C::kOutStage + (g.one ? 1 : b);
+      uint8_t* const stage = stage_at(out_st);
+      if (whole && !mbar_wait_warp(&sm.empty[out_st], (tl.ph >> out_st & 1) ^ 1, abort_flag)) {
+        ok = false;
+        break;
+      }
+#pragma unroll 1
+      for (int q = 0; q < chunks; ++q) {
+        const int dim = dim0 + q * 32;
+        uint32_t x[32];
+        tmem_ld_32cols(o_col + dim, x);
+        tmem_ld_wait_regs(x);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) x[j] = own_there && f_own != 0.0f ? __float_as_uint(__uint_as_float(x[j]) * f_own) : 0u;
+        if (other_there) {
+          uint32_t y[32];
+          tmem_ld_32cols(other_col + dim, y);
+          tmem_ld_wait_regs(y);
+          if (f_other != 0.0f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(fmaf(__uint_as_float(y[j]), f_other, __uint_as_float(x[j])));
+          }
+        }
+        if (whole) {
+          uint8_t* const to = stage + (dim >> 6) * 16384 + r * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t h[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = pack_bf16(__uint_as_float(x[8 * k + 2 * i]), __uint_as_float(x[8 * k + 2 * i + 1]));
+            const int chunk = (dim >> 3 & 4) + k;
+            *reinterpret_cast<uint4*>(to + ((chunk ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+        } else {
+          // partials: four dims of 128 rows after four dims of 128 rows
+          float* const to = p.part_o + ((part_at * 32 + dim / 4) * 128 + r) * 4;
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            *reinterpret_cast<uint4*>(to + k * 512) = make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+        }
       }
       tc_fence_before();
-      warp_arrive(&sm.o_free);
+      warp_arrive(&sm.o_free);  // (synchronises the warp)
+      if (mine && (!g.one || b == 0)) {
+        if (whole) p.lse[(static_cast<long long>(g.q_start) + tok) * p.hq + g.head * G + my_h] = (m + log2f(l)) * kLn2;
+        else p.part_ml[part_at * 128 + r] = make_float2(m, l);
+      }
+      if (whole) {
+        __nv_bfloat16* const out = p.o + ((static_cast<long long>(g.q_start) + t_tile) * p.hq + g.head * G) * kHeadDim;
+        const int left = min(T, g.q_len - t_tile);
+        const int per = g.one ? 8 : 16;                  // lanes to a row
+        const int c = lane & (per - 1), half = g.one ? b : c >> 3;
+#pragma unroll 4
+        for (int i = lane / per; i < 32; i += 32 / per) {
+          const int row = (warp & 3) * 32 + i;
+          const int t = static_cast<int>(static_cast<uint32_t>(row) * group_inv >> 16), h = row - t * G;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + half * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+          if (t < left)
+            *reinterpret_cast<uint4*>(out + (static_cast<long long>(t) * p.hq + h) * kHeadDim + half * 64 + (c & 7) * 8) = w;
+        }
+        fence_proxy_async_smem();  // before the stage is loaded again
+      }
+      warp_arrive(&sm.out_free);
       ++parts;
     }
     if (!ok && lane == 0) gave_up();
   } else if (FP8 && warp >= 12) {
     // ------------------------------------------------------------ codes to bf16
     const int thread = threadIdx.x - 384;
-    uint32_t tile = 0;
+    uint32_t tile = 0, used = 0, parts = 0;  // tiles so far; a bit per stage that has been filled
     bool ok = true;
     while (ok && walk.next(g)) {
-      for (int i = 0; i < 2 * g.count; ++i, ++tile) {
-        const int cs = FP8 ? tile % 4 : 0, st = tile % C::kStages;
-        if (!mbar_wait_warp(&sm.code_full[cs], (tile / 4) & 1, abort_flag) ||
-            (tile >= C::kStages && !mbar_wait_warp(&sm.empty[st], (tile / C::kStages - 1) & 1, abort_flag))) {
+      tl.part(g);
+      bool out_read = parts == 0;
+      for (int t = 0; t < tl.total; ++t, ++tile) {
+        const int cs = tile & 3, st = tl.stage(t);
+        // the second tile of queries is lent by a part of one: the part before has read its own
+        const bool borrow = st == C::kStages && t == st;
+        if (st >= C::kOutStage && !out_read) {  // the part before has read its output's stages
+          ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+          if (!ok) break;
+          out_read = true;
+        }
+        if (!mbar_wait_warp(&sm.code_full[cs], (tile >> 2) & 1, abort_flag) ||
+            ((used >> st & 1) && !mbar_wait_warp(&sm.empty[st], tl.parity(t) ^ 1, abort_flag)) ||
+            (borrow && !mbar_wait_warp(&sm.q_full, parts & 1, abort_flag))) {
           ok = false;
           break;
         }
+        used |= 1u << st;
         if (thread == 0) sm.scale[tile & 7] = sm.code_scale[cs];
+        bool v;
+        const int blk = tl.block(t, v);
         // rows past the sequence's end: zeros, as 0 * NaN is NaN (V)
-        const int valid = g.past + g.q_len - (g.block + (i >> 1)) * kBlock;
-        widen<true>(codes + cs * C::kCodes, ring + st * C::kTile, thread, valid);
+        widen_tile(codes + cs * C::kCodes, stage_at(st), thread, g.past + g.q_len - (g.block + blk) * kBlock);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -803,6 +940,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           mbar_arrive(&sm.full[st]);
         }
       }
+      if (ok && !out_read) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+      tl.done();
+      ++parts;
     }
     if (!ok && lane == 0) gave_up();
   }
@@ -817,68 +957,87 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- join
-// Merges the partials of an item that crosses runs: CTA (x, y) the item, if any, that begins in run x and goes on; a warp
-// to a row, four dims to a lane, eight partials in flight.
+// Merges the partials of an item that crosses runs: CTA (x, y) the item, if any, that begins in run x and goes on, 32 of its
+// 256 rows.  A row to a lane, 16 dims to a warp, so that what it reads (four dims of 32 rows) lies together; the
+// output is turned in shared memory.
 constexpr int kJoinWarps = 8;
 __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptParams p) {
+  __shared__ uint2 turned[32][33];
   griddep_wait();
   const int runs = p.plan->runs;
   const int run = blockIdx.x;
   if (run + 1 >= runs) return;
   const long long total = p.plan->total;
   const long long edge = total * (run + 1) / runs;  // the first unit of the next run
-  const int j = item_of(p, p.plan->n_items, edge);
-  const int2 it = p.items[j];
-  const SeqInfo si = p.seq[it.x];
-  const int n = item_blocks(p, si, it.y);
-  const long long base = static_cast<long long>(p.block_base[j]) * p.hkv;
+  // the item that goes on behind run `run`: that of the next run's first block
+  const PromptItem it = p.items[p.run_item[run + 1]];
+  const int n = it.blocks;
+  const long long base = static_cast<long long>(it.base) * p.hkv;
   const int head = static_cast<int>((edge - base) / n);
   const long long start = base + static_cast<long long>(head) * n;
   if (start == edge || start < total * run / runs) return;  // no item goes on here, or it began in an earlier run
   const int last = static_cast<int>(((start + n) * runs - 1) / total);
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.y * kJoinWarps + (threadIdx.x >> 5);
-  const int b = row >> 7, t = (row & 127) / p.group, h = (row & 127) - t * p.group;
-  const int tok = it.y + b * p.tile_tokens + t;
-  if (t >= p.tile_tokens || tok >= si.q_len) return;
+  const int b = blockIdx.y >> 2, row0 = (blockIdx.y & 3) * 32;  // tile and first row
+  if (it.t0 + b * p.tile_tokens >= it.q_len || row0 >= p.tile_tokens * p.group) return;  // nobody's rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = row0 + lane;
   float m = -INFINITY, l = 0.0f;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = run; i0 <= last; i0 += 8) {
-    float2 x[8];
-    float4 v[8];
+  float4 a[4];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      const int i = i0 + u;
-      x[u] = make_float2(-INFINITY, 0.0f);
-      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i <= last) {
-        const long long at = (static_cast<long long>(i) * 2 + (i == run ? 1 : 0)) * 256 + row;
-        x[u] = p.part_ml[at];
-        v[u] = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + lane * 4);
-      }
+  for (int c = 0; c < 4; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = run; i0 <= last; i0 += 4) {
+    float2 x[4];
+    float4 v[4][4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int i = min(i0 + u, last);
+      const long long at = static_cast<long long>(i) * 4 + (i == run ? 2 : 0) + b;
+      x[u] = p.part_ml[at * 128 + row];
+      if (i0 + u > last) x[u] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        v[u][c] = *reinterpret_cast<const float4*>(p.part_o + ((at * 32 + warp * 4 + c) * 128 + row) * 4);
     }
-    float nm = m;
-#pragma unroll
-    for (int u = 0; u < 8; ++u) nm = fmaxf(nm, x[u].x);
+    const float nm = fmaxf(fmax3(m, x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
     const float k = exp2_diff(m, nm);
-    a.x *= k; a.y *= k; a.z *= k; a.w *= k;
     l *= k;
     m = nm;
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int c = 0; c < 4; ++c) {
+      a[c].x *= k; a[c].y *= k; a[c].z *= k; a[c].w *= k;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
       const float f = exp2_diff(x[u].x, m);
+      if (f == 0.0f) continue;  // what a part without a key that counts left does not
       l = fmaf(x[u].y, f, l);
-      a.x = fmaf(v[u].x, f, a.x);
-      a.y = fmaf(v[u].y, f, a.y);
-      a.z = fmaf(v[u].z, f, a.z);
-      a.w = fmaf(v[u].w, f, a.w);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        a[c].x = fmaf(v[u][c].x, f, a[c].x);
+        a[c].y = fmaf(v[u][c].y, f, a[c].y);
+        a[c].z = fmaf(v[u][c].z, f, a[c].z);
+        a[c].w = fmaf(v[u][c].w, f, a[c].w);
+      }
     }
   }
   const float inv = inverse(l);
-  const long long out = (static_cast<long long>(si.q_start) + tok) * p.hq + head * p.group + h;
-  *reinterpret_cast<uint2*>(p.o + out * kHeadDim + lane * 4) =
-      make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
-  if (lane == 0) p.lse[out] = (m + log2f(l)) * kLn2;
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    turned[lane][warp * 4 + c] = make_uint2(pack_bf16(a[c].x * inv, a[c].y * inv), pack_bf16(a[c].z * inv, a[c].w * inv));
+  auto out_row = [&](int r) {  // of the output, or -1: a row of nobody
+    const int t = r / p.group, h = r - t * p.group, tok = it.t0 + b * p.tile_tokens + t;
+    if (t >= p.tile_tokens || tok >= it.q_len) return -1LL;
+    return (static_cast<long long>(it.q_start) + tok) * p.hq + head * p.group + h;
+  };
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = warp * 4 + i;
+    const long long out = out_row(row0 + r);
+    if (out >= 0) *reinterpret_cast<uint2*>(p.o + out * kHeadDim + lane * 4) = turned[r][lane];
+  }
+  const long long out = out_row(row);
+  if (warp == 0 && out >= 0) p.lse[out] = (m + log2f(l)) * kLn2;
 }
 
 template <bool FP8>
@@ -902,7 +1061,7 @@ cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bo
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (!p.part_o || p.ctas < 2) return cudaSuccess;
-  e = launch_pdl(prompt_join_kernel, dim3(p.ctas - 1, 256 / kJoinWarps), dim3(kJoinWarps * 32), 0, stream, p);
+  e = launch_pdl(prompt_join_kernel, dim3(p.ctas - 1, 8), dim3(kJoinWarps * 32), 0, stream, p);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }

@@ -570,7 +570,7 @@ msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const voi
  *               max_seqlen_k <= 2^30, softmax_scale < 1e30.
  *   q, k, v     packed, as in the conventions above.
  *   o, lse      written for every query row.
- * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (about 42 MB, whatever the lengths, plus 12
+ * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (about 42 MB, whatever the lengths, plus 32
  * bytes per pair of tiles of 128 / group tokens).
  * Numbers.  Logits, references, sums, O and lse are fp32; a weight that meets V is
  * rounded to bf16 (2^-8 of the weight), the sum takes it unrounded.  Exponentials
