@@ -301,6 +301,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// Waits for two barriers as mbar_wait_warp does for one.
+__device__ __forceinline__ bool mbar_wait_both_warp(uint64_t* x, uint32_t x_parity, uint64_t* y, uint32_t y_parity,
+                                                    volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  bool ok = true;
+  for (uint32_t n = 0;; ++n) {
+    const bool xs = mbar_try_wait(x, x_parity), ys = mbar_try_wait(y, y_parity);
+    if (__all_sync(0xFFFFFFFFu, xs && ys)) return true;
+    if ((n & 63) == 63) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kWaitLimitNs) ok = false;
+      if (*abort_flag) ok = false;
+      if (!__all_sync(0xFFFFFFFFu, ok)) return false;
+    }
+  }
+}
+
 // Bits of the keys j0 .. j0 + 31 that a new token sees: every key below `past`, and of the `n` new ones behind it those
 // whose bit is set in `mask` (`words` words; what is set past n does not count).
 __device__ __forceinline__ uint32_t tree_bits(const int32_t* mask, int words, int past, int n, int j0) {
@@ -497,7 +515,26 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       int row = __shfl_sync(0xFFFFFFFFu, now.row, 0);
       float sc = FP8 ? __shfl_sync(0xFFFFFFFFu, now.sk, 0) : 1.0f;
       bool out_read = parts == 0;  // the part before has read its output's stages
-      for (int t = 0; t < tl.total; ++t, v = next_v) {
+      // Q: behind two tiles where it waits for the part before
+      auto load_q = [&] {
+        if (!((parts == 0 || mbar_wait_warp(&sm.q_empty, (parts - 1) & 1, abort_flag)) &&
+              (g.one || !lent || mbar_wait_warp(&sm.empty[C::kStages], lent_parity, abort_flag))))
+          return false;
+        if (!g.one) lent = false;
+        if (lane == 0) {
+          const int n = g.one ? 1 : 2;
+          mbar_arrive_expect_tx(&sm.q_full, n * T * G * 256);
+          for (int b = 0; b < n; ++b)
+            for (int half = 0; half < 2; ++half)
+              tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * 64, g.head * G,
+                          g.q_start + g.t0 + b * T);
+        }
+        __syncwarp();
+        ++queries;
+        return true;
+      };
+      if (parts == 0) ok = load_q();
+      for (int t = 0; ok && t < tl.total; ++t, v = next_v) {
         if (((t + 1) & 63) == 0) {  // 32 blocks in either order
           now = then;
           then = look_up(((t + 1) >> 1) + 32);
@@ -539,21 +576,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         }
         row = next_row;
         sc = next_sc;
-        if (t == 1) {  // Q behind two tiles: it waits for the part before
-          ok = (parts == 0 || mbar_wait_warp(&sm.q_empty, (parts - 1) & 1, abort_flag)) &&
-               (g.one || !lent || mbar_wait_warp(&sm.empty[C::kStages], lent_parity, abort_flag));
+        if (t == 1 && parts > 0) {
+          ok = load_q();
           if (!ok) break;
-          if (!g.one) lent = false;
-          if (lane == 0) {
-            const int n = g.one ? 1 : 2;
-            mbar_arrive_expect_tx(&sm.q_full, n * T * G * 256);
-            for (int b = 0; b < n; ++b)
-              for (int half = 0; half < 2; ++half)
-                tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * 64, g.head * G,
-                            g.q_start + g.t0 + b * T);
-          }
-          __syncwarp();
-          ++queries;
         }
       }
       if (!FP8 && ok && !out_read) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
@@ -607,10 +632,10 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           ok = ok && mbar_wait_warp(&sm.full[v_st], tl.parity(v_tile), abort_flag);
           // O of the part before has been read
           if (i == 0 && parts > 0) ok = ok && mbar_wait_warp(&sm.o_free, (parts - 1) & 1, abort_flag);
-          ok = ok && mbar_wait_warp(&sm.p_full[b], p_ph, abort_flag);
-          p_ph ^= 1;
         }
-        ok = ok && mbar_wait_warp(&sm.turn[b], turn_ph, abort_flag);
+        // two looks at once take no longer than one
+        ok = ok && mbar_wait_both_warp(&sm.turn[b], turn_ph, pv ? &sm.p_full[b] : &sm.turn[b], pv ? p_ph : turn_ph, abort_flag);
+        if (pv) p_ph ^= 1;
         turn_ph ^= 1;
         if (!ok) break;
         tc_fence_after();
@@ -914,19 +939,18 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       bool out_read = parts == 0;
       for (int t = 0; t < tl.total; ++t, ++tile) {
         const int cs = tile & 3, st = tl.stage(t);
-        // the second tile of queries is lent by a part of one: the part before has read its own
-        const bool borrow = st == C::kStages && t == st;
         if (st >= C::kOutStage && !out_read) {  // the part before has read its output's stages
           ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
           if (!ok) break;
           out_read = true;
         }
         if (!mbar_wait_warp(&sm.code_full[cs], (tile >> 2) & 1, abort_flag) ||
-            ((used >> st & 1) && !mbar_wait_warp(&sm.empty[st], tl.parity(t) ^ 1, abort_flag)) ||
-            (borrow && !mbar_wait_warp(&sm.q_full, parts & 1, abort_flag))) {
+            ((used >> st & 1) && !mbar_wait_warp(&sm.empty[st], tl.parity(t) ^ 1, abort_flag))) {
           ok = false;
           break;
         }
+        // (The lent stage: its codes were loaded behind the part's Q, for which the loads waited until the part before had read
+        // its own.)
         used |= 1u << st;
         if (thread == 0) sm.scale[tile & 7] = sm.code_scale[cs];
         bool v;
@@ -957,46 +981,45 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- join
-// Merges the partials of an item that crosses runs: CTA (x, y) the item, if any, that begins in run x and goes on, 32 of its
-// 256 rows.  A row to a lane, 16 dims to a warp, so that what it reads (four dims of 32 rows) lies together; the
-// output is turned in shared memory.
+// Merges the partials of the items that cross runs.  Every CTA lists them (one thread per pair of runs) and takes its share of
+// the tasks: 32 of an item's 256 rows and 32 of the dims.  A row to a lane, so that what a warp reads (four dims of 32
+// rows) lies together; 16 dims to a warp and every fourth partial (a sequence alone has one per run, and few rows),
+// four of them in flight.
 constexpr int kJoinWarps = 8;
-__global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptParams p) {
-  __shared__ uint2 turned[32][33];
-  griddep_wait();
-  const int runs = p.plan->runs;
-  const int run = blockIdx.x;
-  if (run + 1 >= runs) return;
-  const long long total = p.plan->total;
-  const long long edge = total * (run + 1) / runs;  // the first unit of the next run
-  // the item that goes on behind run `run`: that of the next run's first block
-  const PromptItem it = p.items[p.run_item[run + 1]];
-  const int n = it.blocks;
-  const long long base = static_cast<long long>(it.base) * p.hkv;
-  const int head = static_cast<int>((edge - base) / n);
-  const long long start = base + static_cast<long long>(head) * n;
-  if (start == edge || start < total * run / runs) return;  // no item goes on here, or it began in an earlier run
-  const int last = static_cast<int>(((start + n) * runs - 1) / total);
-  const int b = blockIdx.y >> 2, row0 = (blockIdx.y & 3) * 32;  // tile and first row
+constexpr int kJoinCtas = 304;
+static_assert(kPromptMaxCtas <= kJoinWarps * 32, "a thread per run");
+struct JoinSmem {
+  float4 sums[kJoinWarps][4][32];
+  float2 ml[kJoinWarps][32];
+  uint2 turned[32][9];
+  int4 item[kPromptMaxCtas];  // first run, last run, item, head
+  int in_warp[kJoinWarps];
+};
+// Rows task / 4 and dims task % 4 of an item.
+__device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, int4 item, int task) {
+  const int run = item.x, last = item.y, head = item.w;
+  const PromptItem it = p.items[item.z];
+  const int b = task >> 4, row0 = (task >> 2 & 3) * 32;  // tile and first row
   if (it.t0 + b * p.tile_tokens >= it.q_len || row0 >= p.tile_tokens * p.group) return;  // nobody's rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int row = row0 + lane;
+  const int row = row0 + lane, sub = warp >> 1;
+  const int quad0 = (task & 3) * 8 + (warp & 1) * 4;  // first of the warp's four quadruples of dims
   float m = -INFINITY, l = 0.0f;
   float4 a[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = run; i0 <= last; i0 += 4) {
+  for (int i0 = run + sub; i0 <= last; i0 += 16) {
     float2 x[4];
     float4 v[4][4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = min(i0 + u, last);
+      const int i = min(i0 + 4 * u, last);
       const long long at = static_cast<long long>(i) * 4 + (i == run ? 2 : 0) + b;
       x[u] = p.part_ml[at * 128 + row];
-      if (i0 + u > last) x[u] = make_float2(-INFINITY, 0.0f);
+      if (i0 + 4 * u > last) x[u] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        v[u][c] = *reinterpret_cast<const float4*>(p.part_o + ((at * 32 + warp * 4 + c) * 128 + row) * 4);
+        v[u][c] = *reinterpret_cast<const float4*>(p.part_o + ((at * 32 + quad0 + c) * 128 + row) * 4);
     }
     const float nm = fmaxf(fmax3(m, x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
     const float k = exp2_diff(m, nm);
@@ -1020,24 +1043,77 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptPara
       }
     }
   }
-  const float inv = inverse(l);
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    turned[lane][warp * 4 + c] = make_uint2(pack_bf16(a[c].x * inv, a[c].y * inv), pack_bf16(a[c].z * inv, a[c].w * inv));
+  for (int c = 0; c < 4; ++c) sm.sums[warp][c][lane] = a[c];
+  sm.ml[warp][lane] = make_float2(m, l);
+  __syncthreads();
+  {
+    // the four warps of the same dims, in order; each takes one of the four quadruples
+    const int c = sub, w0 = warp & 1;
+    float top = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top = fmaxf(top, sm.ml[w0 + 2 * u][lane].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = 0.0f;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float2 x = sm.ml[w0 + 2 * u][lane];
+      const float4 v = sm.sums[w0 + 2 * u][c][lane];
+      const float f = exp2_diff(x.x, top);
+      l = fmaf(x.y, f, l);
+      o.x = fmaf(v.x, f, o.x);
+      o.y = fmaf(v.y, f, o.y);
+      o.z = fmaf(v.z, f, o.z);
+      o.w = fmaf(v.w, f, o.w);
+    }
+    m = top;
+    const float inv = inverse(l);
+    sm.turned[lane][w0 * 4 + c] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+  }
   auto out_row = [&](int r) {  // of the output, or -1: a row of nobody
     const int t = r / p.group, h = r - t * p.group, tok = it.t0 + b * p.tile_tokens + t;
     if (t >= p.tile_tokens || tok >= it.q_len) return -1LL;
     return (static_cast<long long>(it.q_start) + tok) * p.hq + head * p.group + h;
   };
   __syncthreads();
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = warp * 4 + i;
-    const long long out = out_row(row0 + r);
-    if (out >= 0) *reinterpret_cast<uint2*>(p.o + out * kHeadDim + lane * 4) = turned[r][lane];
+  const int r = threadIdx.x >> 3, c = threadIdx.x & 7;  // 8 lanes write 64 bytes of a row
+  const long long out = out_row(row0 + r);
+  if (out >= 0) *reinterpret_cast<uint2*>(p.o + out * kHeadDim + (task & 3) * 32 + c * 4) = sm.turned[r][c];
+  const long long lse_at = out_row(row);
+  if (threadIdx.x < 32 && (task & 3) == 0 && lse_at >= 0) p.lse[lse_at] = (m + log2f(l)) * kLn2;
+  __syncthreads();  // the next task's sums
+}
+
+__global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptParams p) {
+  __shared__ JoinSmem sm;
+  griddep_wait();
+  const int runs = p.plan->runs;
+  const long long total = p.plan->total;
+  const int run = threadIdx.x;
+  int4 item = make_int4(-1, 0, 0, 0);
+  if (run + 1 < runs) {
+    const long long edge = total * (run + 1) / runs;  // the first unit of the next run
+    // the item that goes on behind run `run`, if one does: that of the next run's first block
+    const int j = p.run_item[run + 1];
+    const int n = p.items[j].blocks;
+    const long long base = static_cast<long long>(p.items[j].base) * p.hkv;
+    const int head = static_cast<int>((edge - base) / n);
+    const long long start = base + static_cast<long long>(head) * n;
+    if (start != edge && start >= total * run / runs)  // it began in this run
+      item = make_int4(run, static_cast<int>(((start + n) * runs - 1) / total), j, head);
   }
-  const long long out = out_row(row);
-  if (warp == 0 && out >= 0) p.lse[out] = (m + log2f(l)) * kLn2;
+  // the list has one order in all CTAs
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, item.x >= 0);
+  if ((threadIdx.x & 31) == 0) sm.in_warp[threadIdx.x >> 5] = __popc(some);
+  __syncthreads();
+  int count = 0, at = __popc(some & ((1u << (threadIdx.x & 31)) - 1u));
+  for (int w = 0; w < kJoinWarps; ++w) {
+    if (w < static_cast<int>(threadIdx.x >> 5)) at += sm.in_warp[w];
+    count += sm.in_warp[w];
+  }
+  if (item.x >= 0) sm.item[at] = item;
+  __syncthreads();
+  for (int task = blockIdx.x; task < count * 32; task += gridDim.x) join_rows(p, sm, sm.item[task >> 5], task & 31);
 }
 
 template <bool FP8>
@@ -1060,8 +1136,8 @@ cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bo
   e = fp8 ? launch_attn<true>(maps, p, stream) : launch_attn<false>(maps, p, stream);
   if (e != cudaSuccess) return e;
   note_launches(1);
-  if (!p.part_o || p.ctas < 2) return cudaSuccess;
-  e = launch_pdl(prompt_join_kernel, dim3(p.ctas - 1, 8), dim3(kJoinWarps * 32), 0, stream, p);
+  if (!p.part_o) return cudaSuccess;
+  e = launch_pdl(prompt_join_kernel, dim3(kJoinCtas), dim3(kJoinWarps * 32), 0, stream, p);
   if (e == cudaSuccess) note_launches(1);
   return e;
 }
