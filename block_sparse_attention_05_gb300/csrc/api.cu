@@ -1010,7 +1010,7 @@ msa_status_t append_rows(const AppendRows* rows, int planes, const int64_t* slot
   const msa_status_t st = device_facts(dev);
   if (st != MSA_OK) return st;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return cuda_status(fp8 ? launch_append_fp8(p, need, s) : launch_append(p, dev.sms, s));
+  return cuda_status(fp8 ? launch_append_fp8(p, need, dev.sms, s) : launch_append(p, dev.sms, s));
 }
 
 msa_status_t add_rms_norm(const void* x, const void* residual, const void* gamma, int64_t rows, int32_t d_model,

@@ -2,15 +2,17 @@
 // K_idx rows into their slots.
 //
 // Tables.  A sequence of n cached tokens that gets m new ones needs ceil((n + m) / 128) - ceil(n / 128) more pages; they
-// are taken from a list of free pages, sequence by sequence, so the result does not depend on timing.  A plan kernel (one
-// CTA) scans the lengths; then every new token finds its sequence in the prefix sums and its page in the table or the
-// list, and the token at a block's first position writes the block's entry.
+// are taken from a list of free pages, sequence by sequence, so the result does not depend on timing.  One CTA scans the
+// lengths; then every new token finds its sequence in the prefix sums and its page in the table or the list, and the
+// token at a block's first position writes the block's entry.  The CTA that scanned does that too where the tokens are few.
 //
 // Rows.  bf16: a copy, a warp per token and tensor.  E4M3: a page has one scale per head, so the new rows of a page are
-// taken together: the tokens that follow one another into one page (a run) by one CTA per head, read once into
-// registers.  Their largest value may ask for a larger scale than the page has; the rows that the page holds already (those
-// before the run's first) are then rounded again.
+// taken together: the tokens that follow one another into one page (a run), per head.  Their largest value may ask for a
+// larger scale than the page has; the rows that the page holds already (those before the run's first) are then rounded
+// again.
 #include <cuda_fp8.h>
+
+#include <cstddef>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -21,49 +23,47 @@ namespace {
 
 // ---------------------------------------------------------------- tables
 constexpr int kTableThreads = 1024;
+constexpr int kPlaceMost = 4096;  // tokens that the scanning CTA places itself: a second kernel takes 3 us more, 1,000 tokens 0.4
 
-// Exclusive scan over the CTA's kTableThreads threads.
-__device__ long long table_scan(long long v, long long* sh, long long* total) {
+struct Sums {
+  long long tokens, keys, pages;
+};
+// Exclusive scan of three numbers over the CTA's kTableThreads threads.
+__device__ __forceinline__ Sums table_scan(Sums v, Sums* sh, Sums* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  long long x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) sh[warp] = x;
-  __syncthreads();
-  if (warp == 0) {
-    long long w = sh[lane];
+  auto warp_scan = [&](Sums x) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xFFFFFFFFu, w, o);
-      if (lane >= o) w += y;
+      const Sums y{__shfl_up_sync(0xFFFFFFFFu, x.tokens, o), __shfl_up_sync(0xFFFFFFFFu, x.keys, o),
+                   __shfl_up_sync(0xFFFFFFFFu, x.pages, o)};
+      if (lane >= o) {
+        x.tokens += y.tokens;
+        x.keys += y.keys;
+        x.pages += y.pages;
+      }
     }
-    sh[lane] = w;
-  }
+    return x;
+  };
+  const Sums x = warp_scan(v);
+  if (lane == 31) sh[warp] = x;
   __syncthreads();
-  const long long before = x - v + (warp > 0 ? sh[warp - 1] : 0);
+  if (warp == 0) sh[lane] = warp_scan(sh[lane]);
+  __syncthreads();
+  const Sums before = warp > 0 ? sh[warp - 1] : Sums{0, 0, 0};
   *total = sh[31];
   __syncthreads();
-  return before;
+  return {before.tokens + x.tokens - v.tokens, before.keys + x.keys - v.keys, before.pages + x.pages - v.pages};
 }
 
-// Token i of the call: its slot and position, and its block's table entry when it is the block's first token.
-__device__ __forceinline__ void place_token(const ExtendParams& p, long long i, int tokens) {
-  if (i >= tokens) {
-    p.slots[i] = -1;
-    p.positions[i] = 0;
-    return;
-  }
-  const int s = find_seq(p.cu_q, p.num_seqs, static_cast<int>(i));
-  const int q0 = p.cu_q[s], len = (p.cu_k[s + 1] - p.cu_k[s]) - (p.cu_q[s + 1] - q0);
-  const int pos = len + static_cast<int>(i) - q0, block = pos >> 7, held = (len + 127) >> 7;
+// New token i, the `t`-th of sequence s, which had `len`: its slot and position, and its block's table entry when it is the
+// block's first token.
+__device__ __forceinline__ void place_token(const ExtendParams& p, long long i, int s, int len, int t, int page_base) {
+  const int pos = len + t, block = pos >> 7, held = (len + 127) >> 7;
   int page = -1;
   if (block < held) {
     page = p.block_table[static_cast<long long>(s) * p.bt_stride + block];
   } else {
-    const long long at = static_cast<long long>(p.page_base[s]) + block - held;
+    const long long at = static_cast<long long>(page_base) + block - held;
     if (at < p.num_free) page = p.free_pages[at];
   }
   if (page < 0 || page >= p.n_pages) {
@@ -75,69 +75,119 @@ __device__ __forceinline__ void place_token(const ExtendParams& p, long long i, 
   p.positions[i] = pos;
 }
 
-__global__ void __launch_bounds__(kTableThreads) extend_plan_kernel(ExtendParams p) {
-  __shared__ long long sh[32];
+__global__ void __launch_bounds__(kTableThreads) extend_plan_kernel(ExtendParams p, bool place) {
+  __shared__ Sums sh[32];
   __shared__ int s_bad;
+  __shared__ int first[kTableThreads + 1], length[kTableThreads], pages[kTableThreads];  // of up to kTableThreads sequences
+  if (threadIdx.x == 0) s_bad = 0;
   griddep_wait();
-  for (int w = threadIdx.x; w < static_cast<int>(sizeof(WsHeader) / 4); w += kTableThreads)
-    reinterpret_cast<uint32_t*>(p.hdr)[w] = 0u;
   const int taken = p.taken ? *p.taken : 0;
   // lengths that cannot be, or that pass the buffers: nothing is taken, every slot is -1
-  if (threadIdx.x == 0) s_bad = taken < 0 || taken > p.num_free;
-  __syncthreads();
-  long long tokens = 0, keys = 0;
+  bool bad = taken < 0 || taken > p.num_free;
+  Sums carry{0, 0, taken};
   for (int base = 0; base < p.num_seqs; base += kTableThreads) {
     const int s = base + threadIdx.x;
     long long n = 0, m = 0;
     if (s < p.num_seqs) {
       n = p.lengths[s];
       m = p.new_tokens[s];
-      if (n < 0 || m < 0 || n + m > p.max_len) s_bad = 1;
+      if (n < 0 || m < 0 || n + m > p.max_len) {
+        bad = true;
+        n = m = 0;
+      }
     }
-    long long t;
-    table_scan(m, sh, &t);
-    tokens += t;
-    table_scan(n + m, sh, &t);
-    keys += t;
-  }
-  __syncthreads();
-  const bool bad = s_bad || tokens > p.capacity || keys > 0x7FFFFFFFLL;
-  long long carry_q = 0, carry_k = 0, carry_p = taken;
-  for (int base = 0; base < p.num_seqs; base += kTableThreads) {
-    const int s = base + threadIdx.x;
-    int n = 0, m = 0;
-    if (s < p.num_seqs && !bad) {
-      n = p.lengths[s];
-      m = p.new_tokens[s];
-    }
-    const int need = ((n + m + 127) >> 7) - ((n + 127) >> 7);
-    long long tq, tk, tp;
-    const long long bq = table_scan(m, sh, &tq), bk = table_scan(n + m, sh, &tk), bp = table_scan(need, sh, &tp);
+    Sums t;
+    const Sums at = table_scan({m, n + m, ((n + m + 127) >> 7) - ((n + 127) >> 7)}, sh, &t);
     if (s < p.num_seqs) {
-      p.cu_q[s + 1] = static_cast<int>(carry_q + bq + m);
-      p.cu_k[s + 1] = static_cast<int>(carry_k + bk + n + m);
-      p.page_base[s] = static_cast<int>(carry_p + bp);
-      if (p.new_lengths && !bad) p.new_lengths[s] = n + m;
+      const int q = static_cast<int>(carry.tokens + at.tokens), pg = static_cast<int>(carry.pages + at.pages);
+      p.cu_q[s + 1] = q + static_cast<int>(m);
+      p.cu_k[s + 1] = static_cast<int>(carry.keys + at.keys + n + m);
+      p.page_base[s] = pg;
+      if (base == 0) {
+        first[threadIdx.x] = q;
+        length[threadIdx.x] = static_cast<int>(n);
+        pages[threadIdx.x] = pg;
+      }
     }
-    carry_q += tq;
-    carry_k += tk;
-    carry_p += tp;
+    carry.tokens += t.tokens;
+    carry.keys += t.keys;
+    carry.pages += t.pages;
   }
+  if (bad) s_bad = 1;
+  __syncthreads();
+  bad = s_bad || carry.tokens > p.capacity || carry.keys > 0x7FFFFFFFLL;
+  if (bad) carry.tokens = 0;
+  for (int s = threadIdx.x; s < p.num_seqs; s += kTableThreads) {
+    if (bad) {
+      p.cu_q[s + 1] = 0;
+      p.cu_k[s + 1] = 0;
+    } else if (p.new_lengths) {
+      p.new_lengths[s] = p.lengths[s] + p.new_tokens[s];
+    }
+  }
+  if (threadIdx.x < sizeof(WsHeader) / 4)
+    reinterpret_cast<uint32_t*>(p.hdr)[threadIdx.x] = threadIdx.x == 0 && bad ? kFlagBadSeqlens : 0u;
+  static_assert(offsetof(WsHeader, status) == 0, "the first word");
   if (threadIdx.x == 0) {
     p.cu_q[0] = 0;
     p.cu_k[0] = 0;
-    *p.taken_out = bad ? taken : static_cast<int>(carry_p < p.num_free ? carry_p : p.num_free);
-    if (bad) atomicOr(&p.hdr->status, kFlagBadSeqlens);
+    *p.taken_out = bad ? taken : static_cast<int>(carry.pages < p.num_free ? carry.pages : p.num_free);
+  }
+  if (!place) return;
+  __syncthreads();  // the header, before flags are raised in it
+  const int tokens = static_cast<int>(carry.tokens);
+  for (int i = threadIdx.x; i < p.capacity; i += kTableThreads) {
+    if (i >= tokens) {
+      p.slots[i] = -1;
+      p.positions[i] = 0;
+      continue;
+    }
+    const int s = find_seq(first, p.num_seqs, i);  // num_seqs <= kTableThreads
+    place_token(p, i, s, length[s], i - first[s], pages[s]);
   }
 }
 
+// Tokens 32 i .. of a warp lie in few sequences: the warp finds the first one's, 32 places at a time, and each lane goes on
+// from there.
 constexpr int kPlaceThreads = 256;
 __global__ void __launch_bounds__(kPlaceThreads) extend_place_kernel(ExtendParams p) {
   griddep_wait();
-  const int tokens = p.cu_q[p.num_seqs];
-  for (long long i = blockIdx.x * static_cast<long long>(kPlaceThreads) + threadIdx.x; i < p.capacity;
-       i += static_cast<long long>(gridDim.x) * kPlaceThreads)
-    place_token(p, i, tokens);
+  const int tokens = p.cu_q[p.num_seqs], lane = threadIdx.x & 31;
+  const long long warps = static_cast<long long>(gridDim.x) * (kPlaceThreads / 32);
+  for (long long i0 = (blockIdx.x * static_cast<long long>(kPlaceThreads / 32) + (threadIdx.x >> 5)) * 128; i0 < p.capacity;
+       i0 += warps * 128) {
+    // the last sequence that begins at or before token i0, with an empty one's successors behind it
+    int lo = 0, n = p.num_seqs;
+    while (i0 < tokens && n > 1) {
+      const int step = (n + 31) / 32;
+      const int at = lo + lane * step;
+      const bool begun = lane * step < n && p.cu_q[at] <= i0;
+      const int k = __popc(__ballot_sync(0xFFFFFFFFu, begun)) - 1;  // lane 0's has begun
+      lo += k * step;
+      n = min(step, n - k * step);
+    }
+    int s = lo, q0 = 0, q1 = 0, len = 0, base = 0;
+    bool known = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const long long i = i0 + u * 32 + lane;
+      if (i >= p.capacity) continue;
+      if (i >= tokens) {
+        p.slots[i] = -1;
+        p.positions[i] = 0;
+        continue;
+      }
+      if (!known || i >= q1) {
+        while (p.cu_q[s + 1] <= i) ++s;
+        q0 = p.cu_q[s];
+        q1 = p.cu_q[s + 1];
+        len = (p.cu_k[s + 1] - p.cu_k[s]) - (q1 - q0);
+        base = p.page_base[s];
+        known = true;
+      }
+      place_token(p, i, s, len, static_cast<int>(i) - q0, base);
+    }
+  }
 }
 
 // ---------------------------------------------------------------- rows, bf16
@@ -173,141 +223,233 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
   return __half22float2(__half2(h));
 }
 
-// CTA (x, y): the runs that begin among tokens [x * chunk, (x + 1) * chunk), head y of the planes.
-__global__ void __launch_bounds__(kRunThreads) append_fp8_kernel(AppendParams p, int chunk) {
-  __shared__ int s_first, s_len, s_low;
+// What a run does to its page's scale, and its rows' quotients.
+struct RunScale {
+  float was, now;
+  float up, down, inv;  // a code is that of x * up / down; 1 / down
+  bool plain;           // by division
+};
+__device__ __forceinline__ RunScale run_scale(float was, float amax, bool live) {
+  RunScale r;
+  const float fresh = amax >= kZeroBelow ? __fdiv_rn(amax, 448.0f) : 0.0f;
+  r.was = was;
+  r.now = live ? fmaxf(was, fresh) : fresh;
+  if (r.now == 0.0f) r.now = 1.0f;
+  // A value's code is that of the exact quotient: where the new rows set the scale (amax / 448, rounded) that is x * 448 /
+  // amax, and x * 448 has 11 significant bits.  bf16 values meet the middle between two codes often (one in 40 of a
+  // normal distribution's), and a rounded scale would put them on either side.
+  const bool ours = fresh > 0.0f && r.now == fresh;
+  // powers of two that keep products and remainders normal numbers
+  const float shift = amax > 1.26765060e30f ? 5.42101086e-20f : amax < 8.8817842e-16f ? 1.84467441e19f : 1.0f;
+  r.up = ours ? 448.0f * shift : 1.0f;
+  r.down = ours ? amax * shift : r.now;
+  r.plain = !(r.down >= 7.8886091e-31f && r.down <= 1.26765060e30f);  // a scale of the caller's outside 2^-100 .. 2^100
+  r.inv = __fdiv_rn(1.0f, r.down);
+  return r;
+}
+// fp32(x / down), correctly rounded: with 1 / down correctly rounded, one step from the remainder, which an fma gives exactly
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  A division each took
+// a third of the kernel's time.
+__device__ __forceinline__ float quotient(float x, const RunScale& r) {
+  if (r.plain) return __fdiv_rn(x, r.down);
+  const float q = x * r.inv;
+  const float exact = fmaf(fmaf(-q, r.down, x), r.inv, q);
+  return fabsf(q) < 1e30f && q != 0.0f ? exact : q;  // inf, NaN and -0 as they are
+}
+__device__ __forceinline__ uint2 codes_of(const uint4& v, const RunScale& r) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  uint32_t c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    c[j] = to_e4m3x2(quotient(__uint_as_float(w[j] << 16) * r.up, r), quotient(__uint_as_float(w[j] & 0xFFFF0000u) * r.up, r));
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+// Eight codes of a row that was there before, at the new scale.
+__device__ __forceinline__ uint2 codes_again(const uint2& old, const RunScale& r) {
+  const uint32_t w[2] = {old.x, old.y};
+  uint32_t out[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float2 f0 = from_e4m3x2(w[j] & 0xFFFFu), f1 = from_e4m3x2(w[j] >> 16);
+    auto again = [&](float f) { return quotient(f * r.up * r.was, r); };
+    out[j] = to_e4m3x2(again(f0.x), again(f0.y)) | to_e4m3x2(again(f1.x), again(f1.y)) << 16;
+  }
+  return make_uint2(out[0], out[1]);
+}
+__device__ __forceinline__ uint32_t bf16x8_max(const uint4& v, uint32_t m) {  // of |x|, as bits; inf and NaN do not count
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t l = w[j] & 0x7FFFu, h = (w[j] >> 16) & 0x7FFFu;
+    if (l < 0x7F80u) m = max(m, l);
+    if (h < 0x7F80u) m = max(m, h);
+  }
+  return m;
+}
+
+// CTA (x, y): the runs that begin among tokens [x * chunk, (x + 1) * chunk), head y of the planes.  16 threads take a row, 8
+// values each.  A short run is one warp's, two rows at a time; a longer one all four warps', eight rows at a time,
+// every row in registers between its maximum and its codes.  Slots are read once, those of the longest run behind the
+// chunk among them.
+constexpr int kShortRun = 16;
+constexpr int kMostChunk = 64;
+__global__ void __launch_bounds__(kRunThreads, 5) append_fp8_kernel(AppendParams p, int chunk) {
+  __shared__ int s_page[2 + kMostChunk + 128];  // page of tokens lo - 1 .. lo + chunk + 127, -1: none
+  __shared__ uint8_t s_row[2 + kMostChunk + 128];
+  __shared__ int s_long[kMostChunk];            // lengths of the runs for all warps, by their first token; 0: none
   __shared__ uint32_t s_max[kRunThreads / 32];
-  __shared__ int s_row[128];
+  __shared__ int s_low[kRunThreads / 32];
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int head = blockIdx.y, pl = 0;
   while (head >= p.plane[pl].width / 128) head -= p.plane[pl++].width / 128;
   const AppendPlane& a = p.plane[pl];
   const int heads = a.width / 128;
-  const long long rows = p.n_pages * 128;
-  const long long lo = static_cast<long long>(blockIdx.x) * chunk, hi = min(lo + chunk, p.tokens);
+  const long long rows = p.n_pages * 128, row_bytes = static_cast<long long>(heads) * 128;
+  const long long lo = static_cast<long long>(blockIdx.x) * chunk;
+  const int n = static_cast<int>(min(static_cast<long long>(chunk), p.tokens - lo));
   const bool marks = blockIdx.y == 0;
-  auto page_of = [&](long long slot) { return slot < 0 || slot >= rows ? -1LL : slot >> 7; };
-  for (long long at = lo; at < hi;) {
-    // the first token of the chunk, from `at` on, whose page is not that of the token before it
-    if (tid == 0) {
-      s_first = kRunThreads;
-      s_len = kRunThreads;
-      s_low = 128;
+  for (int t = tid; t < 1 + chunk + 128; t += kRunThreads) {
+    const long long i = lo - 1 + t;
+    long long slot = -1;
+    if (i >= 0 && i < p.tokens) slot = p.slots[i];
+    const bool there = slot >= 0 && slot < rows;
+    if (!there && slot != -1 && marks) atomicOr(&p.hdr->status, kFlagBadIndex);
+    s_page[t] = there ? static_cast<int>(slot >> 7) : -1;
+    s_row[t] = static_cast<uint8_t>(slot & 127);
+  }
+  if (tid < kMostChunk) s_long[tid] = 0;
+  __syncthreads();
+  const int sub = lane & 15, half = lane >> 4;
+  const __nv_bfloat16* const x0 = a.x + lo * a.stride + head * 128 + sub * 8;
+  bool any_long = false;
+  for (int t = warp; t < n; t += kRunThreads / 32) {
+    const int page = s_page[1 + t];
+    if (page < 0 || s_page[t] == page) continue;  // not a run's first token
+    int len = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t same = __ballot_sync(0xFFFFFFFFu, s_page[1 + t + u * 32 + lane] == page);
+      if (len == u * 32) len += same == 0xFFFFFFFFu ? 32 : __ffs(~same) - 1;
     }
-    __syncthreads();
-    const long long i = at + tid;
-    if (i < hi) {
-      const long long slot = p.slots[i], page = page_of(slot);
-      if (page < 0) {
-        if (slot != -1 && marks) atomicOr(&p.hdr->status, kFlagBadIndex);
-      } else if (i == 0 || page_of(p.slots[i - 1]) != page) {
-        atomicMin(&s_first, tid);
-      }
-    }
-    __syncthreads();
-    const int first = s_first;
-    if (first == kRunThreads) {
-      at += kRunThreads;
-      __syncthreads();
-      continue;
-    }
-    const long long start = at + first;
-    const long long page = p.slots[start] >> 7;
-    {
-      const long long j = start + tid;
-      const long long slot = j < p.tokens ? p.slots[j] : -1;
-      if (page_of(slot) != page) atomicMin(&s_len, tid);
-      s_row[tid] = static_cast<int>(slot & 127);
-    }
-    if (tid == 0 && marks) {
+    if (marks && lane == 0) {
       // a page's rows come in one run of at most 128 tokens
-      const bool more = start + 128 < p.tokens && page_of(p.slots[start + 128]) == page && page_of(p.slots[start + 127]) == page;
+      const bool more = len == 128 && s_page[1 + t + 128] == page;  // t < chunk: within what was read
       if (atomicExch(&p.marks[page], 1u) != 0u || more) atomicOr(&p.hdr->status, kFlagBadIndex);
     }
-    __syncthreads();
-    const int len = s_len;
-    if (tid < len) atomicMin(&s_low, s_row[tid]);
-    // 16 threads to a row, 8 values each
-    const int sub = tid & 15, r0 = tid >> 4;
-    const __nv_bfloat16* x = a.x + start * a.stride + head * 128 + sub * 8;
+    if (len > kShortRun) {
+      if (lane == 0) s_long[t] = len;
+      any_long = true;
+      continue;
+    }
+    float* const scale_at = a.scale + static_cast<long long>(page) * heads + head;
+    const float was = *scale_at;
+    uint4 v[kShortRun / 2];
+    uint32_t m = 0;
+    int low = 127;
+#pragma unroll
+    for (int k = 0; k < kShortRun / 2; ++k) {
+      const int r = k * 2 + half;
+      v[k] = make_uint4(0, 0, 0, 0);
+      if (r < len) {
+        v[k] = *reinterpret_cast<const uint4*>(x0 + (t + r) * a.stride);
+        low = min(low, static_cast<int>(s_row[1 + t + r]));
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kShortRun / 2; ++k) m = bf16x8_max(v[k], m);
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    const RunScale r = run_scale(was, __uint_as_float(m << 16), low > 0);
+    uint8_t* const cache = static_cast<uint8_t*>(a.cache) + (static_cast<long long>(page) * 128 * heads + head) * 128 + sub * 8;
+    __syncwarp();  // every lane has read the scale
+    if (lane == 0) *scale_at = r.now;
+    if (low > 0 && r.now != was) {
+      for (int row = half; row < low; row += 16) {
+        uint2 old[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (row + 2 * k < low) old[k] = *reinterpret_cast<const uint2*>(cache + (row + 2 * k) * row_bytes);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (row + 2 * k < low) *reinterpret_cast<uint2*>(cache + (row + 2 * k) * row_bytes) = codes_again(old[k], r);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kShortRun / 2; ++k)
+      if (k * 2 + half < len) *reinterpret_cast<uint2*>(cache + s_row[1 + t + k * 2 + half] * row_bytes) = codes_of(v[k], r);
+  }
+  if (!__syncthreads_or(any_long)) return;
+  const int r0 = tid >> 4;
+  for (int t = 0; t < n; ++t) {
+    const int len = s_long[t];
+    if (len == 0) continue;
+    const int page = s_page[1 + t];
+    float* const scale_at = a.scale + static_cast<long long>(page) * heads + head;
+    const float was = *scale_at;
     uint4 v[16];
     uint32_t m = 0;
+    int low = 127;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
+      const int r = k * 8 + r0;
       v[k] = make_uint4(0, 0, 0, 0);
-      if (k * 8 + r0 < len) v[k] = *reinterpret_cast<const uint4*>(x + (k * 8 + r0) * a.stride);
-    }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t l = w[j] & 0x7FFFu, h = (w[j] >> 16) & 0x7FFFu;
-        if (l < 0x7F80u) m = max(m, l);  // inf and NaN do not count
-        if (h < 0x7F80u) m = max(m, h);
+      if (r < len) {
+        v[k] = *reinterpret_cast<const uint4*>(x0 + (t + r) * a.stride);
+        low = min(low, static_cast<int>(s_row[1 + t + r]));
       }
     }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) m = bf16x8_max(v[k], m);
     m = __reduce_max_sync(0xFFFFFFFFu, m);
-    if (lane == 0) s_max[warp] = m;
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    if (lane == 0) {
+      s_max[warp] = m;
+      s_low[warp] = low;
+    }
     __syncthreads();
-    const int low = s_low;
-    const float amax = __uint_as_float(max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3])) << 16);
-    const float fresh = amax >= kZeroBelow ? __fdiv_rn(amax, 448.0f) : 0.0f;
-    float* scale_at = a.scale + page * heads + head;
-    const float was = *scale_at;
-    float now = low > 0 ? fmaxf(was, fresh) : fresh;
-    if (now == 0.0f) now = 1.0f;
-    // A value's code is that of the exact quotient: where the new rows set the scale (amax / 448, rounded) that is x * 448 /
-    // amax, and x * 448 has 11 significant bits.  bf16 values meet the middle between two codes often (one in 40 of a
-    // normal distribution's), and a rounded scale would put them on either side.
-    const bool ours = fresh > 0.0f && now == fresh;
-    const float shift = amax > 1.26765060e30f ? 5.42101086e-20f : 1.0f;  // 2^100, 2^-64: a product that does not overflow
-    const float up = ours ? 448.0f * shift : 1.0f, down = ours ? amax * shift : now;
-    uint8_t* cache = static_cast<uint8_t*>(a.cache) + (page * 128 * heads + head) * 128 + sub * 8;
-    const long long row_bytes = static_cast<long long>(heads) * 128;
-    __syncthreads();  // every thread has read the scale
-    if (tid == 0) *scale_at = now;
-    if (low > 0 && now != was) {
-      for (int r = r0; r < low; r += 8) {
-        uint2* c = reinterpret_cast<uint2*>(cache + r * row_bytes);
-        const uint2 old = *c;
-        const uint32_t w[2] = {old.x, old.y};
-        uint32_t out[2];
+    m = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
+    low = min(min(s_low[0], s_low[1]), min(s_low[2], s_low[3]));
+    const RunScale r = run_scale(was, __uint_as_float(m << 16), low > 0);
+    uint8_t* const cache = static_cast<uint8_t*>(a.cache) + (static_cast<long long>(page) * 128 * heads + head) * 128 + sub * 8;
+    __syncthreads();  // every thread has read the scale, and the maxima
+    if (tid == 0) *scale_at = r.now;
+    if (low > 0 && r.now != was) {
+      for (int row = r0; row < low; row += 64) {
+        uint2 old[8];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float2 f0 = from_e4m3x2(w[j] & 0xFFFFu), f1 = from_e4m3x2(w[j] >> 16);
-          auto again = [&](float f) { return __fdiv_rn(f * up * was, down); };
-          out[j] = to_e4m3x2(again(f0.x), again(f0.y)) | to_e4m3x2(again(f1.x), again(f1.y)) << 16;
-        }
-        *c = make_uint2(out[0], out[1]);
+        for (int k = 0; k < 8; ++k)
+          if (row + 8 * k < low) old[k] = *reinterpret_cast<const uint2*>(cache + (row + 8 * k) * row_bytes);
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (row + 8 * k < low) *reinterpret_cast<uint2*>(cache + (row + 8 * k) * row_bytes) = codes_again(old[k], r);
       }
     }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      if (k * 8 + r0 >= len) continue;
-      const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-      uint32_t c[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        c[j] = to_e4m3x2(__fdiv_rn(__uint_as_float(w[j] << 16) * up, down),
-                         __fdiv_rn(__uint_as_float(w[j] & 0xFFFF0000u) * up, down));
-      *reinterpret_cast<uint2*>(cache + s_row[k * 8 + r0] * row_bytes) = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
-    }
-    at = start + 1;
-    __syncthreads();
+    for (int k = 0; k < 16; ++k)
+      if (k * 8 + r0 < len) *reinterpret_cast<uint2*>(cache + s_row[1 + t + k * 8 + r0] * row_bytes) = codes_of(v[k], r);
   }
+}
+
+constexpr int kClearThreads = 256;
+__global__ void __launch_bounds__(kClearThreads) clear_kernel(uint4* at, long long n) {
+  griddep_wait();
+  for (long long i = blockIdx.x * static_cast<long long>(kClearThreads) + threadIdx.x; i < n;
+       i += static_cast<long long>(gridDim.x) * kClearThreads)
+    at[i] = make_uint4(0, 0, 0, 0);
 }
 
 }  // namespace
 
 cudaError_t launch_extend(const ExtendParams& p, int sms, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(extend_plan_kernel, dim3(1), dim3(kTableThreads), 0, stream, p);
+  const bool place = p.capacity <= kPlaceMost && p.num_seqs <= kTableThreads;
+  cudaError_t e = launch_pdl(extend_plan_kernel, dim3(1), dim3(kTableThreads), 0, stream, p, place);
   if (e != cudaSuccess) return e;
   note_launches(1);
-  if (p.capacity == 0) return cudaSuccess;
-  long long ctas = (p.capacity + kPlaceThreads - 1) / kPlaceThreads;
+  if (place) return cudaSuccess;
+  long long ctas = (p.capacity + 4 * kPlaceThreads - 1) / (4 * kPlaceThreads);
   if (ctas > sms * 8) ctas = sms * 8;
+  if (ctas < 1) ctas = 1;
   e = launch_pdl(extend_place_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPlaceThreads), 0, stream, p);
   if (e == cudaSuccess) note_launches(1);
   return e;
@@ -327,15 +469,19 @@ cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream) {
   return e;
 }
 
-cudaError_t launch_append_fp8(const AppendParams& p, size_t clear_bytes, cudaStream_t stream) {
-  cudaError_t e = cudaMemsetAsync(p.hdr, 0, clear_bytes, stream);
+cudaError_t launch_append_fp8(const AppendParams& p, size_t clear_bytes, int sms, cudaStream_t stream) {
+  const long long words = static_cast<long long>(clear_bytes / 16);  // the workspace's parts are multiples of 256 bytes
+  long long clear_ctas = (words + 4 * kClearThreads - 1) / (4 * kClearThreads);
+  if (clear_ctas > sms) clear_ctas = sms;
+  cudaError_t e = launch_pdl(clear_kernel, dim3(static_cast<unsigned>(clear_ctas)), dim3(kClearThreads), 0, stream,
+                             reinterpret_cast<uint4*>(p.hdr), words);
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (p.tokens == 0) return cudaSuccess;
-  // few tokens are mostly runs of their own (a decode step), many are prompts with a run per page: the CTAs of a chunk
-  // without a run's first token end at once
-  int chunk = 1;
-  while (chunk < 64 && p.tokens > 512LL * chunk) chunk *= 2;
+  // Few tokens are mostly runs of their own (a decode step), one to a warp; many are prompts with a run per page: the CTAs of
+  // a chunk without a run's first token end at once.
+  int chunk = kRunThreads / 32;
+  while (chunk < kMostChunk && p.tokens > 512LL * chunk) chunk *= 2;
   int heads = 0;
   for (int i = 0; i < p.planes; ++i) heads += p.plane[i].width / 128;
   e = launch_pdl(append_fp8_kernel, dim3(static_cast<unsigned>((p.tokens + chunk - 1) / chunk), heads), dim3(kRunThreads),

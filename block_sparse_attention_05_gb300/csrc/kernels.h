@@ -411,7 +411,7 @@ struct AppendParams {
   uint32_t* marks;         // fp8: [n_pages] behind the header
 };
 cudaError_t launch_append(const AppendParams& p, int sms, cudaStream_t stream);
-cudaError_t launch_append_fp8(const AppendParams& p, size_t clear_bytes, cudaStream_t stream);
+cudaError_t launch_append_fp8(const AppendParams& p, size_t clear_bytes, int sms, cudaStream_t stream);
 
 // ---------------------------------------------------------------- eviction
 struct EvictParams {

@@ -159,14 +159,19 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       if (j < items) {
         it.base = static_cast<int>(before);  // total < ctas * (max_nb + slack): fits
         p.items[j] = it;
-        const long long lo = before * p.hkv, hi = lo + static_cast<long long>(it.blocks) * p.hkv;
-        for (int r = static_cast<int>((lo * runs + total - 1) / total); r < runs; ++r) {
-          const long long at = total * r / runs;
-          if (at >= hi) break;
-          if (at >= lo) p.run_item[r] = j;
-        }
       }
       carry += t;
+    }
+    __syncthreads();
+    if (static_cast<int>(threadIdx.x) < runs) {
+      const long long at = total * threadIdx.x / runs;
+      int lo = 0, hi = items - 1;  // the last item that begins at or before it
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (static_cast<long long>(p.items[mid].base) * p.hkv <= at) lo = mid;
+        else hi = mid - 1;
+      }
+      p.run_item[threadIdx.x] = lo;
     }
     return;
   }
