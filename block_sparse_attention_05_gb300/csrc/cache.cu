@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(AppendParams 
 }
 
 // ---------------------------------------------------------------- rows, E4M3
-constexpr int kRunThreads = 128;
+constexpr int kRunThreads = 256;
 constexpr float kZeroBelow = 3.0092655e-36f;  // 2^-118: an amax / 448 is a normal number from here on
 
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
@@ -247,68 +247,83 @@ __device__ __forceinline__ RunScale run_scale(float was, float amax, bool live) 
   r.inv = __fdiv_rn(1.0f, r.down);
   return r;
 }
-// fp32(x / down), correctly rounded: with 1 / down correctly rounded, one step from the remainder, which an fma gives exactly
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990).  A division each took
-// a third of the kernel's time.
-__device__ __forceinline__ float quotient(float x, const RunScale& r) {
-  if (r.plain) return __fdiv_rn(x, r.down);
-  const float q = x * r.inv;
-  const float exact = fmaf(fmaf(-q, r.down, x), r.inv, q);
-  return fabsf(q) < 1e30f && q != 0.0f ? exact : q;  // inf, NaN and -0 as they are
+// fp32(x / down), correctly rounded, of two numbers: with 1 / down correctly rounded, one step from the remainder, which an
+// fma gives exactly (Markstein, "Computation of elementary functions on the IBM RISC System/6000 processor", 1990); the
+// sign is put back for zeros.  With a division for each value the kernel ran 45 instructions a value.  Not for inf and NaN.
+__device__ __forceinline__ float2 quotients(float2 x, const RunScale& r) {
+  const float2 inv = make_float2(r.inv, r.inv), q = fmul2(x, inv);
+  const float2 rest = ffma2(make_float2(-q.x, -q.y), make_float2(r.down, r.down), x), e = ffma2(rest, inv, q);
+  auto with_sign = [](float a, float b) { return __uint_as_float(__float_as_uint(a) | (__float_as_uint(b) & 0x80000000u)); };
+  return make_float2(with_sign(e.x, q.x), with_sign(e.y, q.y));
 }
+__device__ __forceinline__ float2 divided(float2 x, const RunScale& r) {
+  return make_float2(__fdiv_rn(x.x, r.down), __fdiv_rn(x.y, r.down));
+}
+template <bool PLAIN>
 __device__ __forceinline__ uint2 codes_of(const uint4& v, const RunScale& r) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t c[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    c[j] = to_e4m3x2(quotient(__uint_as_float(w[j] << 16) * r.up, r), quotient(__uint_as_float(w[j] & 0xFFFF0000u) * r.up, r));
+  for (int j = 0; j < 4; ++j) {
+    const float2 x = fmul2(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), make_float2(r.up, r.up));
+    const float2 q = PLAIN ? divided(x, r) : quotients(x, r);
+    c[j] = to_e4m3x2(q.x, q.y);
+  }
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
+// Out of line: where a scale is outside 2^-100 .. 2^100, or a value is inf or NaN.
+__device__ __noinline__ uint2 codes_of_any(uint4 v, RunScale r) { return codes_of<true>(v, r); }
 // Eight codes of a row that was there before, at the new scale.
+template <bool PLAIN>
 __device__ __forceinline__ uint2 codes_again(const uint2& old, const RunScale& r) {
-  const uint32_t w[2] = {old.x, old.y};
-  uint32_t out[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float2 f0 = from_e4m3x2(w[j] & 0xFFFFu), f1 = from_e4m3x2(w[j] >> 16);
-    auto again = [&](float f) { return quotient(f * r.up * r.was, r); };
-    out[j] = to_e4m3x2(again(f0.x), again(f0.y)) | to_e4m3x2(again(f1.x), again(f1.y)) << 16;
-  }
-  return make_uint2(out[0], out[1]);
-}
-__device__ __forceinline__ uint32_t bf16x8_max(const uint4& v, uint32_t m) {  // of |x|, as bits; inf and NaN do not count
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const uint32_t w[4] = {old.x & 0xFFFFu, old.x >> 16, old.y & 0xFFFFu, old.y >> 16};
+  uint32_t c[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const uint32_t l = w[j] & 0x7FFFu, h = (w[j] >> 16) & 0x7FFFu;
-    if (l < 0x7F80u) m = max(m, l);
-    if (h < 0x7F80u) m = max(m, h);
+    const float2 x = fmul2(fmul2(from_e4m3x2(w[j]), make_float2(r.up, r.up)), make_float2(r.was, r.was));
+    const float2 q = PLAIN ? divided(x, r) : quotients(x, r);
+    c[j] = to_e4m3x2(q.x, q.y);
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+__device__ __noinline__ uint2 codes_again_any(uint2 old, RunScale r) { return codes_again<true>(old, r); }
+// |x| as bits, two values to a word: the largest of eight and of m.
+__device__ __forceinline__ uint32_t bf16x8_max(const uint4& v, uint32_t m) {
+  return __vmaxu2(__vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)), m);
+}
+// The same of finite values, where there are others.
+__device__ __noinline__ uint32_t bf16x8_max_finite(uint4 v, uint32_t m) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = w[j >> 1] >> (j & 1) * 16 & 0x7FFFu;
+    if (b < 0x7F80u) m = max(m, b);
   }
   return m;
 }
 
-// CTA (x, y): the runs that begin among tokens [x * chunk, (x + 1) * chunk), head y of the planes.  16 threads take a row, 8
-// values each.  A short run is one warp's, two rows at a time; a longer one all four warps', eight rows at a time,
-// every row in registers between its maximum and its codes.  Slots are read once, those of the longest run behind the
-// chunk among them.
+// A CTA: the runs that begin among the tokens of a chunk, one head of the planes.  16 threads take a row, 8
+// values each.  A short run is one warp's, two rows at a time; a longer one all warps', 16 rows at a time; its rows stay in
+// registers between their maximum and their codes.  Slots are read once, those of the longest run behind the chunk
+// among them.
 constexpr int kShortRun = 16;
-constexpr int kMostChunk = 64;
-__global__ void __launch_bounds__(kRunThreads, 5) append_fp8_kernel(AppendParams p, int chunk) {
+constexpr int kMostChunk = 128;
+__global__ void __launch_bounds__(kRunThreads, 3) append_fp8_kernel(AppendParams p, int chunk, uint32_t all_heads) {
   __shared__ int s_page[2 + kMostChunk + 128];  // page of tokens lo - 1 .. lo + chunk + 127, -1: none
   __shared__ uint8_t s_row[2 + kMostChunk + 128];
-  __shared__ int s_long[kMostChunk];            // lengths of the runs for all warps, by their first token; 0: none
+  __shared__ int2 s_long[kMostChunk / kShortRun + 1];  // runs for all warps: first token, length
+  __shared__ int s_count;
   __shared__ uint32_t s_max[kRunThreads / 32];
   __shared__ int s_low[kRunThreads / 32];
   griddep_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int head = blockIdx.y, pl = 0;
+  int head = static_cast<int>(blockIdx.x % all_heads), pl = 0;  // the heads of a chunk run together: their rows share pages of DRAM
+  const bool marks = head == 0;
   while (head >= p.plane[pl].width / 128) head -= p.plane[pl++].width / 128;
   const AppendPlane& a = p.plane[pl];
   const int heads = a.width / 128;
   const long long rows = p.n_pages * 128, row_bytes = static_cast<long long>(heads) * 128;
-  const long long lo = static_cast<long long>(blockIdx.x) * chunk;
+  const long long lo = static_cast<long long>(blockIdx.x / all_heads) * chunk;
   const int n = static_cast<int>(min(static_cast<long long>(chunk), p.tokens - lo));
-  const bool marks = blockIdx.y == 0;
   for (int t = tid; t < 1 + chunk + 128; t += kRunThreads) {
     const long long i = lo - 1 + t;
     long long slot = -1;
@@ -318,14 +333,18 @@ __global__ void __launch_bounds__(kRunThreads, 5) append_fp8_kernel(AppendParams
     s_page[t] = there ? static_cast<int>(slot >> 7) : -1;
     s_row[t] = static_cast<uint8_t>(slot & 127);
   }
-  if (tid < kMostChunk) s_long[tid] = 0;
+  if (tid == 0) s_count = 0;
   __syncthreads();
   const int sub = lane & 15, half = lane >> 4;
   const __nv_bfloat16* const x0 = a.x + lo * a.stride + head * 128 + sub * 8;
-  bool any_long = false;
-  for (int t = warp; t < n; t += kRunThreads / 32) {
-    const int page = s_page[1 + t];
-    if (page < 0 || s_page[t] == page) continue;  // not a run's first token
+  // the warp's share of the chunk's tokens, one to a lane: which are a run's first
+  constexpr int kWarps = kRunThreads / 32;
+  static_assert(kMostChunk <= 32 * kWarps, "a lane per token");
+  const int at = warp + lane * kWarps;
+  uint32_t starts = __ballot_sync(0xFFFFFFFFu, at < n && s_page[min(1 + at, 1 + kMostChunk)] >= 0 &&
+                                                   s_page[min(at, kMostChunk)] != s_page[min(1 + at, 1 + kMostChunk)]);
+  for (; starts; starts &= starts - 1) {
+    const int t = warp + (__ffs(starts) - 1) * kWarps, page = s_page[1 + t];
     int len = 0;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -338,8 +357,7 @@ __global__ void __launch_bounds__(kRunThreads, 5) append_fp8_kernel(AppendParams
       if (atomicExch(&p.marks[page], 1u) != 0u || more) atomicOr(&p.hdr->status, kFlagBadIndex);
     }
     if (len > kShortRun) {
-      if (lane == 0) s_long[t] = len;
-      any_long = true;
+      if (lane == 0) s_long[atomicAdd(&s_count, 1)] = make_int2(t, len);  // at most one in kShortRun tokens begins one
       continue;
     }
     float* const scale_at = a.scale + static_cast<long long>(page) * heads + head;
@@ -358,6 +376,13 @@ __global__ void __launch_bounds__(kRunThreads, 5) append_fp8_kernel(AppendParams
     }
 #pragma unroll
     for (int k = 0; k < kShortRun / 2; ++k) m = bf16x8_max(v[k], m);
+    m = max(m & 0xFFFFu, m >> 16);
+    const bool odd = __any_sync(0xFFFFFFFFu, m >= 0x7F80u);  // an inf or NaN
+    if (odd) {
+      m = 0;
+#pragma unroll
+      for (int k = 0; k < kShortRun / 2; ++k) m = bf16x8_max_finite(v[k], m);
+    }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     low = __reduce_min_sync(0xFFFFFFFFu, low);
     const RunScale r = run_scale(was, __uint_as_float(m << 16), low > 0);
@@ -372,35 +397,46 @@ __global__ void __launch_bounds__(kRunThreads, 5) append_fp8_kernel(AppendParams
           if (row + 2 * k < low) old[k] = *reinterpret_cast<const uint2*>(cache + (row + 2 * k) * row_bytes);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (row + 2 * k < low) *reinterpret_cast<uint2*>(cache + (row + 2 * k) * row_bytes) = codes_again(old[k], r);
+          if (row + 2 * k < low) *reinterpret_cast<uint2*>(cache + (row + 2 * k) * row_bytes) =
+                r.plain ? codes_again_any(old[k], r) : codes_again<false>(old[k], r);
       }
     }
+    const bool any = r.plain || odd;
 #pragma unroll
-    for (int k = 0; k < kShortRun / 2; ++k)
-      if (k * 2 + half < len) *reinterpret_cast<uint2*>(cache + s_row[1 + t + k * 2 + half] * row_bytes) = codes_of(v[k], r);
+    for (int k = 0; k < kShortRun / 2; ++k) {
+      const int q = k * 2 + half;
+      if (q < len)
+        *reinterpret_cast<uint2*>(cache + s_row[1 + t + q] * row_bytes) = any ? codes_of_any(v[k], r) : codes_of<false>(v[k], r);
+    }
   }
-  if (!__syncthreads_or(any_long)) return;
+  __syncthreads();
   const int r0 = tid >> 4;
-  for (int t = 0; t < n; ++t) {
-    const int len = s_long[t];
-    if (len == 0) continue;
+  for (int j = 0; j < s_count; ++j) {
+    const int t = s_long[j].x, len = s_long[j].y;
     const int page = s_page[1 + t];
     float* const scale_at = a.scale + static_cast<long long>(page) * heads + head;
     const float was = *scale_at;
-    uint4 v[16];
+    uint4 v[8];
     uint32_t m = 0;
     int low = 127;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const int r = k * 8 + r0;
+    for (int k = 0; k < 8; ++k) {
+      const int q = k * 16 + r0;
       v[k] = make_uint4(0, 0, 0, 0);
-      if (r < len) {
-        v[k] = *reinterpret_cast<const uint4*>(x0 + (t + r) * a.stride);
-        low = min(low, static_cast<int>(s_row[1 + t + r]));
+      if (q < len) {
+        v[k] = *reinterpret_cast<const uint4*>(x0 + (t + q) * a.stride);
+        low = min(low, static_cast<int>(s_row[1 + t + q]));
       }
     }
 #pragma unroll
-    for (int k = 0; k < 16; ++k) m = bf16x8_max(v[k], m);
+    for (int k = 0; k < 8; ++k) m = bf16x8_max(v[k], m);
+    m = max(m & 0xFFFFu, m >> 16);
+    const bool odd = __any_sync(0xFFFFFFFFu, m >= 0x7F80u);  // an inf or NaN among the warp's rows
+    if (odd) {
+      m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) m = bf16x8_max_finite(v[k], m);
+    }
     m = __reduce_max_sync(0xFFFFFFFFu, m);
     low = __reduce_min_sync(0xFFFFFFFFu, low);
     if (lane == 0) {
@@ -408,26 +444,34 @@ __global__ void __launch_bounds__(kRunThreads, 5) append_fp8_kernel(AppendParams
       s_low[warp] = low;
     }
     __syncthreads();
-    m = max(max(s_max[0], s_max[1]), max(s_max[2], s_max[3]));
-    low = min(min(s_low[0], s_low[1]), min(s_low[2], s_low[3]));
+#pragma unroll
+    for (int w = 0; w < kRunThreads / 32; ++w) {
+      m = max(m, s_max[w]);
+      low = min(low, s_low[w]);
+    }
     const RunScale r = run_scale(was, __uint_as_float(m << 16), low > 0);
     uint8_t* const cache = static_cast<uint8_t*>(a.cache) + (static_cast<long long>(page) * 128 * heads + head) * 128 + sub * 8;
     __syncthreads();  // every thread has read the scale, and the maxima
     if (tid == 0) *scale_at = r.now;
     if (low > 0 && r.now != was) {
-      for (int row = r0; row < low; row += 64) {
+      for (int row = r0; row < low; row += 128) {
         uint2 old[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (row + 8 * k < low) old[k] = *reinterpret_cast<const uint2*>(cache + (row + 8 * k) * row_bytes);
+          if (row + 16 * k < low) old[k] = *reinterpret_cast<const uint2*>(cache + (row + 16 * k) * row_bytes);
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          if (row + 8 * k < low) *reinterpret_cast<uint2*>(cache + (row + 8 * k) * row_bytes) = codes_again(old[k], r);
+          if (row + 16 * k < low) *reinterpret_cast<uint2*>(cache + (row + 16 * k) * row_bytes) =
+                r.plain ? codes_again_any(old[k], r) : codes_again<false>(old[k], r);
       }
     }
+    const bool any = r.plain || odd;
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (k * 8 + r0 < len) *reinterpret_cast<uint2*>(cache + s_row[1 + t + k * 8 + r0] * row_bytes) = codes_of(v[k], r);
+    for (int k = 0; k < 8; ++k) {
+      const int q = k * 16 + r0;
+      if (q < len)
+        *reinterpret_cast<uint2*>(cache + s_row[1 + t + q] * row_bytes) = any ? codes_of_any(v[k], r) : codes_of<false>(v[k], r);
+    }
   }
 }
 
@@ -484,8 +528,8 @@ cudaError_t launch_append_fp8(const AppendParams& p, size_t clear_bytes, int sms
   while (chunk < kMostChunk && p.tokens > 512LL * chunk) chunk *= 2;
   int heads = 0;
   for (int i = 0; i < p.planes; ++i) heads += p.plane[i].width / 128;
-  e = launch_pdl(append_fp8_kernel, dim3(static_cast<unsigned>((p.tokens + chunk - 1) / chunk), heads), dim3(kRunThreads),
-                 0, stream, p, chunk);
+  e = launch_pdl(append_fp8_kernel, dim3(static_cast<unsigned>((p.tokens + chunk - 1) / chunk * heads)), dim3(kRunThreads), 0,
+                 stream, p, chunk, static_cast<uint32_t>(heads));
   if (e == cudaSuccess) note_launches(1);
   return e;
 }
