@@ -346,6 +346,9 @@ struct PromptParams {
   long long n_pages;
   const float* k_scale;         // fp8: [n_pages, hkv]
   const float* v_scale;
+  const __nv_bfloat16* q;       // [total_q, hq, 128]
+  uint8_t* q8;                  // fp8, workspace: [total_q, hq, 2, 128] the queries' codes and
+  float* q_scale;               // [total_q, hq] their scales
   const int32_t* visible;       // [total_q, mask_words] bits of the new tokens that a new token sees, or null: causal
   int mask_words;
   __nv_bfloat16* o;             // [total_q, hq, 128]
@@ -364,7 +367,7 @@ struct PromptParams {
 };
 bool prompt_may_split(int max_nb);  // whether a call with so many key blocks can be cut into runs
 struct PromptMaps {
-  CUtensorMap q;     // boxes of 64 dims of a group's heads of tile_tokens tokens
+  CUtensorMap q;     // boxes of a group's heads of tile_tokens tokens (64 dims in bf16, 128 codes in fp8)
   CUtensorMap k, v;  // boxes of 128 rows of a head (64 dims in bf16, 128 codes in fp8)
 };
 cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bool fp8, cudaStream_t stream);

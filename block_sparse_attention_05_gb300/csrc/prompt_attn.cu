@@ -23,6 +23,10 @@
 // Items differ in cost.  Where there are enough of them the CTAs take them whole, largest first; where the longest alone
 // would hold up the call (few rows over a long cache) all blocks are cut into equal runs, one per CTA, and an item that
 // crosses runs leaves (O, m, l) per run, which a join kernel merges.  A plan kernel decides from the lengths.
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
 #include "attn.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -71,11 +75,55 @@ __device__ __forceinline__ int item_blocks(const PromptParams& p, const SeqInfo&
   return (si.kv_len - si.q_len + end + kBlock - 1) / kBlock;
 }
 
+// fp8: K's codes are multiplied as they are, so the queries are codes too, two per value: the first its E4M3 rounding, the
+// second that of the rest.  Four and four significant bits hold bf16's eight exactly, down to 2^-10 of the row's largest value
+// (below that the second is off by 2^-18 of the largest).  A row's scale is a power of two that brings its largest value to
+// 224 .. 448.  16 threads to a row of 128.
+__device__ __forceinline__ void query_codes(const PromptParams& p, long long first, long long stride) {
+  const int sub = threadIdx.x & 15;
+  const long long rows = static_cast<long long>(p.total_q) * p.hq;
+  for (long long row0 = first; row0 < rows; row0 += stride) {
+    const long long row = row0 + (threadIdx.x >> 4);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (row < rows) v = *reinterpret_cast<const uint4*>(p.q + row * kHeadDim + sub * 8);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    // 448 = 1.75 * 2^8; a row without an inf or NaN has an exponent below 255
+    const int e = static_cast<int>(m >> 7) - 127, up = m == 0 ? 0 : min(8 - e - ((m & 127) > 96 ? 1 : 0), 120);
+    const bool finite = m < 0x7F80u;
+    const float lift = __int_as_float((127 + max(up, -126)) << 23);  // up >= -120
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = __uint_as_float(w[j] << 16) * lift, b = __uint_as_float(w[j] & 0xFFFF0000u) * lift;
+      hi[j] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t h = e4m3x2_to_f16x2(hi[j]);
+      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      lo[j] = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
+    }
+    if (row < rows) {
+      uint8_t* to = p.q8 + row * 256 + sub * 8;
+      *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+      *reinterpret_cast<uint2*>(to + 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+      // a row with an inf or NaN has logits of NaN
+      if (sub == 0) p.q_scale[row] = finite ? __int_as_float((127 - up) << 23) : __int_as_float(0x7FC00000);
+    }
+  }
+}
+
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
   __shared__ long long sh[32];
   __shared__ int bins[kPlanBins];
   __shared__ int s_bad, s_most;
   griddep_wait();  // the kernel before may still read this workspace
+  if (blockIdx.x > 0) {  // fp8: the queries' codes
+    query_codes(p, (blockIdx.x - 1) * static_cast<long long>(kPlanThreads / 16), (gridDim.x - 1) * static_cast<long long>(kPlanThreads / 16));
+    return;
+  }
   for (int w = threadIdx.x; w < static_cast<int>(sizeof(WsHeader) / 4); w += kPlanThreads)
     reinterpret_cast<uint32_t*>(p.hdr)[w] = 0u;
   if (threadIdx.x == 0) {
@@ -266,23 +314,22 @@ struct PromptCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
   // a warpgroup's registers per thread; the launch has 65,536 for all
   static constexpr int kSoftmaxRegs = FP8 ? 184 : 208, kOtherRegs = FP8 ? 72 : 88;
-  // Stages of tiles of 128 keys as the MMAs read them.  A part of one tile of rows has the second tile's room as one more.
-  static constexpr int kStages = FP8 ? 3 : 5;
-  static constexpr int kOutStage = kStages - 2;  // a part's output passes through this and the next one
-  static constexpr int kCodeStages = FP8 ? 4 : 0;  // tiles as they land
-  static_assert(!FP8 || kCodeStages == 4, "as the widening warps count them");
+  // bf16: stages of tiles of 128 keys.  A part of one tile of rows has the second tile's room as one more.
+  static constexpr int kStages = 5;
+  static constexpr int kOutStage = kStages - 2;  // bf16: a part's output passes through this and the next one
+  // fp8: stages of K's codes, of V's as they land, of V's values (the output passes through these)
+  static constexpr int kK8 = 4, kV8 = 2, kV16 = 2;
   static constexpr int kTile = 32768, kCodes = 16384;
   static constexpr uint32_t kColS = 0, kColO = 256;
 };
 struct PromptSmem {
   uint64_t full[6], empty[6];            // a stage holds a tile / its MMAs are done
-  uint64_t code_full[4], code_empty[4];  // fp8
+  uint64_t code_full[2], code_empty[2];  // fp8: V's codes
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], o_full[2], turn[2];  // by warpgroup
   uint64_t ml_full, o_free, out_free, mma_done;
   float2 ml[2][128];
-  float scale[8];       // fp8: scales of the last tiles (no more than 3 behind the one that a warpgroup is at)
-  float code_scale[4];  // and a code stage's
+  float k_scale[8], v_scale[8];  // fp8: scales of the last blocks (loaded at most 5 ahead of the one that a warpgroup is at)
   uint32_t tmem_base;
   int abort_flag;
   uint32_t err;
@@ -345,8 +392,13 @@ __device__ __forceinline__ uint32_t tree_bits(const int32_t* mask, int words, in
 
 // The tiles of a part in the order in which they are loaded.  Two tiles of rows: K and V of a block by turns.  One: K of two
 // blocks (one per warpgroup), then their V, so that stages come free in the order in which they are wanted.
-template <int STAGES>
+struct Fill {
+  int st;           // stage
+  uint32_t parity;  // of its barrier's phase
+};
+template <bool FP8>
 struct Tiles {
+  static constexpr int STAGES = PromptCfg<false>::kStages;
   int total;     // tiles of the part
   bool one;      // one tile of rows: a stage more
   uint32_t ph;   // a bit per stage: parity of its next fill
@@ -380,17 +432,48 @@ struct Tiles {
     const uint32_t t = tile;
     return (ph >> stage(tile) ^ (one ? t / (STAGES + 1) : t / STAGES)) & 1u;
   }
+  __device__ __forceinline__ Fill k(int block) const { return {stage(k_tile(block)), parity(k_tile(block))}; }
+  __device__ __forceinline__ Fill v(int block) const { return {stage(v_tile(block)), parity(v_tile(block))}; }
+  // The last fill of the stage that a warpgroup's output passes through.
+  __device__ __forceinline__ Fill out(int b) const {
+    const int st = PromptCfg<false>::kOutStage + (one ? 1 : b);
+    return {st, (ph >> st & 1) ^ 1};
+  }
   __device__ __forceinline__ void done() {
     const int n = STAGES + (one ? 1 : 0);
     const int q = total / n, r = total - q * n;
     ph ^= ((q & 1) ? (1u << n) - 1u : 0u) ^ ((1u << r) - 1u);
   }
 };
+// fp8: K and V have stages of their own, 0 .. 3 and 4 .. 5, taken by the blocks of all parts in turn.
+template <>
+struct Tiles<true> {
+  uint32_t base;  // blocks before the part's
+  int count;
+  bool one;
+  __device__ __forceinline__ void part(const Part& g) {
+    count = g.count;
+    one = g.one;
+  }
+  __device__ __forceinline__ Fill k(int block) const {
+    const uint32_t n = base + block;
+    return {static_cast<int>(n & 3), n >> 2 & 1};
+  }
+  __device__ __forceinline__ Fill v(int block) const {
+    const uint32_t n = base + block;
+    return {static_cast<int>(4 + (n & 1)), n >> 1 & 1};
+  }
+  __device__ __forceinline__ Fill out(int b) const {
+    const int st = one ? 0 : b;
+    return {4 + st, ((base + 1 - st >> 1) - 1) & 1};
+  }
+  __device__ __forceinline__ void done() { base += count; }
+};
 
-// E4M3 codes of a tile (rows of 128 bytes, TMA's 128-byte swizzle) to bf16 in the layout in which TMA lands bf16 rows; exact.
-// 128 threads, 16 codes at a time, four pieces in flight: shared memory answers in 150 clocks beside the MMAs.  Eight lanes
-// read a row, and those of its second half write their pieces in the other order, so that eight lanes' stores meet all
-// banks.  Rows from `valid` on become zeros (V: 0 * NaN is NaN).
+// E4M3 codes of a tile (rows of 128 bytes, TMA's 128-byte swizzle) to fp16 in the layout in which TMA lands 16-bit rows;
+// exact.  128 threads, 16 codes at a time, four pieces in flight: shared memory answers in 150 clocks beside the MMAs.  Eight
+// lanes read a row, and those of its second half write their pieces in the other order, so that eight lanes' stores
+// meet all banks.  Rows from `valid` on become zeros (0 * NaN is NaN).
 __device__ __forceinline__ void widen_tile(const uint8_t* codes, uint8_t* to, int thread, int valid) {
   const int chunk = thread & 7, half = chunk >> 2, x = (thread >> 3) & 7;  // x: the row mod 8, the same in every pass
   const uint32_t flip = half;
@@ -410,11 +493,7 @@ __device__ __forceinline__ void widen_tile(const uint8_t* codes, uint8_t* to, in
       const uint32_t w[4] = {in[k].x, in[k].y, in[k].z, in[k].w};
       uint32_t out[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {  // four significant bits: the upper half of the value in fp32
-        const uint32_t h = e4m3x2_to_f16x2(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-        out[j] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x7632);
-      }
+      for (int j = 0; j < 8; ++j) out[j] = e4m3x2_to_f16x2(j & 1 ? w[j >> 1] >> 16 : w[j >> 1]);
       const uint4 a = make_uint4(out[0], out[1], out[2], out[3]), b = make_uint4(out[4], out[5], out[6], out[7]);
       uint4* d = dst + (pass + k) * 128;
       d[(at + flip) ^ x] = flip ? b : a;
@@ -428,19 +507,22 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ PromptMaps maps, PromptParams p) {
   using C = PromptCfg<FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* const q_buf = smem;             // two tiles, each two 64-dim halves of 128 rows
-  uint8_t* const ring = smem + 2 * 32768;  // stages, as the queries' tiles; the last one is the second tile of queries
-  uint8_t* const codes = ring + C::kStages * C::kTile;
+  // Two tiles of queries, each two 64-dim halves of 128 rows (fp8: two tiles of codes); the stages.  bf16: as the queries'
+  // tiles, the last one is the second tile of queries.  fp8: K's codes, V's codes, V's values.
+  uint8_t* const q_buf = smem;
+  uint8_t* const ring = smem + 2 * 32768;
+  uint8_t* const v_codes = ring + C::kK8 * C::kCodes;
+  uint8_t* const v_ring = v_codes + C::kV8 * C::kCodes;
   PromptSmem& sm = *reinterpret_cast<PromptSmem*>(smem + 7 * 32768);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group, T = p.tile_tokens;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i <= C::kStages; ++i) {
-      mbar_init(&sm.full[i], FP8 ? 4 : 1);
+    for (int i = 0; i < 6; ++i) {
+      mbar_init(&sm.full[i], FP8 && i >= C::kK8 ? 4 : 1);
       mbar_init(&sm.empty[i], 2);
     }
-    for (int i = 0; i < C::kCodeStages; ++i) {
+    for (int i = 0; i < C::kV8; ++i) {
       mbar_init(&sm.code_full[i], 1);
       mbar_init(&sm.code_empty[i], 4);
     }
@@ -480,15 +562,19 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
   };
   if (warp >= 8) regs_release<C::kOtherRegs>();
 
-  auto stage_at = [&](int st) { return st < C::kStages ? ring + st * C::kTile : q_buf + 32768; };
+  // stages of values: bf16 all of them, fp8 those of V
+  auto stage_at = [&](int st) {
+    if (FP8) return v_ring + (st - C::kK8) * C::kTile;
+    return st < C::kStages ? ring + st * C::kTile : q_buf + 32768;
+  };
   PartWalker walk(p);
   Part g{};
-  Tiles<C::kStages> tl{};
+  Tiles<FP8> tl{};
   if (warp == 9) {
     // ------------------------------------------------------------ loads: Q of a part, its tiles
-    uint32_t landed = 0, parts = 0, queries = 0, bad = 0;  // landed: fp8, code tiles
+    uint32_t parts = 0, queries = 0, bad = 0, blocks = 0;
     uint32_t used = 0, filled = 0;  // bf16: a bit per stage that has been filled; its last fill's parity
-    bool ok = true, lent = false;   // lent: the second tile of queries has been a stage since it was loaded last
+    bool ok = true, lent = false;   // bf16: the second tile of queries has been a stage since it was loaded last
     uint32_t lent_parity = 0;
     // Rows of a part's blocks, 32 at a time, one per lane, and their scales; the next 32 are on their way while these load.
     struct Rows {
@@ -511,55 +597,84 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       }
       return x;
     };
+    // Q: behind the first block where it waits for the part before
+    auto load_q = [&] {
+      if (!((parts == 0 || mbar_wait_warp(&sm.q_empty, (parts - 1) & 1, abort_flag)) &&
+            (g.one || !lent || mbar_wait_warp(&sm.empty[C::kStages], lent_parity, abort_flag))))
+        return false;
+      if (!g.one) lent = false;
+      if (lane == 0) {
+        const int n = g.one ? 1 : 2;
+        mbar_arrive_expect_tx(&sm.q_full, n * T * G * 256);
+        for (int b = 0; b < n; ++b)
+          for (int half = 0; half < 2; ++half)
+            tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * (FP8 ? 128 : 64), g.head * G,
+                        g.q_start + g.t0 + b * T);
+      }
+      __syncwarp();
+      ++queries;
+      return true;
+    };
     // Every wait and shuffle takes 150 clocks beside the MMAs, and a tile has 1,000: the whole warp waits, and a tile's row
     // is fetched from its lane while the tile before it is waited for.
     while (ok && walk.next(g)) {
       tl.part(g);
       Rows now = look_up(0), then = look_up(32);
-      bool v = false, next_v;
       int row = __shfl_sync(0xFFFFFFFFu, now.row, 0);
-      float sc = FP8 ? __shfl_sync(0xFFFFFFFFu, now.sk, 0) : 1.0f;
-      bool out_read = parts == 0;  // the part before has read its output's stages
-      // Q: behind two tiles where it waits for the part before
-      auto load_q = [&] {
-        if (!((parts == 0 || mbar_wait_warp(&sm.q_empty, (parts - 1) & 1, abort_flag)) &&
-              (g.one || !lent || mbar_wait_warp(&sm.empty[C::kStages], lent_parity, abort_flag))))
-          return false;
-        if (!g.one) lent = false;
-        if (lane == 0) {
-          const int n = g.one ? 1 : 2;
-          mbar_arrive_expect_tx(&sm.q_full, n * T * G * 256);
-          for (int b = 0; b < n; ++b)
-            for (int half = 0; half < 2; ++half)
-              tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * 64, g.head * G,
-                          g.q_start + g.t0 + b * T);
-        }
-        __syncwarp();
-        ++queries;
-        return true;
-      };
       if (parts == 0) ok = load_q();
-      for (int t = 0; ok && t < tl.total; ++t, v = next_v) {
-        if (((t + 1) & 63) == 0) {  // 32 blocks in either order
-          now = then;
-          then = look_up(((t + 1) >> 1) + 32);
-        }
-        const int next = tl.block(t + 1, next_v) & 31;
-        const int next_row = __shfl_sync(0xFFFFFFFFu, now.row, next);
-        const float next_sc = FP8 ? __shfl_sync(0xFFFFFFFFu, next_v ? now.sv : now.sk, next) : 1.0f;
-        const CUtensorMap* map = v ? &maps.v : &maps.k;
-        if (FP8) {
-          const int st = landed & 3;
-          ok = landed < 4 || mbar_wait_warp(&sm.code_empty[st], (landed / 4 - 1) & 1, abort_flag);
+      if constexpr (FP8) {
+        float sk = __shfl_sync(0xFFFFFFFFu, now.sk, 0), sv = __shfl_sync(0xFFFFFFFFu, now.sv, 0);
+        for (int i = 0; ok && i < g.count; ++i, ++blocks) {
+          if (((i + 1) & 31) == 0) {
+            now = then;
+            then = look_up(i + 1 + 32);
+          }
+          const int next = (i + 1) & 31;
+          const int next_row = __shfl_sync(0xFFFFFFFFu, now.row, next);
+          const float next_sk = __shfl_sync(0xFFFFFFFFu, now.sk, next), next_sv = __shfl_sync(0xFFFFFFFFu, now.sv, next);
+          const Fill k = tl.k(i);
+          ok = blocks < C::kK8 || mbar_wait_warp(&sm.empty[k.st], k.parity ^ 1, abort_flag);
           if (!ok) break;
           if (lane == 0) {
-            sm.code_scale[st] = sc;
-            mbar_arrive_expect_tx(&sm.code_full[st], C::kCodes);
-            tma_load_3d(codes + st * C::kCodes, map, &sm.code_full[st], 0, g.head, row);
+            sm.k_scale[blocks & 7] = sk;
+            sm.v_scale[blocks & 7] = sv;
+            mbar_arrive_expect_tx(&sm.full[k.st], C::kCodes);
+            tma_load_3d(ring + k.st * C::kCodes, &maps.k, &sm.full[k.st], 0, g.head, row);
           }
           __syncwarp();
-          ++landed;
-        } else {
+          const int st = blocks & 1;
+          ok = blocks < C::kV8 || mbar_wait_warp(&sm.code_empty[st], (blocks / 2 - 1) & 1, abort_flag);
+          if (!ok) {
+            ++blocks;  // K's tile is on its way
+            break;
+          }
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&sm.code_full[st], C::kCodes);
+            tma_load_3d(v_codes + st * C::kCodes, &maps.v, &sm.code_full[st], 0, g.head, row);
+          }
+          __syncwarp();
+          row = next_row;
+          sk = next_sk;
+          sv = next_sv;
+          if (i == 0 && parts > 0) {
+            ok = load_q();
+            if (!ok) {
+              ++blocks;
+              break;
+            }
+          }
+        }
+      } else {
+        bool v = false, next_v;
+        bool out_read = parts == 0;  // the part before has read its output's stages
+        for (int t = 0; ok && t < tl.total; ++t, v = next_v) {
+          if (((t + 1) & 63) == 0) {  // 32 blocks in either order
+            now = then;
+            then = look_up(((t + 1) >> 1) + 32);
+          }
+          const int next = tl.block(t + 1, next_v) & 31;
+          const int next_row = __shfl_sync(0xFFFFFFFFu, now.row, next);
+          const CUtensorMap* map = v ? &maps.v : &maps.k;
           const int st = tl.stage(t);
           if (st >= C::kOutStage && !out_read) {
             ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
@@ -578,19 +693,18 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           __syncwarp();
           used |= 1u << st;
           filled = (filled & ~(1u << st)) | tl.parity(t) << st;
+          row = next_row;
+          if (t == 1 && parts > 0) {
+            ok = load_q();
+            if (!ok) break;
+          }
         }
-        row = next_row;
-        sc = next_sc;
-        if (t == 1 && parts > 0) {
-          ok = load_q();
-          if (!ok) break;
+        if (ok && !out_read) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+        if (g.one && tl.total > C::kStages) {  // the lent stage's last fill in this part
+          const int n = C::kStages + 1;
+          lent = true;
+          lent_parity = tl.parity(C::kStages + (tl.total - n) / n * n);
         }
-      }
-      if (!FP8 && ok && !out_read) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
-      if (g.one && tl.total > C::kStages) {  // the lent stage's last fill in this part
-        const int n = C::kStages + 1;
-        lent = true;
-        lent_parity = tl.parity(C::kStages + (tl.total - n) / n * n);
       }
       tl.done();
       ++parts;
@@ -598,11 +712,13 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     if (!ok && lane == 0) gave_up();
     if (bad) atomicOr(&sm.err, kFlagBadIndex);
     if (lane == 0) {  // no copy may land after this CTA has left (all have, but after a wait that gave up)
-      if (FP8)
-        for (uint32_t f = landed > 4 ? landed - 4 : 0; f < landed; ++f) mbar_wait(&sm.code_full[f & 3], (f / 4) & 1, nullptr);
-      else
+      if (FP8) {
+        for (uint32_t f = blocks > 4 ? blocks - 4 : 0; f < blocks; ++f) mbar_wait(&sm.full[f & 3], (f / 4) & 1, nullptr);
+        for (uint32_t f = blocks > 2 ? blocks - 2 : 0; f < blocks; ++f) mbar_wait(&sm.code_full[f & 1], (f / 2) & 1, nullptr);
+      } else {
         for (int st = 0; st <= C::kStages; ++st)
           if (used >> st & 1) mbar_wait(&sm.full[st], filled >> st & 1, nullptr);
+      }
       if (queries > 0) mbar_wait(&sm.q_full, (queries - 1) & 1, nullptr);
     }
   } else if (warp == 8 || warp == 10) {
@@ -613,9 +729,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     // and they take turns (without turns their MMAs mix, and both warpgroups wait for both).  The turn is passed on while
     // three MMAs are still to be issued, which covers its way.
     const int b = warp == 8 ? 0 : 1;
-    const uint32_t idesc_s = idesc_bf16(128, 128, false), idesc_o = idesc_bf16(128, kHeadDim, true);
+    const uint32_t idesc_s = FP8 ? idesc_e4m3(128, 128) : idesc_bf16(128, 128, false), idesc_o = FP8 ? idesc_f16(128, kHeadDim, true) : idesc_bf16(128, kHeadDim, true);
     const uint64_t q_desc = sdesc_sw128(smem_u32(q_buf), 16, 1024), k_desc = sdesc_sw128(smem_u32(ring), 16, 1024);
-    const uint64_t v_desc = sdesc_sw128(smem_u32(ring), 16384, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(FP8 ? v_ring : ring), 16384, 1024);
     const uint32_t s_col = tmem + C::kColS + b * 128, o_col = tmem + C::kColO + b * 128;
     uint32_t parts = 0;  // parts before this one
     uint32_t p_ph = 0, turn_ph = 0;
@@ -630,11 +746,10 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       ok = mbar_wait_warp(&sm.q_full, parts & 1, abort_flag);
       for (int i = -1; ok && i < steps; ++i) {
         const bool pv = i >= 0 && i < blocks, s = i + 1 < blocks;
-        const int v_tile = tl.v_tile(pv ? first + i * every : 0), k_tile = tl.k_tile(s ? first + (i + 1) * every : 0);
-        const int v_st = tl.stage(v_tile), k_st = tl.stage(k_tile);
-        if (s) ok = mbar_wait_warp(&sm.full[k_st], tl.parity(k_tile), abort_flag);
+        const Fill v = tl.v(pv ? first + i * every : 0), k = tl.k(s ? first + (i + 1) * every : 0);
+        if (s) ok = mbar_wait_warp(&sm.full[k.st], k.parity, abort_flag);
         if (pv) {
-          ok = ok && mbar_wait_warp(&sm.full[v_st], tl.parity(v_tile), abort_flag);
+          ok = ok && mbar_wait_warp(&sm.full[v.st], v.parity, abort_flag);
           // O of the part before has been read
           if (i == 0 && parts > 0) ok = ok && mbar_wait_warp(&sm.o_free, (parts - 1) & 1, abort_flag);
         }
@@ -644,8 +759,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         turn_ph ^= 1;
         if (!ok) break;
         tc_fence_after();
-        // (the lent stage lies one tile before the first)
-        const uint64_t ka = k_desc + (k_st < C::kStages ? k_st : -1) * 2048, va = v_desc + (v_st < C::kStages ? v_st : -1) * 2048;
+        // (bf16: the lent stage lies one tile before the first)
+        const uint64_t ka = k_desc + (FP8 ? k.st * 1024 : (k.st < C::kStages ? k.st : -1) * 2048);
+        const uint64_t va = v_desc + (FP8 ? v.st - C::kK8 : v.st < C::kStages ? v.st : -1) * 2048;
         const uint32_t more = i > 0 ? 1u : 0u;
         auto issue_pv = [&](bool pass) {
 #pragma unroll
@@ -658,8 +774,10 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         auto issue_s = [&] {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
+            // 64 dims (fp8: the queries' first or second codes) and 32 bytes of them
             const uint32_t off = (kk >> 2) * 1024 + (kk & 3) * 2;
-            umma_bf16(s_col, qa + off, ka + off, idesc_s, kk ? 1u : 0u);
+            if (FP8) umma_e4m3(s_col, qa + off, ka + (kk & 3) * 2, idesc_s, kk ? 1u : 0u);
+            else umma_bf16(s_col, qa + off, ka + off, idesc_s, kk ? 1u : 0u);
             if (kk == 4) mbar_arrive(&sm.turn[b ^ 1]);
           }
           umma_commit(&sm.s_full[b]);
@@ -675,9 +793,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           if (!pv && !s) mbar_arrive(&sm.turn[b ^ 1]);
           if (pv) {
             if (!s) umma_commit(&sm.o_full[b]);
-            give(&sm.empty[v_st]);
+            give(&sm.empty[v.st]);
           }
-          if (s) give(&sm.empty[k_st]);
+          if (s) give(&sm.empty[k.st]);
         }
         __syncwarp();
         if (i + 1 == (blocks > 0 ? blocks - 1 : 0)) {  // its last S of the part (or the first step, if it has none)
@@ -702,7 +820,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     const uint32_t group_inv = 65536u / G + 1;  // row * group_inv >> 16 = row / G for rows below 128
     const uint32_t la = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = la + C::kColS + b * 128, o_col = la + C::kColO + b * 128;
-    uint32_t tiles = 0, parts = 0, steps = 0, outs = 0, merges = 0;
+    uint32_t parts = 0, steps = 0, outs = 0, merges = 0;
     bool ok = true;
     auto warp_arrive = [&](uint64_t* bar) {
       __syncwarp();
@@ -715,6 +833,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       const int sees = p.visible ? g.past : g.past + t_tile + 1;  // keys that every row of the tile sees
       const int32_t* mask = p.visible && mine ? p.visible + static_cast<long long>(g.q_start + tok) * p.mask_words : nullptr;
       tl.part(g);
+      // fp8: the row's queries are codes of a scale of their own
+      const float qc = FP8 && mine ? normal_factor(p.scale_log2 * p.q_scale[(static_cast<long long>(g.q_start) + tok) * p.hq + g.head * G + my_h]) : 1.0f;
       float m = -INFINITY;
       float2 l2 = make_float2(0.0f, 0.0f);
       int blk = g.one ? b : 0;
@@ -727,32 +847,50 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           break;
         }
         tc_fence_after();
-        const int v_tile = tl.v_tile(blk), v_st = tl.stage(v_tile);
-        float c = p.scale_log2, sv = 1.0f;
-        if (FP8) {
-          // the scales come with their tiles, K's before V's (every earlier fill of the stage is past: its P V came before S of this step)
-          if (!mbar_wait_warp(&sm.full[v_st], tl.parity(v_tile), abort_flag)) {
+        const Fill vf = tl.v(blk);
+        float c = p.scale_log2, lv = 0.0f;
+        if constexpr (FP8) {
+          // the scales come before V's codes (every earlier fill of the stage is past: its P V came before S of this step)
+          if (!mbar_wait_warp(&sm.full[vf.st], vf.parity, abort_flag)) {
             ok = false;
             break;
           }
-          c = normal_factor(c * sm.scale[(tiles + tl.k_tile(blk)) & 7]);
-          sv = sm.scale[(tiles + v_tile) & 7];
+          c = normal_factor(qc * sm.k_scale[tl.base + blk & 7]);
+          lv = log2f(sm.v_scale[tl.base + blk & 7]);
         } else if (edge && j0 + kBlock > g.past + g.q_len && (g.one || b == 0)) {
           // V rows past the sequence's end hold anything, and 0 * NaN is NaN: zero them
-          if (!mbar_wait_warp(&sm.full[v_st], tl.parity(v_tile), abort_flag)) {
+          if (!mbar_wait_warp(&sm.full[vf.st], vf.parity, abort_flag)) {
             ok = false;
             break;
           }
-          uint4* v = reinterpret_cast<uint4*>(stage_at(v_st));
+          uint4* v = reinterpret_cast<uint4*>(stage_at(vf.st));
           for (int i = (g.past + g.q_len - j0) * 8 + r; i < kBlock * 8; i += 128) {
             v[i] = make_uint4(0, 0, 0, 0);
             v[1024 + i] = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
         }
+        // Hides what the row does not see of 32 columns, and gives the maximum of the others.
+        auto hide = [&](uint32_t (&v)[32], int q) {
+          uint32_t bits;
+          if (p.visible) {
+            bits = mask ? tree_bits(mask, p.mask_words, g.past, g.q_len, j0 + 32 * q) : 0u;
+          } else {
+            const int n = g.past + tok + 1 - j0 - 32 * q;
+            bits = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
+          }
+          float x = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (!(bits >> j & 1)) v[j] = 0xFF800000u;
+            x = fmaxf(x, __uint_as_float(v[j]));
+          }
+          return x;
+        };
+        // The row of S stays in registers from its maximum to its weights.
         uint32_t v[4][32];
-        float mx[4];
-        auto load = [&] {
+        auto row_max = [&] {
+          float mx[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) tmem_ld_max_32cols(s_col + 32 * q, v[q], mx[q]);
           tmem_ld_wait_regs_max(v[0], mx[0]);
@@ -760,26 +898,13 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           for (int q = 1; q < 4; ++q) tmem_regs_written(v[q], mx[q]);
           if (edge) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint32_t bits;
-              if (p.visible) {
-                bits = mask ? tree_bits(mask, p.mask_words, g.past, g.q_len, j0 + 32 * q) : 0u;
-              } else {
-                const int n = g.past + tok + 1 - j0 - 32 * q;
-                bits = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
-              }
-              float x = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                if (!(bits >> j & 1)) v[q][j] = 0xFF800000u;
-                x = fmaxf(x, __uint_as_float(v[q][j]));
-              }
-              mx[q] = x;
-            }
+            for (int q = 0; q < 4; ++q) mx[q] = hide(v[q], q);
           }
+          return fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
         };
-        load();
-        const float x = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * c;
+        // fp8: V's scale goes to the weights as a summand of their exponents, so that they are at most 2^8 whatever the pages'
+        // scales, and one fp16 value each (11 significant bits, down to 2^-24)
+        const float x = fmaf(row_max(), c, lv);
         const bool fresh = m == -INFINITY;  // no key counts so far: O and l are 0, or not there yet
         // (rows of nobody hold what the stages held before: they neither rescale nor round)
         const bool rise = mine && !fresh && x - m > 8.0f;
@@ -788,39 +913,44 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           l2.x *= k;
           l2.y *= k;
           scale_row(o_col, k);
-          load();
+          row_max();  // the row again
         }
         if (fresh || rise) m = x;
-        if (__any_sync(0xFFFFFFFFu, mine && fabsf(m) >= kRoundLogits && m != -INFINITY)) {
-          // products rounded to fp32 logits before the reference is taken off: see kRoundLogits
-          const float k = fabsf(m) >= kRoundLogits ? c : 1.0f;
+        // products rounded to fp32 logits before the reference is taken off: see kRoundLogits
+        const bool big = __any_sync(0xFFFFFFFFu, mine && fabsf(m) >= kRoundLogits && m != -INFINITY);
+        const float first_c = big && fabsf(m) >= kRoundLogits ? c : 1.0f;
+        if (big && fabsf(m) >= kRoundLogits) c = 1.0f;
+        const float off = m == -INFINITY ? 0.0f : lv - m;  // -inf - -inf is NaN
+        const float2 c2 = make_float2(c, c), nm = make_float2(off, off);
+        float2 sum = FP8 ? make_float2(0.0f, 0.0f) : l2;
+        auto weights = [&](uint32_t (&v)[32], int q) {
+          if (big) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[q][j] = __float_as_uint(__uint_as_float(v[q][j]) * k);
-          if (fabsf(m) >= kRoundLogits) c = 1.0f;
-        }
-        const float off = m == -INFINITY ? 0.0f : -m;  // -inf - -inf is NaN
-        const float2 c2 = make_float2(c, c), nm = make_float2(off, off), s2 = make_float2(sv, sv);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
+            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * first_c);
+          }
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const float2 z = ffma2(make_float2(__uint_as_float(v[q][2 * j]), __uint_as_float(v[q][2 * j + 1])), c2, nm);
-            float2 e = make_float2(exp2_approx(z.x), exp2_approx(z.y));
-            l2 = fadd2(l2, e);
-            if (FP8) e = fmul2(e, s2);
-            w[j] = pack_bf16(e.x, e.y);
+            const float2 z = ffma2(make_float2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1])), c2, nm);
+            const float2 e = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+            sum = fadd2(sum, e);
+            w[j] = FP8 ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
           }
           tmem_st_16cols(s_col + 16 * q, w);
+        };
+#pragma unroll
+        for (int q = 0; q < 4; ++q) weights(v[q], q);
+        if (FP8) {
+          const float back = exp2_approx(-lv);
+          l2 = ffma2(sum, make_float2(back, back), l2);
+        } else {
+          l2 = sum;
         }
         tmem_st_wait();
         tc_fence_before();
         warp_arrive(&sm.p_full[b]);
       }
       if (!ok) break;
-      tiles += tl.total;
       tl.done();
 
       // ---- output
@@ -868,9 +998,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       // The output goes through a stage of the ring (whose last tile has been multiplied), each warp's rows by the warp
       // itself, so that a store writes whole rows: with 16 bytes of 32 rows to a store the output took 7,200 clocks of every
       // part, through shuffles (150 clocks each beside the MMAs) more.
-      const int out_st = C::kOutStage + (g.one ? 1 : b);
-      uint8_t* const stage = stage_at(out_st);
-      if (whole && !mbar_wait_warp(&sm.empty[out_st], (tl.ph >> out_st & 1) ^ 1, abort_flag)) {
+      const Fill of = tl.out(b);
+      uint8_t* const stage = stage_at(of.st);
+      if (whole && !mbar_wait_warp(&sm.empty[of.st], of.parity, abort_flag)) {
         ok = false;
         break;
       }
@@ -935,43 +1065,33 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     }
     if (!ok && lane == 0) gave_up();
   } else if (FP8 && warp >= 12) {
-    // ------------------------------------------------------------ codes to bf16
+    // ------------------------------------------------------------ V's codes to fp16
     const int thread = threadIdx.x - 384;
-    uint32_t tile = 0, used = 0, parts = 0;  // tiles so far; a bit per stage that has been filled
+    uint32_t blocks = 0, parts = 0;
     bool ok = true;
     while (ok && walk.next(g)) {
-      tl.part(g);
-      bool out_read = parts == 0;
-      for (int t = 0; t < tl.total; ++t, ++tile) {
-        const int cs = tile & 3, st = tl.stage(t);
-        if (st >= C::kOutStage && !out_read) {  // the part before has read its output's stages
-          ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+      if constexpr (FP8) {
+        tl.part(g);
+        // the part before has read its output's stages
+        if (parts > 0) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+        for (int i = 0; ok && i < g.count; ++i, ++blocks) {
+          const int cs = blocks & 1;
+          const Fill v = tl.v(i);
+          ok = mbar_wait_warp(&sm.code_full[cs], blocks >> 1 & 1, abort_flag) &&
+               (blocks < C::kV16 || mbar_wait_warp(&sm.empty[v.st], v.parity ^ 1, abort_flag));
           if (!ok) break;
-          out_read = true;
+          // rows past the sequence's end: zeros, as 0 * NaN is NaN
+          widen_tile(v_codes + cs * C::kCodes, stage_at(v.st), thread, g.past + g.q_len - (g.block + i) * kBlock);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&sm.code_empty[cs]);
+            mbar_arrive(&sm.full[v.st]);
+          }
         }
-        if (!mbar_wait_warp(&sm.code_full[cs], (tile >> 2) & 1, abort_flag) ||
-            ((used >> st & 1) && !mbar_wait_warp(&sm.empty[st], tl.parity(t) ^ 1, abort_flag))) {
-          ok = false;
-          break;
-        }
-        // (The lent stage: its codes were loaded behind the part's Q, for which the loads waited until the part before had read
-        // its own.)
-        used |= 1u << st;
-        if (thread == 0) sm.scale[tile & 7] = sm.code_scale[cs];
-        bool v;
-        const int blk = tl.block(t, v);
-        // rows past the sequence's end: zeros, as 0 * NaN is NaN (V)
-        widen_tile(codes + cs * C::kCodes, stage_at(st), thread, g.past + g.q_len - (g.block + blk) * kBlock);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&sm.code_empty[cs]);
-          mbar_arrive(&sm.full[st]);
-        }
+        tl.done();
+        ++parts;
       }
-      if (ok && !out_read) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
-      tl.done();
-      ++parts;
     }
     if (!ok && lane == 0) gave_up();
   }
@@ -1134,7 +1254,9 @@ cudaError_t launch_attn(const PromptMaps& maps, const PromptParams& p, cudaStrea
 bool prompt_may_split(int max_nb) { return max_nb > kRunsSlack; }
 
 cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bool fp8, cudaStream_t stream) {
-  cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
+  long long ctas = 1;
+  if (fp8) ctas += std::min(static_cast<long long>(2 * p.ctas), (static_cast<long long>(p.total_q) * p.hq * 16 + kPlanThreads - 1) / kPlanThreads);
+  cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPlanThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (p.total_q == 0) return cudaSuccess;  // the lengths have been checked; there is no row to compute

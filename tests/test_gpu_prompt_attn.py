@@ -3,7 +3,8 @@
 Error bounds (u = 2^-24; a bf16 rounding is off by at most 2^-8 of the value): a logit is an fp32 sum of 128 exact
 products, off by at most 130 * 2u * scale * sum_d |q_d k_d| (tensor cores may truncate); a weight exp(s - lse) by that of
 its own logit and of lse, 2^x and the fp32 steps, and by 2^-8 of itself where it meets V; the sum over n keys adds
-(n + 16) * 2u, a rescale 2u each, of which a row has at most one per block; the output's own rounding 2^-8.
+(n + 16) * 2u, a rescale 2u each, of which a row has at most one per block; the output's own rounding 2^-8.  Over E4M3
+pages a query's value is two codes: off by at most 2^-18 of the row's largest, 2^-17 with the sum's own.
 """
 import math
 
@@ -54,6 +55,8 @@ def reference(q_lens, kv_lens, key_rows, q, k, v, k_scale, v_scale, scale, visib
                 qd = q[at:at + ql, h].double()
                 logits = (qd @ kd.T * scale).masked_fill(~seen, -math.inf)
                 err = 130 * U2 * scale * (qd.abs() @ kd.abs().T)
+                if k_scale is not None:
+                    err = err + 2.0 ** -17 * scale * qd.abs().amax(dim=1)[:, None] * kd.abs().sum(dim=1)[None, :]
                 top = torch.logsumexp(logits, dim=1)
                 p = torch.exp(logits - top.masked_fill(~some, 0.0)[:, None])
                 most = logits.masked_fill(~seen, 0.0).abs().amax(dim=1)
