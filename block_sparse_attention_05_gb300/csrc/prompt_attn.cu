@@ -916,18 +916,19 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           row_max();  // the row again
         }
         if (fresh || rise) m = x;
-        // products rounded to fp32 logits before the reference is taken off: see kRoundLogits
-        const bool big = __any_sync(0xFFFFFFFFu, mine && fabsf(m) >= kRoundLogits && m != -INFINITY);
-        const float first_c = big && fabsf(m) >= kRoundLogits ? c : 1.0f;
-        if (big && fabsf(m) >= kRoundLogits) c = 1.0f;
+        if (__any_sync(0xFFFFFFFFu, mine && fabsf(m) >= kRoundLogits && m != -INFINITY)) {
+          // products rounded to fp32 logits before the reference is taken off: see kRoundLogits
+          const float k = fabsf(m) >= kRoundLogits ? c : 1.0f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[q][j] = __float_as_uint(__uint_as_float(v[q][j]) * k);
+          if (fabsf(m) >= kRoundLogits) c = 1.0f;
+        }
         const float off = m == -INFINITY ? 0.0f : lv - m;  // -inf - -inf is NaN
         const float2 c2 = make_float2(c, c), nm = make_float2(off, off);
         float2 sum = FP8 ? make_float2(0.0f, 0.0f) : l2;
         auto weights = [&](uint32_t (&v)[32], int q) {
-          if (big) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * first_c);
-          }
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
