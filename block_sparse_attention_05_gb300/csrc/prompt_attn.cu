@@ -10,12 +10,22 @@
 // size runs the same kernel, and prompts of few tokens still fill the rows of an MMA.  An item is two such tiles of a
 // sequence and KV head.  Per block of 128 keys and tile
 //   S = Q K^T   128 x 128 x 128, both operands in shared memory, S in TMEM
-//   P = 2^(S c - m)   a row per thread, bf16, written over S in TMEM
+//   P = 2^(S c - m)   a row per thread, 16 bits, written over S in TMEM
 //   O += P V    128 x 128 x 128, P from TMEM, O in TMEM
 // A warpgroup per tile computes P while the MMAs of the other tile run.  m is a row's reference: the maximum of its first
-// block, replaced (and O and l rescaled) only when a block's maximum passes it by more than 2^8.  P is rounded to bf16
-// (2^-8 of each weight, as V's type asks: the MMA multiplies two operands of one type); l and lse sum the unrounded
-// weights, everything else is fp32.
+// block, replaced (and O and l rescaled) only when a block's maximum passes it by more than 2^8.  P is rounded to
+// bf16 (2^-8 of each weight), as V's type asks: the MMA multiplies two operands of one type, and a second product with the
+// rest would take half as much time again; l and lse sum the unrounded weights, everything else is fp32.
+//
+// E4M3 pages: K's codes are multiplied as they are (kind::f8f6f4), by queries that are two codes each; V's are widened to fp16
+// by four warps of their own, and P is fp16 (2^-11).  Widening K as well had those warps bound the kernel: 6.2 against 5.2 ms
+// for a 20,000-token prompt of 64/4 heads.
+//
+// What bounds it.  A block takes a pair of tiles 2,048 clocks of MMAs, which also read shared memory at its full rate (128 bytes
+// a clock: S alone 64 KB per tile).  Measured 2,900 at 1.86 GHz: a warpgroup's chain of S, its way to the softmax (390),
+// the softmax (1,200), P's way back (180) and P V is longer than the other's MMAs.  A 20,000-token prompt of 64/4 heads:
+// 3.95 ms, 1,660 TFLOP/s, 97 % of what the library's matrix product holds under the power limit.  P V begun at half of P
+// shortens the chain and changes nothing there.
 //
 // An item of one tile (a tree of few drafts, the end of a prompt) would leave one warpgroup idle: its blocks go to the
 // two warpgroups in turn, each with its own m, l and O, merged at the end.
@@ -820,6 +830,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     const uint32_t group_inv = 65536u / G + 1;  // row * group_inv >> 16 = row / G for rows below 128
     const uint32_t la = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     const uint32_t s_col = la + C::kColS + b * 128, o_col = la + C::kColO + b * 128;
+    constexpr float kLift = FP8 ? 7.0f : 0.0f;  // O is 2^kLift times larger than m says
     uint32_t parts = 0, steps = 0, outs = 0, merges = 0;
     bool ok = true;
     auto warp_arrive = [&](uint64_t* bar) {
@@ -902,8 +913,9 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           }
           return fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
         };
-        // fp8: V's scale goes to the weights as a summand of their exponents, so that they are at most 2^8 whatever the pages'
-        // scales, and one fp16 value each (11 significant bits, down to 2^-24)
+        // fp8: V's scale goes to the weights as a summand of their exponents, and they are 2^7 times larger: one fp16 value each,
+        // at most 2^15 whatever the pages' scales, with its 11 significant bits down to 2^-21 of the row's largest (four
+        // more, with references replaced from 2^4 on, made ragged prompts 20 % slower)
         const float x = fmaf(row_max(), c, lv);
         const bool fresh = m == -INFINITY;  // no key counts so far: O and l are 0, or not there yet
         // (rows of nobody hold what the stages held before: they neither rescale nor round)
@@ -925,7 +937,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
             for (int j = 0; j < 32; ++j) v[q][j] = __float_as_uint(__uint_as_float(v[q][j]) * k);
           if (fabsf(m) >= kRoundLogits) c = 1.0f;
         }
-        const float off = m == -INFINITY ? 0.0f : lv - m;  // -inf - -inf is NaN
+        const float off = m == -INFINITY ? 0.0f : lv - m + kLift;  // -inf - -inf is NaN
         const float2 c2 = make_float2(c, c), nm = make_float2(off, off);
         float2 sum = FP8 ? make_float2(0.0f, 0.0f) : l2;
         auto weights = [&](uint32_t (&v)[32], int q) {
@@ -942,7 +954,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) weights(v[q], q);
         if (FP8) {
-          const float back = exp2_approx(-lv);
+          const float back = exp2_approx(-lv - kLift);
           l2 = ffma2(sum, make_float2(back, back), l2);
         } else {
           l2 = sum;
@@ -965,6 +977,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         tc_fence_after();
       }
       float l = l2.x + l2.y;
+      if (l != l) m = INFINITY;  // a NaN among the logits, of which the maximum may know nothing: it passes every merge
       const bool whole = g.first && g.last;
       const long long part_at = static_cast<long long>(blockIdx.x) * 4 + (g.first ? 2 : 0) + (g.one ? 0 : b);  // a tile's
       float f_own = 1.0f, f_other = 0.0f;  // what this warpgroup's and the other's O count with
@@ -989,7 +1002,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         m = top;
       }
       // A row without a key that counts has O = 0.
-      const float inv = l == 0.0f ? 0.0f : whole ? 1.0f / l : 1.0f;
+      const float inv = l == 0.0f ? 0.0f : (whole ? 1.0f / l : 1.0f) * (FP8 ? 0x1p-7f : 1.0f);
       f_own *= inv;
       f_other *= inv;
       // Where a warpgroup had no block of the part its O holds an older one's (uniform: by the part alone).

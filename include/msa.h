@@ -570,15 +570,20 @@ msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const voi
  *               max_seqlen_k <= 2^30, softmax_scale < 1e30.
  *   q, k, v     packed, as in the conventions above.
  *   o, lse      written for every query row.
- * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (about 42 MB, whatever the lengths, plus 32
- * bytes per pair of tiles of 128 / group tokens).
+ * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (42 MB, 32 bytes per pair of tiles of
+ * 128 / group tokens, and for E4M3 pages 260 bytes per query row and head; bf16
+ * calls take a workspace without the last).
  * Numbers.  Logits, references, sums, O and lse are fp32; a weight that meets V is
- * rounded to bf16 (2^-8 of the weight), the sum takes it unrounded.  Exponentials
- * are the hardware's 2^x (2^-22 of the value).  Any finite logit gives finite
- * results; a logit of +inf gives NaN, keys of -inf do not count.  A key that a
- * query does not see does not count whatever its K holds; an inf or NaN in V shows
- * in the queries that see a key of its block of 128.  What lies past a sequence's
- * last key does not matter.  The same inputs give the same bits.
+ * rounded to bf16 (2^-8 of the weight; E4M3 pages: fp16, 2^-11, down to 2^-21 of the
+ * row's largest weight times page scale), the sum takes it unrounded.  Over E4M3
+ * pages a query's values are two E4M3 codes each: exact down to 2^-10 of the row's
+ * largest, 2^-18 of the largest below that.  Exponentials are the hardware's 2^x
+ * (2^-22 of the value).  Any finite logit gives finite results; a logit of +inf gives
+ * NaN, keys of -inf do not count.  A key that a query does not see does not count
+ * whatever its K holds; an inf or NaN in V shows in the queries that see it, and can
+ * show in those of the 255 places before it (in a tree: of the whole sequence).  What
+ * one query row or sequence holds does not change another's results, and what lies
+ * past a sequence's last key does not matter.  The same inputs give the same bits.
  * Lengths that contradict the host sizes make the kernels skip the call
  * (MSA_DEVICE_BAD_SEQLENS).
  * ------------------------------------------------------------------------ */

@@ -2,7 +2,7 @@
 
 Error bounds (u = 2^-24; a bf16 rounding is off by at most 2^-8 of the value): a logit is an fp32 sum of 128 exact
 products, off by at most 130 * 2u * scale * sum_d |q_d k_d| (tensor cores may truncate); a weight exp(s - lse) by that of
-its own logit and of lse, 2^x and the fp32 steps, and by 2^-8 of itself where it meets V; the sum over n keys adds
+its own logit and of lse, 2^x and the fp32 steps, and by 2^-8 of itself where it meets V (E4M3 pages: 2^-11); the sum over n keys adds
 (n + 16) * 2u, a rescale 2u each, of which a row has at most one per block; the output's own rounding 2^-8.  Over E4M3
 pages a query's value is two codes: off by at most 2^-18 of the row's largest, 2^-17 with the sum's own.
 """
@@ -61,11 +61,14 @@ def reference(q_lens, kv_lens, key_rows, q, k, v, k_scale, v_scale, scale, visib
                 p = torch.exp(logits - top.masked_fill(~some, 0.0)[:, None])
                 most = logits.masked_fill(~seen, 0.0).abs().amax(dim=1)
                 lt = (p * err).sum(dim=1) + U2 + (kl + 16) * U2 + 4 * U2 * (top.masked_fill(~some, 0.0).abs() + most)
-                rel = err + lt[:, None] + 4 * U2 * most[:, None] + 2.0 ** -8
+                rel = err + lt[:, None] + 4 * U2 * most[:, None] + (2.0 ** -8 if k_scale is None else 2.0 ** -11)
                 lse[at:at + ql, h], lse_tol[at:at + ql, h] = top, lt
                 o[at:at + ql, h] = p @ vd
                 o_tol[at:at + ql, h] = (2.0 ** -8 * (p @ vd).abs() + (p * rel) @ vd.abs()
                                         + (kl + 16 + kl // 128) * U2 * (p @ vd.abs()) + 2.0 ** -120)
+                if v_scale is not None:  # fp16 weights below 2^-21 of the largest weight times page scale: 2^-32 of it
+                    sv = v_scale.double()[rows // PAGE, g]
+                    o_tol[at:at + ql, h] += 2.0 ** -32 * (p * sv).amax(dim=1)[:, None] * (vd.abs() / sv[:, None]).sum(dim=0)
         at += ql
     return o, lse, o_tol, lse_tol
 
@@ -208,6 +211,52 @@ def test_rising_and_large_logits(msa, layout, gain):
     if layout == "packed":
         b.k *= torch.linspace(0.1, 4.0, b.k.shape[0], device="cuda").to(torch.bfloat16)[:, None, None]
     b.check()
+
+
+def test_pages_of_very_different_scales(msa):
+    """Pages of zeros (scale 1), of tiny and of large values side by side."""
+    for tree in (False, True):
+        b = Batch(msa, [40, 3], [900, 5000], 16, 2, "fp8", seed=31, tree=tree)
+        gen = torch.Generator(device="cuda").manual_seed(1)
+        f = 2.0 ** torch.randint(-30, 12, b.vs.shape, generator=gen, device="cuda").float()
+        b.vs *= f
+        b.ks *= 2.0 ** torch.randint(-6, 2, b.ks.shape, generator=gen, device="cuda").float()
+        zero = b.rows[0][128:256].cuda()
+        b.v[zero] = 0
+        b.vs[zero[0] // PAGE] = 1.0
+        b.check()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_rows_apart(msa, layout):
+    """What one query row holds (large values, inf, NaN) does not change another's bits; nor does a sequence's V."""
+    b = Batch(msa, [70, 9], [400, 3000], 16, 2, layout, seed=37)
+    o, lse = b.run()
+    b.q[5, 3] = 1e4
+    b.q[60, 0, 7] = math.inf
+    b.q[72, 9, 1] = math.nan
+    o2, lse2 = b.run()
+    same = torch.ones(79, 16, dtype=torch.bool, device="cuda")
+    same[5, 3] = same[60, 0] = same[72, 9] = False
+    assert torch.equal(o[same], o2[same]) and torch.equal(lse[same], lse2[same])
+    assert torch.isnan(o2[72, 9]).all() and torch.isnan(lse2[72, 9])
+    last = b.rows[1][-1].item()   # the last key of the second sequence: no query of the first meets it
+    b.v[last] = 0x7F if layout == "fp8" else math.nan
+    o3, _ = b.run()
+    same[70:] = False
+    assert torch.equal(o[same], o3[same])
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_hidden_keys(msa, layout):
+    """K of keys that a query does not see: NaN and inf there change nothing."""
+    n = 300
+    b = Batch(msa, [n], [n], 16, 1, layout, seed=41)
+    o, lse = b.run()
+    late = b.rows[0][200:].cuda()
+    b.k[late] = 0x7F if layout == "fp8" else math.inf
+    o2, lse2 = b.run()
+    assert torch.equal(o[:200], o2[:200]) and torch.equal(lse[:200], lse2[:200])
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
