@@ -175,6 +175,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     }
     return;
   }
+  __syncthreads();  // item_base is there
   const int items = static_cast<int>(n_items);
   // costs: their sum, the largest, and how many items there are of each size
   int shift = 0;

@@ -281,6 +281,21 @@ def test_same_bits(msa, q, kv):
         assert torch.equal(a[0], c[0]) and torch.equal(a[1], c[1])
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("seqs", [5, 1024, 2050])
+def test_a_workspace_may_hold_anything(msa, layout, seqs):
+    """What a workspace holds before a call does not matter: many sequences' lists are built in it."""
+    q = [1 + s % 3 for s in range(seqs)]
+    b = Batch(msa, q, [n + 7 * (s % 41) for s, n in enumerate(q)], 4, 2, layout, seed=47)
+    want = b.run()
+    ws = torch.empty_like(msa.workspace(b.prob, b.op()))
+    for fill in (0xFF, 0x7F, 0x01):
+        ws.fill_(fill)
+        o, lse = b.run(ws=ws)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert msa.msa_read_device_status(ws) == 0
+
+
 def test_packed_and_paged_agree(msa):
     """The same keys by either way: the same bits."""
     p = Batch(msa, [100, 3], [500, 9000], 16, 2, "paged", seed=23)
