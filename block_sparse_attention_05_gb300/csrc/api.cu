@@ -845,6 +845,7 @@ msa_status_t derive_prompt(const msa_problem_t* p, PromptShape& d) {
   d.G = d.hq / d.hkv;
   if (d.G > 128 || d.hkv > 1024 || d.S > (1 << 20) || d.T >= (1 << 25) || p->max_seqlen_k > (1 << 30))
     return MSA_ERR_UNSUPPORTED;
+  if (p->total_q > p->total_k || p->max_seqlen_q > p->max_seqlen_k) return MSA_ERR_INVALID_ARG;  // q_len <= kv_len
   d.max_q = p->max_seqlen_q;
   d.max_k = p->max_seqlen_k;
   d.max_nb = (d.max_k + 127) / 128;
@@ -858,7 +859,7 @@ struct PromptLayout {
   size_t hdr, plan, seq, item_base, items, run_item, part_o, part_ml, q8, q_scale, total;
 };
 
-PromptLayout prompt_layout(const PromptShape& d, bool fp8) {
+PromptLayout prompt_layout(const PromptShape& d) {
   PromptLayout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
@@ -876,10 +877,8 @@ PromptLayout prompt_layout(const PromptShape& d, bool fp8) {
     L.part_o = take(sizeof(float) * kPromptMaxCtas * 2 * 256 * kHeadDim);
     L.part_ml = take(sizeof(float2) * kPromptMaxCtas * 2 * 256);
   }
-  if (fp8) {
-    L.q8 = take(static_cast<size_t>(d.T) * d.hq * 256);
-    L.q_scale = take(sizeof(float) * static_cast<size_t>(d.T) * d.hq);
-  }
+  L.q8 = take(static_cast<size_t>(d.T) * d.hq * 256);  // E4M3 pages only; one size for an op
+  L.q_scale = take(sizeof(float) * static_cast<size_t>(d.T) * d.hq);
   L.total = off;
   return L;
 }
@@ -923,7 +922,7 @@ msa_status_t prompt_attn(const msa_problem_t* problem, const PromptCall& c, void
     if (rows && !c.visible) return MSA_ERR_INVALID_ARG;
     if (!aligned4(c.visible)) return MSA_ERR_ALIGNMENT;
   }
-  const PromptLayout L = prompt_layout(d, c.fp8);
+  const PromptLayout L = prompt_layout(d);
   if (!ws || ws_bytes < L.total) return MSA_ERR_WORKSPACE;
   if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MSA_ERR_ALIGNMENT;
   DeviceFacts dev;
@@ -1007,6 +1006,11 @@ msa_status_t append_rows(const AppendRows* rows, int planes, const int64_t* slot
     if (r.stride < r.width) return MSA_ERR_INVALID_ARG;
     if (!aligned16(r.x) || !aligned16(r.cache) || !aligned4(r.scale) || r.stride % 8) return MSA_ERR_ALIGNMENT;
     p.plane[i] = {static_cast<const __nv_bfloat16*>(r.x), r.stride, r.width, r.cache, r.scale};
+  }
+  if (fp8) {  // a CTA per head and 128 tokens
+    long long heads = 0;
+    for (int i = 0; i < planes; ++i) heads += rows[i].width / 128;
+    if ((tokens + 127) / 128 * heads > 0x7FFFFFFFLL) return MSA_ERR_UNSUPPORTED;
   }
   p.planes = planes;
   p.slots = reinterpret_cast<const long long*>(slots);
@@ -1164,7 +1168,7 @@ msa_status_t msa_workspace_size(const msa_problem_t* problem, msa_op_t op, size_
   if (op == MSA_OP_DENSE_ATTN_PREFILL || op == MSA_OP_TREE_ATTN) {
     PromptShape d;
     const msa_status_t st = derive_prompt(problem, d);
-    if (st == MSA_OK) *bytes = prompt_layout(d, true).total;  // for every type of pages
+    if (st == MSA_OK) *bytes = prompt_layout(d).total;  // for every type of pages
     return st;
   }
   if (op < MSA_OP_INDEX_POOL || op > MSA_OP_DENSE_ATTN_DECODE_WEIGHT) return MSA_ERR_INVALID_ARG;

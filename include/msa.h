@@ -569,10 +569,10 @@ msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const voi
  *               num_kv_heads <= 1024, num_seqs <= 2^20, total_q < 2^25,
  *               max_seqlen_k <= 2^30, softmax_scale < 1e30.
  *   q, k, v     packed, as in the conventions above.
- *   o, lse      written for every query row.
+ *   o, lse      written for every query row; o must not overlap q.
  * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (42 MB, 32 bytes per pair of tiles of
- * 128 / group tokens, and for E4M3 pages 260 bytes per query row and head; bf16
- * calls take a workspace without the last).
+ * 128 / group tokens, and 260 bytes per query row and head, which calls over E4M3
+ * pages use).
  * Numbers.  Logits, references, sums, O and lse are fp32; a weight that meets V is
  * rounded to bf16 (2^-8 of the weight; E4M3 pages: fp16, 2^-11, down to 2^-21 of the
  * row's largest weight times page scale), the sum takes it unrounded.  Over E4M3
@@ -601,7 +601,8 @@ msa_status_t msa_dense_attn_prefill_paged(const msa_problem_t *problem, const vo
                                           void *workspace, size_t workspace_bytes, msa_stream_t stream);
 
 /* The same over E4M3 pages with one scale per (page, KV head): the attention over
- * the dequantized values.  Scales from 2^-100 to 2^100. */
+ * the dequantized values.  Scales from 2^-80 to 2^80, those of a sequence's V at most
+ * 2^100 apart. */
 msa_status_t msa_dense_attn_prefill_paged_fp8(const msa_problem_t *problem, const void *q, const void *k8_cache,
                                               const void *v8_cache, const float *k_scale, const float *v_scale,
                                               const int32_t *block_table, int32_t max_blocks_per_seq,
@@ -645,10 +646,10 @@ msa_status_t msa_tree_attn_paged_fp8(const msa_problem_t *problem, const void *q
  *   slots        int64 [capacity], 8-byte aligned: the cache row of each new token,
  *                sequence by sequence; -1 past the last one.
  *   positions    int32 [capacity]: its place in its sequence; 0 past the last one.
- *   num_pages    pages of the cache; a page outside it (in the table's last old
- *                block or the free list), and a block that the list has no page
- *                for, becomes -1 in the table and its tokens' slots -1
- *                (MSA_DEVICE_BAD_INDEX).
+ *   num_pages    pages of the cache.  Tokens whose page is outside it (in the
+ *                table's last old block or the free list), or for whose block the
+ *                list has no page, get slots of -1, and such a new block's entry
+ *                is -1 (MSA_DEVICE_BAD_INDEX).
  * Negative lengths, sequences that the table has no room for, *taken past the list
  * and more new tokens than `capacity` (or 2^31 keys) make the call do nothing but
  * fill slots with -1 and positions and prefix sums with 0
@@ -687,7 +688,8 @@ msa_status_t msa_append_paged(const void *k, int64_t k_stride, const void *v, in
  * and where scale' > scale the codes of the rows below L become those of code * scale *
  * 448 / max |new| (two fp32 roundings).  Other rows are left as they
  * were.  A page that comes twice raises MSA_DEVICE_BAD_INDEX and its contents are
- * undefined.  Workspace: msa_append_workspace_size. */
+ * undefined.  tokens * num_kv_heads below 2^37.  Workspace:
+ * msa_append_workspace_size. */
 msa_status_t msa_append_workspace_size(int64_t num_pages, size_t *bytes);
 msa_status_t msa_append_paged_fp8(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
                                   const void *k_idx, int64_t k_idx_stride, const int64_t *slots, int64_t tokens,

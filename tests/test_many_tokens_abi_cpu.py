@@ -95,6 +95,16 @@ def test_attention_refusals(msa, name):
         assert accepted(call(problem=none, q=None, o=None, lse=None, vis=None))
 
 
+@pytest.mark.parametrize("name", list(CALLS))
+@pytest.mark.parametrize("kw", [dict(total_q=500, total_k=400, max_seqlen_k=400), dict(total_q=1, total_k=0, max_seqlen_q=1,
+                                max_seqlen_k=0), dict(max_seqlen_q=100, max_seqlen_k=99)])
+def test_more_queries_than_keys(msa, name, kw):
+    p = batch(msa, **kw)
+    n = ctypes.c_size_t(0)
+    assert msa._lib.msa_workspace_size(p, int(msa.Op.TREE_ATTN), ctypes.byref(n)) == -1
+    assert CALLS[name](msa._lib, p, FINE) == -1
+
+
 def test_any_group(msa):
     n = ctypes.c_size_t(0)
     for hq, hkv in ((1, 1), (5, 1), (128, 1), (35, 7), (1024, 1024), (96, 2)):
@@ -162,6 +172,7 @@ def test_append_refusals(msa, fp8):
     assert call(pages=1 << 24) == -1 and call(n=need - 1 if fp8 else 255) == -4 and call(ws=FAKE + 16) == -3
     if fp8:
         assert call(ws=None) == -4
+        assert call(hkv=1024, sk=1 << 17, sv=1 << 17, tokens=1 << 31) == -2   # more CTAs than a launch has
     else:
         assert call(d=32) == -2
 
