@@ -856,7 +856,7 @@ msa_status_t derive_prompt(const msa_problem_t* p, PromptShape& d) {
 }
 
 struct PromptLayout {
-  size_t hdr, plan, seq, item_base, items, run_item, part_o, part_ml, q8, q_scale, total;
+  size_t hdr, plan, seq, item_base, items, run_item, run_at, part_o, part_ml, q8, q_scale, total;
 };
 
 PromptLayout prompt_layout(const PromptShape& d) {
@@ -873,6 +873,7 @@ PromptLayout prompt_layout(const PromptShape& d) {
   L.item_base = take(sizeof(int32_t) * d.S);
   L.items = take(sizeof(PromptItem) * d.max_items);
   L.run_item = take(sizeof(int32_t) * kPromptMaxCtas);
+  L.run_at = take(sizeof(long long) * (kPromptMaxCtas + 1));
   if (prompt_may_split(d.max_nb)) {
     L.part_o = take(sizeof(float) * kPromptMaxCtas * 2 * 256 * kHeadDim);
     L.part_ml = take(sizeof(float2) * kPromptMaxCtas * 2 * 256);
@@ -972,6 +973,7 @@ msa_status_t prompt_attn(const msa_problem_t* problem, const PromptCall& c, void
   p.item_base = at<int32_t>(ws, L.item_base);
   p.items = at<PromptItem>(ws, L.items);
   p.run_item = at<int32_t>(ws, L.run_item);
+  p.run_at = at<long long>(ws, L.run_at);
   p.part_o = prompt_may_split(d.max_nb) ? at<float>(ws, L.part_o) : nullptr;
   p.part_ml = prompt_may_split(d.max_nb) ? at<float2>(ws, L.part_ml) : nullptr;
   StageScope scope(MSA_STAGE_ATTN, reinterpret_cast<cudaStream_t>(stream));

@@ -323,7 +323,7 @@ cudaError_t launch_dense_decode(const DenseMaps& maps, const DenseDecodeParams& 
 constexpr int kPromptMaxCtas = 160;  // CTAs of the attention kernel at most (one per SM)
 // What the plan kernel leaves for the others.
 struct PromptPlan {
-  long long total;  // blocks of all items and KV heads
+  long long total;  // cost of all items and KV heads
   int n_items;
   int runs;         // > 0: all blocks are cut into so many runs; 0: items are taken whole
 };
@@ -332,7 +332,7 @@ struct PromptItem {
   int seq, t0;                     // its first token
   int q_start, q_len, k_start, past;  // the sequence: first query row, new tokens, first key row, cached keys
   int blocks;                      // key blocks of the item
-  int base;                        // with runs: blocks of one KV head before it
+  uint32_t base;                   // with runs: cost of the items before it, for one KV head
 };
 struct PromptParams {
   int num_seqs, hq, hkv, group, total_q, total_k, max_q, max_k, max_nb;
@@ -361,6 +361,7 @@ struct PromptParams {
   int32_t* item_base;           // [num_seqs] items before a sequence's
   PromptItem* items;            // [max_items]
   int32_t* run_item;            // [kPromptMaxCtas] with runs: the item that each begins in
+  long long* run_at;            // [kPromptMaxCtas + 1] and where, in units of cost; behind the last one the total
   // [ctas, 2, 2 tiles, 32, 128, 4] four dims of 128 rows each: slot 1 the item that goes on behind the run; null: never runs
   float* part_o;
   float2* part_ml;              // [ctas, 2, 2, 128] (reference, sum)

@@ -31,7 +31,7 @@
 // two warpgroups in turn, each with its own m, l and O, merged at the end.
 //
 // Items differ in cost.  Where there are enough of them the CTAs take them whole, largest first; where the longest alone
-// would hold up the call (few rows over a long cache) all blocks are cut into equal runs, one per CTA, and an item that
+// would hold up the call (few rows over a long cache) all blocks are cut into runs of equal cost, one per CTA, and an item that
 // crosses runs leaves (O, m, l) per run, which a join kernel merges.  A plan kernel decides from the lengths.
 #include <cuda_fp8.h>
 
@@ -47,8 +47,13 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 1024;
-// A call is cut into runs when its longest item has this many blocks more than an even share: what a partial's way
-// through memory and the join cost.
+// What the CTAs' shares of a call are measured in.  A block of a pair of tiles takes two warpgroups' time, one of a single tile
+// one's.  An item costs more than its blocks: its queries' way in, the first block's through the pipeline, the output.  Over
+// 16 trees of 2 to 31 drafts, runs of equally many blocks left the CTAs idle for a third of the time: 139 us, with
+// 2 to 1 130, with 3 to 1 164; with an item's own cost 128.  32 trees of 8 drafts: 104 to 86 us, over E4M3 pages 106 to 78.
+constexpr int kPairCost = 2, kOneCost = 1, kItemCost = 4;
+// A call is cut into runs when its longest item costs so much more than an even share: what a partial's way through memory
+// and the join take.
 constexpr int kRunsSlack = 6;
 
 // Exclusive scan over the CTA (kPlanThreads threads); `sh` holds 32 values.
@@ -83,6 +88,18 @@ __device__ __forceinline__ int item_blocks(const PromptParams& p, const SeqInfo&
   if (p.visible) return (si.kv_len + kBlock - 1) / kBlock;
   const int end = min(si.q_len, t0 + 2 * p.tile_tokens);
   return (si.kv_len - si.q_len + end + kBlock - 1) / kBlock;
+}
+
+// Cost of a block of the item that begins at token t0 of q_len, and of the item.
+__device__ __forceinline__ int block_cost(const PromptParams& p, int q_len, int t0) {
+  return q_len - t0 <= p.tile_tokens ? kOneCost : kPairCost;
+}
+__device__ __forceinline__ int item_cost(const PromptParams& p, const PromptItem& it) {
+  return it.blocks * block_cost(p, it.q_len, it.t0) + kItemCost;
+}
+// The block that lies `off` behind an item's beginning: its first one for what the item costs beside them, too.
+__device__ __forceinline__ int block_at(long long off, int cost) {
+  return static_cast<int>(max(off - kItemCost, 0LL)) / cost;
 }
 
 // fp8: K's codes are multiplied as they are, so the queries are codes too, two per value: the first its E4M3 rounding, the
@@ -128,7 +145,7 @@ __device__ __forceinline__ void query_codes(const PromptParams& p, long long fir
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
   __shared__ long long sh[32];
   __shared__ int bins[kPlanBins];
-  __shared__ int s_bad, s_most;
+  __shared__ int s_bad, s_most, s_cost;
   griddep_wait();  // the kernel before may still read this workspace
   if (blockIdx.x > 0) {  // fp8: the queries' codes
     query_codes(p, (blockIdx.x - 1) * static_cast<long long>(kPlanThreads / 16), (gridDim.x - 1) * static_cast<long long>(kPlanThreads / 16));
@@ -139,6 +156,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   if (threadIdx.x == 0) {
     s_bad = 0;
     s_most = 0;
+    s_cost = kOneCost;
   }
   for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
   __syncthreads();
@@ -179,12 +197,14 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   const int items = static_cast<int>(n_items);
   // costs: their sum, the largest, and how many items there are of each size
   int shift = 0;
-  while ((p.max_nb >> shift) >= kPlanBins) ++shift;
+  while ((static_cast<long long>(p.max_nb) * kPairCost + kItemCost >> shift) >= kPlanBins) ++shift;
   long long sum = 0;
   int most = 0;
   for (int j = threadIdx.x; j < items; j += kPlanThreads) {
     const int s = find_seq(p.item_base, p.num_seqs, j);
-    const int n = item_blocks(p, p.seq[s], (j - p.item_base[s]) * per_item);
+    const int t0 = (j - p.item_base[s]) * per_item, cost = block_cost(p, p.seq[s].q_len, t0);
+    const int n = item_blocks(p, p.seq[s], t0) * cost + kItemCost;
+    if (cost == kPairCost) s_cost = kPairCost;
     sum += n;
     most = max(most, n);
     atomicAdd(&bins[n >> shift], 1);
@@ -195,28 +215,28 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   total *= p.hkv;
   most = s_most;
   const bool split = p.part_o != nullptr && most > total / p.ctas + kRunsSlack;
+  const int runs = split ? static_cast<int>(min(total / s_cost, static_cast<long long>(p.ctas))) : 0;  // a block each at least
   if (threadIdx.x == 0) {
     plan->n_items = items;
-    plan->runs = split ? static_cast<int>(min(total, static_cast<long long>(p.ctas))) : 0;
+    plan->runs = runs;
     plan->total = total;
   }
-  auto item = [&](int j, int base) {
+  auto item = [&](int j, uint32_t base) {
     const int s = find_seq(p.item_base, p.num_seqs, j), t0 = (j - p.item_base[s]) * per_item;
     const SeqInfo si = p.seq[s];
     return PromptItem{s, t0, si.q_start, si.q_len, si.k_start, si.kv_len - si.q_len, item_blocks(p, si, t0), base};
   };
   if (split) {
-    // the items in order, with the blocks before each (of one KV head), and the item that each run begins in
-    const int runs = static_cast<int>(min(total, static_cast<long long>(p.ctas)));
+    // the items in order, with the cost of those before each (for one KV head), and the item that each run begins in
     long long carry = 0;
     for (int base = 0; base < items; base += kPlanThreads) {
       const int j = base + threadIdx.x;
       PromptItem it{};
       if (j < items) it = item(j, 0);
       long long t;
-      const long long before = carry + plan_scan(it.blocks, sh, &t);
+      const long long before = carry + plan_scan(j < items ? item_cost(p, it) : 0, sh, &t);
       if (j < items) {
-        it.base = static_cast<int>(before);  // total < ctas * (max_nb + slack): fits
+        it.base = static_cast<uint32_t>(before);  // less than ctas * most < 2^8 * 2^24
         p.items[j] = it;
       }
       carry += t;
@@ -230,8 +250,15 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
         if (static_cast<long long>(p.items[mid].base) * p.hkv <= at) lo = mid;
         else hi = mid - 1;
       }
+      const PromptItem it = p.items[lo];
       p.run_item[threadIdx.x] = lo;
+      // back to where its block begins
+      const int cost = block_cost(p, it.q_len, it.t0);
+      const long long off = (at - static_cast<long long>(it.base) * p.hkv) % item_cost(p, it);
+      const int blk = block_at(off, cost);
+      p.run_at[threadIdx.x] = at - off + (blk > 0 ? kItemCost + static_cast<long long>(blk) * cost : 0);
     }
+    if (threadIdx.x == 0) p.run_at[runs] = total;
     return;
   }
   // the items by size, largest first (those of a size in any order: each is computed by itself)
@@ -246,7 +273,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   __syncthreads();
   for (int j = threadIdx.x; j < items; j += kPlanThreads) {
     const PromptItem it = item(j, 0);
-    p.items[atomicAdd(&bins[it.blocks >> shift], 1)] = it;
+    p.items[atomicAdd(&bins[item_cost(p, it) >> shift], 1)] = it;
   }
 }
 
@@ -263,18 +290,19 @@ struct Part {
 struct PartWalker {
   const PromptParams& p;
   int items, runs, item, round;
-  long long at, hi;
+  long long at, hi;  // where the run is and ends, in units of cost
   __device__ explicit PartWalker(const PromptParams& params) : p(params) {
-    const int start = p.run_item[blockIdx.x];  // (without runs: not a value, and not used)
+    // (without runs: not values, and not used)
+    const int start = p.run_item[blockIdx.x];
+    const long long first = p.run_at[blockIdx.x], behind = p.run_at[blockIdx.x + 1];
     items = p.plan->n_items;
     runs = p.plan->runs;
-    const long long total = p.plan->total;
     round = 0;
     item = 0;
     at = hi = 0;
     if (static_cast<int>(blockIdx.x) < runs) {
-      at = total * blockIdx.x / runs;
-      hi = total * (blockIdx.x + 1) / runs;
+      at = first;
+      hi = behind;
       item = start;
     }
   }
@@ -302,11 +330,14 @@ struct PartWalker {
     g.past = it.past;
     g.one = it.q_len - it.t0 <= p.tile_tokens;
     if (runs > 0) {
-      const long long off = at - static_cast<long long>(it.base) * p.hkv;
-      g.head = static_cast<int>(off / it.blocks);
-      blk = static_cast<int>(off - static_cast<long long>(g.head) * it.blocks);
-      g.count = static_cast<int>(min(static_cast<long long>(it.blocks - blk), hi - at));
-      at += g.count;
+      const int cost = g.one ? kOneCost : kPairCost;
+      const int n = it.blocks * cost + kItemCost;
+      const long long base = static_cast<long long>(it.base) * p.hkv;
+      g.head = static_cast<int>((at - base) / n);
+      const long long begin = base + static_cast<long long>(g.head) * n;
+      blk = block_at(at - begin, cost);
+      g.count = (hi - begin >= n ? it.blocks : block_at(hi - begin, cost)) - blk;
+      at = min(begin + n, hi);
       if (blk + g.count == it.blocks && g.head == p.hkv - 1) ++item;
     } else {
       g.count = it.blocks;
@@ -1232,14 +1263,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptPara
   const int run = threadIdx.x;
   int4 item = make_int4(-1, 0, 0, 0);
   if (run + 1 < runs) {
-    const long long edge = total * (run + 1) / runs;  // the first unit of the next run
     // the item that goes on behind run `run`, if one does: that of the next run's first block
     const int j = p.run_item[run + 1];
-    const int n = p.items[j].blocks;
-    const long long base = static_cast<long long>(p.items[j].base) * p.hkv;
+    const long long lo = p.run_at[run], edge = p.run_at[run + 1];  // where the two begin
+    const PromptItem it = p.items[j];
+    const long long base = static_cast<long long>(it.base) * p.hkv, n = item_cost(p, it);
     const int head = static_cast<int>((edge - base) / n);
-    const long long start = base + static_cast<long long>(head) * n;
-    if (start != edge && start >= total * run / runs)  // it began in this run
+    const long long start = base + head * n;
+    if (start != edge && start >= lo)  // it began in this run; the last run that begins before its end has its end
       item = make_int4(run, static_cast<int>(((start + n) * runs - 1) / total), j, head);
   }
   // the list has one order in all CTAs
