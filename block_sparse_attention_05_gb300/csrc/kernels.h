@@ -332,7 +332,7 @@ struct PromptItem {
   int seq, t0;                     // its first token
   int q_start, q_len, k_start, past;  // the sequence: first query row, new tokens, first key row, cached keys
   int blocks;                      // key blocks of the item
-  uint32_t base;                   // with runs: cost of the items before it, for one KV head
+  long long base;                  // with runs: cost of the items before it, for one KV head
 };
 struct PromptParams {
   int num_seqs, hq, hkv, group, total_q, total_k, max_q, max_k, max_nb;

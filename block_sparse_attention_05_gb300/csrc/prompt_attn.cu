@@ -47,14 +47,20 @@ namespace {
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanBins = 1024;
-// What the CTAs' shares of a call are measured in.  A block of a pair of tiles takes two warpgroups' time, one of a single tile
-// one's.  An item costs more than its blocks: its queries' way in, the first block's through the pipeline, the output.  Over
-// 16 trees of 2 to 31 drafts, runs of equally many blocks left the CTAs idle for a third of the time: 139 us, with
-// 2 to 1 130, with 3 to 1 164; with an item's own cost 128.  32 trees of 8 drafts: 104 to 86 us, over E4M3 pages 106 to 78.
-constexpr int kPairCost = 2, kOneCost = 1, kItemCost = 4;
+// What the CTAs' shares of a call are measured in: a block of a pair of tiles takes 1.55 us, one of a single tile (most of its
+// time is the memory's) 1.2, and an item beside its blocks 4.5: its queries' way in, the first block's through the pipeline,
+// the output.  E4M3 pages: 1.9, 1.0, 4.5.  With runs of equally many blocks the CTAs of 16 trees of 2 to 31 drafts end
+// after 75 to 113 us.
+struct PromptCosts {
+  int pair, one, item;
+};
+constexpr int kPairCost = 4;  // the largest
+__device__ __forceinline__ PromptCosts costs(const PromptParams& p) {
+  return p.q8 ? PromptCosts{kPairCost, 2, 9} : PromptCosts{kPairCost, 3, 12};
+}
 // A call is cut into runs when its longest item costs so much more than an even share: what a partial's way through memory
 // and the join take.
-constexpr int kRunsSlack = 6;
+constexpr int kRunsSlack = 36;
 
 // Exclusive scan over the CTA (kPlanThreads threads); `sh` holds 32 values.
 __device__ long long plan_scan(long long v, long long* sh, long long* total) {
@@ -92,14 +98,14 @@ __device__ __forceinline__ int item_blocks(const PromptParams& p, const SeqInfo&
 
 // Cost of a block of the item that begins at token t0 of q_len, and of the item.
 __device__ __forceinline__ int block_cost(const PromptParams& p, int q_len, int t0) {
-  return q_len - t0 <= p.tile_tokens ? kOneCost : kPairCost;
+  return q_len - t0 <= p.tile_tokens ? costs(p).one : costs(p).pair;
 }
 __device__ __forceinline__ int item_cost(const PromptParams& p, const PromptItem& it) {
-  return it.blocks * block_cost(p, it.q_len, it.t0) + kItemCost;
+  return it.blocks * block_cost(p, it.q_len, it.t0) + costs(p).item;
 }
 // The block that lies `off` behind an item's beginning: its first one for what the item costs beside them, too.
-__device__ __forceinline__ int block_at(long long off, int cost) {
-  return static_cast<int>(max(off - kItemCost, 0LL)) / cost;
+__device__ __forceinline__ int block_at(const PromptParams& p, long long off, int cost) {
+  return static_cast<int>(max(off - costs(p).item, 0LL)) / cost;
 }
 
 // fp8: K's codes are multiplied as they are, so the queries are codes too, two per value: the first its E4M3 rounding, the
@@ -156,7 +162,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   if (threadIdx.x == 0) {
     s_bad = 0;
     s_most = 0;
-    s_cost = kOneCost;
+    s_cost = costs(p).one;
   }
   for (int i = threadIdx.x; i < kPlanBins; i += kPlanThreads) bins[i] = 0;
   __syncthreads();
@@ -197,13 +203,13 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   const int items = static_cast<int>(n_items);
   // costs: their sum, the largest, and how many items there are of each size
   int shift = 0;
-  while ((static_cast<long long>(p.max_nb) * kPairCost + kItemCost >> shift) >= kPlanBins) ++shift;
+  while ((static_cast<long long>(p.max_nb) * kPairCost + costs(p).item >> shift) >= kPlanBins) ++shift;
   long long sum = 0;
   int most = 0;
   for (int j = threadIdx.x; j < items; j += kPlanThreads) {
     const int s = find_seq(p.item_base, p.num_seqs, j);
     const int t0 = (j - p.item_base[s]) * per_item, cost = block_cost(p, p.seq[s].q_len, t0);
-    const int n = item_blocks(p, p.seq[s], t0) * cost + kItemCost;
+    const int n = item_blocks(p, p.seq[s], t0) * cost + costs(p).item;
     if (cost == kPairCost) s_cost = kPairCost;
     sum += n;
     most = max(most, n);
@@ -221,10 +227,10 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     plan->runs = runs;
     plan->total = total;
   }
-  auto item = [&](int j, uint32_t base) {
+  auto item = [&](int j) {
     const int s = find_seq(p.item_base, p.num_seqs, j), t0 = (j - p.item_base[s]) * per_item;
     const SeqInfo si = p.seq[s];
-    return PromptItem{s, t0, si.q_start, si.q_len, si.k_start, si.kv_len - si.q_len, item_blocks(p, si, t0), base};
+    return PromptItem{s, t0, si.q_start, si.q_len, si.k_start, si.kv_len - si.q_len, item_blocks(p, si, t0), 0};
   };
   if (split) {
     // the items in order, with the cost of those before each (for one KV head), and the item that each run begins in
@@ -232,11 +238,11 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
     for (int base = 0; base < items; base += kPlanThreads) {
       const int j = base + threadIdx.x;
       PromptItem it{};
-      if (j < items) it = item(j, 0);
+      if (j < items) it = item(j);
       long long t;
       const long long before = carry + plan_scan(j < items ? item_cost(p, it) : 0, sh, &t);
       if (j < items) {
-        it.base = static_cast<uint32_t>(before);  // less than ctas * most < 2^8 * 2^24
+        it.base = before; 
         p.items[j] = it;
       }
       carry += t;
@@ -247,16 +253,16 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       int lo = 0, hi = items - 1;  // the last item that begins at or before it
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (static_cast<long long>(p.items[mid].base) * p.hkv <= at) lo = mid;
+        if (p.items[mid].base * p.hkv <= at) lo = mid;
         else hi = mid - 1;
       }
       const PromptItem it = p.items[lo];
       p.run_item[threadIdx.x] = lo;
       // back to where its block begins
       const int cost = block_cost(p, it.q_len, it.t0);
-      const long long off = (at - static_cast<long long>(it.base) * p.hkv) % item_cost(p, it);
-      const int blk = block_at(off, cost);
-      p.run_at[threadIdx.x] = at - off + (blk > 0 ? kItemCost + static_cast<long long>(blk) * cost : 0);
+      const long long off = (at - it.base * p.hkv) % item_cost(p, it);
+      const int blk = block_at(p, off, cost);
+      p.run_at[threadIdx.x] = at - off + (blk > 0 ? costs(p).item + static_cast<long long>(blk) * cost : 0);
     }
     if (threadIdx.x == 0) p.run_at[runs] = total;
     return;
@@ -272,7 +278,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   }
   __syncthreads();
   for (int j = threadIdx.x; j < items; j += kPlanThreads) {
-    const PromptItem it = item(j, 0);
+    const PromptItem it = item(j);
     p.items[atomicAdd(&bins[item_cost(p, it) >> shift], 1)] = it;
   }
 }
@@ -330,13 +336,12 @@ struct PartWalker {
     g.past = it.past;
     g.one = it.q_len - it.t0 <= p.tile_tokens;
     if (runs > 0) {
-      const int cost = g.one ? kOneCost : kPairCost;
-      const int n = it.blocks * cost + kItemCost;
-      const long long base = static_cast<long long>(it.base) * p.hkv;
+      const int cost = block_cost(p, it.q_len, it.t0), n = item_cost(p, it);
+      const long long base = it.base * p.hkv;
       g.head = static_cast<int>((at - base) / n);
       const long long begin = base + static_cast<long long>(g.head) * n;
-      blk = block_at(at - begin, cost);
-      g.count = (hi - begin >= n ? it.blocks : block_at(hi - begin, cost)) - blk;
+      blk = block_at(p, at - begin, cost);
+      g.count = (hi - begin >= n ? it.blocks : block_at(p, hi - begin, cost)) - blk;
       at = min(begin + n, hi);
       if (blk + g.count == it.blocks && g.head == p.hkv - 1) ++item;
     } else {
@@ -1267,7 +1272,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptPara
     const int j = p.run_item[run + 1];
     const long long lo = p.run_at[run], edge = p.run_at[run + 1];  // where the two begin
     const PromptItem it = p.items[j];
-    const long long base = static_cast<long long>(it.base) * p.hkv, n = item_cost(p, it);
+    const long long base = it.base * p.hkv, n = item_cost(p, it);
     const int head = static_cast<int>((edge - base) / n);
     const long long start = base + head * n;
     if (start != edge && start >= lo)  // it began in this run; the last run that begins before its end has its end
@@ -1297,7 +1302,7 @@ cudaError_t launch_attn(const PromptMaps& maps, const PromptParams& p, cudaStrea
 
 }  // namespace
 
-bool prompt_may_split(int max_nb) { return max_nb > kRunsSlack; }
+bool prompt_may_split(int max_nb) { return max_nb * static_cast<long long>(kPairCost) + 12 > kRunsSlack; }
 
 cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bool fp8, cudaStream_t stream) {
   long long ctas = 1;
