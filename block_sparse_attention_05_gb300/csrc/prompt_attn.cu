@@ -1168,15 +1168,15 @@ struct JoinSmem {
   float4 sums[kJoinWarps][4][32];
   float2 ml[kJoinWarps][32];
   uint2 turned[32][9];
-  int4 item[kPromptMaxCtas];  // first run, last run, item, head
+  int4 item[kPromptMaxCtas];  // first run, last run, first query row, head
+  int2 rows[kPromptMaxCtas];  // first token, new tokens of the sequence
   int in_warp[kJoinWarps];
 };
 // Rows task / 4 and dims task % 4 of an item.
-__device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, int4 item, int task) {
-  const int run = item.x, last = item.y, head = item.w;
-  const PromptItem it = p.items[item.z];
+__device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, int4 item, int2 rows, int task) {
+  const int run = item.x, last = item.y, q_start = item.z, head = item.w, t0 = rows.x, q_len = rows.y;
   const int b = task >> 4, row0 = (task >> 2 & 3) * 32;  // tile and first row
-  if (it.t0 + b * p.tile_tokens >= it.q_len || row0 >= p.tile_tokens * p.group) return;  // nobody's rows
+  if (t0 + b * p.tile_tokens >= q_len || row0 >= p.tile_tokens * p.group) return;  // nobody's rows
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int row = row0 + lane, sub = warp >> 1;
   const int quad0 = (task & 3) * 8 + (warp & 1) * 4;  // first of the warp's four quadruples of dims
@@ -1189,10 +1189,13 @@ __device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, i
     float4 v[4][4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int i = min(i0 + 4 * u, last);
+      const int i = i0 + 4 * u;
       const long long at = static_cast<long long>(i) * 4 + (i == run ? 2 : 0) + b;
+      x[u] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i > last) continue;
       x[u] = p.part_ml[at * 128 + row];
-      if (i0 + 4 * u > last) x[u] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         v[u][c] = *reinterpret_cast<const float4*>(p.part_o + ((at * 32 + quad0 + c) * 128 + row) * 4);
@@ -1247,9 +1250,9 @@ __device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, i
     sm.turned[lane][w0 * 4 + c] = make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   }
   auto out_row = [&](int r) {  // of the output, or -1: a row of nobody
-    const int t = r / p.group, h = r - t * p.group, tok = it.t0 + b * p.tile_tokens + t;
-    if (t >= p.tile_tokens || tok >= it.q_len) return -1LL;
-    return (static_cast<long long>(it.q_start) + tok) * p.hq + head * p.group + h;
+    const int t = r / p.group, h = r - t * p.group, tok = t0 + b * p.tile_tokens + t;
+    if (t >= p.tile_tokens || tok >= q_len) return -1LL;
+    return (static_cast<long long>(q_start) + tok) * p.hq + head * p.group + h;
   };
   __syncthreads();
   const int r = threadIdx.x >> 3, c = threadIdx.x & 7;  // 8 lanes write 64 bytes of a row
@@ -1263,20 +1266,24 @@ __device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, i
 __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptParams p) {
   __shared__ JoinSmem sm;
   griddep_wait();
-  const int runs = p.plan->runs;
-  const long long total = p.plan->total;
   const int run = threadIdx.x;
   int4 item = make_int4(-1, 0, 0, 0);
-  if (run + 1 < runs) {
-    // the item that goes on behind run `run`, if one does: that of the next run's first block
-    const int j = p.run_item[run + 1];
-    const long long lo = p.run_at[run], edge = p.run_at[run + 1];  // where the two begin
-    const PromptItem it = p.items[j];
-    const long long base = it.base * p.hkv, n = item_cost(p, it);
-    const int head = static_cast<int>((edge - base) / n);
-    const long long start = base + head * n;
-    if (start != edge && start >= lo)  // it began in this run; the last run that begins before its end has its end
-      item = make_int4(run, static_cast<int>(((start + n) * runs - 1) / total), j, head);
+  int2 rows = make_int2(0, 0);
+  if (run + 1 < kPromptMaxCtas) {
+    // the item that goes on behind run `run`, if one does: that of the next run's first block (past the last run
+    // neither is a value, and not used)
+    const int runs = p.plan->runs, j = p.run_item[run + 1];
+    const long long total = p.plan->total, lo = p.run_at[run], edge = p.run_at[run + 1];  // where the two begin
+    if (run + 1 < runs) {
+      const PromptItem it = p.items[j];
+      const long long base = it.base * p.hkv, n = item_cost(p, it);
+      const int head = static_cast<int>((edge - base) / n);
+      const long long start = base + head * n;
+      if (start != edge && start >= lo) {  // it began in this run; the last run that begins before its end has its end
+        item = make_int4(run, static_cast<int>(((start + n) * runs - 1) / total), it.q_start, head);
+        rows = make_int2(it.t0, it.q_len);
+      }
+    }
   }
   // the list has one order in all CTAs
   const uint32_t some = __ballot_sync(0xFFFFFFFFu, item.x >= 0);
@@ -1287,9 +1294,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptPara
     if (w < static_cast<int>(threadIdx.x >> 5)) at += sm.in_warp[w];
     count += sm.in_warp[w];
   }
-  if (item.x >= 0) sm.item[at] = item;
+  if (item.x >= 0) {
+    sm.item[at] = item;
+    sm.rows[at] = rows;
+  }
   __syncthreads();
-  for (int task = blockIdx.x; task < count * 32; task += gridDim.x) join_rows(p, sm, sm.item[task >> 5], task & 31);
+  for (int task = blockIdx.x; task < count * 32; task += gridDim.x) join_rows(p, sm, sm.item[task >> 5], sm.rows[task >> 5], task & 31);
 }
 
 template <bool FP8>
