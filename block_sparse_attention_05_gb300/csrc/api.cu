@@ -255,12 +255,10 @@ bool map_2d_u8(CUtensorMap& m, const void* ptr, long long rows, int cols, int bo
 }
 
 // E4M3 codes [n, heads, width] (one byte each), box = 128 codes x box_heads heads x box_rows rows
-bool map_3d_u8(CUtensorMap& m, const void* ptr, long long n, int heads, int box_rows = 128, int box_heads = 1,
-               int width = 128) {
-  const cuuint64_t bytes = static_cast<cuuint64_t>(width);
-  cuuint64_t dims[3] = {bytes, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n > 0 ? n : 1)};
-  cuuint64_t strides[2] = {bytes, static_cast<cuuint64_t>(heads) * bytes};
-  cuuint32_t box[3] = {128, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+bool map_3d_u8(CUtensorMap& m, const void* ptr, long long n, int heads, int box_rows = 128) {
+  cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n > 0 ? n : 1)};
+  cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(heads) * 128};
+  cuuint32_t box[3] = {128, 1, static_cast<cuuint32_t>(box_rows)};
   return make_map(m, ptr, 3, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
@@ -856,7 +854,7 @@ msa_status_t derive_prompt(const msa_problem_t* p, PromptShape& d) {
 }
 
 struct PromptLayout {
-  size_t hdr, plan, seq, item_base, items, run_item, run_at, part_o, part_ml, q8, q_scale, total;
+  size_t hdr, plan, seq, item_base, items, run_item, run_at, part_o, part_ml, total;
 };
 
 PromptLayout prompt_layout(const PromptShape& d) {
@@ -878,8 +876,6 @@ PromptLayout prompt_layout(const PromptShape& d) {
     L.part_o = take(sizeof(float) * kPromptMaxCtas * 2 * 256 * kHeadDim);
     L.part_ml = take(sizeof(float2) * kPromptMaxCtas * 2 * 256);
   }
-  L.q8 = take(static_cast<size_t>(d.T) * d.hq * 256);  // E4M3 pages only; one size for an op
-  L.q_scale = take(sizeof(float) * static_cast<size_t>(d.T) * d.hq);
   L.total = off;
   return L;
 }
@@ -934,9 +930,7 @@ msa_status_t prompt_attn(const msa_problem_t* problem, const PromptCall& c, void
     auto map = [&](CUtensorMap& m, const void* x) {
       return c.fp8 ? map_3d_u8(m, x, n, d.hkv) : map_3d(m, x, n, d.hkv, 1, 128);
     };
-    const bool q_map = c.fp8 ? map_3d_u8(maps.q, at<uint8_t>(ws, L.q8), d.T, d.hq, d.tile_tokens, d.G, 256)
-                             : map_3d(maps.q, c.q, d.T, d.hq, d.G, d.tile_tokens);
-    if (!q_map || !map(maps.k, c.k) || !map(maps.v, c.v))
+    if (!map_3d(maps.q, c.q, d.T, d.hq, d.G, d.tile_tokens) || !map(maps.k, c.k) || !map(maps.v, c.v))
       return MSA_ERR_CUDA;
   }
   PromptParams p{};
@@ -959,9 +953,6 @@ msa_status_t prompt_attn(const msa_problem_t* problem, const PromptCall& c, void
   p.n_pages = c.num_pages;
   p.k_scale = c.k_scale;
   p.v_scale = c.v_scale;
-  p.q = static_cast<const __nv_bfloat16*>(c.q);
-  p.q8 = c.fp8 ? at<uint8_t>(ws, L.q8) : nullptr;
-  p.q_scale = c.fp8 ? at<float>(ws, L.q_scale) : nullptr;
   p.visible = c.tree ? c.visible : nullptr;
   p.mask_words = c.mask_words;
   p.o = static_cast<__nv_bfloat16*>(c.o);

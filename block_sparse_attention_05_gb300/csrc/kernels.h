@@ -346,9 +346,6 @@ struct PromptParams {
   long long n_pages;
   const float* k_scale;         // fp8: [n_pages, hkv]
   const float* v_scale;
-  const __nv_bfloat16* q;       // [total_q, hq, 128]
-  uint8_t* q8;                  // fp8, workspace: [total_q, hq, 2, 128] the queries' codes and
-  float* q_scale;               // [total_q, hq] their scales
   const int32_t* visible;       // [total_q, mask_words] bits of the new tokens that a new token sees, or null: causal
   int mask_words;
   __nv_bfloat16* o;             // [total_q, hq, 128]

@@ -18,7 +18,7 @@
 // rest would take half as much time again; l and lse sum the unrounded weights, everything else is fp32.
 //
 // E4M3 pages: K's codes are multiplied as they are (kind::f8f6f4), by queries that are two codes each; V's are widened to fp16
-// by four warps of their own, and P is fp16 (2^-11).  Widening K as well had those warps bound the kernel: 6.2 against 5.2 ms
+// by four warps of their own, and P is fp16 (2^-11).  Widening K as well had those warps bound the kernel: 6.2 against 5.0 ms
 // for a 20,000-token prompt of 64/4 heads.
 //
 // What bounds it.  A block takes a pair of tiles 2,048 clocks of MMAs, which also read shared memory at its full rate (128 bytes
@@ -34,8 +34,6 @@
 // would hold up the call (few rows over a long cache) all blocks are cut into runs of equal cost, one per CTA, and an item that
 // crosses runs leaves (O, m, l) per run, which a join kernel merges.  A plan kernel decides from the lengths.
 #include <cuda_fp8.h>
-
-#include <algorithm>
 
 #include "attn.cuh"
 #include "common.cuh"
@@ -56,7 +54,7 @@ struct PromptCosts {
 };
 constexpr int kPairCost = 4;  // the largest
 __device__ __forceinline__ PromptCosts costs(const PromptParams& p) {
-  return p.q8 ? PromptCosts{kPairCost, 2, 9} : PromptCosts{kPairCost, 3, 12};
+  return p.k_scale ? PromptCosts{kPairCost, 2, 9} : PromptCosts{kPairCost, 3, 12};
 }
 // A call is cut into runs when its longest item costs so much more than an even share: what a partial's way through memory
 // and the join take.
@@ -108,46 +106,6 @@ __device__ __forceinline__ int block_at(const PromptParams& p, long long off, in
   return static_cast<int>(max(off - costs(p).item, 0LL)) / cost;
 }
 
-// fp8: K's codes are multiplied as they are, so the queries are codes too, two per value: the first its E4M3 rounding, the
-// second that of the rest.  Four and four significant bits hold bf16's eight exactly, down to 2^-10 of the row's largest value
-// (below that the second is off by 2^-18 of the largest).  A row's scale is a power of two that brings its largest value to
-// 224 .. 448.  16 threads to a row of 128.
-__device__ __forceinline__ void query_codes(const PromptParams& p, long long first, long long stride) {
-  const int sub = threadIdx.x & 15;
-  const long long rows = static_cast<long long>(p.total_q) * p.hq;
-  for (long long row0 = first; row0 < rows; row0 += stride) {
-    const long long row = row0 + (threadIdx.x >> 4);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (row < rows) v = *reinterpret_cast<const uint4*>(p.q + row * kHeadDim + sub * 8);
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m = max(m, max(w[j] & 0x7FFFu, w[j] >> 16 & 0x7FFFu));
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    // 448 = 1.75 * 2^8; a row without an inf or NaN has an exponent below 255
-    const int e = static_cast<int>(m >> 7) - 127, up = m == 0 ? 0 : min(8 - e - ((m & 127) > 96 ? 1 : 0), 120);
-    const bool finite = m < 0x7F80u;
-    const float lift = __int_as_float((127 + max(up, -126)) << 23);  // up >= -120
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float a = __uint_as_float(w[j] << 16) * lift, b = __uint_as_float(w[j] & 0xFFFF0000u) * lift;
-      hi[j] = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-      const uint32_t h = e4m3x2_to_f16x2(hi[j]);
-      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      lo[j] = __nv_cvt_float2_to_fp8x2(make_float2(a - back.x, b - back.y), __NV_SATFINITE, __NV_E4M3);
-    }
-    if (row < rows) {
-      uint8_t* to = p.q8 + row * 256 + sub * 8;
-      *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
-      *reinterpret_cast<uint2*>(to + 128) = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
-      // a row with an inf or NaN has logits of NaN
-      if (sub == 0) p.q_scale[row] = finite ? __int_as_float((127 - up) << 23) : __int_as_float(0x7FC00000);
-    }
-  }
-}
-
 // One CTA plans the call.  Everything here waits for something before it, so what it makes of up to kPlanThreads sequences
 // and items stays in shared memory: with the lists in global memory 16 sequences took 4.7 us.
 __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams p) {
@@ -158,10 +116,6 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   __shared__ int bins[kPlanBins];
   __shared__ int s_bad, s_most, s_cost;
   griddep_wait();  // the kernel before may still read this workspace
-  if (blockIdx.x > 0) {  // fp8: the queries' codes
-    query_codes(p, (blockIdx.x - 1) * static_cast<long long>(kPlanThreads / 16), (gridDim.x - 1) * static_cast<long long>(kPlanThreads / 16));
-    return;
-  }
   for (int w = threadIdx.x; w < static_cast<int>(sizeof(WsHeader) / 4); w += kPlanThreads)
     reinterpret_cast<uint32_t*>(p.hdr)[w] = 0u;
   if (threadIdx.x == 0) {
@@ -395,11 +349,12 @@ struct PromptCfg {
 struct PromptSmem {
   uint64_t full[6], empty[6];            // a stage holds a tile / its MMAs are done
   uint64_t code_full[2], code_empty[2];  // fp8: V's codes
-  uint64_t q_full, q_empty;
+  uint64_t q_full, q_empty, q_ready;     // fp8: ready when they are codes
   uint64_t s_full[2], p_full[2], o_full[2], turn[2];  // by warpgroup
   uint64_t ml_full, o_free, out_free, mma_done;
   float2 ml[2][128];
   float k_scale[8], v_scale[8];  // fp8: scales of the last blocks (loaded at most 5 ahead of the one that a warpgroup is at)
+  int8_t q_up[2][256];  // fp8: exponents of the queries' scales, by the part's parity
   uint32_t tmem_base;
   int abort_flag;
   uint32_t err;
@@ -572,12 +527,82 @@ __device__ __forceinline__ void widen_tile(const uint8_t* codes, uint8_t* to, in
   }
 }
 
+// K's codes are multiplied as they are, so the queries are codes too, two per value: the first its E4M3 rounding, the second
+// that of the rest.  Four and four significant bits hold bf16's eight exactly, down to 2^-10 of the row's largest value
+// (below that the second is off by 2^-18 of the largest).  A row's scale is a power of two that brings its largest value to
+// 224 .. 448.  Both take a value's 16 bits: row `row` of a tile, as TMA landed it (two halves of 64 dims), becomes 128 first and
+// 128 second codes in its place.  A thread per row; returns the scale's exponent, or -128 where the row has an inf or NaN
+// (its logits are NaN).  The warps that widen codes do it while the softmax warps are at the output of the part before: 20 ragged
+// prompts of 40 heads take 627 us; with the softmax warps doing it 669, as a pass of its own over memory 720.
+__device__ __forceinline__ int query_codes(uint8_t* tile, int row) {
+  uint8_t* const at = tile + row * 128;
+  const int x = row & 7;
+  auto piece = [&](int half, int c) { return reinterpret_cast<uint4*>(at + half * 16384 + ((c ^ x) << 4)); };
+  uint32_t m = 0;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int c0 = 0; c0 < 8; c0 += 4) {
+      uint4 v[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[c] = *piece(half, c0 + c);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        m = __vmaxu2(__vmaxu2(__vmaxu2(v[c].x & 0x7FFF7FFFu, v[c].y & 0x7FFF7FFFu), __vmaxu2(v[c].z & 0x7FFF7FFFu, v[c].w & 0x7FFF7FFFu)), m);
+    }
+  }
+  m = max(m & 0xFFFFu, m >> 16);
+  // 448 = 1.75 * 2^8; a row without an inf or NaN has an exponent below 255
+  const int e = static_cast<int>(m >> 7) - 127, up = m == 0 ? 0 : min(8 - e - ((m & 127) > 96 ? 1 : 0), 120);
+  const float lift = __int_as_float((127 + max(up, -126)) << 23);  // up >= -120
+  auto codes = [&](const uint4& v, uint2& first, uint2& second) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 a = fmul2(make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u)), make_float2(lift, lift));
+      hi[j] = __nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+      const uint32_t h = e4m3x2_to_f16x2(hi[j]);
+      const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&h));
+      lo[j] = __nv_cvt_float2_to_fp8x2(make_float2(a.x - back.x, a.y - back.y), __NV_SATFINITE, __NV_E4M3);
+    }
+    first = make_uint2(hi[0] | hi[1] << 16, hi[2] | hi[3] << 16);
+    second = make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+  };
+  // In an order in which a code goes where every value has been read: the upper half's second codes from behind, its first
+  // codes at the end.
+  auto sixteen = [&](int half, int k, uint4& first, uint4& second) {
+    uint2 a, b, c, d;
+    codes(*piece(half, 2 * k), a, b);
+    codes(*piece(half, 2 * k + 1), c, d);
+    first = make_uint4(a.x, a.y, c.x, c.y);
+    second = make_uint4(b.x, b.y, d.x, d.y);
+  };
+  uint4 upper[4];
+#pragma unroll
+  for (int k = 3; k >= 0; --k) {
+    uint4 second;
+    sixteen(1, k, upper[k], second);
+    *piece(1, 4 + k) = second;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint4 first, second;
+    sixteen(0, k, first, second);
+    *piece(0, k) = first;
+    *piece(1, k) = second;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) *piece(0, 4 + k) = upper[k];
+  return m < 0x7F80u ? up : -128;
+}
+
 template <bool FP8>
 __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ PromptMaps maps, PromptParams p) {
   using C = PromptCfg<FP8>;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // Two tiles of queries, each two 64-dim halves of 128 rows (fp8: two tiles of codes); the stages.  bf16: as the queries'
+  // Two tiles of queries, each two 64-dim halves of 128 rows (fp8: which become two tiles of codes); the stages.  bf16: as the queries'
   // tiles, the last one is the second tile of queries.  fp8: K's codes, V's codes, V's values.
   uint8_t* const q_buf = smem;
   uint8_t* const ring = smem + 2 * 32768;
@@ -598,6 +623,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     }
     mbar_init(&sm.q_full, 1);
     mbar_init(&sm.q_empty, 2);
+    mbar_init(&sm.q_ready, 4);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.p_full[i], 4);
@@ -678,7 +704,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         mbar_arrive_expect_tx(&sm.q_full, n * T * G * 256);
         for (int b = 0; b < n; ++b)
           for (int half = 0; half < 2; ++half)
-            tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * (FP8 ? 128 : 64), g.head * G,
+            tma_load_3d(q_buf + b * 32768 + half * 16384, &maps.q, &sm.q_full, half * 64, g.head * G,
                         g.q_start + g.t0 + b * T);
       }
       __syncwarp();
@@ -813,7 +839,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       const int blocks = g.one ? (g.count + 1 - b) / 2 : g.count;
       const uint64_t qa = q_desc + (g.one ? 0 : b * 2048);
       tl.part(g);
-      ok = mbar_wait_warp(&sm.q_full, parts & 1, abort_flag);
+      ok = mbar_wait_warp(FP8 ? &sm.q_ready : &sm.q_full, parts & 1, abort_flag);
       for (int i = -1; ok && i < steps; ++i) {
         const bool pv = i >= 0 && i < blocks, s = i + 1 < blocks;
         const Fill v = tl.v(pv ? first + i * every : 0), k = tl.k(s ? first + (i + 1) * every : 0);
@@ -904,8 +930,16 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       const int sees = p.visible ? g.past : g.past + t_tile + 1;  // keys that every row of the tile sees
       const int32_t* mask = p.visible && mine ? p.visible + static_cast<long long>(g.q_start + tok) * p.mask_words : nullptr;
       tl.part(g);
-      // fp8: the row's queries are codes of a scale of their own
-      const float qc = FP8 && mine ? normal_factor(p.scale_log2 * p.q_scale[(static_cast<long long>(g.q_start) + tok) * p.hq + g.head * G + my_h]) : 1.0f;
+      float qc = 1.0f;  // fp8: the row's queries are codes of a scale of their own
+      if constexpr (FP8) {
+        // (the part after the next one's queries come when that one's V is widened, behind this part's output)
+        if (!mbar_wait_warp(&sm.q_ready, parts & 1, abort_flag)) {
+          ok = false;
+          break;
+        }
+        const int up = sm.q_up[parts & 1][(g.one ? 0 : b * 128) + r];
+        if (mine) qc = normal_factor(p.scale_log2 * __int_as_float(up == -128 ? 0x7FC00000 : (127 - up) << 23));
+      }
       float m = -INFINITY;
       float2 l2 = make_float2(0.0f, 0.0f);
       int blk = g.one ? b : 0;
@@ -1146,6 +1180,14 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     while (ok && walk.next(g)) {
       if constexpr (FP8) {
         tl.part(g);
+        // the queries, while the part before ends
+        ok = mbar_wait_warp(&sm.q_full, parts & 1, abort_flag);
+        if (!ok) break;
+#pragma unroll 1
+        for (int b = 0; b < (g.one ? 1 : 2); ++b) sm.q_up[parts & 1][b * 128 + thread] = static_cast<int8_t>(query_codes(q_buf + b * 32768, thread));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm.q_ready);
         // the part before has read its output's stages
         if (parts > 0) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
         for (int i = 0; ok && i < g.count; ++i, ++blocks) {
@@ -1338,9 +1380,7 @@ cudaError_t launch_attn(const PromptMaps& maps, const PromptParams& p, cudaStrea
 bool prompt_may_split(int max_nb) { return max_nb * static_cast<long long>(kPairCost) + 12 > kRunsSlack; }
 
 cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bool fp8, cudaStream_t stream) {
-  long long ctas = 1;
-  if (fp8) ctas += std::min(static_cast<long long>(2 * p.ctas), (static_cast<long long>(p.total_q) * p.hq * 16 + kPlanThreads - 1) / kPlanThreads);
-  cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(static_cast<unsigned>(ctas)), dim3(kPlanThreads), 0, stream, p);
+  cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   note_launches(1);
   if (p.total_q == 0) return cudaSuccess;  // the lengths have been checked; there is no row to compute

@@ -570,9 +570,8 @@ msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const voi
  *               max_seqlen_k <= 2^30, softmax_scale < 1e30.
  *   q, k, v     packed, as in the conventions above.
  *   o, lse      written for every query row; o must not overlap q.
- * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (42 MB, 40 bytes per pair of tiles of
- * 128 / group tokens, and 260 bytes per query row and head, which calls over E4M3
- * pages use).
+ * Workspace: op MSA_OP_DENSE_ATTN_PREFILL (42 MB and 40 bytes per pair of tiles of
+ * 128 / group tokens).
  * Numbers.  Logits, references, sums, O and lse are fp32; a weight that meets V is
  * rounded to bf16 (2^-8 of the weight; E4M3 pages: fp16, 2^-11, down to 2^-21 of the
  * row's largest weight times page scale), the sum takes it unrounded.  Over E4M3
