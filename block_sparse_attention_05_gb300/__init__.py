@@ -766,7 +766,7 @@ def extend_workspace(num_seqs: int, device="cuda") -> torch.Tensor:
 
 def _out(t, dtype, shape, dev, name):
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=f"cuda:{dev}")
+        t = torch.empty(shape, dtype=dtype, device=dev)
         return t, t.data_ptr()
     return t, _is(t, dtype, shape, dev, name)
 
@@ -820,6 +820,8 @@ def _rows(t, tokens, inner, dev, name):
     """The address and token stride of new rows: contiguous but for the distance between tokens."""
     if t.dtype is torch.bfloat16 and t.get_device() == dev and t.shape == (tokens, *inner):
         strides, n = t.stride(), 1
+        if tokens > 1 and strides[-1] == 1 and (len(inner) == 1 or strides[1] == 128):  # (a head's row has 128)
+            return t.data_ptr(), strides[0]
         for size, stride in zip(inner[::-1], strides[:0:-1]):
             if stride != n and size != 1:
                 raise ValueError(f"{name}: a token's row must be contiguous, got strides {list(strides)}")
