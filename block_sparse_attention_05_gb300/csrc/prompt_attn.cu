@@ -18,13 +18,13 @@
 // rest would take half as much time again; l and lse sum the unrounded weights, everything else is fp32.
 //
 // E4M3 pages: K's codes are multiplied as they are (kind::f8f6f4), by queries that are two codes each; V's are widened to fp16
-// by four warps of their own, and P is fp16 (2^-11).  Widening K as well had those warps bound the kernel: 6.2 against 5.0 ms
+// by four warps of their own, and P is fp16 (2^-11).  Widening K as well had those warps bound the kernel: 6.2 against 4.6 ms
 // for a 20,000-token prompt of 64/4 heads.
 //
 // What bounds it.  A block takes a pair of tiles 2,048 clocks of MMAs, which also read shared memory at its full rate (128 bytes
 // a clock: S alone 64 KB per tile).  Measured 2,900 at 1.86 GHz: a warpgroup's chain of S, its way to the softmax (390),
 // the softmax (1,200), P's way back (180) and P V is longer than the other's MMAs.  A 20,000-token prompt of 64/4 heads:
-// 3.95 ms, 1,660 TFLOP/s, 97 % of what the library's matrix product holds under the power limit.  P V begun at half of P
+// 3.9 ms, 1,670 TFLOP/s, 97 % of what the library's matrix product holds under the power limit.  P V begun at half of P
 // shortens the chain and changes nothing there.
 //
 // An item of one tile (a tree of few drafts, the end of a prompt) would leave one warpgroup idle: its blocks go to the
@@ -270,6 +270,7 @@ struct Part {
 };
 
 // Every warp walks the same parts.
+template <bool FP8>
 struct PartWalker {
   const PromptParams& p;
   int items, runs, item, round;
@@ -295,13 +296,14 @@ struct PartWalker {
       if (at >= hi) return false;
       j = item;
     } else {
-      // largest first, there and back over the CTAs: what one has more in a round it has less in the next
+      // largest first, there and back over the CTAs: what one has more in a round it has less in the next.  (A 32-bit division
+      // for E4M3 alone: bf16 prompts are 1 % slower with it.)
       const long long n = static_cast<long long>(items) * p.hkv;
       const long long base = static_cast<long long>(round) * gridDim.x;
       const long long i = base + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
       ++round;
       if (i >= n) return false;  // in a last round that has only the other end, or behind it
-      j = static_cast<int>(i / p.hkv);
+      j = FP8 && n >> 31 == 0 ? static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(p.hkv)) : static_cast<int>(i / p.hkv);
       g.head = static_cast<int>(i - static_cast<long long>(j) * p.hkv);
     }
     const PromptItem it = p.items[j];
@@ -336,8 +338,9 @@ struct PartWalker {
 template <bool FP8>
 struct PromptCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
-  // a warpgroup's registers per thread; the launch has 65,536 for all
-  static constexpr int kSoftmaxRegs = FP8 ? 184 : 208, kOtherRegs = FP8 ? 72 : 88;
+  // A warpgroup's registers per thread; their sum is the launch's.  What the compiler keeps out of the softmax loop hangs on them and
+  // on the unrolling of the output: a 20,000-token prompt over E4M3 pages takes 4.57 ms as it is, 5.03 with 184 and 72.
+  static constexpr int kSoftmaxRegs = FP8 ? 176 : 216, kOtherRegs = FP8 ? 80 : 72;
   // bf16: stages of tiles of 128 keys.  A part of one tile of rows has the second tile's room as one more.
   static constexpr int kStages = 5;
   static constexpr int kOutStage = kStages - 2;  // bf16: a part's output passes through this and the next one
@@ -663,7 +666,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
     if (FP8) return v_ring + (st - C::kK8) * C::kTile;
     return st < C::kStages ? ring + st * C::kTile : q_buf + 32768;
   };
-  PartWalker walk(p);
+  PartWalker<FP8> walk(p);
   Part g{};
   Tiles<FP8> tl{};
   if (warp == 9) {
@@ -923,7 +926,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar);
     };
-    while (ok && walk.next(g)) {
+    bool there = walk.next(g);
+    while (ok && there) {
       const int t_tile = g.t0 + (g.one ? 0 : b * T);  // the tile's first token
       const int tok = t_tile + my_t;
       const bool mine = my_t < T && tok < g.q_len;
@@ -1061,6 +1065,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       tl.done();
 
       // ---- output
+      Part then{};
+      there = walk.next(then);  // looked up while P V runs
       const bool some = had < g.count;
       if (some) {
         if (!mbar_wait_warp(&sm.o_full[b], outs & 1, abort_flag)) {
@@ -1158,7 +1164,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         const int left = min(T, g.q_len - t_tile);
         const int per = g.one ? 8 : 16;                  // lanes to a row
         const int c = lane & (per - 1), half = g.one ? b : c >> 3;
-#pragma unroll 4
+#pragma unroll(FP8 ? 4 : 2)
         for (int i = lane / per; i < 32; i += 32 / per) {
           const int row = (warp & 3) * 32 + i;
           const int t = static_cast<int>(static_cast<uint32_t>(row) * group_inv >> 16), h = row - t * G;
@@ -1169,6 +1175,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         fence_proxy_async_smem();  // before the stage is loaded again
       }
       warp_arrive(&sm.out_free);
+      g = then;
       ++parts;
     }
     if (!ok && lane == 0) gave_up();

@@ -296,6 +296,15 @@ def test_a_workspace_may_hold_anything(msa, layout, seqs):
         assert msa.msa_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("many", [40, 1100])
+def test_long_caches_among_short_prompts(msa, layout, many):
+    """Runs over items of very different cost: ends of two tiles and of one, items of a block, two long ones."""
+    q = [1 + 7 * (s % 23) for s in range(many)] + [3, 40]
+    kv = [n + (s % 5) * 90 for s, n in enumerate(q[:-2])] + [9000, 20000]
+    Batch(msa, q, kv, 16, 2, layout, seed=53).check()
+
+
 def test_packed_and_paged_agree(msa):
     """The same keys by either way: the same bits."""
     p = Batch(msa, [100, 3], [500, 9000], 16, 2, "paged", seed=23)
