@@ -1236,13 +1236,19 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
 constexpr int kJoinWarps = 8;
 constexpr int kJoinCtas = 304;
 static_assert(kPromptMaxCtas <= kJoinWarps * 32, "a thread per run");
+constexpr int kJoinFew = 4;  // an item of so many partials: its rows' dims go to the warps, not its partials
 struct JoinSmem {
-  float4 sums[kJoinWarps][4][32];
-  float2 ml[kJoinWarps][32];
-  uint2 turned[32][9];
+  union {
+    struct {
+      float4 sums[kJoinWarps][4][32];
+      float2 ml[kJoinWarps][32];
+      uint2 turned[32][9];
+    };
+    uint2 rows_turned[32][34];
+  };
   int4 item[kPromptMaxCtas];  // first run, last run, first query row, head
   int2 rows[kPromptMaxCtas];  // first token, new tokens of the sequence
-  int in_warp[kJoinWarps];
+  int2 in_warp[kJoinWarps];  // items of many and of few partials
 };
 // Rows task / 4 and dims task % 4 of an item.
 __device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, int4 item, int2 rows, int task) {
@@ -1335,6 +1341,68 @@ __device__ __forceinline__ void join_rows(const PromptParams& p, JoinSmem& sm, i
   __syncthreads();  // the next task's sums
 }
 
+// The same for few partials: 32 rows (task) and every dim, 16 of them a warp's, all partials in flight at once.  With the
+// tasks above 50 items of two or three partials took 11 us (now 7), and most warps had nothing to read.
+__device__ __forceinline__ void join_few(const PromptParams& p, JoinSmem& sm, int4 item, int2 rows, int task) {
+  const int run = item.x, last = item.y, q_start = item.z, head = item.w, t0 = rows.x, q_len = rows.y;
+  const int b = task >> 2, row0 = (task & 3) * 32;  // tile and first row
+  if (t0 + b * p.tile_tokens >= q_len || row0 >= p.tile_tokens * p.group) return;  // nobody's rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int row = row0 + lane;
+  float2 x[kJoinFew];
+  float4 v[kJoinFew][4];
+#pragma unroll
+  for (int u = 0; u < kJoinFew; ++u) {
+    const long long at = static_cast<long long>(run + u) * 4 + (u == 0 ? 2 : 0) + b;
+    x[u] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) v[u][c] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (run + u > last) continue;
+    x[u] = p.part_ml[at * 128 + row];
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      v[u][c] = *reinterpret_cast<const float4*>(p.part_o + ((at * 32 + warp * 4 + c) * 128 + row) * 4);
+  }
+  static_assert(kJoinFew == 4, "the maximum of four");
+  const float m = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+  float l = 0.0f;
+  float4 a[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) a[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int u = 0; u < kJoinFew; ++u) {
+    const float f = exp2_diff(x[u].x, m);
+    if (f == 0.0f) continue;  // what a part without a key that counts left does not
+    l = fmaf(x[u].y, f, l);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      a[c].x = fmaf(v[u][c].x, f, a[c].x);
+      a[c].y = fmaf(v[u][c].y, f, a[c].y);
+      a[c].z = fmaf(v[u][c].z, f, a[c].z);
+      a[c].w = fmaf(v[u][c].w, f, a[c].w);
+    }
+  }
+  const float inv = inverse(l);
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    sm.rows_turned[lane][warp * 4 + c] = make_uint2(pack_bf16(a[c].x * inv, a[c].y * inv), pack_bf16(a[c].z * inv, a[c].w * inv));
+  auto out_row = [&](int r) {  // of the output, or -1: a row of nobody
+    const int t = r / p.group, h = r - t * p.group, tok = t0 + b * p.tile_tokens + t;
+    if (t >= p.tile_tokens || tok >= q_len) return -1LL;
+    return (static_cast<long long>(q_start) + tok) * p.hq + head * p.group + h;
+  };
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // 16 lanes write a row
+    const int r = (threadIdx.x >> 4) + 16 * i, c = threadIdx.x & 15;
+    const long long out = out_row(row0 + r);
+    if (out >= 0) *reinterpret_cast<uint4*>(p.o + out * kHeadDim + c * 8) = *reinterpret_cast<const uint4*>(&sm.rows_turned[r][2 * c]);
+  }
+  const long long lse_at = out_row(row);
+  if (threadIdx.x < 32 && lse_at >= 0) p.lse[lse_at] = (m + log2f(l)) * kLn2;
+  __syncthreads();  // the next task's rows
+}
+
 __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptParams p) {
   __shared__ JoinSmem sm;
   griddep_wait();
@@ -1357,21 +1425,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptPara
       }
     }
   }
-  // the list has one order in all CTAs
-  const uint32_t some = __ballot_sync(0xFFFFFFFFu, item.x >= 0);
-  if ((threadIdx.x & 31) == 0) sm.in_warp[threadIdx.x >> 5] = __popc(some);
+  // the lists have one order in all CTAs: items of many partials from the front, those of few from behind
+  const bool is = item.x >= 0, few = is && item.y - item.x < kJoinFew;
+  const uint32_t some = __ballot_sync(0xFFFFFFFFu, is), some_few = __ballot_sync(0xFFFFFFFFu, few), some_many = some & ~some_few;
+  const uint32_t below = (1u << (threadIdx.x & 31)) - 1u;
+  if ((threadIdx.x & 31) == 0) sm.in_warp[threadIdx.x >> 5] = make_int2(__popc(some_many), __popc(some_few));
   __syncthreads();
-  int count = 0, at = __popc(some & ((1u << (threadIdx.x & 31)) - 1u));
+  int n_many = 0, n_few = 0, at = __popc((few ? some_few : some_many) & below);
   for (int w = 0; w < kJoinWarps; ++w) {
-    if (w < static_cast<int>(threadIdx.x >> 5)) at += sm.in_warp[w];
-    count += sm.in_warp[w];
+    const int2 n = sm.in_warp[w];
+    if (w < static_cast<int>(threadIdx.x >> 5)) at += few ? n.y : n.x;
+    n_many += n.x;
+    n_few += n.y;
   }
-  if (item.x >= 0) {
+  if (is) {
+    if (few) at = kPromptMaxCtas - 1 - at;
     sm.item[at] = item;
     sm.rows[at] = rows;
   }
   __syncthreads();
-  for (int task = blockIdx.x; task < count * 32; task += gridDim.x) join_rows(p, sm, sm.item[task >> 5], sm.rows[task >> 5], task & 31);
+  for (int task = blockIdx.x; task < n_many * 32 + n_few * 8; task += gridDim.x) {
+    if (task < n_many * 32) {
+      join_rows(p, sm, sm.item[task >> 5], sm.rows[task >> 5], task & 31);
+    } else {
+      const int t = task - n_many * 32, i = kPromptMaxCtas - 1 - (t >> 3);
+      join_few(p, sm, sm.item[i], sm.rows[i], t & 7);
+    }
+  }
 }
 
 template <bool FP8>
