@@ -50,15 +50,16 @@ constexpr int kPlanBins = 1024;
 // the output.  E4M3 pages: 1.9, 1.0, 4.5.  With runs of equally many blocks the CTAs of 16 trees of 2 to 31 drafts end
 // after 75 to 113 us.
 struct PromptCosts {
-  int pair, one, item;
+  int pair, one, item, slack;
 };
 constexpr int kPairCost = 4;  // the largest
 __device__ __forceinline__ PromptCosts costs(const PromptParams& p) {
-  return p.k_scale ? PromptCosts{kPairCost, 2, 9} : PromptCosts{kPairCost, 3, 12};
+  return p.k_scale ? PromptCosts{kPairCost, 2, 9, 20} : PromptCosts{kPairCost, 3, 12, 30};
 }
-// A call is cut into runs when its longest item costs so much more than an even share: what a partial's way through memory
-// and the join take.
-constexpr int kRunsSlack = 36;
+// A call is cut into runs when its longest item costs `slack` more than an even share, which is about what a partial's way
+// through memory and the join take (6 drafts over 1,500 E4M3 keys: 27.1 us whole, 19.7 in runs; over 880 bf16 keys 19.2 and 16.4);
+// never where no item has more than so many blocks.
+constexpr int kWholeBlocks = 6;
 
 // Exclusive scan over the CTA (kPlanThreads threads); `sh` holds 32 values.
 __device__ long long plan_scan(long long v, long long* sh, long long* total) {
@@ -182,7 +183,7 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   plan_scan(sum, sh, &total);  // synchronises
   total *= p.hkv;
   most = s_most;
-  const bool split = p.part_o != nullptr && most > total / p.ctas + kRunsSlack;
+  const bool split = p.part_o != nullptr && most > total / p.ctas + costs(p).slack;
   const int runs = split ? static_cast<int>(min(total / s_cost, static_cast<long long>(p.ctas))) : 0;  // a block each at least
   if (threadIdx.x == 0) {
     plan->n_items = items;
@@ -1464,7 +1465,7 @@ cudaError_t launch_attn(const PromptMaps& maps, const PromptParams& p, cudaStrea
 
 }  // namespace
 
-bool prompt_may_split(int max_nb) { return max_nb * static_cast<long long>(kPairCost) + 12 > kRunsSlack; }
+bool prompt_may_split(int max_nb) { return max_nb > kWholeBlocks; }
 
 cudaError_t launch_prompt_attn(const PromptMaps& maps, const PromptParams& p, bool fp8, cudaStream_t stream) {
   cudaError_t e = launch_pdl(prompt_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p);
