@@ -159,6 +159,21 @@ def test_streams_at_once(msa):
             assert msa.msa_read_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_rows_beyond_32_bits(msa, fp8):
+    """The last pages of caches of more than 2^32 bytes, and of more than 2^31 values."""
+    pages = 66000 if fp8 else 33000
+    lp = Loop(msa, 3, 16, 4, fp8, pages=pages)
+    lp.free = torch.arange(pages - 1, pages - 60, -1, dtype=torch.int32, device="cuda")
+    prefill = msa.msa_dense_attn_prefill_paged_fp8 if fp8 else msa.msa_dense_attn_prefill_paged
+    for new in ([300, 17, 0], [5, 900, 129]):
+        prob, q = lp.grow(new)
+        rows = lp.key_rows()
+        assert min(int(r.min()) for r in rows if len(r)) * lp.k.shape[1] * DIM > 2 ** (32 if fp8 else 31)
+        got = prefill(prob, q, lp.k, lp.v, *lp.scales(), lp.table)
+        check(got, reference(new, lp.lens, rows, q, lp.k, lp.v, lp.ks, lp.vs, 0.0, None), f"{new}")
+
+
 def test_captured_loop(msa):
     """Tables, rows and attention of a step in one graph, replayed: the cache grows by itself."""
     S, hq, hkv, steps = 3, 16, 2, 40
