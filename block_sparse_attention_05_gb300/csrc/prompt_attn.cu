@@ -928,6 +928,13 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       if (lane == 0) mbar_arrive(bar);
     };
     bool there = walk.next(g);
+    // fp8: V of a part is widened when every warp has seen that its queries are codes (and has read the output's stages of the part
+    // before).  Without that the next part's q_ready could come before a late warp has looked at this one's: it would wait
+    // for a phase that is past.
+    if (FP8 && there) {
+      ok = mbar_wait_warp(&sm.q_ready, 0, abort_flag);
+      if (ok) warp_arrive(&sm.out_free);
+    }
     while (ok && there) {
       const int t_tile = g.t0 + (g.one ? 0 : b * T);  // the tile's first token
       const int tok = t_tile + my_t;
@@ -937,11 +944,6 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       tl.part(g);
       float qc = 1.0f;  // fp8: the row's queries are codes of a scale of their own
       if constexpr (FP8) {
-        // (the part after the next one's queries come when that one's V is widened, behind this part's output)
-        if (!mbar_wait_warp(&sm.q_ready, parts & 1, abort_flag)) {
-          ok = false;
-          break;
-        }
         const int up = sm.q_up[parts & 1][(g.one ? 0 : b * 128) + r];
         if (mine) qc = normal_factor(p.scale_log2 * __int_as_float(up == -128 ? 0x7FC00000 : (127 - up) << 23));
       }
@@ -1175,9 +1177,13 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         }
         fence_proxy_async_smem();  // before the stage is loaded again
       }
+      ++parts;
+      if (FP8 && there && !mbar_wait_warp(&sm.q_ready, parts & 1, abort_flag)) {
+        ok = false;
+        break;
+      }
       warp_arrive(&sm.out_free);
       g = then;
-      ++parts;
     }
     if (!ok && lane == 0) gave_up();
   } else if (FP8 && warp >= 12) {
@@ -1196,8 +1202,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm.q_ready);
-        // the part before has read its output's stages
-        if (parts > 0) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
+        // the part before has read its output's stages, and these queries have been seen
+        ok = mbar_wait_warp(&sm.out_free, parts & 1, abort_flag);
         for (int i = 0; ok && i < g.count; ++i, ++blocks) {
           const int cs = blocks & 1;
           const Fill v = tl.v(i);
