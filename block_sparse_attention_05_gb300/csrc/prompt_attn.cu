@@ -776,7 +776,14 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           const int next_row = __shfl_sync(0xFFFFFFFFu, now.row, next);
           const CUtensorMap* map = v ? &maps.v : &maps.k;
           const int st = tl.stage(t);
-          if (st >= C::kOutStage && !out_read) {
+          // Q of a part of one block comes before its V, which waits for the output of the part before: a look behind V could
+          // come after that of this part too, and take its phase for one that is still to come.
+          const bool last = t == tl.total - 1;
+          if (last && t == 1 && parts > 0) {
+            ok = load_q();
+            if (!ok) break;
+          }
+          if ((st >= C::kOutStage || last) && !out_read) {
             ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
             if (!ok) break;
             out_read = true;
@@ -794,12 +801,11 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
           used |= 1u << st;
           filled = (filled & ~(1u << st)) | tl.parity(t) << st;
           row = next_row;
-          if (t == 1 && parts > 0) {
+          if (t == 1 && !last && parts > 0) {
             ok = load_q();
             if (!ok) break;
           }
         }
-        if (ok && !out_read) ok = mbar_wait_warp(&sm.out_free, (parts - 1) & 1, abort_flag);
         if (g.one && tl.total > C::kStages) {  // the lent stage's last fill in this part
           const int n = C::kStages + 1;
           lent = true;

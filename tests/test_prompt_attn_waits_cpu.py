@@ -227,7 +227,7 @@ class Kernel:
                     yield []
                     if t == 1 and pi and not (ring.total == 2 and last):
                         yield from self.load_q(pi, one, state)
-                if not read:
+                if not read:   # (only without the look before the last tile)
                     yield [(self.out_free, pi - 1)]
                 if one and ring.total > STAGES:
                     state["lent"] = ring.at(STAGES + (ring.total - ring.n) // ring.n * ring.n)[1]
@@ -406,6 +406,7 @@ def test_the_source_has_the_order_of_the_model():
     softmax = text[text.index("- softmax and output"):]
     first, last = re.search(r"q_ready, 0, .*?out_free", softmax, re.S), re.search(r"\+\+parts;.*?q_ready, parts & 1.*?out_free\);\s+g = then", softmax, re.S)
     assert first and last and first.start() < softmax.index("while (ok && there)") < last.start()
+    assert re.search(r"\(st >= C::kOutStage \|\| last\) && !out_read", text)
     assert re.search(r"mbar_arrive\(&sm.q_ready\);[^;]*out_free, parts & 1", softmax)
 
 
@@ -423,14 +424,15 @@ def schedules(fp8, n, without=()):
     return bad
 
 
-@pytest.mark.parametrize("fp8", [True])
+@pytest.mark.parametrize("fp8", [False, True])
 def test_every_schedule_ends(fp8):
     bad = schedules(fp8, 600)
     assert not bad, bad[:3]
 
 
 @pytest.mark.parametrize("fp8,without", [(True, "softmax sees the next queries before it is done with a part"),
-                                         (True, "softmax sees the first queries")])
+                                         (True, "softmax sees the first queries"),
+                                         (False, "loader looks before the last tile")])
 def test_a_look_that_comes_too_late_is_found(fp8, without):
     """Each of these orders is needed: without it some schedules never end."""
     bad = schedules(fp8, 600, (without,))
