@@ -1024,25 +1024,36 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         // at most 2^15 whatever the pages' scales, with its 11 significant bits down to 2^-21 of the row's largest (four
         // more, with references replaced from 2^4 on, made ragged prompts 20 % slower)
         const float x = fmaf(row_max(), c, lv);
-        const bool fresh = m == -INFINITY;  // no key counts so far: O and l are 0, or not there yet
+        if (m == -INFINITY) m = x;  // no key counts so far: O and l are 0, or not there yet
+        const float up = x - m, back = FP8 ? exp2_approx(-lv - kLift) : 1.0f;  // back: fp8: what the weights' sum counts with
+        auto is_large = [&] { return fabsf(m) >= kRoundLogits && m != -INFINITY; };
         // (rows of nobody hold what the stages held before: they neither rescale nor round)
-        const bool rise = mine && !fresh && x - m > 8.0f;
-        if (__any_sync(0xFFFFFFFFu, rise)) {  // O is complete: its P V came before this S
-          const float k = rise ? exp2_approx(m - x) : 1.0f;
-          l2.x *= k;
-          l2.y *= k;
-          scale_row(o_col, k);
-          row_max();  // the row again
-        }
-        if (fresh || rise) m = x;
-        if (__any_sync(0xFFFFFFFFu, mine && fabsf(m) >= kRoundLogits && m != -INFINITY)) {
-          // products rounded to fp32 logits before the reference is taken off: see kRoundLogits
-          const float k = fabsf(m) >= kRoundLogits ? c : 1.0f;
+        if (__any_sync(0xFFFFFFFFu, mine && (up > 8.0f || is_large()))) {
+          const bool rise = mine && up > 8.0f;
+          if (__any_sync(0xFFFFFFFFu, rise)) {  // O is complete: its P V came before this S
+            const float k = rise ? exp2_approx(-up) : 1.0f;
+            l2.x *= k;
+            l2.y *= k;
+            scale_row(o_col, k);
+            row_max();  // the row again
+            if (rise) m = x;
+          }
+          const bool large = is_large();
+          if (__any_sync(0xFFFFFFFFu, mine && large)) {
+            // Products rounded to fp32 logits before the reference is taken off: see kRoundLogits.  fp8: with V's scale in the same
+            // rounding, which is the reference's, and the lift behind the difference: from logits of 2^23 on either would be
+            // rounded away by itself, and the largest weights pass fp16.
+            const float k = large ? c : 1.0f, add = FP8 && large ? lv : 0.0f, less = FP8 && large ? m : 0.0f;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[q][j] = __float_as_uint(__uint_as_float(v[q][j]) * k);
-          if (fabsf(m) >= kRoundLogits) c = 1.0f;
+              for (int j = 0; j < 32; ++j) {
+                const float s = __uint_as_float(v[q][j]);
+                v[q][j] = __float_as_uint(FP8 ? fmaf(s, k, add) - less : s * k);
+              }
+            if (large) c = 1.0f;
+            if (FP8 && large) lv = m;
+          }
         }
         const float off = m == -INFINITY ? 0.0f : lv - m + kLift;  // -inf - -inf is NaN
         const float2 c2 = make_float2(c, c), nm = make_float2(off, off);
@@ -1061,7 +1072,6 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) weights(v[q], q);
         if (FP8) {
-          const float back = exp2_approx(-lv - kLift);
           l2 = ffma2(sum, make_float2(back, back), l2);
         } else {
           l2 = sum;
