@@ -340,8 +340,8 @@ template <bool FP8>
 struct PromptCfg {
   static constexpr int kThreads = FP8 ? 512 : 384;
   // A warpgroup's registers per thread; their sum is the launch's.  What the compiler keeps out of the softmax loop hangs on them and
-  // on the unrolling of the output: a 20,000-token prompt over E4M3 pages takes 4.57 ms as it is, 5.03 with 184 and 72.
-  static constexpr int kSoftmaxRegs = FP8 ? 176 : 216, kOtherRegs = FP8 ? 80 : 72;
+  // on the unrolling of the output: a 20,000-token prompt over E4M3 pages takes 4.25 ms as it is, 4.80 with 176 and 80.
+  static constexpr int kSoftmaxRegs = FP8 ? 184 : 216, kOtherRegs = 72;
   // bf16: stages of tiles of 128 keys.  A part of one tile of rows has the second tile's room as one more.
   static constexpr int kStages = 5;
   static constexpr int kOutStage = kStages - 2;  // bf16: a part's output passes through this and the next one
@@ -357,7 +357,7 @@ struct PromptSmem {
   uint64_t s_full[2], p_full[2], o_full[2], turn[2];  // by warpgroup
   uint64_t ml_full, o_free, out_free, mma_done;
   float2 ml[2][128];
-  float k_scale[8], v_scale[8];  // fp8: scales of the last blocks (loaded at most 5 ahead of the one that a warpgroup is at)
+  float k_scale[8], v_scale[8];  // fp8: scales of the last blocks, V's as log2 (loaded at most 5 ahead of the one that a warpgroup is at)
   int8_t q_up[2][256];  // fp8: exponents of the queries' scales, by the part's parity
   uint32_t tmem_base;
   int abort_flag;
@@ -682,7 +682,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       float sk, sv;
     };
     auto look_up = [&](int from) {
-      Rows x{0, 1.0f, 1.0f};
+      Rows x{0, 1.0f, 0.0f};
       const int b = g.block + from + lane;
       x.row = g.k_start + b * kBlock;
       if (p.block_table && from + lane < g.count) {
@@ -692,7 +692,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         x.row = (there ? e : static_cast<int>(p.n_pages)) * kBlock;  // past the cache: TMA reads zeros
         if (FP8) {
           x.sk = there ? p.k_scale[static_cast<long long>(e) * p.hkv + g.head] : 1.0f;
-          x.sv = there ? p.v_scale[static_cast<long long>(e) * p.hkv + g.head] : 1.0f;
+          const float sv = there ? p.v_scale[static_cast<long long>(e) * p.hkv + g.head] : 1.0f;
+          x.sv = sv == 0.0f ? -149.0f : log2f(sv);  // (a scale of 0: below the smallest)
         }
       }
       return x;
@@ -946,7 +947,6 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
       const int tok = t_tile + my_t;
       const bool mine = my_t < T && tok < g.q_len;
       const int sees = p.visible ? g.past : g.past + t_tile + 1;  // keys that every row of the tile sees
-      const int32_t* mask = p.visible && mine ? p.visible + static_cast<long long>(g.q_start + tok) * p.mask_words : nullptr;
       tl.part(g);
       float qc = 1.0f;  // fp8: the row's queries are codes of a scale of their own
       if constexpr (FP8) {
@@ -954,6 +954,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         if (mine) qc = normal_factor(p.scale_log2 * __int_as_float(up == -128 ? 0x7FC00000 : (127 - up) << 23));
       }
       float m = -INFINITY;
+      float d = 0.0f;  // fp8: l is that of 2^(logit - (m - d)), O that of 2^(logit + log2(V's scale) - m)
       float2 l2 = make_float2(0.0f, 0.0f);
       int blk = g.one ? b : 0;
       const int had = blk;
@@ -974,7 +975,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
             break;
           }
           c = normal_factor(qc * sm.k_scale[tl.base + blk & 7]);
-          lv = log2f(sm.v_scale[tl.base + blk & 7]);
+          lv = sm.v_scale[tl.base + blk & 7];
         } else if (edge && j0 + kBlock > g.past + g.q_len && (g.one || b == 0)) {
           // V rows past the sequence's end hold anything, and 0 * NaN is NaN: zero them
           if (!mbar_wait_warp(&sm.full[vf.st], vf.parity, abort_flag)) {
@@ -992,7 +993,7 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         auto hide = [&](uint32_t (&v)[32], int q) {
           uint32_t bits;
           if (p.visible) {
-            bits = mask ? tree_bits(mask, p.mask_words, g.past, g.q_len, j0 + 32 * q) : 0u;
+            bits = mine ? tree_bits(p.visible + static_cast<long long>(g.q_start + tok) * p.mask_words, p.mask_words, g.past, g.q_len, j0 + 32 * q) : 0u;
           } else {
             const int n = g.past + tok + 1 - j0 - 32 * q;
             bits = n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u;
@@ -1022,28 +1023,49 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         };
         // fp8: V's scale goes to the weights as a summand of their exponents, and they are 2^7 times larger: one fp16 value each,
         // at most 2^15 whatever the pages' scales, with its 11 significant bits down to 2^-21 of the row's largest (four
-        // more, with references replaced from 2^4 on, made ragged prompts 20 % slower)
+        // more, with references replaced from 2^4 on, made ragged prompts 20 % slower).  The sum of weights knows no scale: its
+        // reference is m less log2 of the scale that m was taken with (d), replaced for itself where a page of a smaller scale
+        // has larger logits.
         const float x = fmaf(row_max(), c, lv);
-        if (m == -INFINITY) m = x;  // no key counts so far: O and l are 0, or not there yet
-        const float up = x - m, back = FP8 ? exp2_approx(-lv - kLift) : 1.0f;  // back: fp8: what the weights' sum counts with
+        if (m == -INFINITY) {  // no key counts so far: O and l are 0, or not there yet
+          m = x;
+          d = lv;
+        }
+        float up = x - m, t = d - lv;
         auto is_large = [&] { return fabsf(m) >= kRoundLogits && m != -INFINITY; };
         // (rows of nobody hold what the stages held before: they neither rescale nor round)
-        if (__any_sync(0xFFFFFFFFu, mine && (up > 8.0f || is_large()))) {
-          const bool rise = mine && up > 8.0f;
-          if (__any_sync(0xFFFFFFFFu, rise)) {  // O is complete: its P V came before this S
-            const float k = rise ? exp2_approx(-up) : 1.0f;
+        if (__any_sync(0xFFFFFFFFu, mine && (FP8 ? up + fmaxf(t, 0.0f) > 8.0f || t > 60.0f || is_large() : up > 8.0f || is_large()))) {
+          const bool rise = mine && up > 8.0f, grow = FP8 ? rise || (mine && up + t > 8.0f) : rise;
+          if (__any_sync(0xFFFFFFFFu, grow)) {  // O is complete: its P V came before this S
+            const float gap = up + t, k = grow && gap > 0.0f ? exp2_approx(-gap) : 1.0f;
             l2.x *= k;
-            l2.y *= k;
-            scale_row(o_col, k);
+            if (!FP8) l2.y *= k;
+            if (FP8 && grow) d = rise ? (gap > 0.0f ? lv : d + up) : d - gap;
+            scale_row(o_col, rise ? exp2_approx(-up) : 1.0f);
             row_max();  // the row again
             if (rise) m = x;
+            t = d - lv;
           }
-          const bool large = is_large();
+          const bool large = is_large(), far = t > 60.0f;
+          const float add = FP8 && large ? lv : 0.0f, less = FP8 && large ? m : 0.0f;
+          if (FP8 && __any_sync(0xFFFFFFFFu, mine && far)) {
+            // a page of a scale so much smaller: weights that still count in the sum are too small for fp32
+            const float off = large ? t : d - m;
+            float sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) sum += exp2_approx(fmaf(__uint_as_float(v[q][j]), c, add) - less + off);
+            if (far) {
+              l2.x += sum;
+              t = -INFINITY;
+            }
+          }
           if (__any_sync(0xFFFFFFFFu, mine && large)) {
             // Products rounded to fp32 logits before the reference is taken off: see kRoundLogits.  fp8: with V's scale in the same
             // rounding, which is the reference's, and the lift behind the difference: from logits of 2^23 on either would be
             // rounded away by itself, and the largest weights pass fp16.
-            const float k = large ? c : 1.0f, add = FP8 && large ? lv : 0.0f, less = FP8 && large ? m : 0.0f;
+            const float k = large ? c : 1.0f;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -1072,7 +1094,8 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
 #pragma unroll
         for (int q = 0; q < 4; ++q) weights(v[q], q);
         if (FP8) {
-          l2 = ffma2(sum, make_float2(back, back), l2);
+          const float back = exp2_approx(t - kLift);
+          l2.x = fmaf(sum.x + sum.y, back, l2.x);
         } else {
           l2 = sum;
         }
@@ -1095,7 +1118,18 @@ __global__ void __launch_bounds__(PromptCfg<FP8>::kThreads, 1)
         ++outs;
         tc_fence_after();
       }
-      float l = l2.x + l2.y;
+      float l = FP8 ? l2.x : l2.x + l2.y;
+      if constexpr (FP8) {
+        // O, m and l with one reference; an excess of d goes to O and m, so that l is within 2^40 of a sum of weights in every part
+        // and the merge's factors do not lose one beside another
+        const float less = d - fminf(fmaxf(d, -40.0f), 40.0f);
+        if (__any_sync(0xFFFFFFFFu, mine && less != 0.0f)) {
+          scale_row(o_col, exp2_approx(less));
+          tc_fence_before();
+          m -= less;
+        }
+        l *= exp2_approx(less - d);
+      }
       if (l != l) m = INFINITY;  // a NaN among the logits, of which the maximum may know nothing: it passes every merge
       const bool whole = g.first && g.last;
       const long long part_at = static_cast<long long>(blockIdx.x) * 4 + (g.first ? 2 : 0) + (g.one ? 0 : b);  // a tile's

@@ -600,8 +600,9 @@ msa_status_t msa_dense_attn_prefill_paged(const msa_problem_t *problem, const vo
                                           void *workspace, size_t workspace_bytes, msa_stream_t stream);
 
 /* The same over E4M3 pages with one scale per (page, KV head): the attention over
- * the dequantized values.  Scales from 2^-80 to 2^80, those of a sequence's V at most
- * 2^100 apart. */
+ * the dequantized values.  Scales of any size from 0 on, in any mixture.  A page of zeros
+ * has a scale too (1, as msa_append_paged_fp8 writes it): beside much smaller scales of V
+ * it can be the largest weight times page scale that the weights' 2^-21 is taken of. */
 msa_status_t msa_dense_attn_prefill_paged_fp8(const msa_problem_t *problem, const void *q, const void *k8_cache,
                                               const void *v8_cache, const float *k_scale, const float *v_scale,
                                               const int32_t *block_table, int32_t max_blocks_per_seq,
