@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
       const long long ql = static_cast<long long>(q1) - q0, kl = static_cast<long long>(k1) - k0;
       bool bad = ql < 0 || kl < ql || ql > p.max_q || kl > p.max_k || q0 < 0 || k0 < 0 || q1 > p.total_q || k1 > p.total_k;
       if (s == 0 && (q0 != 0 || k0 != 0)) bad = true;
-      if (s == p.num_seqs - 1 && (q1 != p.total_q || k1 != p.total_k)) bad = true;
+      // (paged: total_k is a bound, so that a captured call can follow a cache that grows)
+      if (s == p.num_seqs - 1 && (q1 != p.total_q || (!p.block_table && k1 != p.total_k))) bad = true;
       if (bad) {
         s_bad = 1;
       } else {

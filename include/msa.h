@@ -593,7 +593,9 @@ msa_status_t msa_dense_attn_prefill(const msa_problem_t *problem, const void *q,
 /* The same over paged keys (the new tokens' rows are in the cache already, see
  * msa_append_paged): k_cache, v_cache, block_table, max_blocks_per_seq and
  * num_pages as for msa_dense_attn_decode_paged; a page outside the cache reads as
- * zeros (MSA_DEVICE_BAD_INDEX). */
+ * zeros (MSA_DEVICE_BAD_INDEX).  total_k may be more than cu_seqlens_k[num_seqs]:
+ * a captured call whose total_k and max_seqlen_k are what the table has room for
+ * follows a cache that grows from replay to replay (total_q is what it is). */
 msa_status_t msa_dense_attn_prefill_paged(const msa_problem_t *problem, const void *q, const void *k_cache,
                                           const void *v_cache, const int32_t *block_table,
                                           int32_t max_blocks_per_seq, int64_t num_pages, void *o, float *lse,
