@@ -839,15 +839,24 @@ def _append(where, k, v, slots, k_cache, v_cache, scales, k_idx, k_idx_cache, k_
     dtype = torch.uint8 if scales else torch.bfloat16
     N = slots.numel()
     at_slots = _is(slots, torch.int64, (N,), dev, "slots")
-    if k_cache.dim() != 3 or k_cache.shape[0] % 128:
-        raise ValueError("the caches must be whole pages of 128 rows, [num_pages * 128, num_kv_heads, 128]")
-    rows, hkv = k_cache.shape[0], k_cache.shape[1]
-    at_k, stride_k = _rows(k, N, (hkv, 128), dev, "k")
-    at_v, stride_v = _rows(v, N, (hkv, 128), dev, "v")
-    caches = (_is(k_cache, dtype, (rows, hkv, 128), dev, "k_cache"), _is(v_cache, dtype, (rows, hkv, 128), dev, "v_cache"))
-    at_i, stride_i, at_ic, at_is, d = None, 0, None, None, 128
     if (k_idx is None) != (k_idx_cache is None):
         raise ValueError("k_idx and its cache come together")
+    if k is None and v is None and k_cache is None and v_cache is None and k_idx is not None and not scales:
+        rows, hkv = k_idx_cache.shape[0], 0
+        if k_idx_cache.dim() != 2 or rows % 128:
+            raise ValueError("the cache must be whole pages of 128 rows, [num_pages * 128, d_idx]")
+        (at_k, stride_k), (at_v, stride_v), caches = (None, 0), (None, 0), (None, None)
+    else:
+        for t, name in ((k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache")):
+            if t is None:
+                raise ValueError(f"{name}: needed (k, v and their caches are left out together, for bf16 k_idx alone)")
+        if k_cache.dim() != 3 or k_cache.shape[0] % 128:
+            raise ValueError("the caches must be whole pages of 128 rows, [num_pages * 128, num_kv_heads, 128]")
+        rows, hkv = k_cache.shape[0], k_cache.shape[1]
+        at_k, stride_k = _rows(k, N, (hkv, 128), dev, "k")
+        at_v, stride_v = _rows(v, N, (hkv, 128), dev, "v")
+        caches = (_is(k_cache, dtype, (rows, hkv, 128), dev, "k_cache"), _is(v_cache, dtype, (rows, hkv, 128), dev, "v_cache"))
+    at_i, stride_i, at_ic, at_is, d = None, 0, None, None, 128
     if k_idx is not None:
         d = k_idx_cache.shape[-1]
         at_i, stride_i = _rows(k_idx, N, (d,), dev, "k_idx")
@@ -874,7 +883,8 @@ def _append(where, k, v, slots, k_cache, v_cache, scales, k_idx, k_idx_cache, k_
 
 def msa_append_paged(k, v, slots, k_cache, v_cache, k_idx=None, k_idx_cache=None, ws=None):
     """Writes new tokens' rows k, v [tokens, Hkv, 128] (and k_idx [tokens, d_idx]), which may be slices of wider rows, to
-    rows ``slots`` (int64, distinct, -1: none) of the caches.  ``ws`` (256 bytes) is for device flags only."""
+    rows ``slots`` (int64, distinct, -1: none) of the caches.  k, v and their caches may all be None: k_idx alone (bf16 index
+    pages beside K and V in E4M3 pages).  ``ws`` (256 bytes) is for device flags only."""
     _append("msa_append_paged", k, v, slots, k_cache, v_cache, None, k_idx, k_idx_cache, None, ws)
 
 

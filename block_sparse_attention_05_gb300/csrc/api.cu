@@ -1820,12 +1820,14 @@ msa_status_t msa_append_paged(const void* k, int64_t k_stride, const void* v, in
                               int64_t k_idx_stride, const int64_t* slots, int64_t tokens, int32_t num_kv_heads,
                               int32_t index_dim, void* k_cache, void* v_cache, void* k_idx_cache, int64_t num_pages,
                               void* workspace, size_t workspace_bytes, msa_stream_t stream) {
-  if (num_kv_heads < 1) return MSA_ERR_INVALID_ARG;
+  const bool index_only = !k && !v && !k_cache && !v_cache && k_idx_cache;
+  if (num_kv_heads < 1 && !index_only) return MSA_ERR_INVALID_ARG;
   if (num_kv_heads > 1024 || (k_idx_cache && index_dim != 64 && index_dim != 128)) return MSA_ERR_UNSUPPORTED;
   if (!k_idx_cache && k_idx) return MSA_ERR_INVALID_ARG;
   const AppendRows rows[3] = {{k, k_stride, num_kv_heads * 128, k_cache, nullptr},
                               {v, v_stride, num_kv_heads * 128, v_cache, nullptr},
                               {k_idx, k_idx_stride, index_dim, k_idx_cache, nullptr}};
+  if (index_only) return append_rows(rows + 2, 1, slots, tokens, num_pages, false, workspace, workspace_bytes, stream);
   return append_rows(rows, k_idx_cache ? 3 : 2, slots, tokens, num_pages, false, workspace, workspace_bytes, stream);
 }
 

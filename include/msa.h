@@ -669,7 +669,9 @@ msa_status_t msa_extend_block_table(int32_t num_seqs, const int32_t *lengths, co
  *   k, v       bf16 [tokens, num_kv_heads, 128], tokens k_stride (v_stride)
  *              elements apart: slices of a wider projection's output, say.
  *   k_idx      bf16 [tokens, index_dim] (k_idx_stride apart) with k_idx_cache, or
- *              NULL for both.  index_dim 64 or 128.
+ *              NULL for both.  index_dim 64 or 128.  k, v and their caches may all be
+ *              NULL: K_idx alone (bf16 index pages beside K and V in E4M3 pages, as
+ *              msa_forward_decode_paged_fp8 reads them; num_kv_heads is not looked at).
  *   slots      int64 [tokens], 8-byte aligned, distinct; -1: the token has no row.
  *              Others outside the cache are skipped (MSA_DEVICE_BAD_INDEX).
  * Strides are multiples of 8 and at least a row; pointers 16-byte aligned.  workspace
