@@ -656,7 +656,15 @@ msa_status_t msa_tree_attn_paged_fp8(const msa_problem_t *problem, const void *q
  * and more new tokens than `capacity` (or 2^31 keys) make the call do nothing but
  * fill slots with -1 and positions and prefix sums with 0
  * (MSA_DEVICE_BAD_SEQLENS).  num_seqs <= 2^20.  Workspace:
- * msa_extend_workspace_size. */
+ * msa_extend_workspace_size.
+ *
+ * Taking tokens back (rejected drafts): lengths is the caller's to shorten, and a
+ * block counts as held as long as ceil(lengths / 128) reaches it.  The pages of the
+ * blocks behind that are then in no list; before the next call the caller puts the
+ * n pages back, in any order, where handed-out ones stood, free_pages[*taken - n] to
+ * free_pages[*taken - 1], and lowers *taken by n.  Accepted drafts that do not lie
+ * together (a path through a tree) are written again with msa_append_paged(_fp8):
+ * their rows of k and v, at the step's first slots. */
 msa_status_t msa_extend_workspace_size(int32_t num_seqs, size_t *bytes);
 msa_status_t msa_extend_block_table(int32_t num_seqs, const int32_t *lengths, const int32_t *new_tokens,
                                     int64_t capacity, const int32_t *free_pages, int32_t num_free,
