@@ -343,6 +343,7 @@ struct PromptCfg {
   // A warpgroup's registers per thread; their sum is the launch's.  What the compiler keeps out of the softmax loop hangs on them and
   // on the unrolling of the output: a 20,000-token prompt over E4M3 pages takes 4.25 ms as it is, 4.80 with 176 and 80.
   static constexpr int kSoftmaxRegs = FP8 ? 184 : 216, kOtherRegs = 72;
+  static constexpr int kRegsNeeded = 256 * kSoftmaxRegs + (kThreads - 256) * kOtherRegs;
   // bf16: stages of tiles of 128 keys.  A part of one tile of rows has the second tile's room as one more.
   static constexpr int kStages = 5;
   static constexpr int kOutStage = kStages - 2;  // bf16: a part's output passes through this and the next one
@@ -1517,6 +1518,12 @@ cudaError_t launch_attn(const PromptMaps& maps, const PromptParams& p, cudaStrea
   const cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kPromptSmemBytes));
   if (e != cudaSuccess) return e;
+  // the register reallocation's increases must fit in the launch allocation, or they would never complete
+  static const int regs = [] {
+    cudaFuncAttributes fa{};
+    return cudaFuncGetAttributes(&fa, prompt_attn_kernel<FP8>) == cudaSuccess ? fa.numRegs : 0;
+  }();
+  if (regs < PromptCfg<FP8>::kOtherRegs || regs * PromptCfg<FP8>::kThreads < PromptCfg<FP8>::kRegsNeeded) return cudaErrorInvalidConfiguration;
   return launch_pdl(prompt_attn_kernel<FP8>, dim3(p.ctas), dim3(PromptCfg<FP8>::kThreads), kPromptSmemBytes, stream, maps, p);
 }
 
