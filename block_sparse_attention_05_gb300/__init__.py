@@ -781,6 +781,7 @@ def msa_extend_block_table(lengths, new_tokens, free_pages, block_table, capacit
     ``new_lengths`` (may be ``lengths``) and ``taken_out`` (may be ``taken``) let a captured step advance by itself.
     Workspace: extend_workspace."""
     _int32(capacity, "capacity")
+    _int32(num_pages, "num_pages")
     if not lengths.is_cuda:
         _need(lengths, torch.int32, "lengths")
     dev = _current_device()
@@ -806,6 +807,7 @@ def msa_extend_block_table(lengths, new_tokens, free_pages, block_table, capacit
 
 
 def msa_append_workspace_size(num_pages: int) -> int:
+    _int32(num_pages, "num_pages")
     n = ctypes.c_size_t(0)
     _check(_lib.msa_append_workspace_size(num_pages, ctypes.byref(n)), "msa_append_workspace_size")
     return int(n.value)
