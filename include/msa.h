@@ -580,7 +580,8 @@ msa_status_t msa_add_rms_norm_fp8(const void *x, const void *residual, const voi
  * (2^-22 of the value).  Any finite logit gives finite results; a logit of +inf gives
  * NaN, keys of -inf do not count.  A key that a query does not see does not count
  * whatever its K holds; an inf or NaN in V shows in the queries that see it, and can
- * show in those of the 255 places before it (in a tree: of the whole sequence).  What
+ * show in those of the 2 floor(128 / group) + 126 places before it (382 for groups of
+ * one head; in a tree: of the whole sequence).  What
  * one query row or sequence holds does not change another's results, and what lies
  * past a sequence's last key does not matter.  The same inputs give the same bits.
  * Lengths that contradict the host sizes make the kernels skip the call
