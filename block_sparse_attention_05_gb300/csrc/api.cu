@@ -254,7 +254,7 @@ bool map_2d_u8(CUtensorMap& m, const void* ptr, long long rows, int cols, int bo
   return make_map(m, ptr, 2, dims, strides, box, CU_TENSOR_MAP_DATA_TYPE_UINT8);
 }
 
-// E4M3 codes [n, heads, width] (one byte each), box = 128 codes x box_heads heads x box_rows rows
+// E4M3 codes [n, heads, 128] (one byte each), box = 128 codes x 1 head x box_rows rows
 bool map_3d_u8(CUtensorMap& m, const void* ptr, long long n, int heads, int box_rows = 128) {
   cuuint64_t dims[3] = {128, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(n > 0 ? n : 1)};
   cuuint64_t strides[2] = {128, static_cast<cuuint64_t>(heads) * 128};

@@ -57,8 +57,9 @@ __device__ __forceinline__ PromptCosts costs(const PromptParams& p) {
   return p.k_scale ? PromptCosts{kPairCost, 2, 9, 20} : PromptCosts{kPairCost, 3, 12, 30};
 }
 // A call is cut into runs when its longest item costs `slack` more than an even share, which is about what a partial's way
-// through memory and the join take (6 drafts over 1,500 E4M3 keys: 27.1 us whole, 19.7 in runs; over 880 bf16 keys 19.2 and 16.4);
-// never where no item has more than so many blocks.
+// through memory and the join take (6 drafts over 1,500 E4M3 keys: 27.1 us whole, 19.7 in runs; over 880 bf16 keys 19.2 and 16.4).
+// Never where no item has more than so many blocks: such calls have no join launch either (8 drafts over 760 keys: bf16 16.2 us, with
+// runs and join 17.9, E4M3 18.4 and 18.9; over 640 keys 15.5 and 17.3, 18.2 and 20.4; over 890, seven blocks, 16.6 either way).
 constexpr int kWholeBlocks = 6;
 
 // Exclusive scan over the CTA (kPlanThreads threads); `sh` holds 32 values.
@@ -185,7 +186,9 @@ __global__ void __launch_bounds__(kPlanThreads) prompt_plan_kernel(PromptParams 
   total *= p.hkv;
   most = s_most;
   const bool split = p.part_o != nullptr && most > total / p.ctas + costs(p).slack;
-  const int runs = split ? static_cast<int>(min(total / s_cost, static_cast<long long>(p.ctas))) : 0;  // a block each at least
+  // A block's cost each at least.  Where an item's own cost passes a run's share several runs are cut back to the item's beginning
+  // below; all of them but the last are empty then.
+  const int runs = split ? static_cast<int>(min(total / s_cost, static_cast<long long>(p.ctas))) : 0;
   if (threadIdx.x == 0) {
     plan->n_items = items;
     plan->runs = runs;
@@ -504,7 +507,8 @@ struct Tiles<true> {
 // E4M3 codes of a tile (rows of 128 bytes, TMA's 128-byte swizzle) to fp16 in the layout in which TMA lands 16-bit rows;
 // exact.  128 threads, 16 codes at a time, four pieces in flight: shared memory answers in 150 clocks beside the MMAs.  Eight
 // lanes read a row, and those of its second half write their pieces in the other order, so that eight lanes' stores
-// meet all banks.  Rows from `valid` on become zeros (0 * NaN is NaN).
+// meet all banks.  Rows from `valid` on become zeros (0 * NaN is NaN).  (The decode kernel's widens one piece at a time: it
+// measured more in flight 2 to 8 % slower.)
 __device__ __forceinline__ void widen_tile(const uint8_t* codes, uint8_t* to, int thread, int valid) {
   const int chunk = thread & 7, half = chunk >> 2, x = (thread >> 3) & 7;  // x: the row mod 8, the same in every pass
   const uint32_t flip = half;
