@@ -18,14 +18,17 @@
 // rest would take half as much time again; l and lse sum the unrounded weights, everything else is fp32.
 //
 // E4M3 pages: K's codes are multiplied as they are (kind::f8f6f4), by queries that are two codes each; V's are widened to fp16
-// by four warps of their own, and P is fp16 (2^-11).  Widening K as well had those warps bound the kernel: 6.2 against 4.6 ms
-// for a 20,000-token prompt of 64/4 heads.
+// by four warps of their own, and P is fp16 (2^-11).  Widening K as well had those warps bound the kernel: 6.2 ms for a
+// 20,000-token prompt of 64/4 heads, which now takes 4.2.
 //
 // What bounds it.  A block takes a pair of tiles 2,048 clocks of MMAs, which also read shared memory at its full rate (128 bytes
-// a clock: S alone 64 KB per tile).  Measured 2,900 at 1.86 GHz: a warpgroup's chain of S, its way to the softmax (390),
-// the softmax (1,200), P's way back (180) and P V is longer than the other's MMAs.  A 20,000-token prompt of 64/4 heads:
-// 3.9 ms, 1,670 TFLOP/s, 97 % of what the library's matrix product holds under the power limit.  P V begun at half of P
-// shortens the chain and changes nothing there.
+// a clock: S alone 64 KB per tile).  Measured 2,900: a warpgroup's chain of S, its way to the softmax (390), the softmax
+// (1,200), P's way back (180) and P V is longer than the other's MMAs.  A 20,000-token prompt of 64/4 heads: 3.84 ms in a
+// burst (1,707 TFLOP/s); back to back for seconds 4.16 (1,577, at the 1,815 MHz that the power limit leaves it), where the library's
+// matrix product holds 1,748 (at 1,477 MHz, its pipe fuller).  P V begun at half of P shortens the chain and changes nothing there.
+//
+// What is rare (a reference that rises, logits above 2^10, V's scales far apart) is found by one vote a block: with two a 20,000-token
+// prompt over E4M3 pages took 4.9 ms instead of 4.5.
 //
 // An item of one tile (a tree of few drafts, the end of a prompt) would leave one warpgroup idle: its blocks go to the
 // two warpgroups in turn, each with its own m, l and O, merged at the end.
