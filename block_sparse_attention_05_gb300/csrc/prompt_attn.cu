@@ -38,6 +38,8 @@
 // crosses runs leaves (O, m, l) per run, which a join kernel merges.  A plan kernel decides from the lengths.
 #include <cuda_fp8.h>
 
+#include <atomic>
+
 #include "attn.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -1522,14 +1524,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prompt_join_kernel(PromptPara
 
 template <bool FP8>
 cudaError_t launch_attn(const PromptMaps& maps, const PromptParams& p, cudaStream_t stream) {
-  const cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  cudaError_t e = cudaFuncSetAttribute(prompt_attn_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(kPromptSmemBytes));
   if (e != cudaSuccess) return e;
   // the register reallocation's increases must fit in the launch allocation, or they would never complete
-  static const int regs = [] {
+  static std::atomic<int> built{0};  // registers of the kernel, once they have been read
+  int regs = built.load(std::memory_order_relaxed);
+  if (regs == 0) {
     cudaFuncAttributes fa{};
-    return cudaFuncGetAttributes(&fa, prompt_attn_kernel<FP8>) == cudaSuccess ? fa.numRegs : 0;
-  }();
+    e = cudaFuncGetAttributes(&fa, prompt_attn_kernel<FP8>);
+    if (e != cudaSuccess) return e;
+    built.store(regs = fa.numRegs, std::memory_order_relaxed);
+  }
   if (regs < PromptCfg<FP8>::kOtherRegs || regs * PromptCfg<FP8>::kThreads < PromptCfg<FP8>::kRegsNeeded) return cudaErrorInvalidConfiguration;
   return launch_pdl(prompt_attn_kernel<FP8>, dim3(p.ctas), dim3(PromptCfg<FP8>::kThreads), kPromptSmemBytes, stream, maps, p);
 }
