@@ -662,10 +662,11 @@ msa_status_t msa_tree_attn_paged_fp8(const msa_problem_t *problem, const void *q
  * Taking tokens back (rejected drafts): lengths is the caller's to shorten, and a
  * block counts as held as long as ceil(lengths / 128) reaches it.  The pages of the
  * blocks behind that are then in no list; before the next call the caller puts the
- * n pages back, in any order, where handed-out ones stood, free_pages[*taken - n] to
- * free_pages[*taken - 1], and lowers *taken by n.  Accepted drafts that do not lie
+ * n pages back (entries of -1 are none), in any order, where handed-out ones stood,
+ * free_pages[*taken - n] to free_pages[*taken - 1], and lowers *taken by n.  Accepted drafts that do not lie
  * together (a path through a tree) are written again with msa_append_paged(_fp8):
- * their rows of k and v, at the step's first slots. */
+ * their rows of k and v, at the step's first slots.  (A page's E4M3 scale that
+ * rejected drafts have raised stays.) */
 msa_status_t msa_extend_workspace_size(int32_t num_seqs, size_t *bytes);
 msa_status_t msa_extend_block_table(int32_t num_seqs, const int32_t *lengths, const int32_t *new_tokens,
                                     int64_t capacity, const int32_t *free_pages, int32_t num_free,
